@@ -10,6 +10,7 @@
 #include <mutex>
 #include <string>
 
+#include "api_internal.h"
 #include "launch.h"
 #include "wllm.h"
 
@@ -115,11 +116,19 @@ int decode_threads(int dtype, int head_dim) {
 }
 }  // namespace wllm
 
-using namespace wllm;
-
 namespace {
 
 thread_local std::string g_last_error;
+
+constexpr int kMaxDevices = 64;
+
+wllm::DeviceState g_devices[kMaxDevices];
+
+}  // namespace
+
+namespace wllm {
+
+std::mutex g_mutex;
 
 int fail(int status, const char* fmt, ...) {
   char buf[512];
@@ -134,21 +143,6 @@ int fail(int status, const char* fmt, ...) {
 int cuda_fail(cudaError_t e, const char* what) {
   return fail(WLLM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
-
-constexpr int kMaxDevices = 64;
-
-struct DeviceState {
-  bool ready = false;
-  int num_sms = 0;
-  int* err = nullptr;               // device error word
-  uint8_t* ws = nullptr;            // split-KV workspace
-  size_t ws_bytes = 0;
-  bool ws_owned = true;
-  size_t counter_bytes = 0;         // leading bytes reserved for arrival counters (kept zero)
-};
-
-std::mutex g_mutex;
-DeviceState g_devices[kMaxDevices];
 
 bool env_flag(const char* name) {
   const char* v = std::getenv(name);
@@ -250,6 +244,19 @@ bool same_shape(const wllm_tensor* a, const wllm_tensor* b) {
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool positive_finite(float x) { return x > 0.f && x < INFINITY; }
+
+bool env_is(const char* name, const char* value) {
+  const char* v = std::getenv(name);
+  return v != nullptr && std::strcmp(v, value) == 0;
+}
+
+}  // namespace wllm
+
+using namespace wllm;
+
+namespace {
 
 // --- TMA descriptors ---------------------------------------------------------
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -359,11 +366,6 @@ struct DecodePlan {
   size_t counter_bytes = 0, ml_bytes = 0, o_bytes = 0;  // all 0 when no sequence is split
 };
 
-bool env_is(const char* name, const char* value) {
-  const char* v = std::getenv(name);
-  return v != nullptr && std::strcmp(v, value) == 0;
-}
-
 // Variant, kernel, partition size and workspace layout of one launch over B
 // sequences.  `q_bulk_ok`: query rows are 16-byte aligned (bulk-copyable).
 // `kv_fp8`: E4M3 caches, which only the persistent kernel reads.
@@ -429,8 +431,6 @@ unsigned long long wllm_launch_count(void) { return g_launches.load(std::memory_
 }  // extern "C"
 
 namespace {
-
-bool positive_finite(float x) { return x > 0.f && x < INFINITY; }
 
 // Check the append arguments and fill `ap` (all but the error word).  Leaves
 // ap.num_tokens == 0 when there is nothing to write.  `kv_fp8`: the caches
