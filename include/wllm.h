@@ -331,6 +331,185 @@ int wllm_paged_attention_decode_noalloc(const wllm_tensor* out, const wllm_tenso
                                         const wllm_tensor* context_lens, int num_kv_heads,
                                         float scale, int block_size, wllm_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary append and block-sparse decode.
+ *
+ * There is no counterpart to these calls in the pages.  They are the steps
+ * around the decode that a layer needs (its keys are normalised and turned to
+ * their positions before they are cached) and a decode for long contexts that
+ * reads only the cache blocks that matter to the query:
+ *
+ *   wllm_rotate_and_cache                 norms, rotary positions, append
+ *   wllm_update_key_bounds                minimum and maximum of a block's keys
+ *   wllm_select_blocks                    blocks whose bounds allow large scores
+ *   wllm_paged_attention_decode_sparse    attention over those blocks
+ *
+ * None of them allocates, uses the device workspace or waits on the host, and
+ * their results do not depend on the order in which threads run; all can be
+ * captured in a CUDA graph.  Calls on one stream that follow one another see
+ * each other's results; calls on different streams share nothing but the
+ * tensors that the caller gives them.
+ * ------------------------------------------------------------------------- */
+
+typedef enum {
+  WLLM_ROTARY_HALVES = 0,   /* element i turns with element i + R/2          */
+  WLLM_ROTARY_ADJACENT = 1  /* element 2i turns with element 2i + 1          */
+} wllm_rotary_style;
+
+typedef struct {
+  int32_t style;        /* a wllm_rotary_style                                */
+  int32_t num_axes;     /* position axes, 1..4                                */
+  int32_t sections[4];  /* pairs turned by each axis, in order; they sum to   */
+                        /* R/2 (ignored with one axis)                        */
+  float eps;            /* of the norms, >= 0                                 */
+} wllm_rotary;
+
+/*
+ * Rotary append: per-head norms of query and key, rotary positions, the query
+ * written out, key and value written to their cache slots, in one pass.
+ *
+ *   q_out, q       [T][Hq][D]; key, value [T][Hkv][D]: one type (F32, F16 or
+ *                  BF16), last dimension contiguous, other strides free (e.g.
+ *                  slices of a fused projection).  q_out may be q itself;
+ *                  otherwise the two spans of memory must not meet, and q_out
+ *                  must not overlap key or value.
+ *   k_cache,
+ *   v_cache        [N_b][Hkv][bs][D] dense, same type.
+ *   slot_mapping   [T] I64 or I32, contiguous, as in wllm_reshape_and_cache.
+ *   positions      [T], or [num_axes][T] (rows contiguous), I64 or I32.
+ *   cos_sin        [P][R] F32, rows contiguous: row p holds the R/2 cosines,
+ *                  then the R/2 sines of position p's angles.  R <= D.
+ *   q_weight,
+ *   k_weight       [D] contiguous, F32 or the type of q (both alike), or NULL:
+ *                  no norm of the query or of the key.
+ *
+ * For every row x of a token's query and key heads
+ *   y = x * weight / sqrt(mean(x^2) + eps)   (y = x without a weight),
+ *   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)
+ * for the R/2 pairs of `style`, with the table row of the token's position on
+ * the pair's axis; elements from R on are not turned.  Everything is computed
+ * in binary32 and rounded once, when stored.  Values are copied bit for bit.
+ * A token with a negative slot is padding: its position is not read and
+ * neither its caches' rows nor its row of q_out is written.  A slot or position
+ * out of range sets bit 0 or 5 of the error word and leaves the token out (in
+ * check mode the call then returns WLLM_ERR_OUT_OF_RANGE; it also rejects
+ * duplicate slots before anything is written).  D and R multiples of 16 up to
+ * 256, bs a power of two.  Rows at 16-byte boundaries take vector accesses.
+ */
+int wllm_rotate_and_cache(const wllm_tensor* q_out, const wllm_tensor* q, const wllm_tensor* key,
+                          const wllm_tensor* value, const wllm_tensor* k_cache,
+                          const wllm_tensor* v_cache, const wllm_tensor* slot_mapping,
+                          const wllm_tensor* positions, const wllm_tensor* cos_sin,
+                          const wllm_tensor* q_weight, const wllm_tensor* k_weight,
+                          const wllm_rotary* how, wllm_stream stream);
+
+/*
+ * The same into E4M3 caches (8-byte aligned): key and value rows are stored as
+ * E4M3(fp32(x) * fp32(1 / scale)), where x is the turned key in binary32 (it is
+ * not rounded to q's type in between) or the value.
+ */
+int wllm_rotate_and_cache_fp8(const wllm_tensor* q_out, const wllm_tensor* q, const wllm_tensor* key,
+                              const wllm_tensor* value, const wllm_tensor* k_cache,
+                              const wllm_tensor* v_cache, const wllm_tensor* slot_mapping,
+                              const wllm_tensor* positions, const wllm_tensor* cos_sin,
+                              const wllm_tensor* q_weight, const wllm_tensor* k_weight,
+                              const wllm_rotary* how, float k_scale, float v_scale,
+                              wllm_stream stream);
+
+/*
+ * Bounds of the blocks that a step's new tokens filled.
+ *
+ *   key_bounds       [N_b][Hkv][2][D] dense, the type of k_cache, 16-byte
+ *                    aligned: [..][0][d] the least, [..][1][d] the greatest
+ *                    k[d] of the block's bs keys (both NaN if one is NaN).
+ *   k_cache          [N_b][Hkv][bs][D] dense; F32, F16, BF16 or FP8_E4M3 (codes;
+ *                    their bounds are codes too).
+ *   block_tables     [B][M_b] I32; context_lens [B] I32, as in the decode.
+ *   query_start_loc  [B+1] I32, contiguous: sequence b has n_b =
+ *                    query_start_loc[b+1] - query_start_loc[b] new tokens, the
+ *                    last n_b of its L_b = context_lens[b] cached ones.  NULL:
+ *                    one new token for every sequence that is not empty.
+ *
+ * Call it after the append.  Every block that holds bs tokens of sequence b
+ * now and did not before its n_b new ones gets its bounds; no other block's
+ * are touched.  Blocks filled by an earlier call (n_b = L_b: all of a
+ * sequence's) can be given again.  D 64, 128 or 256, bs a power of two in
+ * [8, 256].  Inconsistent lengths (bit 2) and table entries outside the pool
+ * (bit 1) are recorded and skipped.  Two sequences that name one block write
+ * the same bounds.
+ */
+int wllm_update_key_bounds(const wllm_tensor* key_bounds, const wllm_tensor* k_cache,
+                           const wllm_tensor* block_tables, const wllm_tensor* context_lens,
+                           const wllm_tensor* query_start_loc, int block_size, wllm_stream stream);
+
+/*
+ * The blocks to read for one query token per sequence.
+ *
+ *   selected      [B][Hkv][top] I32, written; rows contiguous.
+ *   q             [B][Hq][D]  F32, F16 or BF16, as the decode takes it.
+ *   key_bounds    as above; the type of q, or FP8_E4M3 with F16/BF16 queries.
+ *   block_tables, context_lens as in the decode.
+ *   num_sink      blocks kept at the start of a sequence, >= 0.
+ *   num_recent    blocks kept at its end, >= 1 (the last block may not have
+ *                 bounds yet); num_sink + num_recent <= top.
+ *
+ * For a sequence of n = ceil(L / bs) blocks and each kv head, selected gets
+ * the min(n, top) blocks (logical numbers: positions in the table row) that
+ * are the first num_sink, the last num_recent, and of the others those with
+ * the largest score
+ *   s_j = sum over the group's query heads and d of max(q_d lo_jd, q_d hi_jd),
+ * a sum of upper bounds of the heads' scores in block j (taken as up.hi_j +
+ * down.lo_j with the sums of the positive and of the negative query elements;
+ * a NaN, which a NaN or infinite bound gives, counts as +infinity).  Equal
+ * scores go to the lower block; the choice is that of the exact
+ * scores (binary64 decides between blocks whose binary32 scores are within
+ * their error of the border).  Blocks come in ascending order, then -1.
+ * Several query tokens of a sequence are several rows of q, block_tables and
+ * context_lens.  D 64, 128 or 256, bs a power of two in [8, 256]; tables of
+ * about 130,000 blocks at most.  Table entries outside the pool are recorded
+ * (bit 1) and scored as block 0, lengths outside [0, M_b bs] (bit 2) clamped.
+ */
+int wllm_select_blocks(const wllm_tensor* selected, const wllm_tensor* q,
+                       const wllm_tensor* key_bounds, const wllm_tensor* block_tables,
+                       const wllm_tensor* context_lens, int num_kv_heads, int block_size,
+                       int num_sink, int num_recent, wllm_stream stream);
+
+/*
+ * Paged decode attention over selected blocks.
+ *
+ *   selected  [B][Hkv][top] I32, rows contiguous: the blocks (logical numbers)
+ *             that the query heads of a kv head read, in any order.  Negative
+ *             entries are skipped; a block listed twice counts twice.
+ *   the rest  as in wllm_paged_attention_decode.
+ *
+ * out[b][h] = sum_t softmax_t(scale * q[b][h].k_t) v_t over the tokens t < L_b
+ * of the listed blocks; a row without any gets zeros.  With every block listed
+ * it is the decode.  Entries past the sequence's last block and table entries
+ * outside the pool are recorded (bit 1) and skipped; an empty sequence's list
+ * is not looked at.  D 64, 128 or 256.  F16/BF16 run on tensor cores with fp32
+ * accumulation, weights rounded to the type of q; F32 on fp32 FMA.  q rows may
+ * have any alignment of their elements.
+ */
+int wllm_paged_attention_decode_sparse(const wllm_tensor* out, const wllm_tensor* q,
+                                       const wllm_tensor* k_cache, const wllm_tensor* v_cache,
+                                       const wllm_tensor* block_tables,
+                                       const wllm_tensor* context_lens,
+                                       const wllm_tensor* selected, int num_kv_heads, float scale,
+                                       int block_size, wllm_stream stream);
+
+/*
+ * The same over E4M3 caches: K = code * k_scale, V = code * v_scale; q and out
+ * F16 or BF16 (bf16 queries are rounded to f16 for the products, as in
+ * wllm_paged_attention_decode_fp8).
+ */
+int wllm_paged_attention_decode_sparse_fp8(const wllm_tensor* out, const wllm_tensor* q,
+                                           const wllm_tensor* k_cache, const wllm_tensor* v_cache,
+                                           const wllm_tensor* block_tables,
+                                           const wllm_tensor* context_lens,
+                                           const wllm_tensor* selected, int num_kv_heads,
+                                           float scale, float k_scale, float v_scale,
+                                           int block_size, wllm_stream stream);
+
 /*
  * Bytes of device workspace that wllm_paged_attention_decode needs for these
  * sizes (0 when no sequence is split).  num_kv_heads is an argument because
@@ -369,7 +548,7 @@ int wllm_partition_tokens(int num_seqs, int num_q_heads, int num_kv_heads, int h
  * the regular calls and the one of wllm_paged_attention_decode_noalloc, OR-ed
  * together): bit 0 slot out of range, bit 1 block id out of range, bit 2
  * context length out of range, bit 3 duplicate slot (check mode), bit 4 a
- * bounded wait timed out.  Clearing also puts the scheduler and merge counters
+ * bounded wait timed out, bit 5 position out of range.  Clearing also puts the scheduler and merge counters
  * back to zero, which a launch that gave up on a wait may have left set.
  * Synchronises the device.  Returns -1 if it could not be read.
  */

@@ -17,7 +17,9 @@ __all__ = ["reshape_and_cache", "paged_attention_decode", "paged_attention_decod
            "load_library",
            "decode_step", "WllmError", "library_path", "BlockManager",
            "reshape_and_cache_fp8", "paged_attention_decode_fp8", "decode_step_fp8",
-           "paged_attention_prefill", "paged_attention_prefill_fp8"]
+           "paged_attention_prefill", "paged_attention_prefill_fp8",
+           "rotate_and_cache", "rotate_and_cache_fp8", "update_key_bounds", "select_blocks",
+           "paged_attention_decode_sparse", "paged_attention_decode_sparse_fp8"]
 
 
 def __getattr__(name):

@@ -27,6 +27,8 @@ EXPORTED = ("wllm_reshape_and_cache", "wllm_paged_attention_decode", "wllm_decod
             "wllm_reshape_and_cache_fp8", "wllm_paged_attention_decode_fp8", "wllm_decode_step_fp8",
             "wllm_paged_attention_prefill", "wllm_paged_attention_prefill_fp8",
             "wllm_paged_attention_decode_noalloc",
+            "wllm_rotate_and_cache", "wllm_rotate_and_cache_fp8", "wllm_update_key_bounds", "wllm_select_blocks",
+            "wllm_paged_attention_decode_sparse", "wllm_paged_attention_decode_sparse_fp8",
             "wllm_paged_attention_workspace_bytes", "wllm_set_workspace",
             "wllm_partition_tokens", "wllm_device_errors", "wllm_selftest_wait_timeout", "wllm_launch_count",
             "wllm_last_error", "wllm_version",
@@ -44,6 +46,14 @@ class WllmError(RuntimeError):
 class WllmTensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("ndim", ctypes.c_int32),
                 ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4)]
+
+
+class WllmRotary(ctypes.Structure):
+    _fields_ = [("style", ctypes.c_int32), ("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+                ("eps", ctypes.c_float)]
+
+
+_ROTARY_STYLE = {"halves": 0, "adjacent": 1}
 
 
 _lib = None
@@ -92,6 +102,20 @@ def load_library():
         lib.wllm_paged_attention_decode_noalloc.argtypes = [P, P, P, P, P, P, ctypes.c_int, ctypes.c_float,
                                                             ctypes.c_int, ctypes.c_void_p]
         lib.wllm_paged_attention_decode_noalloc.restype = ctypes.c_int
+        how = ctypes.POINTER(WllmRotary)
+        lib.wllm_rotate_and_cache.argtypes = [P] * 11 + [how, ctypes.c_void_p]
+        lib.wllm_rotate_and_cache.restype = ctypes.c_int
+        lib.wllm_rotate_and_cache_fp8.argtypes = [P] * 11 + [how, f32, f32, ctypes.c_void_p]
+        lib.wllm_rotate_and_cache_fp8.restype = ctypes.c_int
+        lib.wllm_update_key_bounds.argtypes = [P] * 5 + [ctypes.c_int, ctypes.c_void_p]
+        lib.wllm_update_key_bounds.restype = ctypes.c_int
+        lib.wllm_select_blocks.argtypes = [P] * 5 + [ctypes.c_int] * 4 + [ctypes.c_void_p]
+        lib.wllm_select_blocks.restype = ctypes.c_int
+        lib.wllm_paged_attention_decode_sparse.argtypes = [P] * 7 + [ctypes.c_int, f32, ctypes.c_int, ctypes.c_void_p]
+        lib.wllm_paged_attention_decode_sparse.restype = ctypes.c_int
+        lib.wllm_paged_attention_decode_sparse_fp8.argtypes = [P] * 7 + [ctypes.c_int, f32, f32, f32, ctypes.c_int,
+                                                                       ctypes.c_void_p]
+        lib.wllm_paged_attention_decode_sparse_fp8.restype = ctypes.c_int
         lib.wllm_paged_attention_workspace_bytes.argtypes = [ctypes.c_int] * 6
         lib.wllm_paged_attention_workspace_bytes.restype = ctypes.c_size_t
         lib.wllm_set_workspace.argtypes = [ctypes.c_void_p, ctypes.c_size_t]
@@ -135,15 +159,12 @@ def load_library():
 
 
 def describe(t: torch.Tensor) -> WllmTensor:
-    if t.dim() > 4:
+    n = t.dim()
+    if n > 4:
         raise ValueError("at most 4 dims")
-    d = WllmTensor()
-    d.data = t.data_ptr() if t.numel() > 0 else None
-    d.dtype = _DTYPE[t.dtype]
-    d.ndim = t.dim()
-    for i in range(t.dim()):
-        d.shape[i] = t.shape[i]
-        d.stride[i] = t.stride(i)
+    d = WllmTensor(t.data_ptr() if t.numel() > 0 else None, _DTYPE[t.dtype], n)
+    d.shape[:n] = t.shape
+    d.stride[:n] = t.stride()
     return d
 
 
@@ -274,6 +295,107 @@ def paged_attention_prefill_fp8(out, q, k_cache, v_cache, block_tables, context_
         _check(lib.wllm_paged_attention_prefill_fp8(*[ctypes.byref(a) for a in args], int(num_kv_heads),
                                                     float(scale), float(k_scale), float(v_scale),
                                                     int(block_size), _stream_handle(dev)))
+    return out
+
+
+def _rotate(name, tensors, q_weight, k_weight, eps, style, sections, scales):
+    if style not in _ROTARY_STYLE:
+        raise ValueError(f"style must be one of {sorted(_ROTARY_STYLE)}, got {style!r}")
+    sections = () if sections is None else tuple(int(n) for n in sections)
+    positions = tensors[7]
+    if sections and positions.dim() == 1 and len(sections) > 1:
+        raise ValueError("several sections need positions [axes, T]")
+    if not sections and positions.dim() == 2 and positions.shape[0] > 1:
+        raise ValueError("positions on several axes need sections")
+    if len(sections) > 4:
+        raise ValueError("at most 4 sections")
+    dev = _require_cuda(*tensors, *[w for w in (q_weight, k_weight) if w is not None])
+    how = WllmRotary(_ROTARY_STYLE[style], max(1, len(sections)))
+    how.sections[:len(sections)] = sections
+    how.eps = float(eps)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        args = [ctypes.byref(describe(x)) for x in tensors]
+        args += [None if w is None else ctypes.byref(describe(w)) for w in (q_weight, k_weight)]
+        _check(getattr(lib, name)(*args, ctypes.byref(how), *scales, _stream_handle(dev)))
+
+
+def rotate_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, *, q_weight=None,
+                     k_weight=None, eps: float = 1e-6, style: str = "halves", sections=None) -> torch.Tensor:
+    """Rotary append: per-head norms of q and key (where a weight [D] is given), rotary positions from the table
+    ``cos_sin`` [P,R] (cosines, then sines), query into ``q_out`` (may be ``q``), key and value to their slots.
+
+    ``positions`` is [T], or [axes,T] with ``sections`` naming the pairs that each axis turns.  ``style``:
+    "halves" pairs elements (i, i+R/2), "adjacent" (2i, 2i+1).  Returns ``q_out``."""
+    _rotate("wllm_rotate_and_cache", (q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin),
+            q_weight, k_weight, eps, style, sections, ())
+    return q_out
+
+
+def rotate_and_cache_fp8(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, k_scale: float,
+                         v_scale: float, *, q_weight=None, k_weight=None, eps: float = 1e-6, style: str = "halves",
+                         sections=None) -> torch.Tensor:
+    """rotate_and_cache into E4M3 caches: stores E4M3(x * (1/scale)) of the turned keys and of the values."""
+    _rotate("wllm_rotate_and_cache_fp8", (q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin),
+            q_weight, k_weight, eps, style, sections, (float(k_scale), float(v_scale)))
+    return q_out
+
+
+def update_key_bounds(key_bounds, k_cache, block_tables, context_lens, block_size: int,
+                      query_start_loc=None) -> torch.Tensor:
+    """Least and greatest key elements, ``key_bounds`` [N_b,Hkv,2,D], of every block that the new tokens filled:
+    the last ``query_start_loc[b+1] - query_start_loc[b]`` of each sequence, or one each.  Returns ``key_bounds``."""
+    tensors = [key_bounds, k_cache, block_tables, context_lens]
+    if query_start_loc is not None:
+        tensors.append(query_start_loc)
+    dev = _require_cuda(*tensors)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        args = [ctypes.byref(describe(x)) for x in tensors]
+        if query_start_loc is None:
+            args.append(None)
+        _check(lib.wllm_update_key_bounds(*args, int(block_size), _stream_handle(dev)))
+    return key_bounds
+
+
+def select_blocks(selected, q, key_bounds, block_tables, context_lens, num_kv_heads: int, block_size: int,
+                  num_sink: int = 0, num_recent: int = 1) -> torch.Tensor:
+    """The blocks that each sequence's query should read, ``selected`` [B,Hkv,top] int32 (ascending, then -1): the
+    first ``num_sink``, the last ``num_recent``, and those whose key bounds allow the largest scores."""
+    tensors = (selected, q, key_bounds, block_tables, context_lens)
+    dev = _require_cuda(*tensors)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        args = [ctypes.byref(describe(x)) for x in tensors]
+        _check(lib.wllm_select_blocks(*args, int(num_kv_heads), int(block_size), int(num_sink), int(num_recent),
+                                      _stream_handle(dev)))
+    return selected
+
+
+def paged_attention_decode_sparse(out, q, k_cache, v_cache, block_tables, context_lens, selected, num_kv_heads: int,
+                                  scale: float, block_size: int) -> torch.Tensor:
+    """Paged decode attention over the blocks listed in ``selected`` [B,Hkv,top] only; returns ``out``."""
+    tensors = (out, q, k_cache, v_cache, block_tables, context_lens, selected)
+    dev = _require_cuda(*tensors)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        args = [ctypes.byref(describe(x)) for x in tensors]
+        _check(lib.wllm_paged_attention_decode_sparse(*args, int(num_kv_heads), float(scale), int(block_size),
+                                                      _stream_handle(dev)))
+    return out
+
+
+def paged_attention_decode_sparse_fp8(out, q, k_cache, v_cache, block_tables, context_lens, selected,
+                                      num_kv_heads: int, scale: float, k_scale: float, v_scale: float,
+                                      block_size: int) -> torch.Tensor:
+    """paged_attention_decode_sparse over E4M3 caches (K = code * k_scale, V = code * v_scale); returns ``out``."""
+    tensors = (out, q, k_cache, v_cache, block_tables, context_lens, selected)
+    dev = _require_cuda(*tensors)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        args = [ctypes.byref(describe(x)) for x in tensors]
+        _check(lib.wllm_paged_attention_decode_sparse_fp8(*args, int(num_kv_heads), float(scale), float(k_scale),
+                                                          float(v_scale), int(block_size), _stream_handle(dev)))
     return out
 
 

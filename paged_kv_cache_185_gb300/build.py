@@ -25,7 +25,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwllm.so")
 
 SOURCES = ["api.cu", "append.cu", "decode_bf16.cu", "decode_f16.cu", "decode_f32.cu", "decode_f8_f16.cu",
-           "decode_f8_bf16.cu", "prefill.cu", "prefill_tc.cu", "block_manager.cpp"]
+           "decode_f8_bf16.cu", "prefill.cu", "prefill_tc.cu", "block_manager.cpp", "api_sparse.cu", "rotate.cu", "key_bounds.cu", "select.cu",
+           "sparse_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -19,6 +19,7 @@ enum : int {
   kErrLen = 4,
   kErrDupSlot = 8,
   kErrWaitTimeout = 16,
+  kErrPosition = 32,
 };
 
 constexpr unsigned kFullMask = 0xffffffffu;

@@ -152,6 +152,89 @@ int prefill_tc_grid_x(int64_t num_tokens, int64_t num_seqs, int group);
 int launch_prefill_tc(int dtype, int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap,
                       const PrefillParams& p, int grid_x, cudaStream_t stream);
 
+// The rotary append (rotate.cu): norms, rotary positions, query out, key and
+// value to their slots.  Strides in elements.
+constexpr int kMaxRotaryAxes = 4;
+struct RotateParams {
+  void* q_out;
+  const void* q;
+  const void* key;
+  const void* value;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  const void* slots;
+  const void* positions;          // [axes][T]
+  const float* cos_sin;           // [num_positions][rot_dim]: cosines, then sines
+  const void* q_weight;           // [D] or null
+  const void* k_weight;
+  int64_t q_st, q_sh, key_st, key_sh, val_st, val_sh, qo_st, qo_sh;
+  int64_t pos_sa;                 // elements between two axes' positions
+  int64_t table_stride, num_positions, num_slots;
+  int slots_are_i64, pos_are_i64;
+  int num_tokens, num_q_heads, num_kv_heads, head_dim, rot_dim, log2_bs;
+  int num_axes, section_end[kMaxRotaryAxes];  // pairs below section_end[a] and not below section_end[a-1] turn by axis a
+  int adjacent;                   // pairs (2p, 2p+1) instead of (p, p + R/2)
+  int src_dtype, weight_dtype;    // wllm_dtype codes
+  int kv_fp8;
+  int vec, weight_vec, table_vec; // 16-byte accesses are aligned
+  int row_lanes, warps_per_token; // set by launch_rotate
+  float eps, inv_dim, k_inv, v_inv;
+  int* err;
+};
+int launch_rotate(RotateParams p, int num_sms, cudaStream_t stream);
+
+// Minimum and maximum of the keys of every block that new tokens filled
+// (key_bounds.cu).  A null query_start_loc means one new token a sequence.
+struct BoundsParams {
+  uint8_t* bounds;                // [N_b][Hkv][2][D] of the cache's type
+  const uint8_t* k_cache;
+  const int32_t* block_tables;
+  int64_t bt_stride;
+  const int32_t* context_lens;
+  const int32_t* query_start_loc;
+  int num_seqs, num_kv_heads, num_blocks, log2_bs;
+  int max_tokens;                 // the most a block table row can name
+  int* err;
+};
+int launch_key_bounds(int dtype, int head_dim, const BoundsParams& p, int num_sms, cudaStream_t stream);
+
+// The blocks that a decode has to read (select.cu), by their key bounds.
+struct SelectParams {
+  int32_t* selected;              // [B][Hkv][top]
+  int64_t sel_sb, sel_sh;
+  const void* q;                  // [B][Hq][D]
+  int64_t q_sb, q_sh;
+  const uint8_t* bounds;          // [N_b][Hkv][2][D]
+  const int32_t* block_tables;
+  int64_t bt_stride;
+  const int32_t* context_lens;
+  int num_seqs, num_kv_heads, group, num_blocks, log2_bs, max_tokens;
+  int top, sink, recent;
+  int share;                      // scores a CTA has room for (set by launch_select)
+  int* err;
+};
+int select_max_blocks(int head_dim);
+int launch_select(int dtype, int bounds_dtype, int head_dim, SelectParams p, int max_blocks, int num_sms,
+                  cudaStream_t stream);
+
+// Decode attention over the listed blocks (sparse_decode.cu).
+struct SparseParams {
+  void* out;                      // [B][Hq][D]
+  const void* q;
+  int64_t q_sb, q_sh, o_sb, o_sh; // strides (elements)
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const int32_t* block_tables;
+  int64_t bt_stride;
+  const int32_t* context_lens;
+  const int32_t* selected;        // [B][Hkv][top]
+  int64_t sel_sb, sel_sh;
+  int num_seqs, num_kv_heads, group, num_head_tiles, num_blocks, log2_bs, max_tokens, top;
+  float scale_log2, v_scale;
+  int* err;
+};
+int launch_sparse_decode(int dtype, bool kv_fp8, int head_dim, SparseParams p, int num_sms, cudaStream_t stream);
+
 // Check-mode kernels: record index errors in the device error word.
 int launch_check_decode(const int32_t* block_tables, int64_t bt_stride,
                         const int32_t* context_lens, int num_seqs, int max_blocks,
