@@ -25,5 +25,6 @@ __all__ = ["reshape_and_cache", "paged_attention_decode", "paged_attention_decod
 def __getattr__(name):
     if name in __all__:
         from . import binding
-        return getattr(binding, name)
+        globals()[name] = found = getattr(binding, name)
+        return found
     raise AttributeError(name)

@@ -1,7 +1,8 @@
 """ctypes binding over libwllm.so (C ABI in include/wllm.h).
 
 Argument marshalling only: each call turns torch tensors into ``wllm_tensor``
-descriptors (device pointer, dtype code, sizes, strides in elements), passes
+descriptors (device pointer, dtype code, sizes, strides in elements; the
+compiled module ``_describe`` fills them), passes
 the current CUDA stream, and raises ``WllmError`` on a non-zero status.  Every
 step of the computation runs in the library's CUDA kernels; there is no CPU
 path.  Loading fails loudly when the library has not been built.
@@ -57,6 +58,8 @@ _ROTARY_STYLE = {"halves": 0, "adjacent": 1}
 
 
 _lib = None
+_entries = {}    # entry points that take tensors first: name -> function taking descriptor addresses
+_describe = None  # _describe.describe
 _lock = threading.Lock()
 
 
@@ -66,7 +69,7 @@ def library_path() -> str:
 
 def load_library():
     """Load libwllm.so (raises if it is missing: build it with ``build()`` first)."""
-    global _lib
+    global _lib, _describe
     if _lib is not None:
         return _lib
     with _lock:
@@ -154,18 +157,18 @@ def load_library():
         lib.wllm_bm_num_cached_blocks.restype = i64
         lib.wllm_bm_block_ref.argtypes = [vp, i32]
         lib.wllm_bm_block_ref.restype = ctypes.c_int
+        from . import _describe as module
+        by_address = ctypes.CDLL(_LIB_PATH)
+        for name in EXPORTED:
+            f = getattr(lib, name)
+            if f.argtypes and f.argtypes[0] is P:
+                g = getattr(by_address, name)
+                g.argtypes = [ctypes.c_void_p if a in (P, how) else a for a in f.argtypes]
+                g.restype = f.restype
+                _entries[name] = g
+        _describe = module.describe
         _lib = lib
     return _lib
-
-
-def describe(t: torch.Tensor) -> WllmTensor:
-    n = t.dim()
-    if n > 4:
-        raise ValueError("at most 4 dims")
-    d = WllmTensor(t.data_ptr() if t.numel() > 0 else None, _DTYPE[t.dtype], n)
-    d.shape[:n] = t.shape
-    d.stride[:n] = t.stride()
-    return d
 
 
 def _stream_handle(device) -> int:
@@ -177,35 +180,32 @@ def _check(rc: int) -> None:
         raise WllmError(rc, load_library().wllm_last_error().decode())
 
 
-def _require_cuda(*ts):
-    for t in ts:
-        if not t.is_cuda:
-            raise ValueError("all tensors must be CUDA tensors (the library has no CPU path)")
-    dev = ts[0].device
-    for t in ts:
-        if t.device != dev:
-            raise ValueError("all tensors must be on one device")
-    return dev
+def _call(name: str, tensors, *scalars) -> None:
+    """Entry point ``name`` on ``tensors`` (None: not given) and ``scalars``, on the current stream of the tensors'
+    device.  Host tensors, or tensors of several devices, raise ValueError."""
+    if _lib is None:
+        load_library()
+    owner, dev, *descriptors = _describe(tensors)  # `owner` holds the descriptors until the call returns
+    f = _entries[name]
+    if dev == torch.cuda.current_device():
+        rc = f(*descriptors, *scalars, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*descriptors, *scalars, torch._C._cuda_getCurrentRawStream(dev))
+    if rc != WLLM_OK:
+        _check(rc)
 
 
 def reshape_and_cache(key, value, k_cache, v_cache, slot_mapping) -> None:
     """KV append: scatter key/value [T,Hkv,D] into caches [N_b,Hkv,bs,D] at ``slot_mapping``."""
-    dev = _require_cuda(key, value, k_cache, v_cache, slot_mapping)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [describe(x) for x in (key, value, k_cache, v_cache, slot_mapping)]
-        _check(lib.wllm_reshape_and_cache(*[ctypes.byref(a) for a in args], _stream_handle(dev)))
+    _call("wllm_reshape_and_cache", (key, value, k_cache, v_cache, slot_mapping))
 
 
 def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens,
                            num_kv_heads: int, scale: float, block_size: int) -> torch.Tensor:
     """Paged decode attention into ``out`` [B,Hq,D]; returns ``out``."""
-    dev = _require_cuda(out, q, k_cache, v_cache, block_tables, context_lens)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [describe(x) for x in (out, q, k_cache, v_cache, block_tables, context_lens)]
-        _check(lib.wllm_paged_attention_decode(*[ctypes.byref(a) for a in args], int(num_kv_heads),
-                                               float(scale), int(block_size), _stream_handle(dev)))
+    _call("wllm_paged_attention_decode", (out, q, k_cache, v_cache, block_tables, context_lens),
+          int(num_kv_heads), float(scale), int(block_size))
     return out
 
 
@@ -213,12 +213,8 @@ def paged_attention_decode_noalloc(out, q, k_cache, v_cache, block_tables, conte
                                    num_kv_heads: int, scale: float, block_size: int) -> torch.Tensor:
     """Paged decode attention that allocates no device memory (fixed scratch
     inside the library; see wllm_paged_attention_decode_noalloc in wllm.h)."""
-    dev = _require_cuda(out, q, k_cache, v_cache, block_tables, context_lens)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [describe(x) for x in (out, q, k_cache, v_cache, block_tables, context_lens)]
-        _check(lib.wllm_paged_attention_decode_noalloc(*[ctypes.byref(a) for a in args], int(num_kv_heads),
-                                                       float(scale), int(block_size), _stream_handle(dev)))
+    _call("wllm_paged_attention_decode_noalloc", (out, q, k_cache, v_cache, block_tables, context_lens),
+          int(num_kv_heads), float(scale), int(block_size))
     return out
 
 
@@ -226,61 +222,37 @@ def decode_step(out, q, key, value, k_cache, v_cache, slot_mapping, block_tables
                 num_kv_heads: int, scale: float, block_size: int) -> torch.Tensor:
     """One decode step of one layer: append this step's K/V, then attend (one
     fused launch where the kernel allows; see wllm_decode_step)."""
-    dev = _require_cuda(out, q, key, value, k_cache, v_cache, slot_mapping, block_tables, context_lens)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [describe(x) for x in (out, q, key, value, k_cache, v_cache, slot_mapping, block_tables,
-                                      context_lens)]
-        _check(lib.wllm_decode_step(*[ctypes.byref(a) for a in args], int(num_kv_heads), float(scale),
-                                    int(block_size), _stream_handle(dev)))
+    _call("wllm_decode_step", (out, q, key, value, k_cache, v_cache, slot_mapping, block_tables, context_lens),
+          int(num_kv_heads), float(scale), int(block_size))
     return out
 
 
 def reshape_and_cache_fp8(key, value, k_cache, v_cache, slot_mapping, k_scale: float, v_scale: float) -> None:
     """KV append into E4M3 caches (uint8 or float8_e4m3fn): stores E4M3(x * (1/scale))."""
-    dev = _require_cuda(key, value, k_cache, v_cache, slot_mapping)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [describe(x) for x in (key, value, k_cache, v_cache, slot_mapping)]
-        _check(lib.wllm_reshape_and_cache_fp8(*[ctypes.byref(a) for a in args], float(k_scale), float(v_scale),
-                                              _stream_handle(dev)))
+    _call("wllm_reshape_and_cache_fp8", (key, value, k_cache, v_cache, slot_mapping), float(k_scale), float(v_scale))
 
 
 def paged_attention_decode_fp8(out, q, k_cache, v_cache, block_tables, context_lens, num_kv_heads: int,
                                scale: float, k_scale: float, v_scale: float, block_size: int) -> torch.Tensor:
     """Paged decode attention over E4M3 caches (K = code * k_scale, V = code * v_scale); returns ``out``."""
-    dev = _require_cuda(out, q, k_cache, v_cache, block_tables, context_lens)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [describe(x) for x in (out, q, k_cache, v_cache, block_tables, context_lens)]
-        _check(lib.wllm_paged_attention_decode_fp8(*[ctypes.byref(a) for a in args], int(num_kv_heads),
-                                                   float(scale), float(k_scale), float(v_scale), int(block_size),
-                                                   _stream_handle(dev)))
+    _call("wllm_paged_attention_decode_fp8", (out, q, k_cache, v_cache, block_tables, context_lens),
+          int(num_kv_heads), float(scale), float(k_scale), float(v_scale), int(block_size))
     return out
 
 
 def decode_step_fp8(out, q, key, value, k_cache, v_cache, slot_mapping, block_tables, context_lens,
                     num_kv_heads: int, scale: float, k_scale: float, v_scale: float, block_size: int) -> torch.Tensor:
     """decode_step over E4M3 caches: the append quantises with the same scales the attention reads back."""
-    dev = _require_cuda(out, q, key, value, k_cache, v_cache, slot_mapping, block_tables, context_lens)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [describe(x) for x in (out, q, key, value, k_cache, v_cache, slot_mapping, block_tables,
-                                      context_lens)]
-        _check(lib.wllm_decode_step_fp8(*[ctypes.byref(a) for a in args], int(num_kv_heads), float(scale),
-                                        float(k_scale), float(v_scale), int(block_size), _stream_handle(dev)))
+    _call("wllm_decode_step_fp8", (out, q, key, value, k_cache, v_cache, slot_mapping, block_tables, context_lens),
+          int(num_kv_heads), float(scale), float(k_scale), float(v_scale), int(block_size))
     return out
 
 
 def paged_attention_prefill(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
                             num_kv_heads: int, scale: float, block_size: int) -> torch.Tensor:
     """Chunked-prefill paged attention into ``out`` [T,Hq,D] (packed chunks, causal); returns ``out``."""
-    dev = _require_cuda(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [describe(x) for x in (out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc)]
-        _check(lib.wllm_paged_attention_prefill(*[ctypes.byref(a) for a in args], int(num_kv_heads),
-                                                float(scale), int(block_size), _stream_handle(dev)))
+    _call("wllm_paged_attention_prefill", (out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc),
+          int(num_kv_heads), float(scale), int(block_size))
     return out
 
 
@@ -288,13 +260,8 @@ def paged_attention_prefill_fp8(out, q, k_cache, v_cache, block_tables, context_
                                 num_kv_heads: int, scale: float, k_scale: float, v_scale: float,
                                 block_size: int) -> torch.Tensor:
     """Chunked-prefill paged attention over E4M3 caches (K = code * k_scale, V = code * v_scale)."""
-    dev = _require_cuda(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [describe(x) for x in (out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc)]
-        _check(lib.wllm_paged_attention_prefill_fp8(*[ctypes.byref(a) for a in args], int(num_kv_heads),
-                                                    float(scale), float(k_scale), float(v_scale),
-                                                    int(block_size), _stream_handle(dev)))
+    _call("wllm_paged_attention_prefill_fp8", (out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc),
+          int(num_kv_heads), float(scale), float(k_scale), float(v_scale), int(block_size))
     return out
 
 
@@ -309,15 +276,10 @@ def _rotate(name, tensors, q_weight, k_weight, eps, style, sections, scales):
         raise ValueError("positions on several axes need sections")
     if len(sections) > 4:
         raise ValueError("at most 4 sections")
-    dev = _require_cuda(*tensors, *[w for w in (q_weight, k_weight) if w is not None])
     how = WllmRotary(_ROTARY_STYLE[style], max(1, len(sections)))
     how.sections[:len(sections)] = sections
     how.eps = float(eps)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [ctypes.byref(describe(x)) for x in tensors]
-        args += [None if w is None else ctypes.byref(describe(w)) for w in (q_weight, k_weight)]
-        _check(getattr(lib, name)(*args, ctypes.byref(how), *scales, _stream_handle(dev)))
+    _call(name, (*tensors, q_weight, k_weight), ctypes.byref(how), *scales)
 
 
 def rotate_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, *, q_weight=None,
@@ -345,16 +307,7 @@ def update_key_bounds(key_bounds, k_cache, block_tables, context_lens, block_siz
                       query_start_loc=None) -> torch.Tensor:
     """Least and greatest key elements, ``key_bounds`` [N_b,Hkv,2,D], of every block that the new tokens filled:
     the last ``query_start_loc[b+1] - query_start_loc[b]`` of each sequence, or one each.  Returns ``key_bounds``."""
-    tensors = [key_bounds, k_cache, block_tables, context_lens]
-    if query_start_loc is not None:
-        tensors.append(query_start_loc)
-    dev = _require_cuda(*tensors)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [ctypes.byref(describe(x)) for x in tensors]
-        if query_start_loc is None:
-            args.append(None)
-        _check(lib.wllm_update_key_bounds(*args, int(block_size), _stream_handle(dev)))
+    _call("wllm_update_key_bounds", (key_bounds, k_cache, block_tables, context_lens, query_start_loc), int(block_size))
     return key_bounds
 
 
@@ -362,26 +315,16 @@ def select_blocks(selected, q, key_bounds, block_tables, context_lens, num_kv_he
                   num_sink: int = 0, num_recent: int = 1) -> torch.Tensor:
     """The blocks that each sequence's query should read, ``selected`` [B,Hkv,top] int32 (ascending, then -1): the
     first ``num_sink``, the last ``num_recent``, and those whose key bounds allow the largest scores."""
-    tensors = (selected, q, key_bounds, block_tables, context_lens)
-    dev = _require_cuda(*tensors)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [ctypes.byref(describe(x)) for x in tensors]
-        _check(lib.wllm_select_blocks(*args, int(num_kv_heads), int(block_size), int(num_sink), int(num_recent),
-                                      _stream_handle(dev)))
+    _call("wllm_select_blocks", (selected, q, key_bounds, block_tables, context_lens),
+          int(num_kv_heads), int(block_size), int(num_sink), int(num_recent))
     return selected
 
 
 def paged_attention_decode_sparse(out, q, k_cache, v_cache, block_tables, context_lens, selected, num_kv_heads: int,
                                   scale: float, block_size: int) -> torch.Tensor:
     """Paged decode attention over the blocks listed in ``selected`` [B,Hkv,top] only; returns ``out``."""
-    tensors = (out, q, k_cache, v_cache, block_tables, context_lens, selected)
-    dev = _require_cuda(*tensors)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [ctypes.byref(describe(x)) for x in tensors]
-        _check(lib.wllm_paged_attention_decode_sparse(*args, int(num_kv_heads), float(scale), int(block_size),
-                                                      _stream_handle(dev)))
+    _call("wllm_paged_attention_decode_sparse", (out, q, k_cache, v_cache, block_tables, context_lens, selected),
+          int(num_kv_heads), float(scale), int(block_size))
     return out
 
 
@@ -389,13 +332,8 @@ def paged_attention_decode_sparse_fp8(out, q, k_cache, v_cache, block_tables, co
                                       num_kv_heads: int, scale: float, k_scale: float, v_scale: float,
                                       block_size: int) -> torch.Tensor:
     """paged_attention_decode_sparse over E4M3 caches (K = code * k_scale, V = code * v_scale); returns ``out``."""
-    tensors = (out, q, k_cache, v_cache, block_tables, context_lens, selected)
-    dev = _require_cuda(*tensors)
-    lib = load_library()
-    with torch.cuda.device(dev):
-        args = [ctypes.byref(describe(x)) for x in tensors]
-        _check(lib.wllm_paged_attention_decode_sparse_fp8(*args, int(num_kv_heads), float(scale), float(k_scale),
-                                                          float(v_scale), int(block_size), _stream_handle(dev)))
+    _call("wllm_paged_attention_decode_sparse_fp8", (out, q, k_cache, v_cache, block_tables, context_lens, selected),
+          int(num_kv_heads), float(scale), float(k_scale), float(v_scale), int(block_size))
     return out
 
 

@@ -1,4 +1,5 @@
-"""Build libwllm.so (the sm_103a CUDA library behind include/wllm.h) in-tree.
+"""Build libwllm.so (the sm_103a CUDA library behind include/wllm.h) and the
+binding's _describe.so (descriptors of torch tensors) in-tree.
 
     python -m paged_kv_cache_185_gb300.build [--force] [--verbose]
 
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwllm.so")
+DESCRIBE = os.path.join(PKG, "_describe.so")
 
 SOURCES = ["api.cu", "append.cu", "decode_bf16.cu", "decode_f16.cu", "decode_f32.cu", "decode_f8_f16.cu",
            "decode_f8_bf16.cu", "prefill.cu", "prefill_tc.cu", "block_manager.cpp", "api_sparse.cu", "rotate.cu", "key_bounds.cu", "select.cu",
@@ -45,14 +48,14 @@ def _inputs():
     files = [os.path.join(CSRC, s) for s in SOURCES]
     files += glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     files += glob.glob(os.path.join(CSRC, "*.inc")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-    files.append(os.path.abspath(__file__))
+    files += [os.path.join(CSRC, "describe.cpp"), os.path.abspath(__file__)]
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(DESCRIBE)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(DESCRIBE))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -72,8 +75,25 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    def describe_module():
+        """The binding's CPython module: one translation unit against torch's headers."""
+        import torch
+        home = os.path.dirname(os.path.abspath(torch.__file__))
+        libs = os.path.join(home, "lib")
+        tmp = DESCRIBE + f".{os.getpid()}.tmp"
+        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+               "-I", sysconfig.get_paths()["include"], "-I", os.path.join(home, "include"),
+               "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(CSRC, "describe.cpp"), "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+               "-Wl,-rpath," + libs]
+        return tmp, subprocess.run(cmd, capture_output=True, text=True)
+
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        described = ex.submit(describe_module)
         results = list(ex.map(compile_one, SOURCES))
+        describe_tmp, r = described.result()
+    results.append(("describe.cpp", None, r))
     failed = False
     for src, _, r in results:
         if verbose or ptxas_verbose or r.returncode != 0:
@@ -82,13 +102,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if failed:
         raise RuntimeError("nvcc failed")
     tmp = LIB + f".{os.getpid()}.tmp"
-    link = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *[o for _, o, _ in results],
+    link = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *[o for _, o, _ in results if o is not None],
             "-Xlinker", "-rpath," + _cuda_lib_dir(nvcc), "-Xlinker", "-z,defs"]
     r = subprocess.run(link, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
+    os.replace(describe_tmp, DESCRIBE)
     return LIB
 
 
