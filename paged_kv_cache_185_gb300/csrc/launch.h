@@ -210,7 +210,7 @@ struct SelectParams {
   const int32_t* context_lens;
   int num_seqs, num_kv_heads, group, num_blocks, log2_bs, max_tokens;
   int top, sink, recent;
-  int share;                      // scores a CTA has room for (set by launch_select)
+  int room, longest_first;        // set by launch_select: scores a row has room for; launch order
   int* err;
 };
 int select_max_blocks(int head_dim);

@@ -9,25 +9,43 @@
 // Kept are the first `sink` blocks, the last `recent` ones and, of the others,
 // those with the largest s_j (NaN as +inf, ties to the lowest j), top in all.
 //
-// The scores are summed in binary32, each with an error of at most
-//   E = c u sum_i |w_i b_i|,  u = 2^-24, c = G + 44
-// (G - 1 roundings in w, a chain of 32 fused products, at most 5 sums across
-// lanes, some spare), so blocks whose scores differ by more than 2 E are in
-// their true order.  The choice between the few blocks that lie within 2 E of
-// the border is made from their scores in binary64, where the products of
-// 16-bit elements and their sums are exact for all but extreme exponents: the
-// selection is the definition's, whatever the order of the sums.
+// The scores are summed in binary32 with an error of at most
+//   E = c 2^-24 sum_i |w_i b_i|,
+// so blocks whose scores differ by more than 2 E are in their true order.  The
+// choice between the few blocks that lie within 2 E of the border is made from
+// their scores in binary64, where the products of 16-bit elements and their
+// sums are exact for all but extreme exponents: the selection is the
+// definition's, whatever the order of the sums.
 //
-// Work split: a cluster of up to 8 CTAs per (sequence, kv head), each with a
-// contiguous share of the blocks, so a long row is on many SMs and the
-// selection still needs neither a second launch nor a workspace.  D/16 lanes
-// read a block's 2D bounds, 16 bytes a lane and load, with their 32 weights in
-// registers.  The cluster then finds the border with one 1024-bin histogram
-// of the scores between their extremes, settles the border bin in binary64,
-// and writes the chosen blocks in ascending order.  Bound: memory, the bounds
+// 16-bit and E4M3 bounds are scored on tensor cores (mma.sync m16n8k16): 16
+// blocks' bounds are the A operand, straight from global memory, and B's first
+// three columns are the weights split into three 16-bit words whose sum has
+// their 24 bits, so every product is exact.  An instruction adds 16 products to
+// the running sum; with at least 22 bits kept of each term that is an error of
+// at most 17 * 2^-22 of the magnitudes in it.  Two instructions at a time start
+// from zero and their sums are added in binary32, so those magnitudes are two
+// steps' and not the whole row's: 136 2^-24 of all of them, 2D/32 additions,
+// the sum of the columns and the G additions of a weight: c = G + 136 + 2D/32 + 8
+// (one chain over the row would need 68 for each of its 2D/16 instructions, and
+// with it 6 times as many binary64 scores).  E4M3 codes are
+// widened to f16, exactly; three f16 words, scaled so that the largest weight is
+// near 2^14, leave off at most 2^-38 of it, which is far inside the same c.
+// F32 bounds take binary32 FMA: c = G + 44 (chains of 32, 5 sums across lanes).
+//
+// Work split: a cluster of 1 to 8 CTAs per (sequence, kv head), each with a
+// share of the blocks, so a long row is on many SMs and the selection still
+// needs neither a second launch nor a workspace.  A warp has 16 blocks' bounds
+// in flight, 16 bytes a lane and load; the scores go straight to the first
+// CTA's shared memory.  That CTA alone finds the border with one 1024-bin
+// histogram between the extremes, settles the blocks at the border in binary64
+// (a handful, a warp each) and writes the chosen ones in ascending order: one
+// barrier of the cluster in all, where every step shared by its CTAs would cost
+// another (the first form had six, 10 us of them).  Bound: memory, the bounds
 // are read once.
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
+
+#include <limits.h>
 
 #include <atomic>
 #include <type_traits>
@@ -44,24 +62,20 @@ namespace {
 constexpr int kSelectThreads = 256;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 1024;
-constexpr int kWindow = 512;          // border blocks ranked in one CTA; more go through the digit passes
+constexpr int kWindow = 256;          // border blocks ranked against each other; more go through digit passes
 constexpr int kMaxCluster = 8;
 
 struct SelectShared {
-  float stat[kMaxCluster][4];         // per CTA: smallest score, largest, bound on the sum of magnitudes, flag
+  float stat[kMaxCluster * kSelectWarps][4];  // per warp: smallest score, largest, bound on the magnitudes, flag
   uint32_t hist[kBins];
-  uint32_t digits[2][256];
   uint32_t warp_sum[kSelectWarps];
-  float warp_stat[kSelectWarps][4];
-  unsigned long long win_key[kWindow];
-  int win_at[kWindow];
-  int win_count;                      // rank 0: border blocks of the cluster
-  int sure_count;                     // rank 0: blocks above the border
-  int my_sure, my_win;
-  unsigned long long cut_key;         // last border block that is kept: its key and index
-  int cut_at;
-  int found_bin, found_above, found_count;
-  int picked[kMaxCluster];            // per CTA, for the offsets of the output
+  double win_score[kWindow];
+  float near_score[kWindow];          // scores around the border and their blocks
+  int near_at[kWindow];
+  int win_at[kWindow];                // those within the error of the border
+  int near_count, win_count, sure_count;
+  int found_bin, found_above;
+  float border;
 };
 
 // Doubles (without NaN) to integers of the same order.
@@ -69,71 +83,6 @@ __device__ __forceinline__ unsigned long long ordered(double x) {
   const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(x + 0.0));  // -0 is 0
   return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
 }
-
-// 16 bytes of bounds as floats.
-template <typename T>
-struct Bounds16;
-template <>
-struct Bounds16<float> {
-  static constexpr int kN = 4;
-  static __device__ __forceinline__ void open(const uint4& x, float (&f)[4], float& most) {
-    f[0] = __uint_as_float(x.x), f[1] = __uint_as_float(x.y), f[2] = __uint_as_float(x.z), f[3] = __uint_as_float(x.w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(f[i]));
-  }
-};
-template <>
-struct Bounds16<__half> {
-  static constexpr int kN = 8;
-  static __device__ __forceinline__ void open(const uint4& x, float (&f)[8], float& most) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    __half2 m = __float2half2_rn(0.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 h = *reinterpret_cast<const __half2*>(&w[i]);
-      const float2 v = __half22float2(h);
-      f[2 * i] = v.x, f[2 * i + 1] = v.y;
-      m = __hmax2(m, __habs2(h));
-    }
-    most = fmaxf(most, fmaxf(__low2float(m), __high2float(m)));
-  }
-};
-template <>
-struct Bounds16<__nv_bfloat16> {
-  static constexpr int kN = 8;
-  static __device__ __forceinline__ void open(const uint4& x, float (&f)[8], float& most) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    __nv_bfloat162 m = __float2bfloat162_rn(0.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
-    }
-    most = fmaxf(most, fmaxf(__low2float(m), __high2float(m)));
-  }
-};
-template <>
-struct Bounds16<uint8_t> {
-  static constexpr int kN = 16;
-  static __device__ __forceinline__ void open(const uint4& x, float (&f)[16], float& most) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    __half2 m = __float2half2_rn(0.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t y[2];
-      e4m3x4_to_f16x2x2(w[i], y[0], y[1]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const __half2 h = *reinterpret_cast<const __half2*>(&y[e]);
-        const float2 v = __half22float2(h);
-        f[4 * i + 2 * e] = v.x, f[4 * i + 2 * e + 1] = v.y;
-        m = __hmax2(m, __habs2(h));
-      }
-    }
-    most = fmaxf(most, fmaxf(__low2float(m), __high2float(m)));
-  }
-};
 
 __device__ __forceinline__ float element(const uint8_t* base, int i, uint8_t) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw(base[i], __NV_E4M3);
@@ -167,16 +116,414 @@ __device__ __forceinline__ uint32_t block_scan(SelectShared& sh, uint32_t x, uin
   return before + y - x;
 }
 
+// A candidate's score by 8 lanes, four candidates a warp at a time, as the time
+// is that of their loads.  All lanes call it.  EXACT: in binary64.  Otherwise as
+// the sum of two binary32 numbers: products with their rounding errors (fma),
+// sums with theirs (Knuth's two-sum), the errors added up in binary32.  Those
+// additions are off by at most 2^-24 of a sum of errors of at most n 2^-24 A
+// each, n <= 70 of them: under 2^-35 A in all, A = sum_i |w_i b_i|.  (Binary64
+// runs at a 64th of binary32's rate here: a dozen exact scores took 15 us.)
+template <typename B, int D, bool EXACT>
+__device__ __forceinline__ double fine_score(const uint8_t* src, const float2* w, int lane) {
+  constexpr int kE = 16 / static_cast<int>(sizeof(B)), kLoads = 2 * D / (8 * kE);
+  uint4 x[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(src) + 8 * i + (lane & 7));
+  double s = 0.0;
+  float hi = 0.f, lo = 0.f;
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+    for (int k = 0; k < kE; ++k) {
+      const float2 f = w[(8 * i + (lane & 7)) * kE + k];
+      const float v = element(reinterpret_cast<const uint8_t*>(&x[i]), k, B());
+      if constexpr (EXACT) {
+        s = fma(static_cast<double>(f.x) + static_cast<double>(f.y), static_cast<double>(v), s);
+      } else {
+        const float prod = __fmul_rn(f.x, v), off = __fmaf_rn(f.x, v, -prod);
+        const float sum = __fadd_rn(hi, prod), z = __fsub_rn(sum, hi);
+        const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, z)), __fsub_rn(prod, z));
+        lo = __fadd_rn(lo, __fadd_rn(err, __fmaf_rn(f.y, v, off)));
+        hi = sum;
+      }
+    }
+#pragma unroll
+  for (int m = 4; m > 0; m >>= 1) {
+    if constexpr (EXACT) {
+      s += __shfl_xor_sync(kFullMask, s, m);
+    } else {
+      const float h = __shfl_xor_sync(kFullMask, hi, m), l = __shfl_xor_sync(kFullMask, lo, m);
+      const float sum = __fadd_rn(hi, h), z = __fsub_rn(sum, hi);
+      lo = __fadd_rn(__fadd_rn(lo, l), __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, z)), __fsub_rn(h, z)));
+      hi = sum;
+    }
+  }
+  if constexpr (!EXACT) return static_cast<double>(hi) + static_cast<double>(lo);
+  return s != s ? static_cast<double>(INFINITY) : s;
+}
+
+// The `left`-th largest of key[j] over the set bits j of `bits`; *left becomes
+// how many of the keys equal to it are among the `left` largest.
+__device__ __forceinline__ uint32_t digit_cut(SelectShared& sh, const uint32_t* key, const uint32_t* bits, int words,
+                                              int* left) {
+  static_assert(kSelectThreads == 256, "one digit value a thread");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t want = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    __syncthreads();
+    sh.hist[tid] = 0;
+    __syncthreads();
+    for (int i = warp; i < words; i += kSelectWarps) {
+      const uint32_t k = key[i * 32 + lane];
+      if (((bits[i] >> lane) & 1u) && (shift == 24 || (k >> (shift + 8)) == (want >> (shift + 8))))
+        atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
+    }
+    __syncthreads();
+    const uint32_t c = sh.hist[255 - tid];
+    uint32_t total;
+    const uint32_t before = block_scan(sh, c, &total);
+    if (before < static_cast<uint32_t>(*left) && before + c >= static_cast<uint32_t>(*left)) {
+      sh.found_bin = 255 - tid;
+      sh.found_above = static_cast<int>(before);
+    }
+    __syncthreads();
+    *left -= sh.found_above;
+    want |= static_cast<uint32_t>(sh.found_bin) << shift;
+  }
+  return want;
+}
+
+// What a warp found out about its scores.
+struct ScoreStats {
+  float least = INFINITY, greatest = -INFINITY;
+  float mag = 0.f;    // bound on sum_i |w_i b_ji| of every block
+  bool odd = false;   // an infinite or NaN score
+  __device__ __forceinline__ void add(float s) {
+    least = fminf(least, s);
+    greatest = fmaxf(greatest, s);
+    odd |= !(fabsf(s) < INFINITY);
+  }
+};
+
+// Physical block of candidate j; one outside the pool is recorded and read as block 0.
+__device__ __forceinline__ int physical(const SelectParams& p, const int32_t* table, int j, int cands, bool record) {
+  if (j >= cands) return 0;
+  const int id = __ldg(table + j);
+  if (id >= 0 && id < p.num_blocks) return id;
+  if (record) atomicOr(p.err, kErrBlock);
+  return 0;
+}
+
+// Fragments of the weights for the tensor cores: step s, column g < 3, pair c
+// of k indices.  The weights are scaled by a power of two so that the largest
+// is near 2^14 and f16 words hold them; *unit undoes it.
+template <typename M>
+__device__ __forceinline__ M split_word(float x, float* rest) {
+  const M y = from_f32<M>(x);
+  *rest = x - to_f32(y);
+  return y;
+}
+
 template <typename T, typename B, int D>
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectParams p) {
+struct Scorer {  // 16-bit and E4M3 bounds
+  static constexpr bool kF8 = sizeof(B) == 1;
+  using M = typename std::conditional<kF8, __half, B>::type;
+  static constexpr int kRow = 2 * D * static_cast<int>(sizeof(B));  // bytes of a block's bounds
+  static constexpr int kLoads = kRow / 64;                          // 16-byte loads of a lane and row
+  static constexpr int kGroup = kLoads < 8 ? kLoads : 8;            // loads of two rows in flight
+  static constexpr int kTiles = kF8 && D <= 128 ? 2 : kGroup < 8 ? 2 : 1;  // tiles of 16 blocks in flight
+  static constexpr int kPerLoad = kF8 ? 4 : 2;                      // k16 steps of one load
+  static constexpr int kSteps = 2 * D / 16;
+  static constexpr int kFragBytes = kSteps * 3 * 4 * 8;             // [step][column][pair] two words
+  static constexpr int kBlocks = 16 * kTiles;                       // blocks of a warp's turn
+
+  // Lane layout of the elements: load i of lane c has elements (4i + c) * E .. + E - 1, E = 16 / sizeof(B); step t of
+  // the load takes its elements 4t .. 4t+3 as k indices 2c, 2c+1, 2c+8, 2c+9.
+  static __device__ __forceinline__ float fragments(uint2* frag, const float2* w, float* unit) {
+    // the largest weight, by every warp for itself
+    const int lane = threadIdx.x & 31;
+    float big = 0.f, sum = 0.f;
+    for (int e = lane; e < 2 * D; e += 32) {
+      big = fmaxf(big, fabsf(w[e].x));
+      sum += fabsf(w[e].x);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+      big = fmaxf(big, __shfl_xor_sync(kFullMask, big, m));
+      sum += __shfl_xor_sync(kFullMask, sum, m);
+    }
+    float scale = 1.f;
+    if (std::is_same<M, __half>::value && big > 0.f && big < INFINITY) {
+      int e;
+      frexpf(big, &e);
+      scale = ldexpf(1.f, min(max(14 - e, -120), 120));
+    }
+    *unit = 1.f / scale;
+    constexpr int kE = 16 / static_cast<int>(sizeof(B));
+    for (int x = threadIdx.x; x < kSteps * 4; x += kSelectThreads) {
+      const int step = x >> 2, c = x & 3;
+      const int e0 = (4 * (step / kPerLoad) + c) * kE + 4 * (step % kPerLoad);
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = w[e0 + k].x * scale;
+#pragma unroll
+      for (int col = 0; col < 3; ++col) {
+        M y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = split_word<M>(v[k], &v[k]);
+        uint2 word;
+        M* half = reinterpret_cast<M*>(&word);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) half[k] = y[k];
+        frag[(step * 3 + col) * 4 + c] = word;
+      }
+    }
+    return sum;
+  }
+
+  int ids[kTiles][2];  // physical blocks of the next turn
+  __device__ __forceinline__ void lookup(const SelectParams& p, const int32_t* table, int cands, int turn) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        ids[t][r] = physical(p, table, (turn * kTiles + t) * 16 + 8 * r + (lane >> 2), cands, (lane & 3) == 0);
+  }
+
+  // Scores of this warp's share: turns of kBlocks candidates, from turn `first` (looked up) on.
+  template <typename Ready>
+  __device__ __forceinline__ void run(const SelectParams& p, const uint2* frag, float unit, float wsum,
+                                             const int32_t* table, int h, int cands, int first, int turns,
+                                             float* scores, Ready ready, ScoreStats& st) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    __half2 most16 = __float2half2_rn(0.f);
+    __nv_bfloat162 mostb = __float2bfloat162_rn(0.f);
+    for (int turn = first; turn * kBlocks < cands; turn += turns) {
+      const uint8_t* src[kTiles][2];
+      bool live[kTiles][2];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          src[t][r] = p.bounds + (int64_t(ids[t][r]) * p.num_kv_heads + h) * kRow + c * 16;
+          live[t][r] = (turn * kTiles + t) * 16 + 8 * r + g < cands;
+        }
+      float acc[kTiles][4];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+#pragma unroll
+      for (int i0 = 0; i0 < kLoads; i0 += kGroup) {
+        uint4 x[kTiles][2][kGroup];
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i)
+              x[t][r][i] = live[t][r] ? __ldg(reinterpret_cast<const uint4*>(src[t][r] + (i0 + i) * 64))
+                                      : make_uint4(0u, 0u, 0u, 0u);
+        if (i0 + kGroup >= kLoads) lookup(p, table, cands, turn + turns);
+        float part[kTiles][4];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+          for (int s = 0; s < kPerLoad; ++s) {
+            uint32_t bf[2] = {0u, 0u};
+            if (g < 3) {
+              const uint2 f = frag[(((i0 + i) * kPerLoad + s) * 3 + g) * 4 + c];
+              bf[0] = f.x, bf[1] = f.y;
+            }
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+              uint32_t af[4];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const uint32_t wds[4] = {x[t][r][i].x, x[t][r][i].y, x[t][r][i].z, x[t][r][i].w};
+                if constexpr (kF8) {
+                  e4m3x4_to_f16x2x2(wds[s], af[r], af[2 + r]);
+                } else {
+                  af[r] = wds[2 * s], af[2 + r] = wds[2 * s + 1];
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if constexpr (std::is_same<M, __half>::value)
+                  most16 = __hmax2(most16, __habs2(*reinterpret_cast<const __half2*>(&af[k])));
+                else
+                  mostb = __hmax2(mostb, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&af[k])));
+              }
+              if (s % 2 == 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) part[t][e] = 0.f;
+              }
+              Mma<M>::run(part[t], af, bf);
+              if (s % 2 == 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t][e] += part[t][e];
+              }
+            }
+          }
+      }
+      ready();
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          // columns 0 and 1 are lane c = 0's, column 2 lane c = 1's
+          float s = c == 0 ? acc[t][2 * r] + acc[t][2 * r + 1] : acc[t][2 * r];
+          s = (s + __shfl_xor_sync(kFullMask, s, 1)) * unit;
+          if (c == 0 && live[t][r]) {
+            scores[(turn * kTiles + t) * 16 + 8 * r + g] = s;
+            st.add(s);
+          }
+        }
+    }
+    float most = std::is_same<M, __half>::value ? fmaxf(__low2float(most16), __high2float(most16))
+                                                : fmaxf(__low2float(mostb), __high2float(mostb));
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(kFullMask, most, m));
+    st.mag = most * wsum;
+  }
+  static __device__ __forceinline__ float chain() { return 136.f + kSteps / 2 + 8.f; }
+};
+
+template <int D>
+struct Scorer<float, float, D> {  // binary32 FMA: D/16 lanes a block, 32 elements each
+  static constexpr int kLanes = D / 16, kPer = 32 / kLanes, kLoads = 8, kDeep = 2;
+  static constexpr int kFragBytes = 0;
+  static constexpr int kBlocks = kPer * kDeep;
+
+  static __device__ __forceinline__ float fragments(uint2*, const float2* w, float* unit) {
+    float sum = 0.f;
+    for (int e = threadIdx.x & 31; e < 2 * D; e += 32) sum += fabsf(w[e].x);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(kFullMask, sum, m);
+    *unit = 1.f;
+    return sum;
+  }
+
+  int ids[kDeep];
+  __device__ __forceinline__ void lookup(const SelectParams& p, const int32_t* table, int cands, int turn) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int t = 0; t < kDeep; ++t)
+      ids[t] = physical(p, table, (turn * kDeep + t) * kPer + lane / kLanes, cands, lane % kLanes == 0);
+  }
+
+  template <typename Ready>
+  __device__ __forceinline__ void run(const SelectParams& p, const float2* w, float wsum, const int32_t* table,
+                                             int h, int cands, int first, int turns, float* scores, Ready ready,
+                                             ScoreStats& st) {
+    const int lane = threadIdx.x & 31, gl = lane % kLanes, gi = lane / kLanes;
+    float wr[32], most = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) wr[4 * i + e] = w[(gl + kLanes * i) * 4 + e].x;
+    for (int turn = first; turn * kBlocks < cands; turn += turns) {
+      float4 x[kDeep][kLoads];
+#pragma unroll
+      for (int t = 0; t < kDeep; ++t)
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          x[t][i] = (turn * kDeep + t) * kPer + gi < cands
+                        ? __ldg(reinterpret_cast<const float4*>(p.bounds) +
+                                (int64_t(ids[t]) * p.num_kv_heads + h) * (D / 2) + gl + kLanes * i)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      lookup(p, table, cands, turn + turns);
+      ready();
+#pragma unroll
+      for (int t = 0; t < kDeep; ++t) {
+        float acc = 0.f;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const float f[4] = {x[t][i].x, x[t][i].y, x[t][i].z, x[t][i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            acc = fmaf(wr[4 * i + e], f[e], acc);
+            most = fmaxf(most, fabsf(f[e]));
+          }
+        }
+#pragma unroll
+        for (int m = 1; m < kLanes; m <<= 1) acc += __shfl_xor_sync(kFullMask, acc, m);
+        const int j = (turn * kDeep + t) * kPer + gi;
+        if (j < cands) {
+          if (gl == 0) scores[j] = acc;
+          st.add(acc);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(kFullMask, most, m));
+    st.mag = most * wsum;
+  }
+  static __device__ __forceinline__ float chain() { return 44.f; }
+};
+
+template <typename T, typename B, int D>
+__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectParams p) {
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int64_t row = static_cast<int64_t>(blockIdx.x) / ctas;
-  const int b = static_cast<int>(row / p.num_kv_heads), h = static_cast<int>(row - int64_t(b) * p.num_kv_heads);
+  int b = static_cast<int>(row / p.num_kv_heads);
+  const int h = static_cast<int>(row - int64_t(b) * p.num_kv_heads);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  extern __shared__ __align__(16) uint8_t raw[];
+  SelectShared& sh = *reinterpret_cast<SelectShared*>(raw);
+  if (p.longest_first) {  // CTAs start in launch order: the b-th longest sequence, equal ones in order
+    const int mine = lane < p.num_seqs ? p.context_lens[lane] : INT_MIN;
+    int before = 0;
+    for (int i = 0; i < p.num_seqs; ++i) {
+      const int other = __shfl_sync(kFullMask, mine, i);
+      before += other > mine || (other == mine && i < lane);
+    }
+    b = __ffs(__ballot_sync(kFullMask, lane < p.num_seqs && before == b)) - 1;
+  }
   int32_t* out = p.selected + b * p.sel_sb + h * p.sel_sh;
+  float2* w = reinterpret_cast<float2*>(raw + ((sizeof(SelectShared) + 15) / 16) * 16);  // [2D]: down, up
+  uint2* frag = reinterpret_cast<uint2*>(w + 2 * D);                                     // weights for the tensor cores
+  static_assert(Scorer<T, B, D>::kFragBytes % 16 == 0 && D % 16 == 0, "scores are read four at a time");
+  float* score = reinterpret_cast<float*>(frag + Scorer<T, B, D>::kFragBytes / 8);       // [room], of the first CTA
+  uint32_t* sure_bits = reinterpret_cast<uint32_t*>(score + p.room);                     // [room / 32]
+  uint32_t* win_bits = sure_bits + p.room / 32;
 
   int len = p.context_lens[b];
+  // the weights, sums over the group's heads in two binary32 words each (the
+  // rounding error of every addition is kept in the second)
+  const T* q = static_cast<const T*>(p.q) + b * p.q_sb + int64_t(h) * p.group * p.q_sh;
+  auto sums = [&](float unit) {
+    bool big = false;
+    for (int d = tid; d < D; d += kSelectThreads) {
+      float hi[2] = {0.f, 0.f}, lo[2] = {0.f, 0.f};
+      for (int g0 = 0; g0 < p.group; g0 += 8) {
+        float x[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) x[g] = g0 + g < p.group ? to_f32(q[(g0 + g) * p.q_sh + d]) * unit : 0.f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          big |= fabsf(x[g]) > 1e30f && fabsf(x[g]) < INFINITY;
+          const float part[2] = {x[g] > 0.f ? 0.f : x[g], x[g] < 0.f ? 0.f : x[g]};  // a NaN goes into both
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float s = __fadd_rn(hi[i], part[i]), z = __fsub_rn(s, hi[i]);
+            lo[i] = __fadd_rn(lo[i], __fadd_rn(__fsub_rn(hi[i], __fsub_rn(s, z)), __fsub_rn(part[i], z)));
+            hi[i] = s;
+          }
+        }
+      }
+      // an infinite sum leaves NaN behind as its error: the sum alone counts
+      w[d] = make_float2(hi[0], fabsf(hi[0]) < INFINITY ? lo[0] : 0.f);
+      w[D + d] = make_float2(hi[1], fabsf(hi[1]) < INFINITY ? lo[1] : 0.f);
+    }
+    return __syncthreads_or(big);
+  };
+  // sums that could leave binary32's range are taken of the queries times 2^-60
+  if (sums(1.f)) sums(8.6736174e-19f);
+
   if (len < 0 || len > p.max_tokens) {
     if (tid == 0 && rank == 0) atomicOr(p.err, kErrLen);
     len = len < 0 ? 0 : p.max_tokens;
@@ -192,285 +539,262 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
     }
     return;
   }
+  auto started = cluster.barrier_arrive();  // waited for before the first store to the first CTA's shared memory
 
-  extern __shared__ __align__(16) uint8_t raw[];
-  SelectShared& sh = *reinterpret_cast<SelectShared*>(raw);
-  double* w64 = reinterpret_cast<double*>(raw + ((sizeof(SelectShared) + 15) / 16) * 16);  // [2D]: down, up
-  float* w32 = reinterpret_cast<float*>(w64 + 2 * D);
-  unsigned long long* key = reinterpret_cast<unsigned long long*>(w32 + 2 * D);            // [share]
-  float* score = reinterpret_cast<float*>(key + p.share);                                  // [share]
-
-  for (int i = tid; i < kBins; i += kSelectThreads) sh.hist[i] = 0;
-  if (tid == 0) sh.win_count = sh.sure_count = sh.my_sure = sh.my_win = 0;
-  const T* q = static_cast<const T*>(p.q) + b * p.q_sb + int64_t(h) * p.group * p.q_sh;
-  for (int d = tid; d < D; d += kSelectThreads) {
-    double up = 0.0, down = 0.0;
-    float up32 = 0.f, down32 = 0.f;
-    for (int g = 0; g < p.group; ++g) {
-      const float x = to_f32(q[g * p.q_sh + d]);
-      // a NaN goes into both sums
-      const float a = x < 0.f ? 0.f : x, c = x > 0.f ? 0.f : x;
-      up += a, down += c;
-      up32 += a, down32 += c;
-    }
-    w64[d] = down, w64[D + d] = up;
-    w32[d] = down32, w32[D + d] = up32;
-  }
-  auto started = cluster.barrier_arrive();  // waited for before the first access to a peer's shared memory
-  __syncthreads();
-
-  // --- scores of this CTA's share of the candidates sink .. n - recent - 1 ---
+  // --- scores of the candidates sink .. n - recent - 1 ---
+  using Score = Scorer<T, B, D>;
   const int cands = n - p.sink - p.recent;
-  const int lo = static_cast<int>(int64_t(cands) * rank / ctas), hi = static_cast<int>(int64_t(cands) * (rank + 1) / ctas);
-  const int mine = hi - lo, first = p.sink + lo;
-  const int32_t* table = p.block_tables + b * p.bt_stride;
-  constexpr int kLanes = D / 16;                       // lanes of one block
-  constexpr int kPer = 32 / kLanes;                    // blocks of one step
-  constexpr int kN = Bounds16<B>::kN, kLoads = 32 / kN;
-  const int gl = lane % kLanes, gi = lane / kLanes;
-  float w[32];
-  float wsum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      w[i * kN + e] = w32[(gl + kLanes * i) * kN + e];
-      wsum += fabsf(w[i * kN + e]);
-    }
-  const int64_t head_bytes = 2 * D * sizeof(B);
-  float smin = INFINITY, smax = -INFINITY, most = 0.f;
-  bool odd = false;
-  for (int j0 = warp * 32; j0 < mine; j0 += kSelectWarps * 32) {
-    int id = 0;
-    if (j0 + lane < mine) {
-      id = table[first + j0 + lane];
-      if (id < 0 || id >= p.num_blocks) {
-        atomicOr(p.err, kErrBlock);
-        id = 0;
-      }
-    }
-    const int count = min(32, mine - j0);
-#pragma unroll 2
-    for (int s = 0; s < count; s += kPer) {
-      const int jj = s + gi;
-      const int phys = __shfl_sync(kFullMask, id, jj & 31);
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.bounds + (int64_t(phys) * p.num_kv_heads + h) * head_bytes) + gl;
-      uint4 x[kLoads];
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) x[i] = jj < count ? __ldg(src + kLanes * i) : make_uint4(0u, 0u, 0u, 0u);
-      float acc = 0.f;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        float f[kN];
-        Bounds16<B>::open(x[i], f, most);
-#pragma unroll
-        for (int e = 0; e < kN; ++e) acc = fmaf(w[i * kN + e], f[e], acc);
-      }
-#pragma unroll
-      for (int m = 1; m < kLanes; m <<= 1) acc += __shfl_xor_sync(kFullMask, acc, m);
-      if (gl == 0 && jj < count) {
-        score[j0 + jj] = acc;
-        odd |= !(fabsf(acc) < INFINITY);
-        smin = fminf(smin, acc);
-        smax = fmaxf(smax, acc);
-      }
-    }
-  }
-  {  // sum_i |w_i b_ji| <= sum over lanes of (its largest |b|) (its sum of |w|), for every j
-    float mag = most * wsum;
-#pragma unroll
-    for (int m = 1; m < kLanes; m <<= 1) mag += __shfl_xor_sync(kFullMask, mag, m);
-#pragma unroll
-    for (int m = kLanes; m < 32; m <<= 1) mag = fmaxf(mag, __shfl_xor_sync(kFullMask, mag, m));
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      smin = fminf(smin, __shfl_xor_sync(kFullMask, smin, m));
-      smax = fmaxf(smax, __shfl_xor_sync(kFullMask, smax, m));
-    }
-    odd = __any_sync(kFullMask, odd || !(mag < 1e37f));
-    if (lane == 0) {
-      sh.warp_stat[warp][0] = smin, sh.warp_stat[warp][1] = smax, sh.warp_stat[warp][2] = mag;
-      sh.warp_stat[warp][3] = odd ? 1.f : 0.f;
-    }
-  }
+  const int32_t* table = p.block_tables + b * p.bt_stride + p.sink;
+  constexpr int64_t head_bytes = 2 * D * sizeof(B);
+  const int first = rank * kSelectWarps + warp, turns = ctas * kSelectWarps;
+  Score scorer;
+  scorer.lookup(p, table, cands, first);
+  float unit;
+  const float wsum = Score::fragments(frag, w, &unit);
   __syncthreads();
-  cluster.barrier_wait(std::move(started));
-  if (tid < ctas) {  // this CTA's extremes, to every CTA of the cluster
-    float a = INFINITY, c = -INFINITY, m = 0.f, o = 0.f;
+  ScoreStats st;
+  {
+    bool waited = false;
+    auto ready = [&] {
+      if (!waited) cluster.barrier_wait(std::move(started));
+      waited = true;
+    };
+    float* scores = cluster.map_shared_rank(score, 0);
+    if constexpr (sizeof(B) == 4)
+      scorer.run(p, w, wsum, table, h, cands, first, turns, scores, ready, st);
+    else
+      scorer.run(p, frag, unit, wsum, table, h, cands, first, turns, scores, ready, st);
+    ready();
+  }
 #pragma unroll
-    for (int i = 0; i < kSelectWarps; ++i) {
-      a = fminf(a, sh.warp_stat[i][0]), c = fmaxf(c, sh.warp_stat[i][1]);
-      m = fmaxf(m, sh.warp_stat[i][2]), o = fmaxf(o, sh.warp_stat[i][3]);
-    }
-    float* dst = cluster.map_shared_rank(&sh.stat[rank][0], tid);
-    dst[0] = a, dst[1] = c, dst[2] = m, dst[3] = o;
+  for (int m = 16; m > 0; m >>= 1) {
+    st.least = fminf(st.least, __shfl_xor_sync(kFullMask, st.least, m));
+    st.greatest = fmaxf(st.greatest, __shfl_xor_sync(kFullMask, st.greatest, m));
+  }
+  st.odd = __any_sync(kFullMask, st.odd || !(st.mag < 1e37f));
+  if (lane == 0)
+    *reinterpret_cast<float4*>(cluster.map_shared_rank(&sh.stat[rank * kSelectWarps + warp][0], 0)) =
+        make_float4(st.least, st.greatest, st.mag, st.odd ? 1.f : 0.f);
+  if (rank == 0) {
+    for (int i = tid; i < kBins; i += kSelectThreads) sh.hist[i] = 0;
+    if (tid == 0) sh.near_count = sh.win_count = sh.sure_count = 0;
   }
   cluster.sync();
-  smin = INFINITY, smax = -INFINITY;
-  float mag = 0.f, flag = 0.f;
-  for (int r = 0; r < ctas; ++r) {
+  if (rank != 0) return;  // nothing of this CTA is accessed any more
+
+  // --- the first CTA: the bin that holds the border ---
+  float smin = INFINITY, smax = -INFINITY, mag = 0.f, flag = 0.f;
+  for (int r = lane; r < ctas * kSelectWarps; r += 32) {
     smin = fminf(smin, sh.stat[r][0]), smax = fmaxf(smax, sh.stat[r][1]);
     mag = fmaxf(mag, sh.stat[r][2]), flag = fmaxf(flag, sh.stat[r][3]);
   }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) {
+    smin = fminf(smin, __shfl_xor_sync(kFullMask, smin, m)), smax = fmaxf(smax, __shfl_xor_sync(kFullMask, smax, m));
+    mag = fmaxf(mag, __shfl_xor_sync(kFullMask, mag, m)), flag = fmaxf(flag, __shfl_xor_sync(kFullMask, flag, m));
+  }
   // two errors of a score; 1e-37 covers products below the smallest binary32 number
-  const float err2 = 2.f * (static_cast<float>(p.group + 44) * 5.9604645e-8f * 1.01f * mag + 1e-37f);
+  const float err2 = 2.f * ((static_cast<float>(p.group) + Score::chain()) * 5.9604645e-8f * 1.01f * mag + 1e-37f);
   // scores that overflowed, infinite or NaN bounds: every candidate is settled in binary64
   const bool all = flag != 0.f;
-  const float per = smax > smin ? static_cast<float>(kBins) / (smax - smin) : 0.f;
-  auto bin = [&](float x) { return static_cast<int>(fminf(fmaxf((x - smin) * per, 0.f), kBins - 1.f)); };
-
-  // --- the bin that holds the border ---
-  int border = 0;
+  const int words = (cands + 31) / 32, quads = (cands + 3) / 4;
+  for (int i = tid; i < words; i += kSelectThreads) sure_bits[i] = win_bits[i] = 0u;
+  float above = INFINITY, below = -INFINITY;  // scores over `above` are in, scores under `below` are not
   if (!all) {
-    for (int j = tid; j < mine; j += kSelectThreads) atomicAdd(&sh.hist[bin(score[j])], 1u);
-    cluster.sync();
-    uint32_t c[4] = {0, 0, 0, 0};
-    const int at = kBins - 4 - 4 * tid;  // thread 0 holds the highest bins
-    for (int r = 0; r < ctas; ++r) {
-      const uint4 x = *cluster.map_shared_rank(reinterpret_cast<const uint4*>(&sh.hist[at]), r);
-      c[0] += x.w, c[1] += x.z, c[2] += x.y, c[3] += x.x;
-    }
-    uint32_t total;
-    uint32_t before = block_scan(sh, c[0] + c[1] + c[2] + c[3], &total);
+    const float per = smax > smin ? static_cast<float>(kBins) / (smax - smin) : 0.f;
+#pragma unroll 4
+    for (int i = tid; i < quads; i += kSelectThreads) {
+      const float4 s = reinterpret_cast<const float4*>(score)[i];
+      const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (before < static_cast<uint32_t>(need) && before + c[i] >= static_cast<uint32_t>(need)) sh.found_bin = at + 3 - i;
+      for (int e = 0; e < 4; ++e)
+        if (4 * i + e < cands)
+          atomicAdd(&sh.hist[static_cast<int>(fminf(fmaxf((v[e] - smin) * per, 0.f), kBins - 1.f))], 1u);
+    }
+    __syncthreads();
+    constexpr int kMine = kBins / kSelectThreads;
+    uint32_t c[kMine], sum = 0, total;
+    const int at = kBins - kMine * (tid + 1);  // thread 0 holds the highest bins
+#pragma unroll
+    for (int i = 0; i < kMine; i += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(&sh.hist[at + kMine - 4 - i]);
+      c[i] = x.w, c[i + 1] = x.z, c[i + 2] = x.y, c[i + 3] = x.x;
+      sum += x.x + x.y + x.z + x.w;
+    }
+    uint32_t before = block_scan(sh, sum, &total);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      if (before < static_cast<uint32_t>(need) && before + c[i] >= static_cast<uint32_t>(need))
+        sh.found_bin = at + kMine - 1 - i;
       before += c[i];
     }
     __syncthreads();
-    border = sh.found_bin;
-  }
-  // 2: above the border for certain, 1: to be settled, 0: below for certain
-  auto place = [&](float s) {
-    if (all) return 1;
-    return bin(s - err2) > border ? 2 : bin(s + err2) < border ? 0 : 1;
-  };
-
-  // --- border blocks in binary64, a warp each ---
-  SelectShared* head = cluster.map_shared_rank(&sh, 0);
-  int sure = 0;
-  for (int j0 = warp * 32; j0 < mine; j0 += kSelectWarps * 32) {
-    const int what = j0 + lane < mine ? place(score[j0 + lane]) : 0;
-    sure += __popc(__ballot_sync(kFullMask, what == 2));
-    unsigned todo = __ballot_sync(kFullMask, what == 1);
-    while (todo) {
-      const int j = j0 + __ffs(todo) - 1;
-      todo &= todo - 1;
-      int phys = table[first + j];
-      if (phys < 0 || phys >= p.num_blocks) phys = 0;
-      const uint8_t* src = p.bounds + (int64_t(phys) * p.num_kv_heads + h) * head_bytes;
-      double s = 0.0;
-#pragma unroll
-      for (int i = 0; i < 2 * D / 32; ++i) {
-        const int e = lane + 32 * i;
-        s = fma(w64[e], static_cast<double>(element(src, e, B())), s);
-      }
-#pragma unroll
-      for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(kFullMask, s, m);
-      if (lane == 0) {
-        const unsigned long long k = ordered(s != s ? static_cast<double>(INFINITY) : s);
-        key[j] = k;
-        const int at = atomicAdd(&head->win_count, 1);
-        if (at < kWindow) {
-          head->win_key[at] = k;
-          head->win_at[at] = first + j;
-        }
-      }
+    // The border score is in the found bin; its edges, with the roundings of the
+    // bin's number (a few 2^-24 of the extremes), moved out by two errors.
+    if (per > 0.f && per < INFINITY) {
+      const float slack = err2 + 16.f * 5.9604645e-8f * (fabsf(smin) + fabsf(smax));
+      above = smin + static_cast<float>(sh.found_bin + 1) / per + slack;
+      below = smin + static_cast<float>(sh.found_bin) / per - slack;
     }
-  }
-  if (lane == 0 && sure > 0) atomicAdd(&head->sure_count, sure);
-  cluster.sync();
-  const int window = head->win_count;
-  int left = need - head->sure_count;  // border blocks to keep: 1 .. window
-  if (window <= kWindow) {
-    if (rank == 0) {
-      for (int i = tid; i < window; i += kSelectThreads) {
-        const unsigned long long k = sh.win_key[i];
-        const int at = sh.win_at[i];
-        int better = 0;
-        for (int o = 0; o < window; ++o) better += sh.win_key[o] > k || (sh.win_key[o] == k && sh.win_at[o] < at);
-        if (better == left - 1) {
-          for (int r = 0; r < ctas; ++r) {
-            SelectShared* peer = cluster.map_shared_rank(&sh, r);
-            peer->cut_key = k;
-            peer->cut_at = at;
-          }
-        }
-      }
-    }
-    cluster.sync();
   } else {
-    // the digits of (key, complement of the index), 8 bits at a time from the top
-    unsigned long long want = 0;
-    uint32_t want_at = 0;
-    for (int pass = 0; pass < 12; ++pass) {
-      uint32_t* dig = sh.digits[pass & 1];
-      dig[tid] = 0;
-      __syncthreads();
-      const int shift = pass < 8 ? 56 - 8 * pass : 24 - 8 * (pass - 8);
-      for (int j = tid; j < mine; j += kSelectThreads) {
-        if (place(score[j]) != 1) continue;
-        const unsigned long long k = key[j];
-        const uint32_t a = ~static_cast<uint32_t>(first + j);
-        bool in;
-        uint32_t d;
-        if (pass < 8) {
-          in = pass == 0 || (k >> (shift + 8)) == (want >> (shift + 8));
-          d = static_cast<uint32_t>(k >> shift) & 255u;
-        } else {
-          in = k == want && (pass == 8 || (a >> (shift + 8)) == (want_at >> (shift + 8)));
-          d = (a >> shift) & 255u;
-        }
-        if (in) atomicAdd(&dig[d], 1u);
-      }
-      cluster.sync();
-      uint32_t c = 0, total;
-      const int at = 255 - tid;
-      for (int r = 0; r < ctas; ++r) c += *cluster.map_shared_rank(&dig[at], r);
-      const uint32_t before = block_scan(sh, c, &total);
-      if (before < static_cast<uint32_t>(left) && before + c >= static_cast<uint32_t>(left)) {
-        sh.found_bin = at;
-        sh.found_above = static_cast<int>(before);
-      }
-      __syncthreads();
-      left -= sh.found_above;
-      if (pass < 8)
-        want |= static_cast<unsigned long long>(sh.found_bin) << shift;
-      else
-        want_at |= static_cast<uint32_t>(sh.found_bin) << shift;
-    }
-    if (tid == 0) {
-      sh.cut_key = want;
-      sh.cut_at = static_cast<int>(~want_at);
-    }
     __syncthreads();
   }
-  const unsigned long long cut_key = sh.cut_key;
-  const int cut_at = sh.cut_at;
-  auto kept = [&](int j) {
-    const int what = place(score[j]);
-    return what == 2 || (what == 1 && (key[j] > cut_key || (key[j] == cut_key && first + j <= cut_at)));
+
+  // --- blocks above the border for certain, and those to be settled ---
+#pragma unroll 4
+  for (int i = tid; i < quads; i += kSelectThreads) {
+    const float4 s = reinterpret_cast<const float4*>(score)[i];
+    const float v[4] = {s.x, s.y, s.z, s.w};
+    uint32_t in = 0, open = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool here = 4 * i + e < cands, over = !all && v[e] > above;
+      in |= here && over ? 1u << e : 0u;
+      open |= here && !over && (all || v[e] >= below) ? 1u << e : 0u;
+    }
+    const int shift = (4 * i) & 31;
+    if (in) {
+      atomicOr(&sure_bits[i >> 3], in << shift);
+      atomicAdd(&sh.sure_count, __popc(in));
+    }
+    if (open) {
+      atomicOr(&win_bits[i >> 3], open << shift);
+      int at = atomicAdd(&sh.near_count, __popc(open));
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((open >> e) & 1u) {
+          if (at < kWindow) {
+            sh.near_at[at] = 4 * i + e;
+            sh.near_score[at] = v[e];
+          }
+          ++at;
+        }
+    }
+  }
+  __syncthreads();
+  int window = sh.near_count;
+  int left = need - sh.sure_count;  // of the near blocks: 1 .. window
+  if (!all && window <= kWindow && window > left) {
+    // the border is the left-th of them; what is more than two errors above it is in
+    for (int i = tid; i < window; i += kSelectThreads) {
+      const float s = sh.near_score[i];
+      const int at = sh.near_at[i];
+      int better = 0;
+      for (int o = 0; o < window; ++o) better += sh.near_score[o] > s || (sh.near_score[o] == s && sh.near_at[o] < at);
+      if (better == left - 1) sh.border = s;
+    }
+    __syncthreads();
+    const float border = sh.border;
+    for (int i = tid; i < window; i += kSelectThreads) {
+      const float s = sh.near_score[i];
+      const int at = sh.near_at[i];
+      const bool in = s - border > err2;
+      if (in || border - s > err2) {
+        atomicAnd(&win_bits[at >> 5], ~(1u << (at & 31)));
+        if (in) {
+          atomicOr(&sure_bits[at >> 5], 1u << (at & 31));
+          atomicAdd(&sh.sure_count, 1);
+        }
+      } else {
+        sh.win_at[atomicAdd(&sh.win_count, 1)] = at;
+      }
+    }
+    __syncthreads();
+    window = sh.win_count;
+    left = need - sh.sure_count;
+  } else if (window <= kWindow) {
+    for (int i = tid; i < window; i += kSelectThreads) sh.win_at[i] = sh.near_at[i];
+    __syncthreads();
+  }
+  auto bounds_of = [&](int j) {
+    int id = table[j];
+    if (id < 0 || id >= p.num_blocks) id = 0;
+    return p.bounds + (int64_t(id) * p.num_kv_heads + h) * head_bytes;
   };
+  if (window == left) {  // all of them
+    for (int i = tid; i < words; i += kSelectThreads) sure_bits[i] |= win_bits[i];
+  } else if (window <= kWindow) {
+    // from scores within 2^-35 of the magnitudes; where that leaves the border
+    // open (or blocks alike), in binary64
+    const double apart = 5.8207661e-11 * static_cast<double>(mag) + 1e-37;
+    for (int exact = all ? 1 : 0; exact < 2; ++exact) {
+      if (tid == 0) sh.found_above = 0;
+      for (int i = tid; i < words; i += kSelectThreads) win_bits[i] = 0u;  // the list holds them; now those that are kept
+      for (int i0 = warp * 4; i0 < window; i0 += kSelectWarps * 4) {
+        const int i = min(i0 + (lane >> 3), window - 1);
+        const double s = exact ? fine_score<B, D, true>(bounds_of(sh.win_at[i]), w, lane)
+                               : fine_score<B, D, false>(bounds_of(sh.win_at[i]), w, lane);
+        if ((lane & 7) == 0) sh.win_score[i] = s;
+      }
+      __syncthreads();
+      for (int i = tid; i < window; i += kSelectThreads) {
+        const double s = sh.win_score[i];
+        const int at = sh.win_at[i];
+        int better = 0, near = 0;
+        for (int o = 0; o < window; ++o) {
+          better += sh.win_score[o] > s || (sh.win_score[o] == s && sh.win_at[o] < at);
+          near += sh.win_score[o] - s < apart && s - sh.win_score[o] < apart;
+        }
+        // the last that is kept and the first that is not may not be told apart by this
+        if (better < left) atomicOr(&win_bits[at >> 5], 1u << (at & 31));
+        if (!exact && (better == left - 1 || better == left) && near > 1) sh.found_above = 1;
+      }
+      __syncthreads();
+      if (exact || sh.found_above == 0) break;
+      __syncthreads();
+    }
+    for (int i = tid; i < words; i += kSelectThreads) sure_bits[i] |= win_bits[i];
+  } else {
+    // many alike: the high words of the exact scores, then the low words of those
+    // that share the border's high word, then the index; the keys take the scores' place
+    uint32_t* key = reinterpret_cast<uint32_t*>(score);
+    for (int half = 0; half < 2; ++half) {
+      for (int i = warp; i < words; i += kSelectWarps) {
+        const uint32_t m = win_bits[i];
+        for (int k0 = 0; k0 < 32; k0 += 4) {
+          if (!((m >> k0) & 15u)) continue;
+          const int j = min(i * 32 + k0 + (lane >> 3), cands - 1);
+          const unsigned long long k = ordered(fine_score<B, D, true>(bounds_of(j), w, lane));
+          if ((lane & 7) == 0 && i * 32 + k0 + (lane >> 3) == j) key[j] = static_cast<uint32_t>(half ? k : k >> 32);
+        }
+      }
+      __syncthreads();
+      const uint32_t want = digit_cut(sh, key, win_bits, words, &left);
+      for (int i = warp; i < words; i += kSelectWarps) {
+        const bool in = (win_bits[i] >> lane) & 1u;
+        const uint32_t above = __ballot_sync(kFullMask, in && key[i * 32 + lane] > want);
+        const uint32_t equal = __ballot_sync(kFullMask, in && key[i * 32 + lane] == want);
+        if (lane == 0) {
+          sure_bits[i] |= above;
+          win_bits[i] = equal;
+        }
+      }
+      __syncthreads();
+    }
+    // the first `left` of the equal ones
+    int taken = 0;
+    for (int i0 = 0; i0 < words; i0 += kSelectThreads) {
+      const uint32_t m = i0 + tid < words ? win_bits[i0 + tid] : 0u;
+      uint32_t total;
+      int room = left - taken - static_cast<int>(block_scan(sh, __popc(m), &total));
+      uint32_t keep = 0;
+      for (uint32_t x = m; x && room > 0; x &= x - 1, --room) keep |= x & (~x + 1u);
+      if (keep) sure_bits[i0 + tid] |= keep;
+      taken += static_cast<int>(total);
+    }
+  }
+  __syncthreads();
 
   // --- the chosen blocks, ascending ---
-  int count = 0;
-  for (int j = tid; j < mine; j += kSelectThreads) count += kept(j);
-  uint32_t total;
-  block_scan(sh, static_cast<uint32_t>(count), &total);
-  if (tid < ctas) *cluster.map_shared_rank(&sh.picked[rank], tid) = static_cast<int>(total);
-  cluster.sync();  // the last access to another CTA's shared memory
   int base = p.sink;
-  for (int r = 0; r < rank; ++r) base += sh.picked[r];
-  for (int j0 = 0; j0 < mine; j0 += kSelectThreads) {
-    const int j = j0 + tid;
-    const bool in = j < mine && kept(j);
-    uint32_t all_in;
-    const uint32_t before = block_scan(sh, in, &all_in);
-    if (in && base + static_cast<int>(before) < p.top) out[base + before] = first + j;
-    base += static_cast<int>(all_in);
+  for (int i0 = 0; i0 < words; i0 += kSelectThreads) {
+    uint32_t m = i0 + tid < words ? sure_bits[i0 + tid] : 0u, total;
+    int at = base + static_cast<int>(block_scan(sh, __popc(m), &total));
+    for (; m; m &= m - 1, ++at)
+      if (at < p.top) out[at] = p.sink + (i0 + tid) * 32 + __ffs(m) - 1;
+    base += static_cast<int>(total);
   }
-  for (int i = rank * kSelectThreads + tid; i < p.sink + p.recent; i += ctas * kSelectThreads) {
+  for (int i = tid; i < p.sink + p.recent; i += kSelectThreads) {
     if (i < p.sink)
       out[i] = i;
     else
@@ -478,15 +802,17 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const SelectPara
   }
 }
 
-size_t select_smem(int head_dim, int share) {
-  return (sizeof(SelectShared) + 15) / 16 * 16 + size_t(2 * head_dim) * 12 + size_t(share) * 12;
+size_t select_smem(int head_dim, int room) {
+  return (sizeof(SelectShared) + 15) / 16 * 16 + size_t(2 * head_dim) * 8 + size_t(head_dim) * 12 + size_t(room) * 4 +
+         size_t(room / 32) * 8;  // weights, their fragments (fewer for f32), scores, two bits a block
 }
 
 template <typename T, typename B, int D>
 int launch_one(const SelectParams& p, int ctas, cudaStream_t stream) {
   static std::atomic<int> configured[64];
-  const size_t smem = select_smem(D, p.share);
-  int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&select_kernel<T, B, D>), static_cast<int>(smem));
+  const size_t smem = select_smem(D, p.room);
+  const void* func = reinterpret_cast<const void*>(&select_kernel<T, B, D>);
+  int e = raise_smem_limit(configured, func, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(int64_t(p.num_seqs) * p.num_kv_heads * ctas));
@@ -514,22 +840,26 @@ int launch_dim(const SelectParams& p, int head_dim, int ctas, cudaStream_t strea
 
 }  // namespace
 
-// Most blocks a table row may have: the largest cluster's shares have to fit
-// its CTAs' shared memory.
+// Most blocks a table row may have: their scores have to fit one CTA's shared memory.
 int select_max_blocks(int head_dim) {
   const size_t room = 200 * 1024 - select_smem(head_dim, 0);
-  return static_cast<int>(room / 12) * kMaxCluster;
+  return static_cast<int>(room / 136 * 32);  // 4 bytes and two bits a block
 }
 
 int launch_select(int dtype, int bounds_dtype, int head_dim, SelectParams p, int max_blocks, int num_sms,
                   cudaStream_t stream) {
-  // CTAs of a row: enough that all rows together give every SM four, but no
-  // CTA under 64 blocks; and as many as the scores' share needs
+  // CTAs of a row: as many as run at once (two an SM), so that the work of every
+  // CTA besides the scores (weights, barrier, the first loads' latency: 6 us) is
+  // paid once, and none with less than a turn of its warps.  Measured, us for 1,
+  // 2, 4, 8 and 16 CTAs a row: 64 rows of 2048-8192 blocks 104, 63, 48, 49, 62;
+  // 256 rows of 190-1500 E4M3 blocks 29, 35, 46, 70, 136; 4 rows of 1000 blocks
+  // 12.5, 10.2, 8.8, 8.8, 9.0.
   const int64_t rows = int64_t(p.num_seqs) * p.num_kv_heads;
   int ctas = 1;
-  while (ctas < kMaxCluster && rows * ctas < int64_t(num_sms) * 4 && max_blocks / (2 * ctas) >= 64) ctas *= 2;
-  while (ctas < kMaxCluster && select_smem(head_dim, (max_blocks + ctas - 1) / ctas) > 100 * 1024) ctas *= 2;
-  p.share = ((max_blocks + ctas - 1) / ctas + 1) / 2 * 2;
+  while (ctas < kMaxCluster && rows * ctas * 2 <= int64_t(num_sms) * 2 && max_blocks / (2 * ctas) >= 16 * kSelectWarps / 2) ctas *= 2;
+  p.room = (max_blocks + 31) / 32 * 32;
+  // batches of more than one wave start the longest rows first
+  p.longest_first = rows * ctas > int64_t(num_sms) * 2 && p.num_seqs > 1 && p.num_seqs <= 32;
   int e = cudaErrorInvalidValue;
   if (dtype == 0 && bounds_dtype == 0) e = launch_dim<float, float>(p, head_dim, ctas, stream);
   if (dtype == 1 && bounds_dtype == 1) e = launch_dim<__half, __half>(p, head_dim, ctas, stream);
