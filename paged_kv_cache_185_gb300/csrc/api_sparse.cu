@@ -207,6 +207,7 @@ int rotate_call(const wllm_tensor* q_out, const wllm_tensor* q, const wllm_tenso
   p.table_vec = aligned(cos_sin->data, 16) && p.table_stride % 4 == 0;
   p.eps = how->eps;
   p.inv_dim = 1.f / static_cast<float>(d);
+  p.wait_limit_ns = static_cast<unsigned long long>(env_int("WLLM_WAIT_LIMIT_NS", 200000000LL));
   p.k_inv = 1.f / k_scale;
   p.v_inv = 1.f / v_scale;
 

@@ -179,6 +179,7 @@ struct RotateParams {
   int vec, weight_vec, table_vec; // 16-byte accesses are aligned
   int row_lanes, warps_per_token; // set by launch_rotate
   float eps, inv_dim, k_inv, v_inv;
+  unsigned long long wait_limit_ns;
   int* err;
 };
 int launch_rotate(RotateParams p, int num_sms, cudaStream_t stream);

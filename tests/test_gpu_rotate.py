@@ -134,6 +134,44 @@ def test_rotate_many_tokens_and_single_heads():
     check(a, call(a), what="no query heads")
 
 
+@pytest.mark.parametrize("dtype,cache,Hq,Hkv,D,R,style,sections,weights", [
+    (BF, BF, 28, 4, 128, 128, "halves", (16, 24, 24), BF), (F16, U8, 32, 8, 128, 64, "adjacent", None, None),
+    (F32, F32, 3, 1, 80, 32, "halves", None, F32), (F32, U8, 8, 8, 64, 64, "adjacent", (5, 27), F32),
+    (BF, BF, 5, 5, 256, 256, "halves", None, F32), (F16, F16, 1, 2, 16, 16, "adjacent", None, F16),
+    (BF, BF, 64, 64, 256, 256, "halves", None, BF), (BF, U8, 0, 4, 128, 128, "halves", None, BF)])
+def test_rotate_a_thousand_tokens(dtype, cache, Hq, Hkv, D, R, style, sections, weights):
+    """Enough tokens for the resident form (the 64-head case's tokens are too large for it), with padding among them."""
+    a = make(2100 if Hq < 64 else 1100, Hq, Hkv, D, R, 16, dtype, cache, axes=len(sections) if sections else 1, weights=weights, pad=37)
+    check(a, call(a, style=style, sections=sections), style=style, sections=sections)
+    assert wllm.device_errors() == 0
+
+
+def test_rotate_a_thousand_tokens_strided_in_place_and_bad():
+    T, Hq, Hkv, D = 1500, 6, 2, 64
+    a = make(T, Hq, Hkv, D, 64, 16, BF, BF, weights=BF, pad=20, index=torch.int32)
+    live = (a["slots"] >= 0).nonzero()[:, 0]
+    a["slots"][live[5]], a["pos"][live[400]], a["pos"][live[-1]] = 10 ** 6, 500, -3
+    skipped = live[[5, 400, -1]].tolist()
+    before = parts(a["fused"], a)[0].clone()
+    got = call(a, in_place=True)
+    assert wllm.device_errors() == 1 | 32
+    check(a, got, skipped=skipped, q_before=before, what="in place")
+    # heads that do not lie next to each other
+    d = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in a.items()}
+    wide = [torch.zeros(T, n, D + 8, dtype=BF, device="cuda") for n in (Hq, Hkv, Hkv)]
+    for w, x in zip(wide, parts(d["fused"], a)):
+        w[:, :, :D] = x
+    q, k, v = (w[:, :, :D] for w in wide)
+    out = torch.zeros(T, Hq, D + 16, dtype=BF, device="cuda")
+    out[:, :, 8:D + 8] = d["q_out"]
+    wllm.rotate_and_cache(out[:, :, 8:D + 8], q, k, v, d["kc"], d["vc"], d["slots"], d["pos"], d["table"],
+                          q_weight=d["q_weight"], k_weight=d["k_weight"])
+    torch.cuda.synchronize()
+    assert wllm.device_errors() == 1 | 32
+    check(a, (out[:, :, 8:D + 8].cpu(), d["kc"].cpu(), d["vc"].cpu()), skipped=skipped, what="strided")
+    assert (out[:, :, :8] == 0).all() and (out[:, :, D + 8:] == 0).all()
+
+
 def test_rotate_leaves_out_tokens_with_a_bad_slot_or_position(monkeypatch):
     assert wllm.device_errors() == 0
     a = make(24, 4, 2, 64, 64, 16, BF, BF, weights=BF)
