@@ -498,8 +498,8 @@ int wllm_paged_attention_decode_sparse(const wllm_tensor* out, const wllm_tensor
                                        int block_size, wllm_stream stream);
 
 /*
- * The same over E4M3 caches: K = code * k_scale, V = code * v_scale; q and out
- * F16 or BF16 (bf16 queries are rounded to f16 for the products, as in
+ * The same over E4M3 caches: K = code * k_scale, V = code * v_scale; D 64 (block
+ * size >= 16), 128 or 256; q and out F16 or BF16 (bf16 queries are rounded to f16 for the products, as in
  * wllm_paged_attention_decode_fp8).
  */
 int wllm_paged_attention_decode_sparse_fp8(const wllm_tensor* out, const wllm_tensor* q,

@@ -278,6 +278,10 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+}  // namespace
+
+namespace wllm {
+
 // 3-D view {D, Hkv*bs, N_b} of a [N_b][Hkv][bs][D] pool; one box is 128 bytes
 // of a row by min(bs, 16) rows, 128-byte swizzled.
 int make_pool_map(CUtensorMap* map, const void* base, int dtype, int64_t num_blocks, int64_t hkv,
@@ -308,6 +312,10 @@ int make_pool_map(CUtensorMap* map, const void* base, int dtype, int64_t num_blo
   if (r != CUDA_SUCCESS) return fail(WLLM_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed: %d", name, (int)r);
   return WLLM_OK;
 }
+
+}  // namespace wllm
+
+namespace {
 
 // --- split-KV sizing -----------------------------------------------------------
 // Grid kernel: one CTA per (sequence, partition, kv-head tile); the largest

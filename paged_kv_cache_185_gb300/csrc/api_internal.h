@@ -3,6 +3,7 @@
 // Defined in api.cu; not part of the public header.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -48,5 +49,10 @@ bool contiguous(const wllm_tensor* t);
 bool same_shape(const wllm_tensor* a, const wllm_tensor* b);
 bool aligned(const void* p, uintptr_t a);
 bool positive_finite(float x);
+
+// TMA map of a [N_b][Hkv][bs][D] pool: 3-D view {D, Hkv*bs, N_b}; one box is
+// 128 bytes of a row by min(bs, 16) rows, 128-byte swizzled.
+int make_pool_map(CUtensorMap* map, const void* base, int dtype, int64_t num_blocks, int64_t hkv, int64_t bs, int64_t d,
+                  const char* name);
 
 }  // namespace wllm

@@ -269,6 +269,8 @@ int sparse_call(const wllm_tensor* out, const wllm_tensor* q, const wllm_tensor*
     return fail(WLLM_ERR_INVALID_ARG, "scale must be finite");
   if (d != 64 && d != 128 && d != 256)
     return fail(WLLM_ERR_UNSUPPORTED, "head_dim %lld not supported (64, 128, 256)", (long long)d);
+  if (kv_fp8 && d == 64 && bs < 16)
+    return fail(WLLM_ERR_UNSUPPORTED, "an fp8 cache with head_dim 64 needs block_size >= 16");
   if (hq > 65535 || top * bs > INT32_MAX || B * hq > INT32_MAX / 8) return fail(WLLM_ERR_UNSUPPORTED, "sizes too large");
   if (B == 0 || hq == 0) return WLLM_OK;
   if (nb < 1) return fail(WLLM_ERR_INVALID_ARG, "the pool has no blocks");
@@ -300,11 +302,20 @@ int sparse_call(const wllm_tensor* out, const wllm_tensor* q, const wllm_tensor*
   // an fp8 cache holds K / k_scale and V / v_scale: the scales return here
   p.scale_log2 = (kv_fp8 ? scale * k_scale : scale) * 1.4426950408889634f;
   p.v_scale = kv_fp8 ? v_scale : 1.f;
+  p.q_pairs = rows_aligned(q, 2, 4);
+  p.wait_limit_ns = static_cast<unsigned long long>(env_int("WLLM_WAIT_LIMIT_NS", 200000000LL));
   DeviceState* s = nullptr;
   if ((rc = locked_state(&s))) return rc;
   p.err = s->err;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = static_cast<cudaError_t>(launch_sparse_decode(dt, kv_fp8, static_cast<int>(d), p, s->num_sms, st));
+  CUtensorMap kmap{}, vmap{};
+  if (dt != WLLM_F32) {
+    const int kv_dt = kv_fp8 ? WLLM_FP8_E4M3 : dt;
+    if ((rc = make_pool_map(&kmap, k_cache->data, kv_dt, nb, hkv, bs, d, "k_cache"))) return rc;
+    if ((rc = make_pool_map(&vmap, v_cache->data, kv_dt, nb, hkv, bs, d, "v_cache"))) return rc;
+  }
+  const cudaError_t e = static_cast<cudaError_t>(
+      launch_sparse_decode(dt, kv_fp8, static_cast<int>(d), kmap, vmap, p, s->num_sms, st));
   if (e != cudaSuccess) return cuda_fail(e, "sparse decode launch");
   return env_flag("WLLM_CHECK") ? collect_device_errors(s, st, "paged_attention_decode_sparse") : WLLM_OK;
 }

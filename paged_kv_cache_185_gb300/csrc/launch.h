@@ -231,10 +231,13 @@ struct SparseParams {
   const int32_t* selected;        // [B][Hkv][top]
   int64_t sel_sb, sel_sh;
   int num_seqs, num_kv_heads, group, num_head_tiles, num_blocks, log2_bs, max_tokens, top;
+  int q_pairs;                    // query rows allow 4-byte loads
   float scale_log2, v_scale;
+  unsigned long long wait_limit_ns;
   int* err;
 };
-int launch_sparse_decode(int dtype, bool kv_fp8, int head_dim, SparseParams p, int num_sms, cudaStream_t stream);
+int launch_sparse_decode(int dtype, bool kv_fp8, int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                         SparseParams p, int num_sms, cudaStream_t stream);
 
 // Check-mode kernels: record index errors in the device error word.
 int launch_check_decode(const int32_t* block_tables, int64_t bt_stride,

@@ -8,21 +8,18 @@
 //   O <- O 2^(m - m') + sum_t 2^(s_t - m') v_t.
 //
 // Tensor-core kernel (f16/bf16 and E4M3 caches).  A warp takes 16 tokens at a
-// time straight from global memory into mma.sync m16n8k16 fragments, without a
-// stage in shared memory:
-//   S[heads x tokens] = Q K^T: a lane (g = lane/4, c = lane%4) loads 16 bytes
-//     of token row g at chunk 4i + c.  Its elements serve as k indices
-//     2c, 2c+1, 2c+8, 2c+9 of consecutive k16 steps; the sum over head_dim
-//     takes any order, so Q's fragment takes the same one.
-//   O^T[dims x heads] += V^T P^T: a lane loads chunk g (+8i) of the rows
-//     2c, 2c+1, 2c+8, 2c+9; one byte permute pairs two rows' element, which is
-//     a word of the A fragment with row g = element 2i and row g+8 = element
-//     2i+1 of the lane's chunk.  P^T's fragment is S's accumulator, rounded to
-//     the 16-bit type (tensor cores take 16-bit weights; the sum l adds the
-//     rounded weights, so numerator and denominator agree).
-// Every 16-byte load is part of a whole 64- or 128-byte run.  E4M3 codes are
-// widened to f16 in registers, which is exact; bf16 queries are rounded to f16
-// for that product, as in the decode over an fp8 cache.
+// time; its K and V rows come by TMA (128-byte swizzle) into the warp's own ring
+// of shared-memory stages, the next units' copies in flight while one is
+// multiplied with mma.sync m16n8k16:
+//   S[heads x tokens] = Q K^T: K rows by ldmatrix are the B operand, Q's heads
+//     the A operand in registers (a tile of 8 heads leaves its lower half zero:
+//     the instructions are not what bounds this);
+//   O^T[dims x heads] += V^T P^T: V by ldmatrix.trans is the A operand, and S's
+//     accumulator, rounded to the 16-bit type, is already P^T's fragment
+//     (tensor cores take 16-bit weights; the sum l adds the rounded weights, so
+//     numerator and denominator agree).
+// E4M3 codes are widened to f16 in registers, which is exact, with the head_dim
+// order of the fp8 decode; bf16 queries are rounded to f16 for that product.
 //
 // Work split: the list of a (sequence, kv head, tile of up to 8 or 16 query
 // heads) is divided over the warps of a cluster of 1 to 8 CTAs; warps meet in
@@ -30,71 +27,69 @@
 // the GPU with neither a second launch nor a workspace, and in a fixed order.
 // Bound: memory, each selected K and V byte is read once per head tile.
 //
-// The f32 kernel keeps the same split with binary32 FMA (no tensor cores).
+// The f32 kernel keeps the same split with binary32 FMA (no tensor cores), its
+// rows straight from global memory.
 #include <cooperative_groups.h>
 
 #include <atomic>
 #include <type_traits>
 
-#include "common.cuh"
+#include "decode_kernel.cuh"
 #include "launch.h"
+#include "mma_e4m3.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace wllm {
 namespace {
 
-constexpr int kSparseWarps = 4;
-constexpr int kSparseThreads = kSparseWarps * 32;
 constexpr int kMaxSparseCluster = 8;
 
-__device__ __forceinline__ uint4 load16(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
-
-// Where a warp's next 16 tokens are: for each half of 8 rows the byte offset
-// of its first row and how many of its rows are below the context length.
-struct UnitRows {
-  int64_t at[2];
-  int live[2];
+// Warps of a CTA and stages of a warp's ring: about 64 KB of stages a CTA, three
+// CTAs an SM.
+template <typename B, int D>
+struct SparseTuning {
+  static constexpr int kStage = Geom<B, D>::kStageBytes;  // 16 tokens' K and V rows
+  static constexpr int kWarps = kStage >= 16384 ? 2 : 4;
+  static constexpr int kStages = kStage >= 8192 ? 2 : kStage >= 4096 ? 3 : 6;
+  static constexpr int kRing = kStages * kStage;          // a warp's
 };
 
-// Units of 16 listed tokens; unit u covers list positions 16u .. 16u+15.
+// A unit of up to 16 listed tokens of one block: its physical block, its first
+// row's offset in it, and how many of its rows are below the context length.
 // Lanes look up 32 units at a time (the caller broadcasts).  Entries that are
 // negative are padding; others outside the sequence are recorded and skipped.
-struct UnitLookup {
-  int64_t at[2];
-  int live[2];
-  __device__ __forceinline__ void fetch(const SparseParams& p, const int32_t* list, const int32_t* table, int len, int h,
-                                        int row_bytes, int64_t unit) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int64_t pos = unit * 16 + half * 8;
-      at[half] = 0;
-      live[half] = 0;
-      if (half == 1 && p.log2_bs > 3) {  // both halves lie in one block
-        at[1] = at[0] + 8 * row_bytes;
-        live[1] = max(0, live[0] - 8);
-        live[0] = min(8, live[0]);
-        continue;
-      }
-      const int64_t e = pos >> p.log2_bs;
-      if (e >= p.top || len == 0) continue;
-      const int id = __ldg(list + e);
-      if (id < 0) continue;
-      const int off = static_cast<int>(pos) & ((1 << p.log2_bs) - 1);
-      if (id > (len - 1) >> p.log2_bs) {
-        atomicOr(p.err, kErrBlock);
-        continue;
-      }
-      const int phys = __ldg(table + id);
-      if (phys < 0 || phys >= p.num_blocks) {
-        atomicOr(p.err, kErrBlock);
-        continue;
-      }
-      at[half] = (((static_cast<int64_t>(phys) * p.num_kv_heads + h) << p.log2_bs) + off) * row_bytes;
-      live[half] = max(0, min(p.log2_bs > 3 ? 16 : 8, len - ((id << p.log2_bs) + off)));
-    }
-  }
+struct Unit {
+  int phys, off, live;
 };
+
+__device__ __forceinline__ Unit find_unit(const SparseParams& p, const int32_t* list, const int32_t* table, int len,
+                                          int64_t unit) {
+  Unit u{0, 0, 0};
+  const int log2_units = max(0, p.log2_bs - 4);  // units of a block
+  const int64_t e = unit >> log2_units;
+  if (e >= p.top || len == 0) return u;
+  const int id = __ldg(list + e);
+  if (id < 0) return u;
+  if (id > (len - 1) >> p.log2_bs) {
+    atomicOr(p.err, kErrBlock);
+    return u;
+  }
+  const int phys = __ldg(table + id);
+  if (phys < 0 || phys >= p.num_blocks) {
+    atomicOr(p.err, kErrBlock);
+    return u;
+  }
+  u.phys = phys;
+  u.off = static_cast<int>(unit & ((1 << log2_units) - 1)) << 4;
+  u.live = max(0, min(min(16, 1 << p.log2_bs), len - ((id << p.log2_bs) + u.off)));
+  return u;
+}
+
+// Units of one list.
+__device__ __forceinline__ int64_t units_of(const SparseParams& p) {
+  return static_cast<int64_t>(p.top) << max(0, p.log2_bs - 4);
+}
 
 // Partial results of one warp or CTA in shared memory: [HT heads][D] outputs,
 // then maxima and sums.
@@ -105,67 +100,56 @@ struct Partial {
   float l[HT];
 };
 
-// Merge of the warps' partials (in `part`, one a warp) and of the cluster's
-// CTAs; the cluster's ranks share the output elements of the tile.
-template <typename T, int D, int HT>
-__device__ __forceinline__ void merge_and_store(const SparseParams& p, cg::cluster_group& cluster, Partial<D, HT>* part,
+// Merge of the warps' partials (one every `stride` bytes from `raw` on) and of
+// the cluster's CTAs; the cluster's ranks share the output elements of the tile.
+template <typename T, int D, int HT, int WARPS>
+__device__ __forceinline__ void merge_and_store(const SparseParams& p, cg::cluster_group& cluster, uint8_t* raw, int stride,
                                                 T* out, int heads) {
+  constexpr int kThreads = WARPS * 32;
   const int tid = threadIdx.x, ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  auto part = [&](int w) { return reinterpret_cast<Partial<D, HT>*>(raw + w * stride); };
   __syncthreads();
-  if (ctas == 1) {
-    for (int i = tid; i < heads * D; i += kSparseThreads) {
-      const int h = i / D, d = i - h * D;
-      float m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kSparseWarps; ++w) m = fmaxf(m, part[w].m[h]);
-      float l = 0.f, o = 0.f;
-#pragma unroll
-      for (int w = 0; w < kSparseWarps; ++w) {
-        const float f = part[w].m[h] == -INFINITY ? 0.f : exp2f(part[w].m[h] - m);
-        l = fmaf(f, part[w].l[h], l);
-        o = fmaf(f, part[w].o[h][d], o);
-      }
-      out[h * p.o_sh + d] = from_f32<T>(l == 0.f ? 0.f : o / l * p.v_scale);
-    }
-    return;
-  }
-  // this CTA's merge, in place of its first warp's partial
-  float mc[kSparseWarps];
-  for (int i = tid; i < heads * D; i += kSparseThreads) {
+  // this CTA's merge; of several, into its first warp's partial
+  for (int i = tid; i < heads * D; i += kThreads) {
     const int h = i / D, d = i - h * D;
     float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kSparseWarps; ++w) m = fmaxf(m, part[w].m[h]);
-    float o = 0.f;
+    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, part(w)->m[h]);
+    float l = 0.f, o = 0.f;
 #pragma unroll
-    for (int w = 0; w < kSparseWarps; ++w) {
-      mc[w] = part[w].m[h] == -INFINITY ? 0.f : exp2f(part[w].m[h] - m);
-      o = fmaf(mc[w], part[w].o[h][d], o);
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = part(w)->m[h] == -INFINITY ? 0.f : exp2f(part(w)->m[h] - m);
+      l = fmaf(f, part(w)->l[h], l);
+      o = fmaf(f, part(w)->o[h][d], o);
     }
-    part[0].o[h][d] = o;
+    if (ctas == 1)
+      out[h * p.o_sh + d] = from_f32<T>(l == 0.f ? 0.f : o / l * p.v_scale);
+    else
+      part(0)->o[h][d] = o;
   }
+  if (ctas == 1) return;
   __syncthreads();
   if (tid < heads) {
     float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kSparseWarps; ++w) m = fmaxf(m, part[w].m[tid]);
+    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, part(w)->m[tid]);
 #pragma unroll
-    for (int w = 0; w < kSparseWarps; ++w) {
-      const float f = part[w].m[tid] == -INFINITY ? 0.f : exp2f(part[w].m[tid] - m);
-      l = fmaf(f, part[w].l[tid], l);
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = part(w)->m[tid] == -INFINITY ? 0.f : exp2f(part(w)->m[tid] - m);
+      l = fmaf(f, part(w)->l[tid], l);
     }
-    part[0].m[tid] = m;
-    part[0].l[tid] = l;
+    part(0)->m[tid] = m;
+    part(0)->l[tid] = l;
   }
   cluster.sync();
-  for (int i = rank * kSparseThreads + tid; i < heads * D; i += ctas * kSparseThreads) {
+  for (int i = rank * kThreads + tid; i < heads * D; i += ctas * kThreads) {
     const int h = i / D, d = i - h * D;
     float ms[kMaxSparseCluster], ls[kMaxSparseCluster], os[kMaxSparseCluster];
     float m = -INFINITY;
 #pragma unroll
     for (int r = 0; r < kMaxSparseCluster; ++r) {
       if (r < ctas) {
-        const Partial<D, HT>* peer = cluster.map_shared_rank(part, r);
+        const Partial<D, HT>* peer = cluster.map_shared_rank(part(0), r);
         ms[r] = peer->m[h], ls[r] = peer->l[h], os[r] = peer->o[h][d];
         m = fmaxf(m, ms[r]);
       }
@@ -184,25 +168,20 @@ __device__ __forceinline__ void merge_and_store(const SparseParams& p, cg::clust
   cluster.sync();  // a CTA's shared memory outlives its peers' reads
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t as_pair(const uint8_t* p) {
-  return *reinterpret_cast<const uint32_t*>(p);
-}
-
 // --- tensor-core kernel --------------------------------------------------------
 // T: query and output type; F8: the caches hold E4M3 codes (M is then f16).
 template <typename T, bool F8, int D, int HT>
-__global__ void __launch_bounds__(kSparseThreads) sparse_mma_kernel(const SparseParams p) {
+__global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, uint8_t, T>::type, D>::kWarps * 32))
+    sparse_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const SparseParams p) {
+  using B = typename std::conditional<F8, uint8_t, T>::type;
   using M = typename std::conditional<F8, __half, T>::type;
-  constexpr int kElt = F8 ? 1 : 2;
-  constexpr int kRow = D * kElt;                        // bytes of a token row
-  constexpr int kNT = HT / 8;                           // head tiles of 8
-  constexpr int kKLoads = kRow / 64;                    // 16-byte K loads of a lane and row
-  constexpr int kVBytes = kRow / 8 < 16 ? 8 : 16;       // bytes of one V load
-  constexpr int kVLoads = kRow / (8 * kVBytes);
-  constexpr int kVWords = kVBytes / 4;                  // 32-bit words of one V load
-  constexpr int kMT = F8 ? 2 * kVWords : kVWords;       // m16 tiles of one V load (2 elements a lane each)
-  constexpr int kSteps = F8 ? 4 : 2;                    // k16 steps of one K load
+  using G = Geom<B, D>;
+  using Tune = SparseTuning<B, D>;
+  constexpr int kWarps = Tune::kWarps, kStages = Tune::kStages;
+  constexpr int kNT = HT / 8;                           // tiles of 8 heads
+  constexpr int kKS = D / 16;                           // k16 steps over head_dim
+  static_assert(sizeof(Partial<D, HT>) <= Tune::kRing, "a warp's partial takes its ring's place");
 
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -214,8 +193,13 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_mma_kernel(const Sparse
   const int heads = min(HT, p.group - tile * HT);
   const int head0 = h * p.group + tile * HT;
 
-  extern __shared__ __align__(16) uint8_t raw[];
-  Partial<D, HT>* part = reinterpret_cast<Partial<D, HT>*>(raw);
+  extern __shared__ __align__(16) uint8_t unaligned[];
+  uint8_t* raw = unaligned + ((1024 - (smem_u32(unaligned) & 1023)) & 1023);  // swizzled boxes start at 1024 bytes
+  uint8_t* ring = raw + warp * Tune::kRing;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(raw + kWarps * Tune::kRing) + warp * kStages;
+  if (lane < kStages) mbar_init(smem_u32(&bars[lane]), 1);
+  fence_mbar_init();
+  __syncwarp();
 
   int len = p.context_lens[b];
   if (len < 0 || len > p.max_tokens) {
@@ -224,111 +208,125 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_mma_kernel(const Sparse
   }
   const int32_t* list = p.selected + b * p.sel_sb + h * p.sel_sh;
   const int32_t* table = p.block_tables + b * p.bt_stride;
+  const int64_t units = units_of(p);
+  const int stride = ctas * kWarps;
 
-  // Q fragments: heads 8a + g, the elements that this lane's K loads bring
-  uint32_t qf[kNT][kKLoads][kSteps][2];
+  // 32 units of this warp, a lane each; those with tokens
+  Unit mine{0, 0, 0};
+  int64_t u0 = rank * kWarps + warp;
+  auto find = [&]() -> unsigned {
+    mine.live = 0;
+    if (u0 + int64_t(lane) * stride < units) mine = find_unit(p, list, table, len, u0 + int64_t(lane) * stride);
+    return __ballot_sync(kFullMask, mine.live > 0);
+  };
+  unsigned to_use = u0 < units ? find() : 0u, to_copy = to_use;
+  int next_stage = 0;  // of the copies; the uses follow in the same order
+  const uint32_t box_bytes = 128u * (G::kPairRows ? 8u : static_cast<uint32_t>(min(16, 1 << p.log2_bs)));
+  auto copy = [&] {  // the next unit's K and V rows, one box a lane
+    const int from = __ffs(to_copy) - 1;
+    to_copy &= to_copy - 1;
+    const int phys = __shfl_sync(kFullMask, mine.phys, from), off = __shfl_sync(kFullMask, mine.off, from);
+    const uint32_t bar = smem_u32(&bars[next_stage]), dst = smem_u32(ring + next_stage * Tune::kStage);
+    if (lane == 0) mbar_arrive_expect_tx(bar, 2 * G::kColBoxes * box_bytes);
+    __syncwarp();
+    if (lane < 2 * G::kColBoxes) {
+      const bool is_v = lane >= G::kColBoxes;
+      const int box = lane - (is_v ? G::kColBoxes : 0);
+      const int at = (h << p.log2_bs) + off;
+      tma_load_3d(dst + (is_v ? G::kTileBytes : 0) + box * 2048, is_v ? &vmap : &kmap, bar, box * G::kBoxCols,
+                  G::kPairRows ? at >> 1 : at, phys);
+    }
+    next_stage = next_stage + 1 == kStages ? 0 : next_stage + 1;
+  };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s)
+    if (to_copy) copy();
+
+  // Q fragments: head 8a + g; elements 16s + 2c (+8) of 16-bit rows, 16s + 4c (+2) where codes are widened
+  uint32_t qf[kNT][kKS][2];
 #pragma unroll
   for (int a = 0; a < kNT; ++a)
 #pragma unroll
-    for (int i = 0; i < kKLoads; ++i)
+    for (int s = 0; s < kKS; ++s)
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t x = 0u;
-          if (8 * a + g < heads) {
-            constexpr int kPer = 16 / kElt;  // elements of one K load
-            const int d = (4 * i + c) * kPer + 4 * s + 2 * e;
-            const T* q = static_cast<const T*>(p.q) + b * p.q_sb + (head0 + 8 * a + g) * p.q_sh + d;
-            if constexpr (std::is_same<T, M>::value) {
-              const uint16_t lo = *reinterpret_cast<const uint16_t*>(q), hi = *reinterpret_cast<const uint16_t*>(q + 1);
-              x = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-            } else {
-              x = Mma<M>::pack(to_f32(q[0]), to_f32(q[1]));
-            }
+      for (int e = 0; e < 2; ++e) {
+        uint32_t x = 0u;
+        if (8 * a + g < heads) {
+          const int d = F8 ? 16 * s + 4 * c + 2 * e : 16 * s + 2 * c + 8 * e;
+          const T* q = static_cast<const T*>(p.q) + b * p.q_sb + (head0 + 8 * a + g) * p.q_sh + d;
+          if (p.q_pairs) {
+            x = *reinterpret_cast<const uint32_t*>(q);
+          } else {
+            const uint16_t lo = *reinterpret_cast<const uint16_t*>(q), hi = *reinterpret_cast<const uint16_t*>(q + 1);
+            x = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
           }
-          qf[a][i][s][e] = x;
+          if constexpr (F8) x = to_f16x2<T>(x);
         }
+        qf[a][s][e] = x;
+      }
 
-  float m[kNT], l[kNT];
-  float o[kVLoads][kMT][kNT][4];
+  float m[kNT], l[kNT], o[kKS][kNT][4];
 #pragma unroll
   for (int a = 0; a < kNT; ++a) m[a] = -INFINITY, l[a] = 0.f;
 #pragma unroll
-  for (int i = 0; i < kVLoads; ++i)
+  for (int t = 0; t < kKS; ++t)
 #pragma unroll
-    for (int t = 0; t < kMT; ++t)
+    for (int a = 0; a < kNT; ++a)
 #pragma unroll
-      for (int a = 0; a < kNT; ++a)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][t][a][e] = 0.f;
+      for (int e = 0; e < 4; ++e) o[t][a][e] = 0.f;
 
-  const int64_t units = ((static_cast<int64_t>(p.top) << p.log2_bs) + 15) / 16;
-  const int stride = ctas * kSparseWarps;
-  for (int64_t u0 = rank * kSparseWarps + warp; u0 < units; u0 += 32LL * stride) {
-    UnitLookup look;
-    look.at[0] = look.at[1] = 0;
-    look.live[0] = look.live[1] = 0;
-    if (u0 + int64_t(lane) * stride < units)
-      look.fetch(p, list, table, len, h, kRow, u0 + int64_t(lane) * stride);
-    unsigned todo = __ballot_sync(kFullMask, look.live[0] + look.live[1] > 0);
-    while (todo) {
-      const int from = __ffs(todo) - 1;
-      todo &= todo - 1;
-      UnitRows r;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        r.at[half] = __shfl_sync(kFullMask, look.at[half], from);
-        r.live[half] = __shfl_sync(kFullMask, look.live[half], from);
+  int stage = 0;
+  uint32_t phase = 0u;  // of every stage, turned when the ring comes round
+  bool lost = false;
+  while (u0 < units && !lost) {
+    while (to_use) {
+      const int from = __ffs(to_use) - 1;
+      to_use &= to_use - 1;
+      const int live = __shfl_sync(kFullMask, mine.live, from);
+      if (!mbar_wait_bounded(smem_u32(&bars[stage]), phase, p.wait_limit_ns)) {
+        // give up: record it, let what is in flight land (again with a limit), and take no more units
+        if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
+        for (int s = 0; s < kStages; ++s) mbar_wait_bounded(smem_u32(&bars[s]), s >= stage ? phase : phase ^ 1u, p.wait_limit_ns);
+        lost = true;
+        break;
       }
-      // K rows g of both halves, V rows 2c, 2c+1 of both halves
-      uint4 kx[2][kKLoads];
+      const uint32_t kt = smem_u32(ring + stage * Tune::kStage), vt = kt + G::kTileBytes;
+      // S = Q K^T, tokens 0-7 and 8-15
+      float s[2][4];
 #pragma unroll
       for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int i = 0; i < kKLoads; ++i)
-          kx[half][i] = g < r.live[half] ? load16(p.k_cache + r.at[half] + g * kRow + (4 * i + c) * 16)
-                                         : make_uint4(0u, 0u, 0u, 0u);
-      uint32_t vx[4][kVLoads][kVWords];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int half = n >> 1, tok = 2 * c + (n & 1);
-        const uint8_t* src = p.v_cache + r.at[half] + tok * kRow + g * kVBytes;
-#pragma unroll
-        for (int i = 0; i < kVLoads; ++i) {
-          if constexpr (kVBytes == 16) {
-            const uint4 x = tok < r.live[half] ? load16(src + i * 8 * kVBytes) : make_uint4(0u, 0u, 0u, 0u);
-            vx[n][i][0] = x.x, vx[n][i][1] = x.y, vx[n][i][2] = x.z, vx[n][i][3] = x.w;
-          } else {
-            const uint2 x = tok < r.live[half] ? __ldg(reinterpret_cast<const uint2*>(src + i * 8 * kVBytes)) : make_uint2(0u, 0u);
-            vx[n][i][0] = x.x, vx[n][i][1] = x.y;
-          }
-        }
-      }
-      // S = Q K^T
-      float s[2][4];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll
         for (int e = 0; e < 4; ++e) s[half][e] = 0.f;
+      if constexpr (F8) {
+        const int k_row = (lane & 7) + (((lane >> 3) & 1) << 3), k_chunk = lane >> 4;
 #pragma unroll
-        for (int i = 0; i < kKLoads; ++i) {
-          const uint32_t w[4] = {kx[half][i].x, kx[half][i].y, kx[half][i].z, kx[half][i].w};
+        for (int kp = 0; kp < kKS / 2; ++kp) {
+          uint32_t r[4];  // tokens 0-7 and 8-15 of chunk 2kp, then of chunk 2kp + 1
+          ldsm_x4(kt + code_offset<D>(k_row, 2 * kp + k_chunk), r);
 #pragma unroll
-          for (int t = 0; t < kSteps; ++t) {
+          for (int x = 0; x < 4; ++x) {
             uint32_t bf[2];
-            if constexpr (F8) {
-              e4m3x4_to_f16x2x2(w[t], bf[0], bf[1]);
-            } else {
-              bf[0] = w[2 * t], bf[1] = w[2 * t + 1];
-            }
-            const uint32_t af[4] = {qf[0][i][t][0], kNT > 1 ? qf[kNT - 1][i][t][0] : 0u, qf[0][i][t][1],
-                                    kNT > 1 ? qf[kNT - 1][i][t][1] : 0u};
-            Mma<M>::run(s[half], af, bf);
+            e4m3x4_to_f16x2x2(r[x], bf[0], bf[1]);
+            const int step = 2 * kp + (x >> 1);
+            const uint32_t af[4] = {qf[0][step][0], kNT > 1 ? qf[kNT - 1][step][0] : 0u, qf[0][step][1],
+                                    kNT > 1 ? qf[kNT - 1][step][1] : 0u};
+            Mma<M>::run(s[x & 1], af, bf);
           }
         }
+      } else {
+        const int k_row = (lane & 7) + ((lane >> 4) << 3), k_chunk = (lane >> 3) & 1;
+#pragma unroll
+        for (int step = 0; step < kKS; ++step) {
+          uint32_t r[4];  // chunks 2 step and 2 step + 1 of tokens 0-7, then of tokens 8-15
+          ldsm_x4(kt + tile_offset(k_row, 2 * step + k_chunk), r);
+          const uint32_t af[4] = {qf[0][step][0], kNT > 1 ? qf[kNT - 1][step][0] : 0u, qf[0][step][1],
+                                  kNT > 1 ? qf[kNT - 1][step][1] : 0u};
+          const uint32_t b0[2] = {r[0], r[1]}, b1[2] = {r[2], r[3]};
+          Mma<M>::run(s[0], af, b0);
+          Mma<M>::run(s[1], af, b1);
+        }
       }
-      // weights: head 8a + g, tokens 2c, 2c+1 of both halves
+      // weights: head 8a + g, tokens 2c, 2c + 1 of both halves
       uint32_t pf[kNT][2];
 #pragma unroll
       for (int a = 0; a < kNT; ++a) {
@@ -337,23 +335,20 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_mma_kernel(const Sparse
         for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            x[2 * half + e] = 2 * c + e < r.live[half] ? s[half][2 * a + e] * p.scale_log2 : -INFINITY;
+            x[2 * half + e] = 8 * half + 2 * c + e < live ? s[half][2 * a + e] * p.scale_log2 : -INFINITY;
         float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
         top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
         const float mn = fmaxf(m[a], top);
-        const bool moved = mn > m[a];
-        if (__any_sync(kFullMask, moved)) {
+        if (__any_sync(kFullMask, mn > m[a])) {
           const float f = m[a] == -INFINITY ? 0.f : exp2f(m[a] - mn);
           l[a] *= f;
           m[a] = mn;
           const float f0 = __shfl_sync(kFullMask, f, 8 * c), f1 = __shfl_sync(kFullMask, f, 8 * c + 4);
 #pragma unroll
-          for (int i = 0; i < kVLoads; ++i)
-#pragma unroll
-            for (int t = 0; t < kMT; ++t) {
-              o[i][t][a][0] *= f0, o[i][t][a][1] *= f1, o[i][t][a][2] *= f0, o[i][t][a][3] *= f1;
-            }
+          for (int t = 0; t < kKS; ++t) {
+            o[t][a][0] *= f0, o[t][a][1] *= f1, o[t][a][2] *= f0, o[t][a][3] *= f1;
+          }
         }
         const float base = m[a] == -INFINITY ? 0.f : m[a];
 #pragma unroll
@@ -363,61 +358,89 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_mma_kernel(const Sparse
           l[a] += to_f32(w[0]) + to_f32(w[1]);
         }
       }
-      // O^T += V^T P^T
+      // O^T += V^T P^T; V rows behind the context are zeroed (they may hold anything)
+      const bool tail = live < 16;
+      const uint32_t keep_lo = (2 * c < live ? 0x0000ffffu : 0u) | (2 * c + 1 < live ? 0xffff0000u : 0u);
+      const uint32_t keep_hi = (2 * c + 8 < live ? 0x0000ffffu : 0u) | (2 * c + 9 < live ? 0xffff0000u : 0u);
+      auto product = [&](int t, uint32_t (&af)[4]) {
+        if (tail) af[0] &= keep_lo, af[1] &= keep_lo, af[2] &= keep_hi, af[3] &= keep_hi;
 #pragma unroll
-      for (int i = 0; i < kVLoads; ++i)
+        for (int a = 0; a < kNT; ++a) Mma<M>::run(o[t][a], af, pf[a]);
+      };
+      if constexpr (F8) {
+        const int v_row = (lane & 7) + (((lane >> 3) & 1) << 3), v_chunk = lane >> 4;
 #pragma unroll
-        for (int w = 0; w < kVWords; ++w) {
-          if constexpr (F8) {
-            uint32_t y[4][2];
+        for (int mp = 0; mp < kKS / 2; ++mp) {
+          uint32_t r[4];  // tokens 0-7 and 8-15 of chunk 2mp, then of chunk 2mp + 1
+          ldsm_x4_trans(vt + code_offset<D>(v_row, 2 * mp + v_chunk), r);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) e4m3x4_to_f16x2x2(vx[n][i][w], y[n][0], y[n][1]);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t af[4] = {__byte_perm(y[0][e], y[1][e], 0x5410), __byte_perm(y[0][e], y[1][e], 0x7632),
-                                      __byte_perm(y[2][e], y[3][e], 0x5410), __byte_perm(y[2][e], y[3][e], 0x7632)};
-#pragma unroll
-              for (int a = 0; a < kNT; ++a) Mma<M>::run(o[i][2 * w + e][a], af, pf[a]);
-            }
-          } else {
-            const uint32_t af[4] = {
-                __byte_perm(vx[0][i][w], vx[1][i][w], 0x5410), __byte_perm(vx[0][i][w], vx[1][i][w], 0x7632),
-                __byte_perm(vx[2][i][w], vx[3][i][w], 0x5410), __byte_perm(vx[2][i][w], vx[3][i][w], 0x7632)};
-#pragma unroll
-            for (int a = 0; a < kNT; ++a) Mma<M>::run(o[i][w][a], af, pf[a]);
+          for (int x = 0; x < 2; ++x) {
+            // bytes (t, e), (t, e+1), (t+1, e), (t+1, e+1) -> (t, e), (t+1, e), (t, e+1), (t+1, e+1)
+            uint32_t af[4];
+            e4m3x4_to_f16x2x2(__byte_perm(r[2 * x], 0u, 0x3120), af[0], af[1]);
+            e4m3x4_to_f16x2x2(__byte_perm(r[2 * x + 1], 0u, 0x3120), af[2], af[3]);
+            product(2 * mp + x, af);
           }
         }
+      } else {
+        const int v_row = (lane & 7) + ((lane >> 4) << 3), v_chunk = (lane >> 3) & 1;
+#pragma unroll
+        for (int t = 0; t < kKS; ++t) {
+          uint32_t af[4];
+          ldsm_x4_trans(vt + tile_offset(v_row, 2 * t + v_chunk), af);
+          product(t, af);
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (to_copy) copy();
+      if (++stage == kStages) stage = 0, phase ^= 1u;
     }
+    if (lost) break;
+    u0 += 32LL * stride;
+    if (u0 >= units) break;
+    to_use = to_copy = find();
+#pragma unroll
+    for (int s = 0; s < kStages; ++s)
+      if (to_copy) copy();
   }
 
-  // this warp's partial: heads 8a + 2c, 8a + 2c + 1, elements (8i + g) * 2 kMT + 2t, + 1
-  Partial<D, HT>& mine = part[warp];
+  // this warp's partial in the place of its ring: heads 8a + 2c, 8a + 2c + 1
+  Partial<D, HT>& out = *reinterpret_cast<Partial<D, HT>*>(ring);
 #pragma unroll
   for (int a = 0; a < kNT; ++a) {
     l[a] += __shfl_xor_sync(kFullMask, l[a], 1);
     l[a] += __shfl_xor_sync(kFullMask, l[a], 2);
     if (c == 0) {
-      mine.m[8 * a + g] = m[a];
-      mine.l[8 * a + g] = l[a];
+      out.m[8 * a + g] = m[a];
+      out.l[8 * a + g] = l[a];
     }
 #pragma unroll
-    for (int i = 0; i < kVLoads; ++i)
-#pragma unroll
-      for (int t = 0; t < kMT; ++t) {
-        const int d = (8 * i + g) * 2 * kMT + 2 * t;
-        *reinterpret_cast<float2*>(&mine.o[8 * a + 2 * c][d]) = make_float2(o[i][t][a][0], o[i][t][a][2]);
-        *reinterpret_cast<float2*>(&mine.o[8 * a + 2 * c + 1][d]) = make_float2(o[i][t][a][1], o[i][t][a][3]);
+    for (int t = 0; t < kKS; ++t) {
+      if constexpr (F8) {  // rows g and g + 8 are elements 16t + 2g and 16t + 2g + 1
+        const int d = 16 * t + 2 * g;
+        *reinterpret_cast<float2*>(&out.o[8 * a + 2 * c][d]) = make_float2(o[t][a][0], o[t][a][2]);
+        *reinterpret_cast<float2*>(&out.o[8 * a + 2 * c + 1][d]) = make_float2(o[t][a][1], o[t][a][3]);
+      } else {
+        const int d = 16 * t + g;
+        out.o[8 * a + 2 * c][d] = o[t][a][0];
+        out.o[8 * a + 2 * c + 1][d] = o[t][a][1];
+        out.o[8 * a + 2 * c][d + 8] = o[t][a][2];
+        out.o[8 * a + 2 * c + 1][d + 8] = o[t][a][3];
       }
+    }
   }
-  merge_and_store<T, D, HT>(p, cluster, part, static_cast<T*>(p.out) + b * p.o_sb + head0 * p.o_sh, heads);
+  merge_and_store<T, D, HT, kWarps>(p, cluster, raw, Tune::kRing, static_cast<T*>(p.out) + b * p.o_sb + head0 * p.o_sh,
+                                    heads);
 }
 
 // --- f32 kernel ------------------------------------------------------------------
 // A warp takes 8 tokens (half a unit) at a time: lane (g, c) holds row g's
 // chunks 4i + c for the products with the tile's 8 query heads (in shared
 // memory), the four lanes of a row sum; then lane owns dims lane + 32i of V.
+constexpr int kF32Warps = 4;
+
 template <int D>
-__global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const SparseParams p) {
+__global__ void __launch_bounds__(kF32Warps * 32) sparse_f32_kernel(const SparseParams p) {
   constexpr int HT = 8, kRow = D * 4, kChunks = D / 16;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -431,7 +454,7 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const Sparse
 
   extern __shared__ __align__(16) uint8_t raw[];
   Partial<D, HT>* part = reinterpret_cast<Partial<D, HT>*>(raw);
-  float* qs = reinterpret_cast<float*>(part + kSparseWarps);             // [HT][D]
+  float* qs = reinterpret_cast<float*>(part + kF32Warps);             // [HT][D]
   float* ps = qs + HT * D + warp * 64;                                   // [8 tokens][HT] weights of this warp
 
   int len = p.context_lens[b];
@@ -441,7 +464,7 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const Sparse
   }
   const int32_t* list = p.selected + b * p.sel_sb + h * p.sel_sh;
   const int32_t* table = p.block_tables + b * p.bt_stride;
-  for (int i = threadIdx.x; i < HT * D; i += kSparseThreads) {
+  for (int i = threadIdx.x; i < HT * D; i += kF32Warps * 32) {
     const int a = i / D, d = i - a * D;
     qs[i] = a < heads ? static_cast<const float*>(p.q)[b * p.q_sb + (head0 + a) * p.q_sh + d] : 0.f;
   }
@@ -454,23 +477,22 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const Sparse
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) o[a][i] = 0.f;
   }
-  const int64_t units = ((static_cast<int64_t>(p.top) << p.log2_bs) + 15) / 16;
-  const int stride = ctas * kSparseWarps;
-  for (int64_t u0 = rank * kSparseWarps + warp; u0 < units; u0 += 32LL * stride) {
-    UnitLookup look;
-    look.at[0] = look.at[1] = 0;
-    look.live[0] = look.live[1] = 0;
-    if (u0 + int64_t(lane) * stride < units)
-      look.fetch(p, list, table, len, h, kRow, u0 + int64_t(lane) * stride);
-    unsigned todo = __ballot_sync(kFullMask, look.live[0] + look.live[1] > 0);
+  const int64_t units = units_of(p);
+  const int stride = ctas * kF32Warps;
+  for (int64_t u0 = rank * kF32Warps + warp; u0 < units; u0 += 32LL * stride) {
+    Unit mine{0, 0, 0};
+    if (u0 + int64_t(lane) * stride < units) mine = find_unit(p, list, table, len, u0 + int64_t(lane) * stride);
+    unsigned todo = __ballot_sync(kFullMask, mine.live > 0);
     while (todo) {
       const int from = __ffs(todo) - 1;
       todo &= todo - 1;
+      const int phys = __shfl_sync(kFullMask, mine.phys, from), off = __shfl_sync(kFullMask, mine.off, from);
+      const int all = __shfl_sync(kFullMask, mine.live, from);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int64_t at = __shfl_sync(kFullMask, look.at[half], from);
-        const int live = __shfl_sync(kFullMask, look.live[half], from);
-        if (live == 0) continue;
+        const int live = min(8, all - 8 * half);
+        const int64_t at = (((static_cast<int64_t>(phys) * p.num_kv_heads + h) << p.log2_bs) + off + 8 * half) * kRow;
+        if (live <= 0) continue;
         float4 kx[kChunks];
 #pragma unroll
         for (int i = 0; i < kChunks; ++i)
@@ -529,85 +551,101 @@ __global__ void __launch_bounds__(kSparseThreads) sparse_f32_kernel(const Sparse
       }
     }
   }
-  Partial<D, HT>& mine = part[warp];
+  Partial<D, HT>& out = part[warp];
 #pragma unroll
   for (int a = 0; a < HT; ++a) {
 #pragma unroll
     for (int k = 1; k < 32; k <<= 1) l[a] += __shfl_xor_sync(kFullMask, l[a], k);
     if (lane == 0) {
-      mine.m[a] = m[a];
-      mine.l[a] = l[a];
+      out.m[a] = m[a];
+      out.l[a] = l[a];
     }
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) mine.o[a][lane + 32 * i] = o[a][i];
+    for (int i = 0; i < D / 32; ++i) out.o[a][lane + 32 * i] = o[a][i];
   }
-  merge_and_store<float, D, HT>(p, cluster, part, static_cast<float*>(p.out) + b * p.o_sb + head0 * p.o_sh, heads);
+  merge_and_store<float, D, HT, kF32Warps>(p, cluster, raw, sizeof(Partial<D, HT>), static_cast<float*>(p.out) + b * p.o_sb + head0 * p.o_sh, heads);
 }
 
-template <typename K>
-int launch_cluster(K kernel, const SparseParams& p, size_t smem, int ctas, cudaStream_t stream) {
+// CTAs of a list: as many as run at once, but no warp under one unit.
+int cluster_size(const SparseParams& p, int warps, int num_sms) {
+  const int64_t rows = int64_t(p.num_seqs) * p.num_kv_heads * p.num_head_tiles;
+  const int64_t units = int64_t(p.top) << (p.log2_bs > 4 ? p.log2_bs - 4 : 0);
+  int ctas = 1;
+  while (ctas < kMaxSparseCluster && rows * ctas < int64_t(num_sms) * 4 && units >= 2 * ctas * warps) ctas *= 2;
+  return ctas;
+}
+
+cudaLaunchConfig_t cluster_config(const SparseParams& p, int threads, size_t smem, int ctas, cudaLaunchAttribute* attr,
+                                  cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(int64_t(p.num_seqs) * p.num_kv_heads * p.num_head_tiles * ctas));
-  cfg.blockDim = dim3(kSparseThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cfg;
 }
 
 template <typename T, bool F8, int D, int HT>
-int launch_mma(const SparseParams& p, int ctas, cudaStream_t stream) {
+int launch_mma(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparseParams& p, int num_sms, cudaStream_t stream) {
+  using Tune = SparseTuning<typename std::conditional<F8, uint8_t, T>::type, D>;
   static std::atomic<int> configured[64];
-  constexpr size_t smem = sizeof(Partial<D, HT>) * kSparseWarps;
+  constexpr size_t smem = 1024 + Tune::kWarps * (Tune::kRing + Tune::kStages * sizeof(uint64_t));
   const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_mma_kernel<T, F8, D, HT>),
                                  static_cast<int>(smem));
-  return e != cudaSuccess ? e : launch_cluster(&sparse_mma_kernel<T, F8, D, HT>, p, smem, ctas, stream);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg =
+      cluster_config(p, Tune::kWarps * 32, smem, cluster_size(p, Tune::kWarps, num_sms), attr, stream);
+  return cudaLaunchKernelEx(&cfg, &sparse_mma_kernel<T, F8, D, HT>, kmap, vmap, p);
 }
 
 template <int D>
-int launch_f32(const SparseParams& p, int ctas, cudaStream_t stream) {
+int launch_f32(const SparseParams& p, int num_sms, cudaStream_t stream) {
   static std::atomic<int> configured[64];
-  constexpr size_t smem = sizeof(Partial<D, 8>) * kSparseWarps + (8 * D + 64 * kSparseWarps) * sizeof(float);
+  constexpr size_t smem = sizeof(Partial<D, 8>) * kF32Warps + (8 * D + 64 * kF32Warps) * sizeof(float);
   const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_f32_kernel<D>), static_cast<int>(smem));
-  return e != cudaSuccess ? e : launch_cluster(&sparse_f32_kernel<D>, p, smem, ctas, stream);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = cluster_config(p, kF32Warps * 32, smem, cluster_size(p, kF32Warps, num_sms), attr, stream);
+  return cudaLaunchKernelEx(&cfg, &sparse_f32_kernel<D>, p);
 }
 
 template <typename T, bool F8>
-int launch_dim(const SparseParams& p, int head_dim, int head_tile, int ctas, cudaStream_t stream) {
-  if (head_dim == 64) return head_tile == 16 ? launch_mma<T, F8, 64, 16>(p, ctas, stream) : launch_mma<T, F8, 64, 8>(p, ctas, stream);
+int launch_dim(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparseParams& p, int head_dim, int head_tile,
+               int num_sms, cudaStream_t stream) {
+  if (head_dim == 64)
+    return head_tile == 16 ? launch_mma<T, F8, 64, 16>(kmap, vmap, p, num_sms, stream)
+                           : launch_mma<T, F8, 64, 8>(kmap, vmap, p, num_sms, stream);
   if (head_dim == 128)
-    return head_tile == 16 ? launch_mma<T, F8, 128, 16>(p, ctas, stream) : launch_mma<T, F8, 128, 8>(p, ctas, stream);
-  if (head_dim == 256) return launch_mma<T, F8, 256, 8>(p, ctas, stream);
+    return head_tile == 16 ? launch_mma<T, F8, 128, 16>(kmap, vmap, p, num_sms, stream)
+                           : launch_mma<T, F8, 128, 8>(kmap, vmap, p, num_sms, stream);
+  if (head_dim == 256) return launch_mma<T, F8, 256, 8>(kmap, vmap, p, num_sms, stream);
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-int launch_sparse_decode(int dtype, bool kv_fp8, int head_dim, SparseParams p, int num_sms, cudaStream_t stream) {
+int launch_sparse_decode(int dtype, bool kv_fp8, int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                         SparseParams p, int num_sms, cudaStream_t stream) {
   // two tiles of 8 query heads share the K/V fragments where registers allow
   const int head_tile = dtype != 0 && p.group > 8 && head_dim <= 128 ? 16 : 8;
   p.num_head_tiles = (p.group + head_tile - 1) / head_tile;
-  // CTAs of a list: enough that all lists together give every SM four, but no
-  // warp under one unit of 16 tokens
-  const int64_t rows = int64_t(p.num_seqs) * p.num_kv_heads * p.num_head_tiles;
-  const int64_t units = ((int64_t(p.top) << p.log2_bs) + 15) / 16;
-  int ctas = 1;
-  while (ctas < kMaxSparseCluster && rows * ctas < int64_t(num_sms) * 4 && units >= 2 * ctas * kSparseWarps) ctas *= 2;
   int e = cudaErrorInvalidValue;
   if (dtype == 0 && !kv_fp8) {
-    e = head_dim == 64 ? launch_f32<64>(p, ctas, stream) : head_dim == 128 ? launch_f32<128>(p, ctas, stream)
-                                                           : launch_f32<256>(p, ctas, stream);
+    e = head_dim == 64    ? launch_f32<64>(p, num_sms, stream)
+        : head_dim == 128 ? launch_f32<128>(p, num_sms, stream)
+                          : launch_f32<256>(p, num_sms, stream);
   } else if (dtype == 1) {
-    e = kv_fp8 ? launch_dim<__half, true>(p, head_dim, head_tile, ctas, stream)
-               : launch_dim<__half, false>(p, head_dim, head_tile, ctas, stream);
+    e = kv_fp8 ? launch_dim<__half, true>(kmap, vmap, p, head_dim, head_tile, num_sms, stream)
+               : launch_dim<__half, false>(kmap, vmap, p, head_dim, head_tile, num_sms, stream);
   } else if (dtype == 2) {
-    e = kv_fp8 ? launch_dim<__nv_bfloat16, true>(p, head_dim, head_tile, ctas, stream)
-               : launch_dim<__nv_bfloat16, false>(p, head_dim, head_tile, ctas, stream);
+    e = kv_fp8 ? launch_dim<__nv_bfloat16, true>(kmap, vmap, p, head_dim, head_tile, num_sms, stream)
+               : launch_dim<__nv_bfloat16, false>(kmap, vmap, p, head_dim, head_tile, num_sms, stream);
   }
   if (e == cudaSuccess) note_launch();
   return e;

@@ -188,6 +188,7 @@ def test_sparse_refuses(lib):
     assert sparse(lib, Hq=5) == INVALID
     assert sparse(lib, D=96) == UNSUPPORTED
     assert sparse(lib, bs=4) == UNSUPPORTED
+    assert sparse(lib, D=64, bs=8, cache=U8, scales=(1.0, 1.0)) == UNSUPPORTED
     assert sparse(lib, cache=U8) == INVALID
     assert sparse(lib, scales=(1.0, 1.0)) == INVALID
     assert sparse(lib, scales=(1.0, -1.0), cache=U8) == INVALID

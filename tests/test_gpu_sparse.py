@@ -252,6 +252,10 @@ def test_sparse_decode_matches_binary64(dtype, kind, D, Hq, Hkv, bs, lens, top):
     bt, pool = H.block_tables(g, lens, bs)
     kc, vc = (H.cache(g, pool, Hkv, bs, D, kind, bt, lens) for _ in range(2))
     q = H.randn(g, len(lens), Hq, D, dtype=dtype)
+    if kind == U8 and D == 64 and bs < 16:  # as for every call over an fp8 cache
+        with pytest.raises(wllm.WllmError, match="block_size >= 16"):
+            run_sparse(q, kc, vc, bt, i32(lens), lists(g, lens, Hkv, bs, top), 0.1)
+        return
     for ordered in (True, False):
         sel = lists(g, lens, Hkv, bs, top, ordered)
         got = run_sparse(q, kc, vc, bt, i32(lens), sel, 1 / math.sqrt(D))
