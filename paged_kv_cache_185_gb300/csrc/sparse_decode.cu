@@ -45,8 +45,8 @@ namespace {
 
 constexpr int kMaxSparseCluster = 8;
 
-// Warps of a CTA and stages of a warp's ring: about 64 KB of stages a CTA, three
-// CTAs an SM.
+// Warps of a CTA and stages of a warp's ring.  Eight warps instead of four: 256
+// sequences over an fp8 cache 76.4 instead of 73.7 us, one sequence 4.8 instead of 5.1.
 template <typename B, int D>
 struct SparseTuning {
   static constexpr int kStage = Geom<B, D>::kStageBytes;  // 16 tokens' K and V rows
@@ -63,20 +63,19 @@ struct Unit {
   int phys, off, live;
 };
 
-__device__ __forceinline__ Unit find_unit(const SparseParams& p, const int32_t* list, const int32_t* table, int len,
-                                          int64_t unit) {
+__device__ __forceinline__ Unit find_unit(const SparseParams& p, const int32_t* list, const int32_t* table,
+                                          const int32_t* len_at, int64_t unit) {
   Unit u{0, 0, 0};
   const int log2_units = max(0, p.log2_bs - 4);  // units of a block
   const int64_t e = unit >> log2_units;
-  if (e >= p.top || len == 0) return u;
-  const int id = __ldg(list + e);
-  if (id < 0) return u;
-  if (id > (len - 1) >> p.log2_bs) {
-    atomicOr(p.err, kErrBlock);
-    return u;
-  }
-  const int phys = __ldg(table + id);
-  if (phys < 0 || phys >= p.num_blocks) {
+  if (e >= p.top) return u;
+  // the length and the entry together, then the table: two round trips, not three
+  const int stored = __ldg(len_at), id = __ldg(list + e);
+  const int max_blocks = p.max_tokens >> p.log2_bs;
+  const int phys = id >= 0 && id < max_blocks ? __ldg(table + id) : -1;
+  const int len = min(max(stored, 0), p.max_tokens);
+  if (id < 0 || len == 0) return u;
+  if (id > (len - 1) >> p.log2_bs || phys < 0 || phys >= p.num_blocks) {
     atomicOr(p.err, kErrBlock);
     return u;
   }
@@ -101,69 +100,86 @@ struct Partial {
 };
 
 // Merge of the warps' partials (one every `stride` bytes from `raw` on) and of
-// the cluster's CTAs; the cluster's ranks share the output elements of the tile.
+// the cluster's CTAs.  A partial's factor 2^(m_i - m) is computed once a head, by
+// a warp with a lane a partial, into `scratch` [HT][parts]; then four
+// neighbouring outputs are summed by a thread.  The warps' merge takes the first
+// warp's partial's place; the CTAs' merge is shared by the cluster's ranks.
 template <typename T, int D, int HT, int WARPS>
 __device__ __forceinline__ void merge_and_store(const SparseParams& p, cg::cluster_group& cluster, uint8_t* raw, int stride,
-                                                T* out, int heads) {
-  constexpr int kThreads = WARPS * 32;
-  const int tid = threadIdx.x, ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+                                                float* scratch, T* out, int heads) {
+  constexpr int kThreads = WARPS * 32, kQuads = D / 4;
+  static_assert(WARPS <= 8 && kMaxSparseCluster <= 8, "a factor a lane of 8");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   auto part = [&](int w) { return reinterpret_cast<Partial<D, HT>*>(raw + w * stride); };
-  __syncthreads();
-  // this CTA's merge; of several, into its first warp's partial
-  for (int i = tid; i < heads * D; i += kThreads) {
-    const int h = i / D, d = i - h * D;
-    float m = -INFINITY;
+  // 8 lanes a head: lane i of them has partial i's maximum and sum; returns the
+  // merged ones and leaves the factors in scratch
+  auto factors = [&](int h, bool have, float m_i, float l_i, float* m, float* l) {
+    *m = have ? m_i : -INFINITY;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, part(w)->m[h]);
-    float l = 0.f, o = 0.f;
+    for (int x = 4; x > 0; x >>= 1) *m = fmaxf(*m, __shfl_xor_sync(kFullMask, *m, x));
+    const float f = !have || m_i == -INFINITY ? 0.f : exp2f(m_i - *m);
+    *l = have ? f * l_i : 0.f;
+#pragma unroll
+    for (int x = 4; x > 0; x >>= 1) *l += __shfl_xor_sync(kFullMask, *l, x);
+    return f;
+  };
+  __syncthreads();
+  float m_cta = 0.f, l_cta = 0.f;
+  for (int h0 = warp * 4; h0 < HT; h0 += WARPS * 4) {
+    const int h = h0 + (lane >> 3), i = lane & 7;
+    const bool have = i < WARPS;
+    const Partial<D, HT>* x = part(have ? i : 0);
+    const float f = factors(h, have, x->m[h], x->l[h], &m_cta, &l_cta);
+    // with one CTA the division is part of the factor
+    if (have) scratch[h * 8 + i] = ctas > 1 ? f : l_cta == 0.f ? 0.f : f * (p.v_scale / l_cta);
+    __syncwarp();  // every lane has read the partials' maxima
+    if (i == 0) part(0)->m[h] = m_cta, part(0)->l[h] = l_cta;
+  }
+  __syncthreads();
+  for (int i = tid; i < heads * kQuads; i += kThreads) {
+    const int h = i / kQuads, d = (i - h * kQuads) * 4;
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      const float f = part(w)->m[h] == -INFINITY ? 0.f : exp2f(part(w)->m[h] - m);
-      l = fmaf(f, part(w)->l[h], l);
-      o = fmaf(f, part(w)->o[h][d], o);
+      const float4 v = *reinterpret_cast<const float4*>(&part(w)->o[h][d]);
+      const float f = scratch[h * 8 + w];
+      o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]), o[2] = fmaf(f, v.z, o[2]), o[3] = fmaf(f, v.w, o[3]);
     }
-    if (ctas == 1)
-      out[h * p.o_sh + d] = from_f32<T>(l == 0.f ? 0.f : o / l * p.v_scale);
-    else
-      part(0)->o[h][d] = o;
+    if (ctas > 1) {
+      *reinterpret_cast<float4*>(&part(0)->o[h][d]) = make_float4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[h * p.o_sh + d + e] = from_f32<T>(o[e]);
+    }
   }
   if (ctas == 1) return;
-  __syncthreads();
-  if (tid < heads) {
-    float m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, part(w)->m[tid]);
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float f = part(w)->m[tid] == -INFINITY ? 0.f : exp2f(part(w)->m[tid] - m);
-      l = fmaf(f, part(w)->l[tid], l);
-    }
-    part(0)->m[tid] = m;
-    part(0)->l[tid] = l;
-  }
   cluster.sync();
-  for (int i = rank * kThreads + tid; i < heads * D; i += ctas * kThreads) {
-    const int h = i / D, d = i - h * D;
-    float ms[kMaxSparseCluster], ls[kMaxSparseCluster], os[kMaxSparseCluster];
-    float m = -INFINITY;
+  for (int h0 = warp * 4; h0 < HT; h0 += WARPS * 4) {
+    const int h = h0 + (lane >> 3), i = lane & 7;
+    const bool have = i < ctas;
+    const Partial<D, HT>* x = cluster.map_shared_rank(part(0), have ? i : 0);
+    float m, l;
+    const float f = factors(h, have, x->m[h], x->l[h], &m, &l);
+    if (have) scratch[h * 8 + i] = l == 0.f ? 0.f : f * (p.v_scale / l);
+  }
+  __syncthreads();
+  for (int i = rank * kThreads + tid; i < heads * kQuads; i += ctas * kThreads) {
+    const int h = i / kQuads, d = (i - h * kQuads) * 4;
+    float4 v[kMaxSparseCluster];
+#pragma unroll
+    for (int r = 0; r < kMaxSparseCluster; ++r)
+      if (r < ctas) v[r] = *reinterpret_cast<const float4*>(&cluster.map_shared_rank(part(0), r)->o[h][d]);
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int r = 0; r < kMaxSparseCluster; ++r) {
       if (r < ctas) {
-        const Partial<D, HT>* peer = cluster.map_shared_rank(part(0), r);
-        ms[r] = peer->m[h], ls[r] = peer->l[h], os[r] = peer->o[h][d];
-        m = fmaxf(m, ms[r]);
+        const float f = scratch[h * 8 + r];
+        o[0] = fmaf(f, v[r].x, o[0]), o[1] = fmaf(f, v[r].y, o[1]), o[2] = fmaf(f, v[r].z, o[2]), o[3] = fmaf(f, v[r].w, o[3]);
       }
     }
-    float l = 0.f, o = 0.f;
 #pragma unroll
-    for (int r = 0; r < kMaxSparseCluster; ++r) {
-      if (r < ctas) {
-        const float f = ms[r] == -INFINITY ? 0.f : exp2f(ms[r] - m);
-        l = fmaf(f, ls[r], l);
-        o = fmaf(f, os[r], o);
-      }
-    }
-    out[h * p.o_sh + d] = from_f32<T>(l == 0.f ? 0.f : o / l * p.v_scale);
+    for (int e = 0; e < 4; ++e) out[h * p.o_sh + d + e] = from_f32<T>(o[e]);
   }
   cluster.sync();  // a CTA's shared memory outlives its peers' reads
 }
@@ -196,16 +212,13 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
   extern __shared__ __align__(16) uint8_t unaligned[];
   uint8_t* raw = unaligned + ((1024 - (smem_u32(unaligned) & 1023)) & 1023);  // swizzled boxes start at 1024 bytes
   uint8_t* ring = raw + warp * Tune::kRing;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(raw + kWarps * Tune::kRing) + warp * kStages;
+  float* scratch = reinterpret_cast<float*>(raw + kWarps * Tune::kRing);  // [HT][8]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scratch + HT * 8) + warp * kStages;
   if (lane < kStages) mbar_init(smem_u32(&bars[lane]), 1);
   fence_mbar_init();
   __syncwarp();
 
-  int len = p.context_lens[b];
-  if (len < 0 || len > p.max_tokens) {
-    if (threadIdx.x == 0 && rank == 0 && h == 0 && tile == 0) atomicOr(p.err, kErrLen);
-    len = len < 0 ? 0 : p.max_tokens;
-  }
+  const int32_t* len_at = p.context_lens + b;
   const int32_t* list = p.selected + b * p.sel_sb + h * p.sel_sh;
   const int32_t* table = p.block_tables + b * p.bt_stride;
   const int64_t units = units_of(p);
@@ -216,7 +229,7 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
   int64_t u0 = rank * kWarps + warp;
   auto find = [&]() -> unsigned {
     mine.live = 0;
-    if (u0 + int64_t(lane) * stride < units) mine = find_unit(p, list, table, len, u0 + int64_t(lane) * stride);
+    if (u0 + int64_t(lane) * stride < units) mine = find_unit(p, list, table, len_at, u0 + int64_t(lane) * stride);
     return __ballot_sync(kFullMask, mine.live > 0);
   };
   unsigned to_use = u0 < units ? find() : 0u, to_copy = to_use;
@@ -429,7 +442,9 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
       }
     }
   }
-  merge_and_store<T, D, HT, kWarps>(p, cluster, raw, Tune::kRing, static_cast<T*>(p.out) + b * p.o_sb + head0 * p.o_sh,
+  if (threadIdx.x == 0 && rank == 0 && h == 0 && tile == 0 && (*len_at < 0 || *len_at > p.max_tokens))
+    atomicOr(p.err, kErrLen);
+  merge_and_store<T, D, HT, kWarps>(p, cluster, raw, Tune::kRing, scratch, static_cast<T*>(p.out) + b * p.o_sb + head0 * p.o_sh,
                                     heads);
 }
 
@@ -456,12 +471,9 @@ __global__ void __launch_bounds__(kF32Warps * 32) sparse_f32_kernel(const Sparse
   Partial<D, HT>* part = reinterpret_cast<Partial<D, HT>*>(raw);
   float* qs = reinterpret_cast<float*>(part + kF32Warps);             // [HT][D]
   float* ps = qs + HT * D + warp * 64;                                   // [8 tokens][HT] weights of this warp
+  float* scratch = qs + HT * D + kF32Warps * 64;                         // [HT][8]
 
-  int len = p.context_lens[b];
-  if (len < 0 || len > p.max_tokens) {
-    if (threadIdx.x == 0 && rank == 0 && h == 0 && tile == 0) atomicOr(p.err, kErrLen);
-    len = len < 0 ? 0 : p.max_tokens;
-  }
+  const int32_t* len_at = p.context_lens + b;
   const int32_t* list = p.selected + b * p.sel_sb + h * p.sel_sh;
   const int32_t* table = p.block_tables + b * p.bt_stride;
   for (int i = threadIdx.x; i < HT * D; i += kF32Warps * 32) {
@@ -481,7 +493,7 @@ __global__ void __launch_bounds__(kF32Warps * 32) sparse_f32_kernel(const Sparse
   const int stride = ctas * kF32Warps;
   for (int64_t u0 = rank * kF32Warps + warp; u0 < units; u0 += 32LL * stride) {
     Unit mine{0, 0, 0};
-    if (u0 + int64_t(lane) * stride < units) mine = find_unit(p, list, table, len, u0 + int64_t(lane) * stride);
+    if (u0 + int64_t(lane) * stride < units) mine = find_unit(p, list, table, len_at, u0 + int64_t(lane) * stride);
     unsigned todo = __ballot_sync(kFullMask, mine.live > 0);
     while (todo) {
       const int from = __ffs(todo) - 1;
@@ -563,15 +575,20 @@ __global__ void __launch_bounds__(kF32Warps * 32) sparse_f32_kernel(const Sparse
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) out.o[a][lane + 32 * i] = o[a][i];
   }
-  merge_and_store<float, D, HT, kF32Warps>(p, cluster, raw, sizeof(Partial<D, HT>), static_cast<float*>(p.out) + b * p.o_sb + head0 * p.o_sh, heads);
+  if (threadIdx.x == 0 && rank == 0 && h == 0 && tile == 0 && (*len_at < 0 || *len_at > p.max_tokens))
+    atomicOr(p.err, kErrLen);
+  merge_and_store<float, D, HT, kF32Warps>(p, cluster, raw, sizeof(Partial<D, HT>), scratch, static_cast<float*>(p.out) + b * p.o_sb + head0 * p.o_sh, heads);
 }
 
-// CTAs of a list: as many as run at once, but no warp under one unit.
-int cluster_size(const SparseParams& p, int warps, int num_sms) {
+// CTAs of a list: as many as run at once (`resident` an SM), but no warp under
+// one unit.  Measured, us for 1, 2, 4 and 8 CTAs a list: 64 lists of 128 blocks
+// (bf16) 23.3, 17.7, 16.5, 22.0; 1024 of 96 (fp8) 73.7, 84.5, 107, 161; 4 of 64
+// (f16, head_dim 64) 10.2, 7.7, 5.9, 5.1.
+int cluster_size(const SparseParams& p, int warps, int resident, int num_sms) {
   const int64_t rows = int64_t(p.num_seqs) * p.num_kv_heads * p.num_head_tiles;
   const int64_t units = int64_t(p.top) << (p.log2_bs > 4 ? p.log2_bs - 4 : 0);
   int ctas = 1;
-  while (ctas < kMaxSparseCluster && rows * ctas < int64_t(num_sms) * 4 && units >= 2 * ctas * warps) ctas *= 2;
+  while (ctas < kMaxSparseCluster && rows * ctas * 2 <= int64_t(num_sms) * resident && units >= 2 * ctas * warps) ctas *= 2;
   return ctas;
 }
 
@@ -594,24 +611,24 @@ template <typename T, bool F8, int D, int HT>
 int launch_mma(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparseParams& p, int num_sms, cudaStream_t stream) {
   using Tune = SparseTuning<typename std::conditional<F8, uint8_t, T>::type, D>;
   static std::atomic<int> configured[64];
-  constexpr size_t smem = 1024 + Tune::kWarps * (Tune::kRing + Tune::kStages * sizeof(uint64_t));
+  constexpr size_t smem = 1024 + Tune::kWarps * (Tune::kRing + Tune::kStages * sizeof(uint64_t)) + HT * 8 * sizeof(float);
   const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_mma_kernel<T, F8, D, HT>),
                                  static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
-      cluster_config(p, Tune::kWarps * 32, smem, cluster_size(p, Tune::kWarps, num_sms), attr, stream);
+      cluster_config(p, Tune::kWarps * 32, smem, cluster_size(p, Tune::kWarps, static_cast<int>(227 * 1024 / (smem + 1024)), num_sms), attr, stream);
   return cudaLaunchKernelEx(&cfg, &sparse_mma_kernel<T, F8, D, HT>, kmap, vmap, p);
 }
 
 template <int D>
 int launch_f32(const SparseParams& p, int num_sms, cudaStream_t stream) {
   static std::atomic<int> configured[64];
-  constexpr size_t smem = sizeof(Partial<D, 8>) * kF32Warps + (8 * D + 64 * kF32Warps) * sizeof(float);
+  constexpr size_t smem = sizeof(Partial<D, 8>) * kF32Warps + (8 * D + 64 * kF32Warps + 64) * sizeof(float);
   const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_f32_kernel<D>), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = cluster_config(p, kF32Warps * 32, smem, cluster_size(p, kF32Warps, num_sms), attr, stream);
+  const cudaLaunchConfig_t cfg = cluster_config(p, kF32Warps * 32, smem, cluster_size(p, kF32Warps, 3, num_sms), attr, stream);
   return cudaLaunchKernelEx(&cfg, &sparse_f32_kernel<D>, p);
 }
 
