@@ -151,6 +151,8 @@ __device__ __forceinline__ void bounds_of_block(const uint8_t* src, uint8_t* dst
 // to the next sequence's first unit.
 template <typename Ops, int COLS>
 __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const BoundsParams p) {
+  grid_wait();
+  grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * kBoundsWarps + (threadIdx.x >> 5);
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kBoundsWarps;
@@ -205,8 +207,7 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const Bou
 
 template <typename Ops, int COLS>
 int launch_one(const BoundsParams& p, unsigned blocks, cudaStream_t stream) {
-  key_bounds_kernel<Ops, COLS><<<blocks, kBoundsWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(&key_bounds_kernel<Ops, COLS>, dim3(blocks), dim3(kBoundsWarps * 32), 0, 0, stream, p);
 }
 
 template <typename Ops, int ELT>

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <utility>
 
 namespace wllm {
 
@@ -38,6 +39,27 @@ inline int raise_smem_limit(std::atomic<int>* configured, const void* func, int 
   if (e != cudaSuccess) return e;
   if (tracked) configured[dev].store(bytes, std::memory_order_release);
   return cudaSuccess;
+}
+
+// Launch as a programmatic dependent of the kernel before it in the stream: its
+// CTAs may start early, so the kernel calls grid_wait() before it touches global
+// memory.  `cluster` > 0: thread-block clusters of that many CTAs along x.
+template <typename... P, typename... A>
+int launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Everything one paged-decode launch needs besides the two tensor maps.

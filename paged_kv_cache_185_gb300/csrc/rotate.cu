@@ -310,6 +310,8 @@ __device__ __forceinline__ int64_t position_of(const RotateParams& p, int axis, 
 template <typename T, bool VEC, bool F8, bool ADJACENT>
 __global__ void __launch_bounds__(kRotateWarps * 32, 4) rotate_kernel(const RotateParams p) {
   constexpr int kDeep = 2;  // steps whose rows are in flight
+  grid_wait();
+  grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t gw = static_cast<int64_t>(blockIdx.x) * kRotateWarps + (threadIdx.x >> 5);
   const int64_t t = gw / p.warps_per_token;
@@ -409,6 +411,8 @@ __global__ void __launch_bounds__(kRingWarps * 32, kRingBlocks) rotate_ring_kern
   if (threadIdx.x < 2) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
   fence_mbar_init();
   __syncthreads();
+  grid_wait();
+  grid_launch_dependents();
 
   const int stride = gridDim.x;
   RowMath<T, true, ADJACENT> math(p, lane);
@@ -519,10 +523,8 @@ __global__ void __launch_bounds__(kRingWarps * 32, kRingBlocks) rotate_ring_kern
 template <typename T, bool VEC, bool F8>
 int launch_few(const RotateParams& p, unsigned blocks, cudaStream_t stream) {
   if (p.adjacent)
-    rotate_kernel<T, VEC, F8, true><<<blocks, kRotateWarps * 32, 0, stream>>>(p);
-  else
-    rotate_kernel<T, VEC, F8, false><<<blocks, kRotateWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+    return launch_dependent(&rotate_kernel<T, VEC, F8, true>, dim3(blocks), dim3(kRotateWarps * 32), 0, 0, stream, p);
+  return launch_dependent(&rotate_kernel<T, VEC, F8, false>, dim3(blocks), dim3(kRotateWarps * 32), 0, 0, stream, p);
 }
 
 template <typename T, bool F8, bool ADJACENT>
@@ -532,9 +534,9 @@ int launch_ring(const RotateParams& p, int smem, int num_sms, cudaStream_t strea
   if (e != cudaSuccess) return e;
   // as many CTAs as shared memory lets be resident (228 KB an SM, 1 KB of it the system's in each CTA)
   const int64_t resident = int64_t(num_sms) * std::max(1, std::min(kRingBlocks, 228 * 1024 / (smem + 1024 + 64)));
-  rotate_ring_kernel<T, F8, ADJACENT>
-      <<<static_cast<unsigned>(std::min<int64_t>(resident, p.num_tokens)), kRingWarps * 32, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(&rotate_ring_kernel<T, F8, ADJACENT>,
+                          dim3(static_cast<unsigned>(std::min<int64_t>(resident, p.num_tokens))), dim3(kRingWarps * 32),
+                          smem, 0, stream, p);
 }
 
 template <typename T>

@@ -465,6 +465,8 @@ struct Scorer<float, float, D> {  // binary32 FMA: D/16 lanes a block, 32 elemen
 
 template <typename T, typename B, int D>
 __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectParams p) {
+  grid_wait();
+  grid_launch_dependents();
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int64_t row = static_cast<int64_t>(blockIdx.x) / ctas;
@@ -814,18 +816,8 @@ int launch_one(const SelectParams& p, int ctas, cudaStream_t stream) {
   const void* func = reinterpret_cast<const void*>(&select_kernel<T, B, D>);
   int e = raise_smem_limit(configured, func, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(int64_t(p.num_seqs) * p.num_kv_heads * ctas));
-  cfg.blockDim = dim3(kSelectThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_kernel<T, B, D>, p);
+  return launch_dependent(&select_kernel<T, B, D>, dim3(static_cast<unsigned>(int64_t(p.num_seqs) * p.num_kv_heads * ctas)),
+                          dim3(kSelectThreads), smem, ctas, stream, p);
 }
 
 template <typename T, typename B>

@@ -216,7 +216,10 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
   uint64_t* bars = reinterpret_cast<uint64_t*>(scratch + HT * 8) + warp * kStages;
   if (lane < kStages) mbar_init(smem_u32(&bars[lane]), 1);
   fence_mbar_init();
+  if (lane == 0) tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
   __syncwarp();
+  grid_wait();
+  grid_launch_dependents();
 
   const int32_t* len_at = p.context_lens + b;
   const int32_t* list = p.selected + b * p.sel_sb + h * p.sel_sh;
@@ -457,6 +460,8 @@ constexpr int kF32Warps = 4;
 template <int D>
 __global__ void __launch_bounds__(kF32Warps * 32) sparse_f32_kernel(const SparseParams p) {
   constexpr int HT = 8, kRow = D * 4, kChunks = D / 16;
+  grid_wait();
+  grid_launch_dependents();
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   int64_t row = static_cast<int64_t>(blockIdx.x) / ctas;
@@ -592,19 +597,8 @@ int cluster_size(const SparseParams& p, int warps, int resident, int num_sms) {
   return ctas;
 }
 
-cudaLaunchConfig_t cluster_config(const SparseParams& p, int threads, size_t smem, int ctas, cudaLaunchAttribute* attr,
-                                  cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(int64_t(p.num_seqs) * p.num_kv_heads * p.num_head_tiles * ctas));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cfg;
+dim3 grid_of(const SparseParams& p, int ctas) {
+  return dim3(static_cast<unsigned>(int64_t(p.num_seqs) * p.num_kv_heads * p.num_head_tiles * ctas));
 }
 
 template <typename T, bool F8, int D, int HT>
@@ -615,10 +609,9 @@ int launch_mma(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparsePar
   const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_mma_kernel<T, F8, D, HT>),
                                  static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg =
-      cluster_config(p, Tune::kWarps * 32, smem, cluster_size(p, Tune::kWarps, static_cast<int>(227 * 1024 / (smem + 1024)), num_sms), attr, stream);
-  return cudaLaunchKernelEx(&cfg, &sparse_mma_kernel<T, F8, D, HT>, kmap, vmap, p);
+  const int ctas = cluster_size(p, Tune::kWarps, static_cast<int>(227 * 1024 / (smem + 1024)), num_sms);
+  return launch_dependent(&sparse_mma_kernel<T, F8, D, HT>, grid_of(p, ctas), dim3(Tune::kWarps * 32), smem, ctas, stream,
+                          kmap, vmap, p);
 }
 
 template <int D>
@@ -627,9 +620,8 @@ int launch_f32(const SparseParams& p, int num_sms, cudaStream_t stream) {
   constexpr size_t smem = sizeof(Partial<D, 8>) * kF32Warps + (8 * D + 64 * kF32Warps + 64) * sizeof(float);
   const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_f32_kernel<D>), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = cluster_config(p, kF32Warps * 32, smem, cluster_size(p, kF32Warps, 3, num_sms), attr, stream);
-  return cudaLaunchKernelEx(&cfg, &sparse_f32_kernel<D>, p);
+  const int ctas = cluster_size(p, kF32Warps, 3, num_sms);
+  return launch_dependent(&sparse_f32_kernel<D>, grid_of(p, ctas), dim3(kF32Warps * 32), smem, ctas, stream, p);
 }
 
 template <typename T, bool F8>
