@@ -466,7 +466,7 @@ int wllm_update_key_bounds(const wllm_tensor* key_bounds, const wllm_tensor* k_c
  * their error of the border).  Blocks come in ascending order, then -1.
  * Several query tokens of a sequence are several rows of q, block_tables and
  * context_lens.  D 64, 128 or 256, bs a power of two in [8, 256]; tables of
- * about 45,000 blocks at most.  Table entries outside the pool are recorded
+ * 30,720 blocks at most.  Table entries outside the pool are recorded
  * (bit 1) and scored as block 0, lengths outside [0, M_b bs] (bit 2) clamped.
  */
 int wllm_select_blocks(const wllm_tensor* selected, const wllm_tensor* q,

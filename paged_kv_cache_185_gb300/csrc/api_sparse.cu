@@ -428,9 +428,9 @@ int wllm_select_blocks(const wllm_tensor* selected, const wllm_tensor* q, const 
   if (hq > 65535 || top > INT32_MAX || B * hkv > INT32_MAX / 8) return fail(WLLM_ERR_UNSUPPORTED, "sizes too large");
   if (B == 0) return WLLM_OK;
   const int64_t mb = block_tables->shape[1];
-  if (mb > select_max_blocks(static_cast<int>(d)))
+  if (mb > select_max_blocks())
     return fail(WLLM_ERR_UNSUPPORTED, "block tables of %lld blocks not supported (%d at most)", (long long)mb,
-                select_max_blocks(static_cast<int>(d)));
+                select_max_blocks());
   if (hq > 0 && nb < 1) return fail(WLLM_ERR_INVALID_ARG, "the pool has no blocks");
   if (!aligned(key_bounds->data, 16)) return fail(WLLM_ERR_INVALID_ARG, "key_bounds must be 16-byte aligned");
   if (!aligned(q->data, static_cast<uintptr_t>(elt_size(dt))))
@@ -453,6 +453,7 @@ int wllm_select_blocks(const wllm_tensor* selected, const wllm_tensor* q, const 
   p.top = static_cast<int>(top);
   p.sink = num_sink;
   p.recent = num_recent;
+  p.wait_limit_ns = static_cast<unsigned long long>(env_int("WLLM_WAIT_LIMIT_NS", 200000000LL));
   DeviceState* s = nullptr;
   if ((rc = locked_state(&s))) return rc;
   p.err = s->err;

@@ -234,10 +234,11 @@ struct SelectParams {
   int num_seqs, num_kv_heads, group, num_blocks, log2_bs, max_tokens;
   int top, sink, recent;
   int room, longest_first;        // set by launch_select: scores a row has room for; launch order
+  unsigned long long wait_limit_ns;
   int* err;
 };
-int select_max_blocks(int head_dim);
-int launch_select(int dtype, int bounds_dtype, int head_dim, SelectParams p, int max_blocks, int num_sms,
+int select_max_blocks();
+int launch_select(int dtype, int bounds_dtype, int head_dim, const SelectParams& p, int max_blocks, int num_sms,
                   cudaStream_t stream);
 
 // Decode attention over the listed blocks (sparse_decode.cu).

@@ -34,19 +34,23 @@
 //
 // Work split: a cluster of 1 to 8 CTAs per (sequence, kv head), each with a
 // share of the blocks, so a long row is on many SMs and the selection still
-// needs neither a second launch nor a workspace.  A warp has 16 blocks' bounds
-// in flight, 16 bytes a lane and load; the scores go straight to the first
-// CTA's shared memory.  That CTA alone finds the border with one 1024-bin
-// histogram between the extremes, settles the blocks at the border in binary64
-// (a handful, a warp each) and writes the chosen ones in ascending order: one
-// barrier of the cluster in all, where every step shared by its CTAs would cost
-// another (the first form had six, 10 us of them).  Bound: memory, the bounds
-// are read once.
+// needs neither a second launch nor a workspace.  The scoring
+// warps of a CTA have two halves of a turn (16 or 32 blocks' minima and their
+// maxima) in shared memory each, filled by asynchronous copies, one half while
+// the other is multiplied, rows with 16 bytes of padding behind them, so that
+// ldmatrix reads eight blocks' chunks without a bank conflict.  The
+// scores go straight to the first CTA's shared memory.  That CTA alone finds the
+// border with one 1024-bin histogram between the extremes, settles the blocks at
+// the border (a handful, 8 lanes each) and writes the chosen ones in ascending
+// order: one barrier of the cluster in all, where every step shared by its CTAs
+// would cost another (the first form had six, 10 us of them).  Bound: memory,
+// the bounds are read once.
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
 #include <limits.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 #include <utility>
@@ -65,8 +69,8 @@ constexpr int kBins = 1024;
 constexpr int kWindow = 256;          // border blocks ranked against each other; more go through digit passes
 constexpr int kMaxCluster = 8;
 
-struct SelectShared {
-  float stat[kMaxCluster * kSelectWarps][4];  // per warp: smallest score, largest, bound on the magnitudes, flag
+// Of the first CTA once the scores are there, in the place of the rings.
+struct alignas(16) SelectShared {
   uint32_t hist[kBins];
   uint32_t warp_sum[kSelectWarps];
   double win_score[kWindow];
@@ -214,9 +218,35 @@ __device__ __forceinline__ int physical(const SelectParams& p, const int32_t* ta
   return 0;
 }
 
-// Fragments of the weights for the tensor cores: step s, column g < 3, pair c
-// of k indices.  The weights are scaled by a power of two so that the largest
-// is near 2^14 and f16 words hold them; *unit undoes it.
+// Larger of two pairs of 16-bit integers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// d = a b with mma.sync m16n8k16.
+__device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], const uint2& b, __nv_bfloat16) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+      " {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(0.f));
+}
+__device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], const uint2& b, __half) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+      " {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(0.f));
+}
+
+// The weights in three words of type M, what is left in *rest.
 template <typename M>
 __device__ __forceinline__ M split_word(float x, float* rest) {
   const M y = from_f32<M>(x);
@@ -229,18 +259,65 @@ struct Scorer {  // 16-bit and E4M3 bounds
   static constexpr bool kF8 = sizeof(B) == 1;
   using M = typename std::conditional<kF8, __half, B>::type;
   static constexpr int kRow = 2 * D * static_cast<int>(sizeof(B));  // bytes of a block's bounds
-  static constexpr int kLoads = kRow / 64;                          // 16-byte loads of a lane and row
-  static constexpr int kGroup = kLoads < 8 ? kLoads : 8;            // loads of two rows in flight
-  static constexpr int kTiles = kF8 && D <= 128 ? 2 : kGroup < 8 ? 2 : 1;  // tiles of 16 blocks in flight
-  static constexpr int kPerLoad = kF8 ? 4 : 2;                      // k16 steps of one load
+  static constexpr int kWarps = kRow >= 1024 ? 4 : 8;               // that score
+  static constexpr int kHalf = kRow / 2;                            // its minima or its maxima
+  static constexpr int kPitch = kHalf + 16;
+  static constexpr int kTiles = kRow >= 512 ? 1 : 2;                // tiles of 16 blocks in a turn
+  static constexpr int kBlocks = 16 * kTiles;                       // blocks of a turn
   static constexpr int kSteps = 2 * D / 16;
-  static constexpr int kFragBytes = kSteps * 3 * 4 * 8;             // [step][column][pair] two words
-  static constexpr int kBlocks = 16 * kTiles;                       // blocks of a warp's turn
+  static constexpr int kFragBytes = kSteps * 8 * 4 * 8;             // [step][column][pair] two words
+  static constexpr int kRing = 2 * kBlocks * kPitch;                // a warp's: minima and maxima of a turn
 
-  // Lane layout of the elements: load i of lane c has elements (4i + c) * E .. + E - 1, E = 16 / sizeof(B); step t of
-  // the load takes its elements 4t .. 4t+3 as k indices 2c, 2c+1, 2c+8, 2c+9.
+  int id, id_after;  // physical blocks of this lane's row (lanes 0 .. kBlocks - 1) of the turn to be copied and the next
+  int copy_turn;     // the turn to be copied
+
+  static __device__ __forceinline__ int lookup(const SelectParams& p, const int32_t* table, int cands, int turn) {
+    const int lane = threadIdx.x & 31;
+    return lane < kBlocks ? physical(p, table, turn * kBlocks + lane, cands, true) : 0;
+  }
+
+  // Start the copies of the turn's minima (which = 0) or maxima (1), zeros for blocks behind the last: one group of
+  // copies, an empty one behind the last turn.  A warp's copy takes 512 bytes in a row: with 64 bytes of each of eight
+  // rows it took 100 cycles to issue (shared-memory banks met four times).
+  __device__ __forceinline__ void copy(const SelectParams& p, const int32_t* table, int h, int cands, int turns, int which,
+                                       uint8_t* ring) {
+    constexpr int kRows = 512 / kHalf;                      // rows of one copy
+    constexpr int kLanes = 32 / kRows;                      // lanes of one row
+    const int lane = threadIdx.x & 31, sub = lane / kLanes;
+    if (copy_turn * kBlocks < cands) {
+      const uint8_t* base = p.bounds + int64_t(h) * kRow + which * kHalf + (lane % kLanes) * 16;
+      const int64_t stride = int64_t(p.num_kv_heads) * kRow;
+      const uint32_t dst = smem_u32(ring) + (which * kBlocks + sub) * kPitch + (lane % kLanes) * 16;
+      const int live = cands - copy_turn * kBlocks;
+#pragma unroll
+      for (int i = 0; i < kBlocks; i += kRows) {
+        const uint8_t* src = base + __shfl_sync(kFullMask, id, i + sub) * stride;
+        const uint32_t bytes = i + sub < live ? 16u : 0u;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * kPitch), "l"(src), "r"(bytes) : "memory");
+      }
+      if (which == 1) {
+        copy_turn += turns;
+        id = id_after;
+        id_after = lookup(p, table, cands, copy_turn + turns);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+
+  // First copies of a scoring warp; its turns are first, first + turns, ...
+  __device__ __forceinline__ void start(const SelectParams& p, const int32_t* table, int h, int cands, int first, int turns,
+                                        uint8_t* ring) {
+    copy_turn = first;
+    id = lookup(p, table, cands, first);
+    id_after = lookup(p, table, cands, first + turns);
+    copy(p, table, h, cands, turns, 0, ring);
+    copy(p, table, h, cands, turns, 1, ring);
+  }
+
+  // The weights' fragments: step s, column g < 3, lane c's words of k indices 2c, 2c+1 and 2c+8, 2c+9: elements 2c and
+  // 2c + 8 of the step's 16 (16-bit bounds), 4c and 4c + 2 where codes are widened.  They are scaled by a power of two
+  // so that the largest is near 2^14 and f16 words hold them; *unit undoes it.  Returns the sum of their magnitudes.
   static __device__ __forceinline__ float fragments(uint2* frag, const float2* w, float* unit) {
-    // the largest weight, by every warp for itself
     const int lane = threadIdx.x & 31;
     float big = 0.f, sum = 0.f;
     for (int e = lane; e < 2 * D; e += 32) {
@@ -252,139 +329,127 @@ struct Scorer {  // 16-bit and E4M3 bounds
       big = fmaxf(big, __shfl_xor_sync(kFullMask, big, m));
       sum += __shfl_xor_sync(kFullMask, sum, m);
     }
-    float scale = 1.f;
-    if (std::is_same<M, __half>::value && big > 0.f && big < INFINITY) {
-      int e;
-      frexpf(big, &e);
-      scale = ldexpf(1.f, min(max(14 - e, -120), 120));
+    // 2^(14 - e) for big in [2^(e-1), 2^e), its own exponent field read as an integer
+    const int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) - 126;
+    const int k = std::is_same<M, __half>::value && big > 0.f && big < INFINITY ? min(max(14 - e, -120), 120) : 0;
+    const float scale = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+    *unit = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+    uint32_t* words = reinterpret_cast<uint32_t*>(frag);
+    for (int x = threadIdx.x; x < kSteps * 40; x += kSelectThreads) {  // columns 3 to 7 are zero
+      const int step = x / 40, y = x - step * 40;
+      words[step * 64 + 24 + y] = 0u;
     }
-    *unit = 1.f / scale;
-    constexpr int kE = 16 / static_cast<int>(sizeof(B));
-    for (int x = threadIdx.x; x < kSteps * 4; x += kSelectThreads) {
-      const int step = x >> 2, c = x & 3;
-      const int e0 = (4 * (step / kPerLoad) + c) * kE + 4 * (step % kPerLoad);
-      float v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = w[e0 + k].x * scale;
+    for (int x = threadIdx.x; x < kSteps * 8; x += kSelectThreads) {
+      const int step = x >> 3, c = (x >> 1) & 3, word = x & 1;
+      const int e0 = 16 * step + (kF8 ? 4 * c + 2 * word : 2 * c + 8 * word);
+      float v[2] = {w[e0].x * scale, w[e0 + 1].x * scale};
 #pragma unroll
       for (int col = 0; col < 3; ++col) {
-        M y[4];
+        M y[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = split_word<M>(v[k], &v[k]);
-        uint2 word;
-        M* half = reinterpret_cast<M*>(&word);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) half[k] = y[k];
-        frag[(step * 3 + col) * 4 + c] = word;
+        for (int i = 0; i < 2; ++i) y[i] = split_word<M>(v[i], &v[i]);
+        const uint32_t lo = *reinterpret_cast<const uint16_t*>(&y[0]), hi = *reinterpret_cast<const uint16_t*>(&y[1]);
+        words[step * 64 + (col * 4 + c) * 2 + word] = lo | (hi << 16);
       }
     }
     return sum;
   }
 
-  int ids[kTiles][2];  // physical blocks of the next turn
-  __device__ __forceinline__ void lookup(const SelectParams& p, const int32_t* table, int cands, int turn) {
-    const int lane = threadIdx.x & 31;
+  // Half of the products of a turn's tile at shared address `at`, and the extremes of what was read: of the maxima the
+  // greatest as signed, of the minima the least, which has the greatest bits.  |b| is at most the larger of the
+  // greatest maximum and the least minimum's magnitude.
+  template <int WHICH>
+  static __device__ __forceinline__ void multiply(uint32_t at, const uint2* frag, int lane, float (&acc)[4], uint32_t (&most)[4]) {
+    // four steps at a time: their chunks first, then two chains of two instructions side by side
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
+    for (int s0 = 0; s0 < kSteps / 2; s0 += 4) {
+      uint32_t af[4][4];
+      uint2 bf[4];
+      if constexpr (kF8) {
+        uint32_t r[2][4];  // blocks 0-7 and 8-15 of a chunk, then of the next
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
-        ids[t][r] = physical(p, table, (turn * kTiles + t) * 16 + 8 * r + (lane >> 2), cands, (lane & 3) == 0);
+        for (int x = 0; x < 2; ++x) ldsm_x4(at + (s0 + 2 * x) * 16, r[x]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          e4m3x4_to_f16x2x2(r[i >> 1][2 * (i & 1)], af[i][0], af[i][2]);
+          e4m3x4_to_f16x2x2(r[i >> 1][2 * (i & 1) + 1], af[i][1], af[i][3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ldsm_x4(at + (s0 + i) * 32, af[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bf[i] = frag[(WHICH * (kSteps / 2) + s0 + i) * 32 + lane];
+      float part[2][4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) mma_zero(part[x], af[2 * x], bf[2 * x], M());
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t b[2] = {bf[2 * x + 1].x, bf[2 * x + 1].y};
+        Mma<M>::run(part[x], af[2 * x + 1], b);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most[k] = WHICH ? max_s16x2(most[k], af[i][k]) : max_u16x2(most[k], af[i][k]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] += part[0][e] + part[1][e];
+    }
   }
 
-  // Scores of this warp's share: turns of kBlocks candidates, from turn `first` (looked up) on.
-  template <typename Ready>
+  // Scores of a warp's turns: while the minima of one are multiplied its maxima
+  // arrive, and then the next one's minima.
   __device__ __forceinline__ void run(const SelectParams& p, const uint2* frag, float unit, float wsum,
-                                             const int32_t* table, int h, int cands, int first, int turns,
-                                             float* scores, Ready ready, ScoreStats& st) {
+                                      const int32_t* table, int h, int cands, int first, int turns, uint8_t* ring,
+                                      float* scores, ScoreStats& st) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    __half2 most16 = __float2half2_rn(0.f);
-    __nv_bfloat162 mostb = __float2bfloat162_rn(0.f);
+    const uint32_t at = smem_u32(ring) + ((lane & 7) + (((lane >> 3) & 1) << 3)) * kPitch + (lane >> 4) * 16;
+    uint32_t least[4] = {0u, 0u, 0u, 0u}, greatest[4] = {0u, 0u, 0u, 0u};
     for (int turn = first; turn * kBlocks < cands; turn += turns) {
-      const uint8_t* src[kTiles][2];
-      bool live[kTiles][2];
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          src[t][r] = p.bounds + (int64_t(ids[t][r]) * p.num_kv_heads + h) * kRow + c * 16;
-          live[t][r] = (turn * kTiles + t) * 16 + 8 * r + g < cands;
-        }
       float acc[kTiles][4];
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();  // every lane's copies of the minima are there
 #pragma unroll
-      for (int i0 = 0; i0 < kLoads; i0 += kGroup) {
-        uint4 x[kTiles][2][kGroup];
+      for (int t = 0; t < kTiles; ++t) multiply<0>(at + 16 * t * kPitch, frag, lane, acc[t], least);
+      __syncwarp();  // every lane has read them
+      // the turn that is copied next: its maxima's copies take the ids along
+      copy(p, table, h, cands, turns, 0, ring);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+      __syncwarp();
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int i = 0; i < kGroup; ++i)
-              x[t][r][i] = live[t][r] ? __ldg(reinterpret_cast<const uint4*>(src[t][r] + (i0 + i) * 64))
-                                      : make_uint4(0u, 0u, 0u, 0u);
-        if (i0 + kGroup >= kLoads) lookup(p, table, cands, turn + turns);
-        float part[kTiles][4];
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i)
-#pragma unroll
-          for (int s = 0; s < kPerLoad; ++s) {
-            uint32_t bf[2] = {0u, 0u};
-            if (g < 3) {
-              const uint2 f = frag[(((i0 + i) * kPerLoad + s) * 3 + g) * 4 + c];
-              bf[0] = f.x, bf[1] = f.y;
-            }
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-              uint32_t af[4];
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const uint32_t wds[4] = {x[t][r][i].x, x[t][r][i].y, x[t][r][i].z, x[t][r][i].w};
-                if constexpr (kF8) {
-                  e4m3x4_to_f16x2x2(wds[s], af[r], af[2 + r]);
-                } else {
-                  af[r] = wds[2 * s], af[2 + r] = wds[2 * s + 1];
-                }
-              }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if constexpr (std::is_same<M, __half>::value)
-                  most16 = __hmax2(most16, __habs2(*reinterpret_cast<const __half2*>(&af[k])));
-                else
-                  mostb = __hmax2(mostb, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&af[k])));
-              }
-              if (s % 2 == 0) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) part[t][e] = 0.f;
-              }
-              Mma<M>::run(part[t], af, bf);
-              if (s % 2 == 1) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[t][e] += part[t][e];
-              }
-            }
-          }
-      }
-      ready();
+      for (int t = 0; t < kTiles; ++t) multiply<1>(at + (kBlocks + 16 * t) * kPitch, frag, lane, acc[t], greatest);
+      __syncwarp();
+      copy(p, table, h, cands, turns, 1, ring);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           // columns 0 and 1 are lane c = 0's, column 2 lane c = 1's
-          float s = c == 0 ? acc[t][2 * r] + acc[t][2 * r + 1] : acc[t][2 * r];
-          s = (s + __shfl_xor_sync(kFullMask, s, 1)) * unit;
-          if (c == 0 && live[t][r]) {
-            scores[(turn * kTiles + t) * 16 + 8 * r + g] = s;
-            st.add(s);
+          float x = c == 0 ? acc[t][2 * r] + acc[t][2 * r + 1] : acc[t][2 * r];
+          x = (x + __shfl_xor_sync(kFullMask, x, 1)) * unit;
+          const int j = turn * kBlocks + 16 * t + 8 * r + g;
+          if (c == 0 && j < cands) {
+            scores[j] = x;
+            st.add(x);
           }
         }
     }
-    float most = std::is_same<M, __half>::value ? fmaxf(__low2float(most16), __high2float(most16))
-                                                : fmaxf(__low2float(mostb), __high2float(mostb));
+    least[0] = max_u16x2(max_u16x2(least[0], least[1]), max_u16x2(least[2], least[3]));
+    greatest[0] = max_s16x2(max_s16x2(greatest[0], greatest[1]), max_s16x2(greatest[2], greatest[3]));
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(kFullMask, most, m));
+    for (int m = 16; m > 0; m >>= 1) {
+      least[0] = max_u16x2(least[0], __shfl_xor_sync(kFullMask, least[0], m));
+      greatest[0] = max_s16x2(greatest[0], __shfl_xor_sync(kFullMask, greatest[0], m));
+    }
+    const uint16_t bits[4] = {static_cast<uint16_t>(least[0]), static_cast<uint16_t>(least[0] >> 16),
+                              static_cast<uint16_t>(greatest[0]), static_cast<uint16_t>(greatest[0] >> 16)};
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(to_f32(*reinterpret_cast<const M*>(&bits[i]))));
     st.mag = most * wsum;
   }
   static __device__ __forceinline__ float chain() { return 136.f + kSteps / 2 + 8.f; }
@@ -393,7 +458,8 @@ struct Scorer {  // 16-bit and E4M3 bounds
 template <int D>
 struct Scorer<float, float, D> {  // binary32 FMA: D/16 lanes a block, 32 elements each
   static constexpr int kLanes = D / 16, kPer = 32 / kLanes, kLoads = 8, kDeep = 2;
-  static constexpr int kFragBytes = 0;
+  static constexpr int kFragBytes = 0, kRing = 0;
+  static constexpr int kWarps = kSelectWarps;
   static constexpr int kBlocks = kPer * kDeep;
 
   static __device__ __forceinline__ float fragments(uint2*, const float2* w, float* unit) {
@@ -413,10 +479,12 @@ struct Scorer<float, float, D> {  // binary32 FMA: D/16 lanes a block, 32 elemen
       ids[t] = physical(p, table, (turn * kDeep + t) * kPer + lane / kLanes, cands, lane % kLanes == 0);
   }
 
-  template <typename Ready>
-  __device__ __forceinline__ void run(const SelectParams& p, const float2* w, float wsum, const int32_t* table,
-                                             int h, int cands, int first, int turns, float* scores, Ready ready,
-                                             ScoreStats& st) {
+  __device__ __forceinline__ void start(const SelectParams& p, const int32_t* table, int, int cands, int first, int, uint8_t*) {
+    lookup(p, table, cands, first);
+  }
+
+  __device__ __forceinline__ void run(const SelectParams& p, const float2* w, float wsum, const int32_t* table, int h,
+                                      int cands, int first, int turns, float* scores, ScoreStats& st) {
     const int lane = threadIdx.x & 31, gl = lane % kLanes, gi = lane / kLanes;
     float wr[32], most = 0.f;
 #pragma unroll
@@ -434,7 +502,6 @@ struct Scorer<float, float, D> {  // binary32 FMA: D/16 lanes a block, 32 elemen
                                 (int64_t(ids[t]) * p.num_kv_heads + h) * (D / 2) + gl + kLanes * i)
                         : make_float4(0.f, 0.f, 0.f, 0.f);
       lookup(p, table, cands, turn + turns);
-      ready();
 #pragma unroll
       for (int t = 0; t < kDeep; ++t) {
         float acc = 0.f;
@@ -463,6 +530,16 @@ struct Scorer<float, float, D> {  // binary32 FMA: D/16 lanes a block, 32 elemen
   static __device__ __forceinline__ float chain() { return 44.f; }
 };
 
+constexpr int kStatBytes = kMaxCluster * kSelectWarps * 16;
+constexpr int kSelectMaxBlocks = 30 * 1024;
+
+template <typename T, typename B, int D>
+struct SelectSize {  // bytes of shared memory besides the scores and their two bits
+  static constexpr int kAll = Scorer<T, B, D>::kWarps * Scorer<T, B, D>::kRing;
+  static constexpr int kRings = kAll > static_cast<int>(sizeof(SelectShared)) ? kAll : static_cast<int>(sizeof(SelectShared));
+  static constexpr int kFixed = kStatBytes + 2 * D * 8 + Scorer<T, B, D>::kFragBytes + kRings;
+};
+
 template <typename T, typename B, int D>
 __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectParams p) {
   grid_wait();
@@ -474,8 +551,17 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
   const int h = static_cast<int>(row - int64_t(b) * p.num_kv_heads);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+  using Score = Scorer<T, B, D>;
   extern __shared__ __align__(16) uint8_t raw[];
-  SelectShared& sh = *reinterpret_cast<SelectShared*>(raw);
+  float* stat = reinterpret_cast<float*>(raw);                    // [CTA][warp][4]: least score, greatest, magnitudes, flag
+  float2* w = reinterpret_cast<float2*>(raw + kStatBytes);        // [2D]: down, up
+  uint2* frag = reinterpret_cast<uint2*>(w + 2 * D);              // weights for the tensor cores
+  uint8_t* rings = reinterpret_cast<uint8_t*>(frag) + Score::kFragBytes;
+  SelectShared& sh = *reinterpret_cast<SelectShared*>(rings);
+  static_assert(Score::kFragBytes % 16 == 0 && Score::kRing % 16 == 0 && sizeof(SelectShared) % 16 == 0, "scores are read four at a time");
+  float* score = reinterpret_cast<float*>(rings + SelectSize<T, B, D>::kRings);  // [room], of the first CTA
+  uint32_t* sure_bits = reinterpret_cast<uint32_t*>(score + p.room);         // [room / 32]
+  uint32_t* win_bits = sure_bits + p.room / 32;
   if (p.longest_first) {  // CTAs start in launch order: the b-th longest sequence, equal ones in order
     const int mine = lane < p.num_seqs ? p.context_lens[lane] : INT_MIN;
     int before = 0;
@@ -486,25 +572,51 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
     b = __ffs(__ballot_sync(kFullMask, lane < p.num_seqs && before == b)) - 1;
   }
   int32_t* out = p.selected + b * p.sel_sb + h * p.sel_sh;
-  float2* w = reinterpret_cast<float2*>(raw + ((sizeof(SelectShared) + 15) / 16) * 16);  // [2D]: down, up
-  uint2* frag = reinterpret_cast<uint2*>(w + 2 * D);                                     // weights for the tensor cores
-  static_assert(Scorer<T, B, D>::kFragBytes % 16 == 0 && D % 16 == 0, "scores are read four at a time");
-  float* score = reinterpret_cast<float*>(frag + Scorer<T, B, D>::kFragBytes / 8);       // [room], of the first CTA
-  uint32_t* sure_bits = reinterpret_cast<uint32_t*>(score + p.room);                     // [room / 32]
-  uint32_t* win_bits = sure_bits + p.room / 32;
-
   int len = p.context_lens[b];
+  // the first 8 heads' elements, asked for together with the length
+  const T* q = static_cast<const T*>(p.q) + b * p.q_sb + int64_t(h) * p.group * p.q_sh;
+  T q8[8];
+#pragma unroll
+  for (int g = 0; g < 8; ++g) q8[g] = tid < D && g < p.group ? q[g * p.q_sh + tid] : from_f32<T>(0.f);
+  if (len < 0 || len > p.max_tokens) {
+    if (tid == 0 && rank == 0) atomicOr(p.err, kErrLen);
+    len = len < 0 ? 0 : p.max_tokens;
+  }
+  const int n = (len + (1 << p.log2_bs) - 1) >> p.log2_bs;
+  const int need = p.top - p.sink - p.recent;  // of the scored blocks
+  if (n <= p.top || need == 0) {               // all of them, or the fixed ones alone: no scores
+    for (int i = rank * kSelectThreads + tid; i < p.top; i += ctas * kSelectThreads) {
+      if (n <= p.top)
+        out[i] = i < n ? i : -1;
+      else
+        out[i] = i < p.sink ? i : n - p.top + i;
+    }
+    return;
+  }
+  auto started = cluster.barrier_arrive();  // waited for before the first store to the first CTA's shared memory
+
+  // --- scores of the candidates sink .. n - recent - 1 ---
+  const int cands = n - p.sink - p.recent;
+  const int32_t* table = p.block_tables + b * p.bt_stride + p.sink;
+  constexpr int64_t head_bytes = 2 * D * sizeof(B);
+  const int first = rank * Score::kWarps + warp, turns = ctas * Score::kWarps;
+  const bool scores_here = warp < Score::kWarps;
+  uint8_t* ring = rings + warp * Score::kRing;
+  Score scorer;
+  if (scores_here) scorer.start(p, table, h, cands, first, turns, ring);
+
   // the weights, sums over the group's heads in two binary32 words each (the
   // rounding error of every addition is kept in the second)
-  const T* q = static_cast<const T*>(p.q) + b * p.q_sb + int64_t(h) * p.group * p.q_sh;
   auto sums = [&](float unit) {
     bool big = false;
-    for (int d = tid; d < D; d += kSelectThreads) {
+    static_assert(D <= kSelectThreads, "an element a thread");
+    if (tid < D) {
+      const int d = tid;
       float hi[2] = {0.f, 0.f}, lo[2] = {0.f, 0.f};
       for (int g0 = 0; g0 < p.group; g0 += 8) {
         float x[8];
 #pragma unroll
-        for (int g = 0; g < 8; ++g) x[g] = g0 + g < p.group ? to_f32(q[(g0 + g) * p.q_sh + d]) * unit : 0.f;
+        for (int g = 0; g < 8; ++g) x[g] = g0 == 0 ? to_f32(q8[g]) * unit : g0 + g < p.group ? to_f32(q[(g0 + g) * p.q_sh + d]) * unit : 0.f;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           big |= fabsf(x[g]) > 1e30f && fabsf(x[g]) < INFINITY;
@@ -526,47 +638,18 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
   // sums that could leave binary32's range are taken of the queries times 2^-60
   if (sums(1.f)) sums(8.6736174e-19f);
 
-  if (len < 0 || len > p.max_tokens) {
-    if (tid == 0 && rank == 0) atomicOr(p.err, kErrLen);
-    len = len < 0 ? 0 : p.max_tokens;
-  }
-  const int n = (len + (1 << p.log2_bs) - 1) >> p.log2_bs;
-  const int need = p.top - p.sink - p.recent;  // of the scored blocks
-  if (n <= p.top || need == 0) {               // all of them, or the fixed ones alone: no scores
-    for (int i = rank * kSelectThreads + tid; i < p.top; i += ctas * kSelectThreads) {
-      if (n <= p.top)
-        out[i] = i < n ? i : -1;
-      else
-        out[i] = i < p.sink ? i : n - p.top + i;
-    }
-    return;
-  }
-  auto started = cluster.barrier_arrive();  // waited for before the first store to the first CTA's shared memory
-
-  // --- scores of the candidates sink .. n - recent - 1 ---
-  using Score = Scorer<T, B, D>;
-  const int cands = n - p.sink - p.recent;
-  const int32_t* table = p.block_tables + b * p.bt_stride + p.sink;
-  constexpr int64_t head_bytes = 2 * D * sizeof(B);
-  const int first = rank * kSelectWarps + warp, turns = ctas * kSelectWarps;
-  Score scorer;
-  scorer.lookup(p, table, cands, first);
   float unit;
   const float wsum = Score::fragments(frag, w, &unit);
   __syncthreads();
+  cluster.barrier_wait(std::move(started));
   ScoreStats st;
-  {
-    bool waited = false;
-    auto ready = [&] {
-      if (!waited) cluster.barrier_wait(std::move(started));
-      waited = true;
-    };
+  if (scores_here) {
     float* scores = cluster.map_shared_rank(score, 0);
-    if constexpr (sizeof(B) == 4)
-      scorer.run(p, w, wsum, table, h, cands, first, turns, scores, ready, st);
-    else
-      scorer.run(p, frag, unit, wsum, table, h, cands, first, turns, scores, ready, st);
-    ready();
+    if constexpr (sizeof(B) == 4) {
+      scorer.run(p, w, wsum, table, h, cands, first, turns, scores, st);
+    } else {
+      scorer.run(p, frag, unit, wsum, table, h, cands, first, turns, ring, scores, st);
+    }
   }
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) {
@@ -575,20 +658,19 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
   }
   st.odd = __any_sync(kFullMask, st.odd || !(st.mag < 1e37f));
   if (lane == 0)
-    *reinterpret_cast<float4*>(cluster.map_shared_rank(&sh.stat[rank * kSelectWarps + warp][0], 0)) =
+    *reinterpret_cast<float4*>(cluster.map_shared_rank(stat + (rank * kSelectWarps + warp) * 4, 0)) =
         make_float4(st.least, st.greatest, st.mag, st.odd ? 1.f : 0.f);
-  if (rank == 0) {
-    for (int i = tid; i < kBins; i += kSelectThreads) sh.hist[i] = 0;
-    if (tid == 0) sh.near_count = sh.win_count = sh.sure_count = 0;
-  }
   cluster.sync();
   if (rank != 0) return;  // nothing of this CTA is accessed any more
+  for (int i = tid; i < kBins; i += kSelectThreads) sh.hist[i] = 0;
+  if (tid == 0) sh.near_count = sh.win_count = sh.sure_count = 0;
+  __syncthreads();
 
   // --- the first CTA: the bin that holds the border ---
   float smin = INFINITY, smax = -INFINITY, mag = 0.f, flag = 0.f;
   for (int r = lane; r < ctas * kSelectWarps; r += 32) {
-    smin = fminf(smin, sh.stat[r][0]), smax = fmaxf(smax, sh.stat[r][1]);
-    mag = fmaxf(mag, sh.stat[r][2]), flag = fmaxf(flag, sh.stat[r][3]);
+    smin = fminf(smin, stat[4 * r]), smax = fmaxf(smax, stat[4 * r + 1]);
+    mag = fmaxf(mag, stat[4 * r + 2]), flag = fmaxf(flag, stat[4 * r + 3]);
   }
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) {
@@ -804,15 +886,26 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectP
   }
 }
 
-size_t select_smem(int head_dim, int room) {
-  return (sizeof(SelectShared) + 15) / 16 * 16 + size_t(2 * head_dim) * 8 + size_t(head_dim) * 12 + size_t(room) * 4 +
-         size_t(room / 32) * 8;  // weights, their fragments (fewer for f32), scores, two bits a block
+size_t select_smem(int fixed, int room) {  // scores and two bits a block behind what the kernel always has
+  return size_t(fixed) + size_t(room) * 4 + size_t(room / 32) * 8;
 }
 
 template <typename T, typename B, int D>
-int launch_one(const SelectParams& p, int ctas, cudaStream_t stream) {
+int launch_one(SelectParams p, int max_blocks, int num_sms, cudaStream_t stream) {
   static std::atomic<int> configured[64];
-  const size_t smem = select_smem(D, p.room);
+  static_assert(SelectSize<T, B, D>::kFixed + kSelectMaxBlocks * 4 + kSelectMaxBlocks / 4 <= 226 * 1024, "scores of the widest table fit");
+  p.room = (max_blocks + 31) / 32 * 32;
+  const size_t smem = select_smem(SelectSize<T, B, D>::kFixed, p.room);
+  // CTAs of a row: as many as run at once, so that the work of every CTA besides
+  // the scores (weights, barrier, the first copies' latency) is paid once, and
+  // none with less than a turn of its warps
+  const int64_t rows = int64_t(p.num_seqs) * p.num_kv_heads;
+  const int64_t resident = int64_t(num_sms) * std::max<int64_t>(1, std::min<int64_t>(2, 227 * 1024 / (smem + 1024)));
+  int ctas = 1;
+  while (ctas < kMaxCluster && rows * ctas * 2 <= resident && max_blocks / (2 * ctas) >= Scorer<T, B, D>::kBlocks * Scorer<T, B, D>::kWarps / 2)
+    ctas *= 2;
+  // batches of more than one wave start the longest rows first
+  p.longest_first = rows * ctas > resident && p.num_seqs > 1 && p.num_seqs <= 32;
   const void* func = reinterpret_cast<const void*>(&select_kernel<T, B, D>);
   int e = raise_smem_limit(configured, func, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -821,43 +914,29 @@ int launch_one(const SelectParams& p, int ctas, cudaStream_t stream) {
 }
 
 template <typename T, typename B>
-int launch_dim(const SelectParams& p, int head_dim, int ctas, cudaStream_t stream) {
+int launch_dim(const SelectParams& p, int head_dim, int max_blocks, int num_sms, cudaStream_t stream) {
   switch (head_dim) {
-    case 64: return launch_one<T, B, 64>(p, ctas, stream);
-    case 128: return launch_one<T, B, 128>(p, ctas, stream);
-    case 256: return launch_one<T, B, 256>(p, ctas, stream);
+    case 64: return launch_one<T, B, 64>(p, max_blocks, num_sms, stream);
+    case 128: return launch_one<T, B, 128>(p, max_blocks, num_sms, stream);
+    case 256: return launch_one<T, B, 256>(p, max_blocks, num_sms, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-// Most blocks a table row may have: their scores have to fit one CTA's shared memory.
-int select_max_blocks(int head_dim) {
-  const size_t room = 200 * 1024 - select_smem(head_dim, 0);
-  return static_cast<int>(room / 136 * 32);  // 4 bytes and two bits a block
-}
+// Most blocks a table row may have: their scores have to fit one CTA's shared
+// memory beside the rings (85 KB with everything else).
+int select_max_blocks() { return kSelectMaxBlocks; }
 
-int launch_select(int dtype, int bounds_dtype, int head_dim, SelectParams p, int max_blocks, int num_sms,
+int launch_select(int dtype, int bounds_dtype, int head_dim, const SelectParams& p, int max_blocks, int num_sms,
                   cudaStream_t stream) {
-  // CTAs of a row: as many as run at once (two an SM), so that the work of every
-  // CTA besides the scores (weights, barrier, the first loads' latency: 6 us) is
-  // paid once, and none with less than a turn of its warps.  Measured, us for 1,
-  // 2, 4, 8 and 16 CTAs a row: 64 rows of 2048-8192 blocks 104, 63, 48, 49, 62;
-  // 256 rows of 190-1500 E4M3 blocks 29, 35, 46, 70, 136; 4 rows of 1000 blocks
-  // 12.5, 10.2, 8.8, 8.8, 9.0.
-  const int64_t rows = int64_t(p.num_seqs) * p.num_kv_heads;
-  int ctas = 1;
-  while (ctas < kMaxCluster && rows * ctas * 2 <= int64_t(num_sms) * 2 && max_blocks / (2 * ctas) >= 16 * kSelectWarps / 2) ctas *= 2;
-  p.room = (max_blocks + 31) / 32 * 32;
-  // batches of more than one wave start the longest rows first
-  p.longest_first = rows * ctas > int64_t(num_sms) * 2 && p.num_seqs > 1 && p.num_seqs <= 32;
   int e = cudaErrorInvalidValue;
-  if (dtype == 0 && bounds_dtype == 0) e = launch_dim<float, float>(p, head_dim, ctas, stream);
-  if (dtype == 1 && bounds_dtype == 1) e = launch_dim<__half, __half>(p, head_dim, ctas, stream);
-  if (dtype == 2 && bounds_dtype == 2) e = launch_dim<__nv_bfloat16, __nv_bfloat16>(p, head_dim, ctas, stream);
-  if (dtype == 1 && bounds_dtype == 5) e = launch_dim<__half, uint8_t>(p, head_dim, ctas, stream);
-  if (dtype == 2 && bounds_dtype == 5) e = launch_dim<__nv_bfloat16, uint8_t>(p, head_dim, ctas, stream);
+  if (dtype == 0 && bounds_dtype == 0) e = launch_dim<float, float>(p, head_dim, max_blocks, num_sms, stream);
+  if (dtype == 1 && bounds_dtype == 1) e = launch_dim<__half, __half>(p, head_dim, max_blocks, num_sms, stream);
+  if (dtype == 2 && bounds_dtype == 2) e = launch_dim<__nv_bfloat16, __nv_bfloat16>(p, head_dim, max_blocks, num_sms, stream);
+  if (dtype == 1 && bounds_dtype == 5) e = launch_dim<__half, uint8_t>(p, head_dim, max_blocks, num_sms, stream);
+  if (dtype == 2 && bounds_dtype == 5) e = launch_dim<__nv_bfloat16, uint8_t>(p, head_dim, max_blocks, num_sms, stream);
   if (e == cudaSuccess) note_launch();
   return e;
 }

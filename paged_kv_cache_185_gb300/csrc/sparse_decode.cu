@@ -313,33 +313,35 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
       for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[half][e] = 0.f;
-      if constexpr (F8) {
-        const int k_row = (lane & 7) + (((lane >> 3) & 1) << 3), k_chunk = lane >> 4;
+      // chunks of four steps first, then their products
+      constexpr int kGroup = kKS < 4 ? kKS : 4;
 #pragma unroll
-        for (int kp = 0; kp < kKS / 2; ++kp) {
-          uint32_t r[4];  // tokens 0-7 and 8-15 of chunk 2kp, then of chunk 2kp + 1
-          ldsm_x4(kt + code_offset<D>(k_row, 2 * kp + k_chunk), r);
+      for (int s0 = 0; s0 < kKS; s0 += kGroup) {
+        uint32_t bf[kGroup][2][2];  // [step][half]
+        if constexpr (F8) {
+          const int k_row = (lane & 7) + (((lane >> 3) & 1) << 3), k_chunk = lane >> 4;
+          uint32_t r[kGroup / 2][4];  // tokens 0-7 and 8-15 of a chunk, then of the next
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t bf[2];
-            e4m3x4_to_f16x2x2(r[x], bf[0], bf[1]);
-            const int step = 2 * kp + (x >> 1);
-            const uint32_t af[4] = {qf[0][step][0], kNT > 1 ? qf[kNT - 1][step][0] : 0u, qf[0][step][1],
-                                    kNT > 1 ? qf[kNT - 1][step][1] : 0u};
-            Mma<M>::run(s[x & 1], af, bf);
+          for (int x = 0; x < kGroup / 2; ++x) ldsm_x4(kt + code_offset<D>(k_row, s0 + 2 * x + k_chunk), r[x]);
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) e4m3x4_to_f16x2x2(r[i >> 1][2 * (i & 1) + half], bf[i][half][0], bf[i][half][1]);
+        } else {
+          const int k_row = (lane & 7) + ((lane >> 4) << 3), k_chunk = (lane >> 3) & 1;
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) {
+            uint32_t r[4];  // chunks 2 step and 2 step + 1 of tokens 0-7, then of tokens 8-15
+            ldsm_x4(kt + tile_offset(k_row, 2 * (s0 + i) + k_chunk), r);
+            bf[i][0][0] = r[0], bf[i][0][1] = r[1], bf[i][1][0] = r[2], bf[i][1][1] = r[3];
           }
         }
-      } else {
-        const int k_row = (lane & 7) + ((lane >> 4) << 3), k_chunk = (lane >> 3) & 1;
 #pragma unroll
-        for (int step = 0; step < kKS; ++step) {
-          uint32_t r[4];  // chunks 2 step and 2 step + 1 of tokens 0-7, then of tokens 8-15
-          ldsm_x4(kt + tile_offset(k_row, 2 * step + k_chunk), r);
-          const uint32_t af[4] = {qf[0][step][0], kNT > 1 ? qf[kNT - 1][step][0] : 0u, qf[0][step][1],
-                                  kNT > 1 ? qf[kNT - 1][step][1] : 0u};
-          const uint32_t b0[2] = {r[0], r[1]}, b1[2] = {r[2], r[3]};
-          Mma<M>::run(s[0], af, b0);
-          Mma<M>::run(s[1], af, b1);
+        for (int i = 0; i < kGroup; ++i) {
+          const uint32_t af[4] = {qf[0][s0 + i][0], kNT > 1 ? qf[kNT - 1][s0 + i][0] : 0u, qf[0][s0 + i][1],
+                                  kNT > 1 ? qf[kNT - 1][s0 + i][1] : 0u};
+          Mma<M>::run(s[0], af, bf[i][0]);
+          Mma<M>::run(s[1], af, bf[i][1]);
         }
       }
       // weights: head 8a + g, tokens 2c, 2c + 1 of both halves
@@ -378,34 +380,33 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
       const bool tail = live < 16;
       const uint32_t keep_lo = (2 * c < live ? 0x0000ffffu : 0u) | (2 * c + 1 < live ? 0xffff0000u : 0u);
       const uint32_t keep_hi = (2 * c + 8 < live ? 0x0000ffffu : 0u) | (2 * c + 9 < live ? 0xffff0000u : 0u);
-      auto product = [&](int t, uint32_t (&af)[4]) {
-        if (tail) af[0] &= keep_lo, af[1] &= keep_lo, af[2] &= keep_hi, af[3] &= keep_hi;
+      const int v_row = F8 ? (lane & 7) + (((lane >> 3) & 1) << 3) : (lane & 7) + ((lane >> 4) << 3);
+      const int v_chunk = F8 ? lane >> 4 : (lane >> 3) & 1;
 #pragma unroll
-        for (int a = 0; a < kNT; ++a) Mma<M>::run(o[t][a], af, pf[a]);
-      };
-      if constexpr (F8) {
-        const int v_row = (lane & 7) + (((lane >> 3) & 1) << 3), v_chunk = lane >> 4;
+      for (int t0 = 0; t0 < kKS; t0 += kGroup) {
+        uint32_t af[kGroup][4];
+        if constexpr (F8) {
+          uint32_t r[kGroup / 2][4];  // tokens 0-7 and 8-15 of a chunk, then of the next
 #pragma unroll
-        for (int mp = 0; mp < kKS / 2; ++mp) {
-          uint32_t r[4];  // tokens 0-7 and 8-15 of chunk 2mp, then of chunk 2mp + 1
-          ldsm_x4_trans(vt + code_offset<D>(v_row, 2 * mp + v_chunk), r);
+          for (int x = 0; x < kGroup / 2; ++x) ldsm_x4_trans(vt + code_offset<D>(v_row, t0 + 2 * x + v_chunk), r[x]);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+          for (int i = 0; i < kGroup; ++i) {
             // bytes (t, e), (t, e+1), (t+1, e), (t+1, e+1) -> (t, e), (t+1, e), (t, e+1), (t+1, e+1)
-            uint32_t af[4];
-            e4m3x4_to_f16x2x2(__byte_perm(r[2 * x], 0u, 0x3120), af[0], af[1]);
-            e4m3x4_to_f16x2x2(__byte_perm(r[2 * x + 1], 0u, 0x3120), af[2], af[3]);
-            product(2 * mp + x, af);
+            e4m3x4_to_f16x2x2(__byte_perm(r[i >> 1][2 * (i & 1)], 0u, 0x3120), af[i][0], af[i][1]);
+            e4m3x4_to_f16x2x2(__byte_perm(r[i >> 1][2 * (i & 1) + 1], 0u, 0x3120), af[i][2], af[i][3]);
           }
-        }
-      } else {
-        const int v_row = (lane & 7) + ((lane >> 4) << 3), v_chunk = (lane >> 3) & 1;
+        } else {
 #pragma unroll
-        for (int t = 0; t < kKS; ++t) {
-          uint32_t af[4];
-          ldsm_x4_trans(vt + tile_offset(v_row, 2 * t + v_chunk), af);
-          product(t, af);
+          for (int i = 0; i < kGroup; ++i) ldsm_x4_trans(vt + tile_offset(v_row, 2 * (t0 + i) + v_chunk), af[i]);
         }
+        if (tail) {
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) af[i][0] &= keep_lo, af[i][1] &= keep_lo, af[i][2] &= keep_hi, af[i][3] &= keep_hi;
+        }
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+          for (int a = 0; a < kNT; ++a) Mma<M>::run(o[t0 + i][a], af[i], pf[a]);
       }
       __syncwarp();  // every lane has read the stage
       if (to_copy) copy();
