@@ -10,6 +10,7 @@ path.  Loading fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -265,21 +266,30 @@ def paged_attention_prefill_fp8(out, q, k_cache, v_cache, block_tables, context_
     return out
 
 
-def _rotate(name, tensors, q_weight, k_weight, eps, style, sections, scales):
+@functools.lru_cache(maxsize=256)
+def _rotary(style, sections, eps):
+    """The options of a rotary call as the C struct's reference (the struct is never written again)."""
     if style not in _ROTARY_STYLE:
         raise ValueError(f"style must be one of {sorted(_ROTARY_STYLE)}, got {style!r}")
-    sections = () if sections is None else tuple(int(n) for n in sections)
-    positions = tensors[7]
-    if sections and positions.dim() == 1 and len(sections) > 1:
-        raise ValueError("several sections need positions [axes, T]")
-    if not sections and positions.dim() == 2 and positions.shape[0] > 1:
-        raise ValueError("positions on several axes need sections")
     if len(sections) > 4:
         raise ValueError("at most 4 sections")
     how = WllmRotary(_ROTARY_STYLE[style], max(1, len(sections)))
     how.sections[:len(sections)] = sections
-    how.eps = float(eps)
-    _call(name, (*tensors, q_weight, k_weight), ctypes.byref(how), *scales)
+    how.eps = eps
+    return ctypes.byref(how)
+
+
+def _rotate(name, tensors, eps, style, sections, scales):
+    positions = tensors[7]
+    if sections is None:
+        sections = ()
+        if positions.dim() == 2 and positions.shape[0] > 1:
+            raise ValueError("positions on several axes need sections")
+    else:
+        sections = tuple(int(n) for n in sections)
+        if len(sections) > 1 and positions.dim() == 1:
+            raise ValueError("several sections need positions [axes, T]")
+    _call(name, tensors, _rotary(style, sections, float(eps)), *scales)
 
 
 def rotate_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, *, q_weight=None,
@@ -289,8 +299,8 @@ def rotate_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mapping, posit
 
     ``positions`` is [T], or [axes,T] with ``sections`` naming the pairs that each axis turns.  ``style``:
     "halves" pairs elements (i, i+R/2), "adjacent" (2i, 2i+1).  Returns ``q_out``."""
-    _rotate("wllm_rotate_and_cache", (q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin),
-            q_weight, k_weight, eps, style, sections, ())
+    _rotate("wllm_rotate_and_cache", (q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight,
+                                      k_weight), eps, style, sections, ())
     return q_out
 
 
@@ -298,8 +308,8 @@ def rotate_and_cache_fp8(q_out, q, key, value, k_cache, v_cache, slot_mapping, p
                          v_scale: float, *, q_weight=None, k_weight=None, eps: float = 1e-6, style: str = "halves",
                          sections=None) -> torch.Tensor:
     """rotate_and_cache into E4M3 caches: stores E4M3(x * (1/scale)) of the turned keys and of the values."""
-    _rotate("wllm_rotate_and_cache_fp8", (q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin),
-            q_weight, k_weight, eps, style, sections, (float(k_scale), float(v_scale)))
+    _rotate("wllm_rotate_and_cache_fp8", (q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                                          q_weight, k_weight), eps, style, sections, (float(k_scale), float(v_scale)))
     return q_out
 
 
