@@ -308,12 +308,10 @@ int sparse_call(const wllm_tensor* out, const wllm_tensor* q, const wllm_tensor*
   if ((rc = locked_state(&s))) return rc;
   p.err = s->err;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  CUtensorMap kmap{}, vmap{};
-  if (dt != WLLM_F32) {
-    const int kv_dt = kv_fp8 ? WLLM_FP8_E4M3 : dt;
-    if ((rc = make_pool_map(&kmap, k_cache->data, kv_dt, nb, hkv, bs, d, "k_cache"))) return rc;
-    if ((rc = make_pool_map(&vmap, v_cache->data, kv_dt, nb, hkv, bs, d, "v_cache"))) return rc;
-  }
+  CUtensorMap kmap, vmap;
+  const int kv_dt = kv_fp8 ? WLLM_FP8_E4M3 : dt;
+  if ((rc = make_pool_map(&kmap, k_cache->data, kv_dt, nb, hkv, bs, d, "k_cache"))) return rc;
+  if ((rc = make_pool_map(&vmap, v_cache->data, kv_dt, nb, hkv, bs, d, "v_cache"))) return rc;
   const cudaError_t e = static_cast<cudaError_t>(
       launch_sparse_decode(dt, kv_fp8, static_cast<int>(d), kmap, vmap, p, s->num_sms, st));
   if (e != cudaSuccess) return cuda_fail(e, "sparse decode launch");

@@ -27,8 +27,7 @@
 // the GPU with neither a second launch nor a workspace, and in a fixed order.
 // Bound: memory, each selected K and V byte is read once per head tile.
 //
-// The f32 kernel keeps the same split with binary32 FMA (no tensor cores), its
-// rows straight from global memory.
+// F32 caches keep the same split and rings with binary32 FMA (no tensor cores).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -47,11 +46,13 @@ constexpr int kMaxSparseCluster = 8;
 
 // Warps of a CTA and stages of a warp's ring.  Eight warps instead of four: 256
 // sequences over an fp8 cache 76.4 instead of 73.7 us, one sequence 4.8 instead of 5.1.
+// f32 units are bound by their FMA and take more warps with a stage each.
 template <typename B, int D>
 struct SparseTuning {
   static constexpr int kStage = Geom<B, D>::kStageBytes;  // 16 tokens' K and V rows
-  static constexpr int kWarps = kStage >= 16384 ? 2 : 4;
-  static constexpr int kStages = kStage >= 8192 ? 2 : kStage >= 4096 ? 3 : 6;
+  static constexpr bool kF32 = sizeof(B) == 4;
+  static constexpr int kWarps = kStage >= 32768 || (kStage >= 16384 && !kF32) ? 2 : 4;
+  static constexpr int kStages = kF32 && kStage >= 16384 ? 1 : kStage >= 8192 ? 2 : kStage >= 4096 ? 3 : 6;
   static constexpr int kRing = kStages * kStage;          // a warp's
 };
 
@@ -127,7 +128,7 @@ __device__ __forceinline__ void merge_and_store(const SparseParams& p, cg::clust
   __syncthreads();
   float m_cta = 0.f, l_cta = 0.f;
   for (int h0 = warp * 4; h0 < HT; h0 += WARPS * 4) {
-    const int h = h0 + (lane >> 3), i = lane & 7;
+    const int h = min(h0 + (lane >> 3), HT - 1), i = lane & 7;
     const bool have = i < WARPS;
     const Partial<D, HT>* x = part(have ? i : 0);
     const float f = factors(h, have, x->m[h], x->l[h], &m_cta, &l_cta);
@@ -156,7 +157,7 @@ __device__ __forceinline__ void merge_and_store(const SparseParams& p, cg::clust
   if (ctas == 1) return;
   cluster.sync();
   for (int h0 = warp * 4; h0 < HT; h0 += WARPS * 4) {
-    const int h = h0 + (lane >> 3), i = lane & 7;
+    const int h = min(h0 + (lane >> 3), HT - 1), i = lane & 7;
     const bool have = i < ctas;
     const Partial<D, HT>* x = cluster.map_shared_rank(part(0), have ? i : 0);
     float m, l;
@@ -184,19 +185,335 @@ __device__ __forceinline__ void merge_and_store(const SparseParams& p, cg::clust
   cluster.sync();  // a CTA's shared memory outlives its peers' reads
 }
 
-// --- tensor-core kernel --------------------------------------------------------
-// T: query and output type; F8: the caches hold E4M3 codes (M is then f16).
+// The products of one warp on tensor cores.
+template <typename T, bool F8, int D, int HT>
+struct MmaMath {
+  using M = typename std::conditional<F8, __half, T>::type;
+  static constexpr int kNT = HT / 8;  // tiles of 8 heads
+  static constexpr int kKS = D / 16;  // k16 steps over head_dim
+  static constexpr int kQueryBytes = 0;
+  uint32_t qf[kNT][kKS][2];
+  float m[kNT], l[kNT], o[kKS][kNT][4];
+
+  __device__ __forceinline__ void load_q(const SparseParams& p, float*, int b, int head0, int heads) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    // Q fragments: head 8a + g; elements 16s + 2c (+8) of 16-bit rows, 16s + 4c (+2) where codes are widened
+#pragma unroll
+    for (int a = 0; a < kNT; ++a)
+#pragma unroll
+      for (int s = 0; s < kKS; ++s)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t x = 0u;
+          if (8 * a + g < heads) {
+            const int d = F8 ? 16 * s + 4 * c + 2 * e : 16 * s + 2 * c + 8 * e;
+            const T* q = static_cast<const T*>(p.q) + b * p.q_sb + (head0 + 8 * a + g) * p.q_sh + d;
+            if (p.q_pairs) {
+              x = *reinterpret_cast<const uint32_t*>(q);
+            } else {
+              const uint16_t lo = *reinterpret_cast<const uint16_t*>(q), hi = *reinterpret_cast<const uint16_t*>(q + 1);
+              x = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+            }
+            if constexpr (F8) x = to_f16x2<T>(x);
+          }
+          qf[a][s][e] = x;
+        }
+#pragma unroll
+    for (int a = 0; a < kNT; ++a) m[a] = -INFINITY, l[a] = 0.f;
+#pragma unroll
+    for (int t = 0; t < kKS; ++t)
+#pragma unroll
+      for (int a = 0; a < kNT; ++a)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][a][e] = 0.f;
+  }
+
+  // 16 tokens whose K rows are at shared address kt and V rows at vt, the first `live` of them.
+  __device__ __forceinline__ void step(uint32_t kt, uint32_t vt, int live, float scale_log2) {
+    const int lane = threadIdx.x & 31, c = lane & 3;
+    // S = Q K^T, tokens 0-7 and 8-15
+    float s[2][4];
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[half][e] = 0.f;
+    // chunks of four steps first, then their products
+    constexpr int kGroup = kKS < 4 ? kKS : 4;
+#pragma unroll
+    for (int s0 = 0; s0 < kKS; s0 += kGroup) {
+      uint32_t bf[kGroup][2][2];  // [step][half]
+      if constexpr (F8) {
+        const int k_row = (lane & 7) + (((lane >> 3) & 1) << 3), k_chunk = lane >> 4;
+        uint32_t r[kGroup / 2][4];  // tokens 0-7 and 8-15 of a chunk, then of the next
+#pragma unroll
+        for (int x = 0; x < kGroup / 2; ++x) ldsm_x4(kt + code_offset<D>(k_row, s0 + 2 * x + k_chunk), r[x]);
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) e4m3x4_to_f16x2x2(r[i >> 1][2 * (i & 1) + half], bf[i][half][0], bf[i][half][1]);
+      } else {
+        const int k_row = (lane & 7) + ((lane >> 4) << 3), k_chunk = (lane >> 3) & 1;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          uint32_t r[4];  // chunks 2 step and 2 step + 1 of tokens 0-7, then of tokens 8-15
+          ldsm_x4(kt + tile_offset(k_row, 2 * (s0 + i) + k_chunk), r);
+          bf[i][0][0] = r[0], bf[i][0][1] = r[1], bf[i][1][0] = r[2], bf[i][1][1] = r[3];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        const uint32_t af[4] = {qf[0][s0 + i][0], kNT > 1 ? qf[kNT - 1][s0 + i][0] : 0u, qf[0][s0 + i][1],
+                                kNT > 1 ? qf[kNT - 1][s0 + i][1] : 0u};
+        Mma<M>::run(s[0], af, bf[i][0]);
+        Mma<M>::run(s[1], af, bf[i][1]);
+      }
+    }
+    // weights: head 8a + g, tokens 2c, 2c + 1 of both halves
+    uint32_t pf[kNT][2];
+#pragma unroll
+    for (int a = 0; a < kNT; ++a) {
+      float x[4];
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          x[2 * half + e] = 8 * half + 2 * c + e < live ? s[half][2 * a + e] * scale_log2 : -INFINITY;
+      float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+      const float mn = fmaxf(m[a], top);
+      if (__any_sync(kFullMask, mn > m[a])) {
+        const float f = m[a] == -INFINITY ? 0.f : exp2f(m[a] - mn);
+        l[a] *= f;
+        m[a] = mn;
+        const float f0 = __shfl_sync(kFullMask, f, 8 * c), f1 = __shfl_sync(kFullMask, f, 8 * c + 4);
+#pragma unroll
+        for (int t = 0; t < kKS; ++t) {
+          o[t][a][0] *= f0, o[t][a][1] *= f1, o[t][a][2] *= f0, o[t][a][3] *= f1;
+        }
+      }
+      const float base = m[a] == -INFINITY ? 0.f : m[a];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        pf[a][half] = Mma<M>::pack(ex2_approx(x[2 * half] - base), ex2_approx(x[2 * half + 1] - base));
+        const M* w = reinterpret_cast<const M*>(&pf[a][half]);
+        l[a] += to_f32(w[0]) + to_f32(w[1]);
+      }
+    }
+    // O^T += V^T P^T; V rows behind the context are zeroed (they may hold anything)
+    const bool tail = live < 16;
+    const uint32_t keep_lo = (2 * c < live ? 0x0000ffffu : 0u) | (2 * c + 1 < live ? 0xffff0000u : 0u);
+    const uint32_t keep_hi = (2 * c + 8 < live ? 0x0000ffffu : 0u) | (2 * c + 9 < live ? 0xffff0000u : 0u);
+    const int v_row = F8 ? (lane & 7) + (((lane >> 3) & 1) << 3) : (lane & 7) + ((lane >> 4) << 3);
+    const int v_chunk = F8 ? lane >> 4 : (lane >> 3) & 1;
+#pragma unroll
+    for (int t0 = 0; t0 < kKS; t0 += kGroup) {
+      uint32_t af[kGroup][4];
+      if constexpr (F8) {
+        uint32_t r[kGroup / 2][4];  // tokens 0-7 and 8-15 of a chunk, then of the next
+#pragma unroll
+        for (int x = 0; x < kGroup / 2; ++x) ldsm_x4_trans(vt + code_offset<D>(v_row, t0 + 2 * x + v_chunk), r[x]);
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          // bytes (t, e), (t, e+1), (t+1, e), (t+1, e+1) -> (t, e), (t+1, e), (t, e+1), (t+1, e+1)
+          e4m3x4_to_f16x2x2(__byte_perm(r[i >> 1][2 * (i & 1)], 0u, 0x3120), af[i][0], af[i][1]);
+          e4m3x4_to_f16x2x2(__byte_perm(r[i >> 1][2 * (i & 1) + 1], 0u, 0x3120), af[i][2], af[i][3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) ldsm_x4_trans(vt + tile_offset(v_row, 2 * (t0 + i) + v_chunk), af[i]);
+      }
+      if (tail) {
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) af[i][0] &= keep_lo, af[i][1] &= keep_lo, af[i][2] &= keep_hi, af[i][3] &= keep_hi;
+      }
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i)
+#pragma unroll
+        for (int a = 0; a < kNT; ++a) Mma<M>::run(o[t0 + i][a], af[i], pf[a]);
+    }
+  }
+
+  __device__ __forceinline__ void store(Partial<D, HT>& out, int) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int a = 0; a < kNT; ++a) {
+      l[a] += __shfl_xor_sync(kFullMask, l[a], 1);
+      l[a] += __shfl_xor_sync(kFullMask, l[a], 2);
+      if (c == 0) {
+        out.m[8 * a + g] = m[a];
+        out.l[8 * a + g] = l[a];
+      }
+#pragma unroll
+      for (int t = 0; t < kKS; ++t) {
+        if constexpr (F8) {  // rows g and g + 8 are elements 16t + 2g and 16t + 2g + 1
+          const int d = 16 * t + 2 * g;
+          *reinterpret_cast<float2*>(&out.o[8 * a + 2 * c][d]) = make_float2(o[t][a][0], o[t][a][2]);
+          *reinterpret_cast<float2*>(&out.o[8 * a + 2 * c + 1][d]) = make_float2(o[t][a][1], o[t][a][3]);
+        } else {
+          const int d = 16 * t + g;
+          out.o[8 * a + 2 * c][d] = o[t][a][0];
+          out.o[8 * a + 2 * c + 1][d] = o[t][a][1];
+          out.o[8 * a + 2 * c][d + 8] = o[t][a][2];
+          out.o[8 * a + 2 * c + 1][d + 8] = o[t][a][3];
+        }
+      }
+    }
+  }
+};
+
+// The same in binary32 FMA.  Scores: lane (token t of 8, quarter of the 16-byte
+// chunks) has tokens t and t + 8, so a query chunk, the same for the 8 lanes of a
+// quarter, serves 8 products and K's chunks meet no bank twice; the quarters are
+// summed by shuffles.  Outputs: D/32 columns a lane, weights from shared memory.
+template <int D, int HT>
+struct FmaMath {
+  static constexpr int kCols = D / 32, kPs = 16 * HT;
+  static constexpr int kQueryBytes = (HT * D + 4 * kPs) * 4;  // queries, then a warp's weights for up to 4 warps
+  float m[HT], l[HT], o[HT][kCols];
+  const float* qs;
+  float* ps;
+
+  __device__ __forceinline__ void load_q(const SparseParams& p, float* queries, int b, int head0, int heads) {
+    for (int i = threadIdx.x; i < HT * D; i += blockDim.x) {
+      const int a = i / D, d = i - a * D;
+      queries[i] = a < heads ? static_cast<const float*>(p.q)[b * p.q_sb + (head0 + a) * p.q_sh + d] : 0.f;
+    }
+    qs = queries;
+    ps = queries + HT * D + (threadIdx.x >> 5) * kPs;
+#pragma unroll
+    for (int a = 0; a < HT; ++a) {
+      m[a] = -INFINITY, l[a] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) o[a][i] = 0.f;
+    }
+    __syncthreads();
+  }
+
+  // One token's V columns of this lane.
+  static __device__ __forceinline__ void value(const uint8_t* v, int token, int lane, float (&x)[kCols]) {
+    if constexpr (kCols == 2) {
+      const float2 y = *reinterpret_cast<const float2*>(v + tile_offset(token, lane >> 1) + (lane & 1) * 8);
+      x[0] = y.x, x[1] = y.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCols / 4; ++i) {
+        const float4 y = *reinterpret_cast<const float4*>(v + tile_offset(token, lane + 32 * i));
+        x[4 * i] = y.x, x[4 * i + 1] = y.y, x[4 * i + 2] = y.z, x[4 * i + 3] = y.w;
+      }
+    }
+  }
+
+  __device__ __forceinline__ void step(uint32_t kt, uint32_t vt, int live, float scale_log2) {
+    const uint8_t* k = static_cast<const uint8_t*>(__cvta_shared_to_generic(kt));
+    const uint8_t* v = static_cast<const uint8_t*>(__cvta_shared_to_generic(vt));
+    const int lane = threadIdx.x & 31, tok = lane & 7, quarter = lane >> 3;
+    float s[2][HT];
+#pragma unroll
+    for (int a = 0; a < HT; ++a) s[0][a] = s[1][a] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / 16; ++c) {
+      const float4 k0 = *reinterpret_cast<const float4*>(k + tile_offset(tok, 4 * c + quarter));
+      const float4 k1 = *reinterpret_cast<const float4*>(k + tile_offset(tok + 8, 4 * c + quarter));
+#pragma unroll
+      for (int a = 0; a < HT; ++a) {
+        const float4 q = *reinterpret_cast<const float4*>(qs + a * D + (4 * c + quarter) * 4);
+        s[0][a] = fmaf(q.x, k0.x, fmaf(q.y, k0.y, fmaf(q.z, k0.z, fmaf(q.w, k0.w, s[0][a]))));
+        s[1][a] = fmaf(q.x, k1.x, fmaf(q.y, k1.y, fmaf(q.z, k1.z, fmaf(q.w, k1.w, s[1][a]))));
+      }
+    }
+    bool moved = false;
+    float f[HT];
+#pragma unroll
+    for (int a = 0; a < HT; ++a) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        s[x][a] += __shfl_xor_sync(kFullMask, s[x][a], 8);
+        s[x][a] += __shfl_xor_sync(kFullMask, s[x][a], 16);
+        s[x][a] = tok + 8 * x < live ? s[x][a] * scale_log2 : -INFINITY;
+      }
+      float top = fmaxf(s[0][a], s[1][a]);
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, x));
+      const float mn = fmaxf(m[a], top);
+      f[a] = m[a] == -INFINITY ? 0.f : exp2f(m[a] - mn);
+      moved |= mn > m[a];
+      m[a] = mn;
+      const float base = mn == -INFINITY ? 0.f : mn;
+      s[0][a] = exp2f(s[0][a] - base);
+      s[1][a] = exp2f(s[1][a] - base);
+      l[a] = fmaf(l[a], f[a], s[0][a] + s[1][a]);
+    }
+    if (moved) {  // the same in every lane
+#pragma unroll
+      for (int a = 0; a < HT; ++a)
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) o[a][i] *= f[a];
+    }
+    __syncwarp();
+    if (quarter < 2) {  // each writes one of its lanes' two tokens
+#pragma unroll
+      for (int a = 0; a < HT; ++a) ps[(tok + 8 * quarter) * HT + a] = quarter ? s[1][a] : s[0][a];
+    }
+    __syncwarp();
+    auto add = [&](int t) {
+      float x[kCols], w[HT];
+      value(v, t, lane, x);
+      if constexpr (HT % 4 == 0) {
+#pragma unroll
+        for (int a = 0; a < HT; a += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(ps + t * HT + a);
+          w[a] = y.x, w[a + 1] = y.y, w[a + 2] = y.z, w[a + 3] = y.w;
+        }
+      } else {
+#pragma unroll
+        for (int a = 0; a < HT; ++a) w[a] = ps[t * HT + a];
+      }
+#pragma unroll
+      for (int a = 0; a < HT; ++a)
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) o[a][i] = fmaf(w[a], x[i], o[a][i]);
+    };
+    if (live == 16) {
+#pragma unroll 8
+      for (int t = 0; t < 16; ++t) add(t);
+    } else {
+      for (int t = 0; t < live; ++t) add(t);  // rows behind the context may hold anything
+    }
+  }
+
+  __device__ __forceinline__ void store(Partial<D, HT>& out, int) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int a = 0; a < HT; ++a) {
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) l[a] += __shfl_xor_sync(kFullMask, l[a], x);
+      if (lane == 0) out.m[a] = m[a], out.l[a] = l[a];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) out.o[a][kCols == 2 ? lane * 2 + i : (lane + 32 * (i >> 2)) * 4 + (i & 3)] = o[a][i];
+    }
+  }
+};
+
+template <typename T, bool F8, int D, int HT>
+struct SparseMath {
+  using type = MmaMath<T, F8, D, HT>;
+};
+template <int D, int HT>
+struct SparseMath<float, false, D, HT> {
+  using type = FmaMath<D, HT>;
+};
+
+// --- the kernel -------------------------------------------------------------------
+// T: query and output type; F8: the caches hold E4M3 codes.
 template <typename T, bool F8, int D, int HT>
 __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, uint8_t, T>::type, D>::kWarps * 32))
-    sparse_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                      const SparseParams p) {
+    sparse_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const SparseParams p) {
   using B = typename std::conditional<F8, uint8_t, T>::type;
-  using M = typename std::conditional<F8, __half, T>::type;
   using G = Geom<B, D>;
   using Tune = SparseTuning<B, D>;
+  using Math = typename SparseMath<T, F8, D, HT>::type;
   constexpr int kWarps = Tune::kWarps, kStages = Tune::kStages;
-  constexpr int kNT = HT / 8;                           // tiles of 8 heads
-  constexpr int kKS = D / 16;                           // k16 steps over head_dim
   static_assert(sizeof(Partial<D, HT>) <= Tune::kRing, "a warp's partial takes its ring's place");
 
   cg::cluster_group cluster = cg::this_cluster();
@@ -205,7 +522,7 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
   const int tile = static_cast<int>(row % p.num_head_tiles);
   row /= p.num_head_tiles;
   const int h = static_cast<int>(row % p.num_kv_heads), b = static_cast<int>(row / p.num_kv_heads);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int heads = min(HT, p.group - tile * HT);
   const int head0 = h * p.group + tile * HT;
 
@@ -213,7 +530,8 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
   uint8_t* raw = unaligned + ((1024 - (smem_u32(unaligned) & 1023)) & 1023);  // swizzled boxes start at 1024 bytes
   uint8_t* ring = raw + warp * Tune::kRing;
   float* scratch = reinterpret_cast<float*>(raw + kWarps * Tune::kRing);  // [HT][8]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(scratch + HT * 8) + warp * kStages;
+  float* queries = scratch + HT * 8;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(queries) + Math::kQueryBytes) + warp * kStages;
   if (lane < kStages) mbar_init(smem_u32(&bars[lane]), 1);
   fence_mbar_init();
   if (lane == 0) tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
@@ -258,38 +576,8 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
   for (int s = 0; s < kStages; ++s)
     if (to_copy) copy();
 
-  // Q fragments: head 8a + g; elements 16s + 2c (+8) of 16-bit rows, 16s + 4c (+2) where codes are widened
-  uint32_t qf[kNT][kKS][2];
-#pragma unroll
-  for (int a = 0; a < kNT; ++a)
-#pragma unroll
-    for (int s = 0; s < kKS; ++s)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t x = 0u;
-        if (8 * a + g < heads) {
-          const int d = F8 ? 16 * s + 4 * c + 2 * e : 16 * s + 2 * c + 8 * e;
-          const T* q = static_cast<const T*>(p.q) + b * p.q_sb + (head0 + 8 * a + g) * p.q_sh + d;
-          if (p.q_pairs) {
-            x = *reinterpret_cast<const uint32_t*>(q);
-          } else {
-            const uint16_t lo = *reinterpret_cast<const uint16_t*>(q), hi = *reinterpret_cast<const uint16_t*>(q + 1);
-            x = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-          }
-          if constexpr (F8) x = to_f16x2<T>(x);
-        }
-        qf[a][s][e] = x;
-      }
-
-  float m[kNT], l[kNT], o[kKS][kNT][4];
-#pragma unroll
-  for (int a = 0; a < kNT; ++a) m[a] = -INFINITY, l[a] = 0.f;
-#pragma unroll
-  for (int t = 0; t < kKS; ++t)
-#pragma unroll
-    for (int a = 0; a < kNT; ++a)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][a][e] = 0.f;
+  Math math;
+  math.load_q(p, queries, b, head0, heads);
 
   int stage = 0;
   uint32_t phase = 0u;  // of every stage, turned when the ring comes round
@@ -307,107 +595,7 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
         break;
       }
       const uint32_t kt = smem_u32(ring + stage * Tune::kStage), vt = kt + G::kTileBytes;
-      // S = Q K^T, tokens 0-7 and 8-15
-      float s[2][4];
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[half][e] = 0.f;
-      // chunks of four steps first, then their products
-      constexpr int kGroup = kKS < 4 ? kKS : 4;
-#pragma unroll
-      for (int s0 = 0; s0 < kKS; s0 += kGroup) {
-        uint32_t bf[kGroup][2][2];  // [step][half]
-        if constexpr (F8) {
-          const int k_row = (lane & 7) + (((lane >> 3) & 1) << 3), k_chunk = lane >> 4;
-          uint32_t r[kGroup / 2][4];  // tokens 0-7 and 8-15 of a chunk, then of the next
-#pragma unroll
-          for (int x = 0; x < kGroup / 2; ++x) ldsm_x4(kt + code_offset<D>(k_row, s0 + 2 * x + k_chunk), r[x]);
-#pragma unroll
-          for (int i = 0; i < kGroup; ++i)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) e4m3x4_to_f16x2x2(r[i >> 1][2 * (i & 1) + half], bf[i][half][0], bf[i][half][1]);
-        } else {
-          const int k_row = (lane & 7) + ((lane >> 4) << 3), k_chunk = (lane >> 3) & 1;
-#pragma unroll
-          for (int i = 0; i < kGroup; ++i) {
-            uint32_t r[4];  // chunks 2 step and 2 step + 1 of tokens 0-7, then of tokens 8-15
-            ldsm_x4(kt + tile_offset(k_row, 2 * (s0 + i) + k_chunk), r);
-            bf[i][0][0] = r[0], bf[i][0][1] = r[1], bf[i][1][0] = r[2], bf[i][1][1] = r[3];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-          const uint32_t af[4] = {qf[0][s0 + i][0], kNT > 1 ? qf[kNT - 1][s0 + i][0] : 0u, qf[0][s0 + i][1],
-                                  kNT > 1 ? qf[kNT - 1][s0 + i][1] : 0u};
-          Mma<M>::run(s[0], af, bf[i][0]);
-          Mma<M>::run(s[1], af, bf[i][1]);
-        }
-      }
-      // weights: head 8a + g, tokens 2c, 2c + 1 of both halves
-      uint32_t pf[kNT][2];
-#pragma unroll
-      for (int a = 0; a < kNT; ++a) {
-        float x[4];
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            x[2 * half + e] = 8 * half + 2 * c + e < live ? s[half][2 * a + e] * p.scale_log2 : -INFINITY;
-        float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-        const float mn = fmaxf(m[a], top);
-        if (__any_sync(kFullMask, mn > m[a])) {
-          const float f = m[a] == -INFINITY ? 0.f : exp2f(m[a] - mn);
-          l[a] *= f;
-          m[a] = mn;
-          const float f0 = __shfl_sync(kFullMask, f, 8 * c), f1 = __shfl_sync(kFullMask, f, 8 * c + 4);
-#pragma unroll
-          for (int t = 0; t < kKS; ++t) {
-            o[t][a][0] *= f0, o[t][a][1] *= f1, o[t][a][2] *= f0, o[t][a][3] *= f1;
-          }
-        }
-        const float base = m[a] == -INFINITY ? 0.f : m[a];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          pf[a][half] = Mma<M>::pack(ex2_approx(x[2 * half] - base), ex2_approx(x[2 * half + 1] - base));
-          const M* w = reinterpret_cast<const M*>(&pf[a][half]);
-          l[a] += to_f32(w[0]) + to_f32(w[1]);
-        }
-      }
-      // O^T += V^T P^T; V rows behind the context are zeroed (they may hold anything)
-      const bool tail = live < 16;
-      const uint32_t keep_lo = (2 * c < live ? 0x0000ffffu : 0u) | (2 * c + 1 < live ? 0xffff0000u : 0u);
-      const uint32_t keep_hi = (2 * c + 8 < live ? 0x0000ffffu : 0u) | (2 * c + 9 < live ? 0xffff0000u : 0u);
-      const int v_row = F8 ? (lane & 7) + (((lane >> 3) & 1) << 3) : (lane & 7) + ((lane >> 4) << 3);
-      const int v_chunk = F8 ? lane >> 4 : (lane >> 3) & 1;
-#pragma unroll
-      for (int t0 = 0; t0 < kKS; t0 += kGroup) {
-        uint32_t af[kGroup][4];
-        if constexpr (F8) {
-          uint32_t r[kGroup / 2][4];  // tokens 0-7 and 8-15 of a chunk, then of the next
-#pragma unroll
-          for (int x = 0; x < kGroup / 2; ++x) ldsm_x4_trans(vt + code_offset<D>(v_row, t0 + 2 * x + v_chunk), r[x]);
-#pragma unroll
-          for (int i = 0; i < kGroup; ++i) {
-            // bytes (t, e), (t, e+1), (t+1, e), (t+1, e+1) -> (t, e), (t+1, e), (t, e+1), (t+1, e+1)
-            e4m3x4_to_f16x2x2(__byte_perm(r[i >> 1][2 * (i & 1)], 0u, 0x3120), af[i][0], af[i][1]);
-            e4m3x4_to_f16x2x2(__byte_perm(r[i >> 1][2 * (i & 1) + 1], 0u, 0x3120), af[i][2], af[i][3]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < kGroup; ++i) ldsm_x4_trans(vt + tile_offset(v_row, 2 * (t0 + i) + v_chunk), af[i]);
-        }
-        if (tail) {
-#pragma unroll
-          for (int i = 0; i < kGroup; ++i) af[i][0] &= keep_lo, af[i][1] &= keep_lo, af[i][2] &= keep_hi, af[i][3] &= keep_hi;
-        }
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i)
-#pragma unroll
-          for (int a = 0; a < kNT; ++a) Mma<M>::run(o[t0 + i][a], af[i], pf[a]);
-      }
+      math.step(kt, vt, live, p.scale_log2);
       __syncwarp();  // every lane has read the stage
       if (to_copy) copy();
       if (++stage == kStages) stage = 0, phase ^= 1u;
@@ -421,169 +609,11 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
       if (to_copy) copy();
   }
 
-  // this warp's partial in the place of its ring: heads 8a + 2c, 8a + 2c + 1
-  Partial<D, HT>& out = *reinterpret_cast<Partial<D, HT>*>(ring);
-#pragma unroll
-  for (int a = 0; a < kNT; ++a) {
-    l[a] += __shfl_xor_sync(kFullMask, l[a], 1);
-    l[a] += __shfl_xor_sync(kFullMask, l[a], 2);
-    if (c == 0) {
-      out.m[8 * a + g] = m[a];
-      out.l[8 * a + g] = l[a];
-    }
-#pragma unroll
-    for (int t = 0; t < kKS; ++t) {
-      if constexpr (F8) {  // rows g and g + 8 are elements 16t + 2g and 16t + 2g + 1
-        const int d = 16 * t + 2 * g;
-        *reinterpret_cast<float2*>(&out.o[8 * a + 2 * c][d]) = make_float2(o[t][a][0], o[t][a][2]);
-        *reinterpret_cast<float2*>(&out.o[8 * a + 2 * c + 1][d]) = make_float2(o[t][a][1], o[t][a][3]);
-      } else {
-        const int d = 16 * t + g;
-        out.o[8 * a + 2 * c][d] = o[t][a][0];
-        out.o[8 * a + 2 * c + 1][d] = o[t][a][1];
-        out.o[8 * a + 2 * c][d + 8] = o[t][a][2];
-        out.o[8 * a + 2 * c + 1][d + 8] = o[t][a][3];
-      }
-    }
-  }
+  math.store(*reinterpret_cast<Partial<D, HT>*>(ring), lane);  // in the place of the ring
   if (threadIdx.x == 0 && rank == 0 && h == 0 && tile == 0 && (*len_at < 0 || *len_at > p.max_tokens))
     atomicOr(p.err, kErrLen);
   merge_and_store<T, D, HT, kWarps>(p, cluster, raw, Tune::kRing, scratch, static_cast<T*>(p.out) + b * p.o_sb + head0 * p.o_sh,
                                     heads);
-}
-
-// --- f32 kernel ------------------------------------------------------------------
-// A warp takes 8 tokens (half a unit) at a time: lane (g, c) holds row g's
-// chunks 4i + c for the products with the tile's 8 query heads (in shared
-// memory), the four lanes of a row sum; then lane owns dims lane + 32i of V.
-constexpr int kF32Warps = 4;
-
-template <int D>
-__global__ void __launch_bounds__(kF32Warps * 32) sparse_f32_kernel(const SparseParams p) {
-  constexpr int HT = 8, kRow = D * 4, kChunks = D / 16;
-  grid_wait();
-  grid_launch_dependents();
-  cg::cluster_group cluster = cg::this_cluster();
-  const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-  int64_t row = static_cast<int64_t>(blockIdx.x) / ctas;
-  const int tile = static_cast<int>(row % p.num_head_tiles);
-  row /= p.num_head_tiles;
-  const int h = static_cast<int>(row % p.num_kv_heads), b = static_cast<int>(row / p.num_kv_heads);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const int heads = min(HT, p.group - tile * HT);
-  const int head0 = h * p.group + tile * HT;
-
-  extern __shared__ __align__(16) uint8_t raw[];
-  Partial<D, HT>* part = reinterpret_cast<Partial<D, HT>*>(raw);
-  float* qs = reinterpret_cast<float*>(part + kF32Warps);             // [HT][D]
-  float* ps = qs + HT * D + warp * 64;                                   // [8 tokens][HT] weights of this warp
-  float* scratch = qs + HT * D + kF32Warps * 64;                         // [HT][8]
-
-  const int32_t* len_at = p.context_lens + b;
-  const int32_t* list = p.selected + b * p.sel_sb + h * p.sel_sh;
-  const int32_t* table = p.block_tables + b * p.bt_stride;
-  for (int i = threadIdx.x; i < HT * D; i += kF32Warps * 32) {
-    const int a = i / D, d = i - a * D;
-    qs[i] = a < heads ? static_cast<const float*>(p.q)[b * p.q_sb + (head0 + a) * p.q_sh + d] : 0.f;
-  }
-  __syncthreads();
-
-  float m[HT], l[HT], o[HT][D / 32];
-#pragma unroll
-  for (int a = 0; a < HT; ++a) {
-    m[a] = -INFINITY, l[a] = 0.f;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[a][i] = 0.f;
-  }
-  const int64_t units = units_of(p);
-  const int stride = ctas * kF32Warps;
-  for (int64_t u0 = rank * kF32Warps + warp; u0 < units; u0 += 32LL * stride) {
-    Unit mine{0, 0, 0};
-    if (u0 + int64_t(lane) * stride < units) mine = find_unit(p, list, table, len_at, u0 + int64_t(lane) * stride);
-    unsigned todo = __ballot_sync(kFullMask, mine.live > 0);
-    while (todo) {
-      const int from = __ffs(todo) - 1;
-      todo &= todo - 1;
-      const int phys = __shfl_sync(kFullMask, mine.phys, from), off = __shfl_sync(kFullMask, mine.off, from);
-      const int all = __shfl_sync(kFullMask, mine.live, from);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int live = min(8, all - 8 * half);
-        const int64_t at = (((static_cast<int64_t>(phys) * p.num_kv_heads + h) << p.log2_bs) + off + 8 * half) * kRow;
-        if (live <= 0) continue;
-        float4 kx[kChunks];
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i)
-          kx[i] = g < live ? __ldg(reinterpret_cast<const float4*>(p.k_cache + at + g * kRow + (4 * i + c) * 16))
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-        float s[HT];
-#pragma unroll
-        for (int a = 0; a < HT; ++a) {
-          float x = 0.f;
-#pragma unroll
-          for (int i = 0; i < kChunks; ++i) {
-            const float4 q = *reinterpret_cast<const float4*>(qs + a * D + (4 * i + c) * 4);
-            x = fmaf(q.x, kx[i].x, fmaf(q.y, kx[i].y, fmaf(q.z, kx[i].z, fmaf(q.w, kx[i].w, x))));
-          }
-          x += __shfl_xor_sync(kFullMask, x, 1);
-          x += __shfl_xor_sync(kFullMask, x, 2);
-          s[a] = g < live ? x * p.scale_log2 : -INFINITY;
-        }
-#pragma unroll
-        for (int a = 0; a < HT; ++a) {
-          float top = s[a];
-#pragma unroll
-          for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, k));
-          const float mn = fmaxf(m[a], top);
-          const float f = m[a] == -INFINITY ? 0.f : exp2f(m[a] - mn);
-          m[a] = mn;
-          l[a] *= f;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) o[a][i] *= f;
-          s[a] = exp2f(s[a] - (mn == -INFINITY ? 0.f : mn));
-          if (c == 0) l[a] += s[a];
-        }
-        __syncwarp();
-        if (c == 0) {
-#pragma unroll
-          for (int a = 0; a < HT; ++a) ps[g * HT + a] = s[a];
-        }
-        __syncwarp();
-#pragma unroll 4
-        for (int t = 0; t < 8; ++t) {
-          if (t >= live) break;
-          float w[HT];
-#pragma unroll
-          for (int a = 0; a < HT; a += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(ps + t * HT + a);
-            w[a] = x.x, w[a + 1] = x.y, w[a + 2] = x.z, w[a + 3] = x.w;
-          }
-          const float* src = reinterpret_cast<const float*>(p.v_cache + at + t * kRow);
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const float v = __ldg(src + lane + 32 * i);
-#pragma unroll
-            for (int a = 0; a < HT; ++a) o[a][i] = fmaf(w[a], v, o[a][i]);
-          }
-        }
-      }
-    }
-  }
-  Partial<D, HT>& out = part[warp];
-#pragma unroll
-  for (int a = 0; a < HT; ++a) {
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) l[a] += __shfl_xor_sync(kFullMask, l[a], k);
-    if (lane == 0) {
-      out.m[a] = m[a];
-      out.l[a] = l[a];
-    }
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) out.o[a][lane + 32 * i] = o[a][i];
-  }
-  if (threadIdx.x == 0 && rank == 0 && h == 0 && tile == 0 && (*len_at < 0 || *len_at > p.max_tokens))
-    atomicOr(p.err, kErrLen);
-  merge_and_store<float, D, HT, kF32Warps>(p, cluster, raw, sizeof(Partial<D, HT>), scratch, static_cast<float*>(p.out) + b * p.o_sb + head0 * p.o_sh, heads);
 }
 
 // CTAs of a list: as many as run at once (`resident` an SM), but no warp under
@@ -603,38 +633,46 @@ dim3 grid_of(const SparseParams& p, int ctas) {
 }
 
 template <typename T, bool F8, int D, int HT>
-int launch_mma(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparseParams& p, int num_sms, cudaStream_t stream) {
+int launch_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparseParams& p, int num_sms, cudaStream_t stream) {
   using Tune = SparseTuning<typename std::conditional<F8, uint8_t, T>::type, D>;
   static std::atomic<int> configured[64];
-  constexpr size_t smem = 1024 + Tune::kWarps * (Tune::kRing + Tune::kStages * sizeof(uint64_t)) + HT * 8 * sizeof(float);
-  const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_mma_kernel<T, F8, D, HT>),
+  constexpr size_t smem = 1024 + Tune::kWarps * (Tune::kRing + Tune::kStages * sizeof(uint64_t)) + HT * 8 * sizeof(float) +
+                          SparseMath<T, F8, D, HT>::type::kQueryBytes;
+  const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_kernel<T, F8, D, HT>),
                                  static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int ctas = cluster_size(p, Tune::kWarps, static_cast<int>(227 * 1024 / (smem + 1024)), num_sms);
-  return launch_dependent(&sparse_mma_kernel<T, F8, D, HT>, grid_of(p, ctas), dim3(Tune::kWarps * 32), smem, ctas, stream,
+  static std::atomic<int> resident{0};  // CTAs an SM, by registers and shared memory
+  int blocks = resident.load(std::memory_order_relaxed);
+  if (blocks == 0) {
+    const cudaError_t err =
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, &sparse_kernel<T, F8, D, HT>, Tune::kWarps * 32, smem);
+    if (err != cudaSuccess) return err;
+    resident.store(blocks, std::memory_order_relaxed);
+  }
+  const int ctas = cluster_size(p, Tune::kWarps, blocks, num_sms);
+  return launch_dependent(&sparse_kernel<T, F8, D, HT>, grid_of(p, ctas), dim3(Tune::kWarps * 32), smem, ctas, stream,
                           kmap, vmap, p);
 }
 
-template <int D>
-int launch_f32(const SparseParams& p, int num_sms, cudaStream_t stream) {
-  static std::atomic<int> configured[64];
-  constexpr size_t smem = sizeof(Partial<D, 8>) * kF32Warps + (8 * D + 64 * kF32Warps + 64) * sizeof(float);
-  const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_f32_kernel<D>), static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  const int ctas = cluster_size(p, kF32Warps, 3, num_sms);
-  return launch_dependent(&sparse_f32_kernel<D>, grid_of(p, ctas), dim3(kF32Warps * 32), smem, ctas, stream, p);
+template <int HT>
+int launch_f32(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparseParams& p, int head_dim, int num_sms,
+               cudaStream_t stream) {
+  if (head_dim == 64) return launch_tile<float, false, 64, HT>(kmap, vmap, p, num_sms, stream);
+  if (head_dim == 128) return launch_tile<float, false, 128, HT>(kmap, vmap, p, num_sms, stream);
+  if (head_dim == 256) return launch_tile<float, false, 256, HT>(kmap, vmap, p, num_sms, stream);
+  return cudaErrorInvalidValue;
 }
 
 template <typename T, bool F8>
 int launch_dim(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparseParams& p, int head_dim, int head_tile,
                int num_sms, cudaStream_t stream) {
   if (head_dim == 64)
-    return head_tile == 16 ? launch_mma<T, F8, 64, 16>(kmap, vmap, p, num_sms, stream)
-                           : launch_mma<T, F8, 64, 8>(kmap, vmap, p, num_sms, stream);
+    return head_tile == 16 ? launch_tile<T, F8, 64, 16>(kmap, vmap, p, num_sms, stream)
+                           : launch_tile<T, F8, 64, 8>(kmap, vmap, p, num_sms, stream);
   if (head_dim == 128)
-    return head_tile == 16 ? launch_mma<T, F8, 128, 16>(kmap, vmap, p, num_sms, stream)
-                           : launch_mma<T, F8, 128, 8>(kmap, vmap, p, num_sms, stream);
-  if (head_dim == 256) return launch_mma<T, F8, 256, 8>(kmap, vmap, p, num_sms, stream);
+    return head_tile == 16 ? launch_tile<T, F8, 128, 16>(kmap, vmap, p, num_sms, stream)
+                           : launch_tile<T, F8, 128, 8>(kmap, vmap, p, num_sms, stream);
+  if (head_dim == 256) return launch_tile<T, F8, 256, 8>(kmap, vmap, p, num_sms, stream);
   return cudaErrorInvalidValue;
 }
 
@@ -642,14 +680,15 @@ int launch_dim(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparsePar
 
 int launch_sparse_decode(int dtype, bool kv_fp8, int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap,
                          SparseParams p, int num_sms, cudaStream_t stream) {
-  // two tiles of 8 query heads share the K/V fragments where registers allow
-  const int head_tile = dtype != 0 && p.group > 8 && head_dim <= 128 ? 16 : 8;
+  // two tiles of 8 query heads share the K/V fragments where registers allow;
+  // binary32 products are not made for heads that are not there
+  const int head_tile = dtype == 0 ? (p.group == 1 ? 1 : p.group <= 4 ? 4 : 8) : p.group > 8 && head_dim <= 128 ? 16 : 8;
   p.num_head_tiles = (p.group + head_tile - 1) / head_tile;
   int e = cudaErrorInvalidValue;
   if (dtype == 0 && !kv_fp8) {
-    e = head_dim == 64    ? launch_f32<64>(p, num_sms, stream)
-        : head_dim == 128 ? launch_f32<128>(p, num_sms, stream)
-                          : launch_f32<256>(p, num_sms, stream);
+    e = head_tile == 1   ? launch_f32<1>(kmap, vmap, p, head_dim, num_sms, stream)
+        : head_tile == 4 ? launch_f32<4>(kmap, vmap, p, head_dim, num_sms, stream)
+                         : launch_f32<8>(kmap, vmap, p, head_dim, num_sms, stream);
   } else if (dtype == 1) {
     e = kv_fp8 ? launch_dim<__half, true>(kmap, vmap, p, head_dim, head_tile, num_sms, stream)
                : launch_dim<__half, false>(kmap, vmap, p, head_dim, head_tile, num_sms, stream);
