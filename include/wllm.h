@@ -346,9 +346,10 @@ int wllm_paged_attention_decode_noalloc(const wllm_tensor* out, const wllm_tenso
  *
  * None of them allocates, uses the device workspace or waits on the host, and
  * their results do not depend on the order in which threads run; all can be
- * captured in a CUDA graph.  Calls on one stream that follow one another see
+ * captured in a CUDA graph (after the library's first call on the device, which
+ * allocates its error word).  Calls on one stream that follow one another see
  * each other's results; calls on different streams share nothing but the
- * tensors that the caller gives them.
+ * tensors that the caller gives them and the device error word.
  * ------------------------------------------------------------------------- */
 
 typedef enum {

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const Bou
   int64_t units = p.num_seqs;
   if (p.query_start_loc != nullptr) {
     const int total = p.query_start_loc[p.num_seqs];
-    if (total < 0) {
+    if (total < 0 || total > int64_t(p.num_seqs) * p.max_tokens) {  // more new tokens than the tables can name
       if (gw == 0 && lane == 0) atomicOr(p.err, kErrLen);
       return;
     }

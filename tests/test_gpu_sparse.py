@@ -79,6 +79,8 @@ def test_bounds_record_bad_lengths_and_blocks(monkeypatch):
     assert torch.equal(S.values(got), ref)
     got = run_bounds(kb, kc, bt, i32(lens), i32([0, 40, 30, 31]))  # more new tokens than cached ones, a step back, one
     assert wllm.device_errors() == 4
+    got = run_bounds(kb, kc, bt, i32(lens), i32([0, 0, 0, 10 ** 9]))  # more than the tables can name
+    assert wllm.device_errors() == 4 and torch.equal(H.bits(got), H.bits(kb))
     monkeypatch.setenv("WLLM_CHECK", "1")
     with pytest.raises(wllm.WllmError, match="0x4"):
         run_bounds(kb, kc, bt, i32([32, 48, -1]))
