@@ -28,7 +28,7 @@ LIB = os.path.join(PKG, "libwllm.so")
 DESCRIBE = os.path.join(PKG, "_describe.so")
 
 SOURCES = ["api.cu", "append.cu", "decode_bf16.cu", "decode_f16.cu", "decode_f32.cu", "decode_f8_f16.cu",
-           "decode_f8_bf16.cu", "prefill.cu", "prefill_tc.cu", "block_manager.cpp", "api_sparse.cu", "rotate.cu", "key_bounds.cu", "select.cu",
+           "decode_f8_bf16.cu", "prefill.cu", "prefill_tc.cu", "block_manager.cpp", "api_sparse.cu", "rotate.cu", "rotate_f32.cu", "rotate_f16.cu", "rotate_bf16.cu", "key_bounds.cu", "select.cu",
            "sparse_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -177,6 +177,7 @@ int launch_prefill_tc(int dtype, int head_dim, const CUtensorMap& kmap, const CU
 // The rotary append (rotate.cu): norms, rotary positions, query out, key and
 // value to their slots.  Strides in elements.
 constexpr int kMaxRotaryAxes = 4;
+constexpr int kRotateWarps = 4;  // warps of a CTA of the form for few tokens
 struct RotateParams {
   void* q_out;
   const void* q;

@@ -146,6 +146,15 @@ def test_rotate_a_thousand_tokens(dtype, cache, Hq, Hkv, D, R, style, sections, 
     assert wllm.device_errors() == 0
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,D,dtype,cache", [
+    (270, 28, 4, 128, BF, BF), (271, 28, 4, 128, BF, BF), (410, 32, 8, 64, F16, U8), (160, 32, 16, 128, F32, F32),
+    (1220, 4, 1, 128, BF, BF), (151, 128, 8, 128, F16, F16), (153, 128, 8, 128, F16, F16), (300, 16, 16, 80, F32, U8)])
+def test_rotate_where_the_resident_form_begins(T, Hq, Hkv, D, dtype, cache):
+    """Token counts about the first that the resident form takes, with norms whose weights are binary32."""
+    a = make(T, Hq, Hkv, D, D // 32 * 16, 16, dtype, cache, weights=F32, seed=5)
+    check(a, call(a))
+
+
 def test_rotate_a_thousand_tokens_strided_in_place_and_bad():
     T, Hq, Hkv, D = 1500, 6, 2, 64
     a = make(T, Hq, Hkv, D, 64, 16, BF, BF, weights=BF, pad=20, index=torch.int32)
