@@ -10,7 +10,9 @@
 // contiguous run; a lane owns one 16-byte column and the warp reads 512
 // contiguous bytes a load, so a row takes D*elt/16 lanes and the lanes above
 // that take further rows, met by shuffles at the end.  Bound: memory, each key
-// is read once and a bs/2-th of it written.
+// is read once and a bs/2-th of it written.  16 chunks of 2048 tokens, 8 kv heads
+// of 128, bf16 (75 MB): 14.7 us, 0.75 of the measured copy rate; a call
+// that fills 17 blocks, all latency, takes 2.0 us.
 #include "common.cuh"
 #include "launch.h"
 

@@ -15,12 +15,12 @@
 // pairs (8-element chunks c and c + R/16 of a row whose halves pair, chunks 2c
 // and 2c + 1 otherwise), so a turn needs no exchange between lanes and the sum
 // of squares log2(D/16) shuffles.  A warp holds 32 / (D/16) rows at a time.
-// Many tokens: CTAs of two warps stay resident and the next token's rows and
+// Many tokens: CTAs of two or four warps stay resident and the next token's rows and
 // table rows come by bulk copies into the other of two buffers meanwhile; a
 // token's factors (cos, sin, weights) are computed once for its rows.  Few
 // tokens: their rows are spread over warps, a step or two each.  The bound is
 // memory, every value is read once and written once; 8192 tokens of 28/4 heads
-// of 128, bf16, norms, three axes (155 MB): 27.9 us, 0.82 of the measured copy
+// of 128, bf16, norms, three axes (155 MB): 27.7 us, 0.82 of the measured copy
 // rate.  Instructions decide, not the copies: with lanes and bounds known only at
 // run time, weights read from global memory for every token and the step loop not
 // unrolled, the same copies took 33.5 us.
@@ -36,8 +36,7 @@
 namespace wllm {
 namespace {
 
-constexpr int kRingWarps = 2;
-constexpr int kRingBlocks = 8;    // CTAs an SM; 1 warp and 16 CTAs take 28.9 us on those 8192 tokens, 3 and 5 29.8, 4 and 4 33.6
+constexpr int kRingThreads = 128;  // at most; 128 registers a thread let an SM hold 4 CTAs of as many, or 8 of half
 
 // Eight elements of a row as floats, or moved as they are.
 template <typename T, bool VEC>
@@ -411,10 +410,10 @@ __global__ void __launch_bounds__(kRotateWarps * 32, 4) rotate_kernel(const Rota
 // warps share a token's steps.  Buffer: query rows, key rows, value rows, one
 // table row an axis.
 template <typename T, bool F8, bool ADJACENT, int LANES>
-__global__ void __launch_bounds__(kRingWarps * 32, kRingBlocks) rotate_ring_kernel(const RotateParams p) {
+__global__ void __launch_bounds__(kRingThreads, 4) rotate_ring_kernel(const RotateParams p) {
   extern __shared__ __align__(128) uint8_t raw[];
   __shared__ __align__(8) uint64_t bars[2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;  // 2 or 4 warps
   const uint32_t row_bytes = p.head_dim * sizeof(T), table_bytes = p.rot_dim * sizeof(float);
   const uint32_t q_bytes = p.num_q_heads * row_bytes, kv_bytes = p.num_kv_heads * row_bytes;
   const uint32_t buffer_bytes = q_bytes + 2 * kv_bytes + p.num_axes * table_bytes;
@@ -424,7 +423,7 @@ __global__ void __launch_bounds__(kRingWarps * 32, kRingBlocks) rotate_ring_kern
   grid_launch_dependents();
   // the norms' weights in binary32, behind the buffers
   float* weights = reinterpret_cast<float*>(raw + 2 * buffer_bytes);
-  for (int i = threadIdx.x; i < p.head_dim / 4; i += kRingWarps * 32) {  // 8 elements of q's, then of k's
+  for (int i = threadIdx.x; i < p.head_dim / 4; i += blockDim.x) {  // 8 elements of q's, then of k's
     const void* w = i < p.head_dim / 8 ? p.q_weight : p.k_weight;
     float f[8];
     if (w != nullptr) {
@@ -525,14 +524,14 @@ __global__ void __launch_bounds__(kRingWarps * 32, kRingBlocks) rotate_ring_kern
       };
       factors_of(math, false);
 #pragma unroll 2
-      for (int s = warp; s < steps_q; s += kRingWarps) {
+      for (int s = warp; s < steps_q; s += warps) {
         const int r = s * rows_per_step + math.sub;
         load(buf, r, p.num_q_heads);
         math.turn(u, v, p.q_weight != nullptr, a, b);
         math.store_q(t, r, a, b);
       }
       bool fresh = p.k_weight == p.q_weight;
-      for (int i = (warp + kRingWarps - steps_q % kRingWarps) % kRingWarps; i < 2 * steps_kv; i += kRingWarps) {
+      for (int i = (warp - steps_q) & (warps - 1); i < 2 * steps_kv; i += warps) {
         const int r = (i >> 1) * rows_per_step + math.sub;
         if (i & 1) {
           load(buf + q_bytes + kv_bytes, r, p.num_kv_heads);
@@ -561,11 +560,21 @@ int launch_ring(const RotateParams& p, int smem, int num_sms, cudaStream_t strea
   static std::atomic<int> configured[64];
   const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&rotate_ring_kernel<T, F8, ADJACENT, LANES>), smem);
   if (e != cudaSuccess) return e;
-  // as many CTAs as shared memory lets be resident (228 KB an SM, 1 KB of it the system's in each CTA)
-  const int64_t resident = int64_t(num_sms) * std::max(1, std::min(kRingBlocks, 228 * 1024 / (smem + 1024 + 64)));
-  return launch_dependent(&rotate_ring_kernel<T, F8, ADJACENT, LANES>,
-                          dim3(static_cast<unsigned>(std::min<int64_t>(resident, p.num_tokens))), dim3(kRingWarps * 32),
-                          smem, 0, stream, p);
+  // CTAs of 2 warps or of 4, as many as are resident (228 KB an SM, 1 KB of it the system's in each CTA): whichever
+  // takes fewer steps one after another, a token counted as one more.  Measured, us for 2 and 4 warps: 8192 tokens of
+  // 28/4 heads 27.7 and 34.4 (9 steps), 3001 of 32/8 15.1 and 13.7, 1000 of 64/8 14.3 and 12.0, 830 of 4/1 4.0 and 4.7.
+  const int rows_per_step = 32 / p.row_lanes;
+  const int steps = (p.num_q_heads + rows_per_step - 1) / rows_per_step + 2 * ((p.num_kv_heads + rows_per_step - 1) / rows_per_step);
+  const int fit = std::max(1, 228 * 1024 / (smem + 1024 + 64));
+  int64_t grid = 0, least = 0;
+  int warps = 0;
+  for (int w = 2; w <= 4; w += 2) {
+    const int64_t resident = int64_t(num_sms) * std::min(fit, 16 / w);
+    const int64_t serial = (p.num_tokens + resident - 1) / resident * ((steps + w - 1) / w + 1);
+    if (warps == 0 || serial < least) grid = std::min<int64_t>(resident, p.num_tokens), least = serial, warps = w;
+  }
+  return launch_dependent(&rotate_ring_kernel<T, F8, ADJACENT, LANES>, dim3(static_cast<unsigned>(grid)), dim3(warps * 32), smem, 0,
+                          stream, p);
 }
 
 template <typename T, bool F8, bool ADJACENT>

@@ -18,8 +18,7 @@
 // definition's, whatever the order of the sums.
 //
 // 16-bit and E4M3 bounds are scored on tensor cores (mma.sync m16n8k16): 16
-// blocks' bounds are the A operand, straight from global memory, and B's first
-// three columns are the weights split into three 16-bit words whose sum has
+// blocks' bounds are the A operand and B's first three columns are the weights split into three 16-bit words whose sum has
 // their 24 bits, so every product is exact.  An instruction adds 16 products to
 // the running sum; with at least 22 bits kept of each term that is an error of
 // at most 17 * 2^-22 of the magnitudes in it.  Two instructions at a time start
@@ -44,7 +43,12 @@
 // the border (a handful, 8 lanes each) and writes the chosen ones in ascending
 // order: one barrier of the cluster in all, where every step shared by its CTAs
 // would cost another (the first form had six, 10 us of them).  Bound: memory,
-// the bounds are read once.
+// the bounds are read once.  Measured, 8 sequences of 32K to 131K tokens, 8 kv
+// heads of 128, bf16 (176 MB of bounds): 46.4 us, of which a row's CTAs score for
+// 20 us on average and 31 us in the longest row; before that come 5 us of
+// lookups, first copies and weights, after it 6 us of border and list on one CTA.  Pairing the longest row with the
+// shortest in one cluster evens the scores out, but its clusters finish two rows
+// after one another's scores: 47.2 us, and 1.2 us more wherever it does not apply.
 #include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
@@ -898,7 +902,9 @@ int launch_one(SelectParams p, int max_blocks, int num_sms, cudaStream_t stream)
   const size_t smem = select_smem(SelectSize<T, B, D>::kFixed, p.room);
   // CTAs of a row: as many as run at once, so that the work of every CTA besides
   // the scores (weights, barrier, the first copies' latency) is paid once, and
-  // none with less than a turn of its warps
+  // none with less than a turn of its warps.  Measured, us for 1, 2, 4 and 8 CTAs
+  // a row: 64 rows of up to 8192 blocks 94.7, 58.9, 46.4 and 46.7; 256 of up to
+  // 1500 26.9, 32.5, 41.0 and 62.0; 4 of 1000 11.6, 9.2, 8.0 and 8.2.
   const int64_t rows = int64_t(p.num_seqs) * p.num_kv_heads;
   const int64_t resident = int64_t(num_sms) * std::max<int64_t>(1, std::min<int64_t>(2, 227 * 1024 / (smem + 1024)));
   int ctas = 1;
