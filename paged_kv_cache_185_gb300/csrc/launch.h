@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 #include <utility>
 
 namespace wllm {
@@ -34,6 +35,9 @@ inline int raise_smem_limit(std::atomic<int>* configured, const void* func, int 
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool tracked = dev >= 0 && dev < 64;
+  if (tracked && configured[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+  static std::mutex one_at_a_time;  // the limit only grows, whichever thread comes last
+  std::lock_guard<std::mutex> lock(one_at_a_time);
   if (tracked && configured[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
