@@ -429,7 +429,7 @@ int wllm_select_blocks(const wllm_tensor* selected, const wllm_tensor* q, const 
   if (mb > select_max_blocks())
     return fail(WLLM_ERR_UNSUPPORTED, "block tables of %lld blocks not supported (%d at most)", (long long)mb,
                 select_max_blocks());
-  if (hq > 0 && nb < 1) return fail(WLLM_ERR_INVALID_ARG, "the pool has no blocks");
+  if (nb < 1) return fail(WLLM_ERR_INVALID_ARG, "the pool has no blocks");
   if (!aligned(key_bounds->data, 16)) return fail(WLLM_ERR_INVALID_ARG, "key_bounds must be 16-byte aligned");
   if (!aligned(q->data, static_cast<uintptr_t>(elt_size(dt))))
     return fail(WLLM_ERR_INVALID_ARG, "q must be aligned to its element size");

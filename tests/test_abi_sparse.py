@@ -158,6 +158,9 @@ def test_select_refuses(lib):
     assert select(lib, bs=24) == UNSUPPORTED
     assert select(lib, bs=8, mb=200_000) == UNSUPPORTED
     assert select(lib, B=0) == 0
+    # a pool without blocks has nothing that a table entry could be clamped to, with query heads or without
+    for heads in (4, 0):
+        assert select(lib, dict(kb=desc((0, 2, 2, 128), BF, data=None)), Hq=heads) == INVALID
 
 
 def sparse(lib, change=(), B=3, Hq=4, Hkv=2, D=128, bs=16, dt=BF, cache=None, scale=0.1, scales=None, heads=None, size=None):
