@@ -451,7 +451,6 @@ int wllm_select_blocks(const wllm_tensor* selected, const wllm_tensor* q, const 
   p.top = static_cast<int>(top);
   p.sink = num_sink;
   p.recent = num_recent;
-  p.wait_limit_ns = static_cast<unsigned long long>(env_int("WLLM_WAIT_LIMIT_NS", 200000000LL));
   DeviceState* s = nullptr;
   if ((rc = locked_state(&s))) return rc;
   p.err = s->err;

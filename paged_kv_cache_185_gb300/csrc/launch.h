@@ -239,7 +239,6 @@ struct SelectParams {
   int num_seqs, num_kv_heads, group, num_blocks, log2_bs, max_tokens;
   int top, sink, recent;
   int room, longest_first;        // set by launch_select: scores a row has room for; launch order
-  unsigned long long wait_limit_ns;
   int* err;
 };
 int select_max_blocks();
