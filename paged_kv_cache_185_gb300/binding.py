@@ -1,9 +1,9 @@
 """ctypes binding over libwllm.so (C ABI in include/wllm.h).
 
 Argument marshalling only: each call turns torch tensors into ``wllm_tensor``
-descriptors (device pointer, dtype code, sizes, strides in elements; the
-compiled module ``_describe`` fills them), passes
-the current CUDA stream, and raises ``WllmError`` on a non-zero status.  Every
+descriptors (device pointer, dtype code, sizes, strides in elements), passes
+the current CUDA stream (the compiled module ``_describe`` does both), and
+raises ``WllmError`` on a non-zero status.  Every
 step of the computation runs in the library's CUDA kernels; there is no CPU
 path.  Loading fails loudly when the library has not been built.
 """
@@ -59,8 +59,8 @@ _ROTARY_STYLE = {"halves": 0, "adjacent": 1}
 
 
 _lib = None
-_entries = {}    # entry points that take tensors first: name -> function taking descriptor addresses
-_describe = None  # _describe.describe
+_entries = {}   # entry points that take tensors first: name -> what _invoke takes
+_invoke = None  # _describe.call
 _lock = threading.Lock()
 
 
@@ -70,7 +70,7 @@ def library_path() -> str:
 
 def load_library():
     """Load libwllm.so (raises if it is missing: build it with ``build()`` first)."""
-    global _lib, _describe
+    global _lib, _invoke
     if _lib is not None:
         return _lib
     with _lock:
@@ -159,15 +159,11 @@ def load_library():
         lib.wllm_bm_block_ref.argtypes = [vp, i32]
         lib.wllm_bm_block_ref.restype = ctypes.c_int
         from . import _describe as module
-        by_address = ctypes.CDLL(_LIB_PATH)
         for name in EXPORTED:
             f = getattr(lib, name)
             if f.argtypes and f.argtypes[0] is P:
-                g = getattr(by_address, name)
-                g.argtypes = [ctypes.c_void_p if a in (P, how) else a for a in f.argtypes]
-                g.restype = f.restype
-                _entries[name] = g
-        _describe = module.describe
+                _entries[name] = module.bind(name, ctypes.cast(f, ctypes.c_void_p).value)
+        _invoke = module.call
         _lib = lib
     return _lib
 
@@ -186,13 +182,7 @@ def _call(name: str, tensors, *scalars) -> None:
     device.  Host tensors, or tensors of several devices, raise ValueError."""
     if _lib is None:
         load_library()
-    owner, dev, *descriptors = _describe(tensors)  # `owner` holds the descriptors until the call returns
-    f = _entries[name]
-    if dev == torch.cuda.current_device():
-        rc = f(*descriptors, *scalars, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        with torch.cuda.device(dev):
-            rc = f(*descriptors, *scalars, torch._C._cuda_getCurrentRawStream(dev))
+    rc = _invoke(_entries[name], tensors, *scalars)
     if rc != WLLM_OK:
         _check(rc)
 
@@ -268,7 +258,7 @@ def paged_attention_prefill_fp8(out, q, k_cache, v_cache, block_tables, context_
 
 @functools.lru_cache(maxsize=256)
 def _rotary(style, sections, eps):
-    """The options of a rotary call as the C struct's reference (the struct is never written again)."""
+    """The options of a rotary call as a C struct, which is never written again, and its address."""
     if style not in _ROTARY_STYLE:
         raise ValueError(f"style must be one of {sorted(_ROTARY_STYLE)}, got {style!r}")
     if len(sections) > 4:
@@ -276,7 +266,7 @@ def _rotary(style, sections, eps):
     how = WllmRotary(_ROTARY_STYLE[style], max(1, len(sections)))
     how.sections[:len(sections)] = sections
     how.eps = eps
-    return ctypes.byref(how)
+    return how, ctypes.addressof(how)
 
 
 def _rotate(name, tensors, eps, style, sections, scales):
@@ -289,7 +279,8 @@ def _rotate(name, tensors, eps, style, sections, scales):
         sections = tuple(int(n) for n in sections)
         if len(sections) > 1 and positions.dim() == 1:
             raise ValueError("several sections need positions [axes, T]")
-    _call(name, tensors, _rotary(style, sections, float(eps)), *scales)
+    how = _rotary(style, sections, float(eps))  # held until the call returns
+    _call(name, tensors, how[1], *scales)
 
 
 def rotate_and_cache(q_out, q, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, *, q_weight=None,

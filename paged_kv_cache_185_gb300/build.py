@@ -1,5 +1,5 @@
 """Build libwllm.so (the sm_103a CUDA library behind include/wllm.h) and the
-binding's _describe.so (descriptors of torch tensors) in-tree.
+binding's _describe.so (calls with torch tensors) in-tree.
 
     python -m paged_kv_cache_185_gb300.build [--force] [--verbose]
 
@@ -28,8 +28,8 @@ LIB = os.path.join(PKG, "libwllm.so")
 DESCRIBE = os.path.join(PKG, "_describe.so")
 
 SOURCES = ["api.cu", "append.cu", "decode_bf16.cu", "decode_f16.cu", "decode_f32.cu", "decode_f8_f16.cu",
-           "decode_f8_bf16.cu", "prefill.cu", "prefill_tc.cu", "block_manager.cpp", "api_sparse.cu", "rotate.cu", "rotate_f32.cu", "rotate_f16.cu", "rotate_bf16.cu", "key_bounds.cu", "select.cu",
-           "sparse_decode.cu"]
+           "decode_f8_bf16.cu", "prefill.cu", "prefill_tc.cu", "block_manager.cpp", "api_sparse.cu", "rotate.cu",
+           "rotate_f32.cu", "rotate_f16.cu", "rotate_bf16.cu", "key_bounds.cu", "select.cu", "sparse_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -85,7 +85,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
                "-I", sysconfig.get_paths()["include"], "-I", os.path.join(home, "include"),
                "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
-               os.path.join(CSRC, "describe.cpp"), "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+               "-I", os.path.join(os.path.dirname(_cuda_lib_dir(nvcc)), "include"),
+               os.path.join(CSRC, "describe.cpp"), "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
                "-Wl,-rpath," + libs]
         return tmp, subprocess.run(cmd, capture_output=True, text=True)
 
