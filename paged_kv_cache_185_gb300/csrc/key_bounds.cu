@@ -11,7 +11,7 @@
 // contiguous bytes a load, so a row takes D*elt/16 lanes and the lanes above
 // that take further rows, met by shuffles at the end.  Bound: memory, each key
 // is read once and a bs/2-th of it written.  16 chunks of 2048 tokens, 8 kv heads
-// of 128, bf16 (75 MB): 14.7 us, 0.75 of the measured copy rate; a call
+// of 128, bf16 (75 MB): 14.8 us, 0.75 of the measured copy rate; a call
 // that fills 17 blocks, all latency, takes 2.0 us.
 #include "common.cuh"
 #include "launch.h"
@@ -156,31 +156,32 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const Bou
   grid_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kBoundsWarps + (threadIdx.x >> 5);
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kBoundsWarps;
+  const unsigned gw = blockIdx.x * kBoundsWarps + (threadIdx.x >> 5), stride = gridDim.x * kBoundsWarps;
   const int bs = 1 << p.log2_bs;
-  int64_t units = p.num_seqs;
+  int units = p.num_seqs;  // of every head
   if (p.query_start_loc != nullptr) {
     const int total = p.query_start_loc[p.num_seqs];
     if (total < 0 || total > int64_t(p.num_seqs) * p.max_tokens) {  // more new tokens than the tables can name
       if (gw == 0 && lane == 0) atomicOr(p.err, kErrLen);
       return;
     }
-    units = (total >> p.log2_bs) + static_cast<int64_t>(p.num_seqs);
+    units += total >> p.log2_bs;
   }
-  units *= p.num_kv_heads;
-  for (int64_t u = gw; u < units; u += stride) {
-    const int64_t slot = u / p.num_kv_heads;
-    const int h = static_cast<int>(u - slot * p.num_kv_heads);
-    int b = static_cast<int>(slot), n = 1;
-    int64_t j = 0;
+  const unsigned heads = p.num_kv_heads;
+  const int hop = stride / heads, hop_h = stride % heads;
+  for (int slot = gw / heads, h = gw % heads; slot < units; slot += hop, h += hop_h) {
+    if (h >= p.num_kv_heads) {
+      h -= p.num_kv_heads;
+      if (++slot >= units) break;
+    }
+    int b = slot, n = 1, j = 0;
     if (p.query_start_loc != nullptr) {
       // largest b whose first unit is not behind this one: 32 probes at a time
       int lo = 0, hi = p.num_seqs - 1;
       while (lo < hi) {
         const int step = (hi - lo + 31) / 32;
         const int at = lo + (lane + 1) * step;
-        const bool before = at <= hi && (int64_t(p.query_start_loc[at]) >> p.log2_bs) + at <= slot;
+        const bool before = at <= hi && (p.query_start_loc[at] >> p.log2_bs) + at <= slot;
         const int k = __popc(__ballot_sync(kFullMask, before));
         hi = min(hi, lo + (k + 1) * step - 1);
         lo += k * step;
@@ -188,14 +189,14 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const Bou
       b = lo;
       const int first = p.query_start_loc[b];
       n = p.query_start_loc[b + 1] - first;
-      j = slot - ((int64_t(first) >> p.log2_bs) + b);
+      j = slot - ((first >> p.log2_bs) + b);
     }
     const int len = p.context_lens[b];
     if (n < 0 || n > len || len > p.max_tokens || j < 0) {
       if (!(p.query_start_loc == nullptr && len == 0) && lane == 0) atomicOr(p.err, kErrLen);
       continue;  // an empty sequence of the one-token form has no new token
     }
-    const int at = ((len - n) >> p.log2_bs) + static_cast<int>(j);
+    const int at = ((len - n) >> p.log2_bs) + j;
     if (at >= (len >> p.log2_bs)) continue;  // not filled yet
     const int id = p.block_tables[b * p.bt_stride + at];
     if (id < 0 || id >= p.num_blocks) {

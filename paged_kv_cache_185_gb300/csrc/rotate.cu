@@ -18,7 +18,7 @@ int launch_rotate(RotateParams p, int num_sms, cudaStream_t stream) {
                               int64_t(p.num_axes) * p.rot_dim * 4;
   // The resident form where every SM has a token and the tokens' steps, one a warp,
   // no longer fit the SMs at once (16 warps each).  GPU time with norms, spread over
-  // warps and resident: 28/4 heads of 128, bf16: 256 tokens 3.5 and 4.0 us, 280: 5.5
+  // warps and resident: 28/4 heads of 128, bf16: 256 tokens 3.3 and 4.0 us, 280: 5.5
   // and 3.9, 1024: 9.8 and 5.3, 4096: 24.6 and 16.7; 32/8 of 64, f16: 400 tokens
   // (just fitting) 3.4 and 3.7; 128/8 of 128: 100 tokens 5.9 and 6.8.
   const bool many = p.num_tokens >= num_sms && int64_t(p.num_tokens) * steps > int64_t(num_sms) * 16;

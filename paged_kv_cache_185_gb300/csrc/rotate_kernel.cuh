@@ -164,13 +164,16 @@ struct RowMath {
   const RotateParams& p;
   int g, sub, c0, c1, p0;
   bool mine, turns;
-  __device__ __forceinline__ int lanes() const { return LANES > 0 ? LANES : p.row_lanes; }
+  __device__ __forceinline__ int lanes() const { return LANES > 0 ? LANES : p.row_lanes; }  // a power of two
+  __device__ __forceinline__ int lanes_log2() const { return __ffs(lanes()) - 1; }
+  __device__ __forceinline__ int rows_per_step() const { return 32 >> lanes_log2(); }
+  __device__ __forceinline__ int steps_of(int heads) const { return (heads + rows_per_step() - 1) >> (5 - lanes_log2()); }
   float cs[8], sn[8];
   // weights folded in: x' = f (fx x - gy y), y' = f (fy y + gx x), f the row's norm
   float fx[8], fy[8], gx[8], gy[8];
 
   __device__ __forceinline__ RowMath(const RotateParams& params, int lane) : p(params) {
-    g = lane & (lanes() - 1), sub = lane / lanes();
+    g = lane & (lanes() - 1), sub = lane >> lanes_log2();
     mine = LANES > 0 || g < p.head_dim / 16;
     p0 = 8 * g;                              // this lane's first pair
     turns = mine && p0 < p.rot_dim / 2;
@@ -322,14 +325,12 @@ __global__ void __launch_bounds__(kRotateWarps * 32, 4) rotate_kernel(const Rota
   grid_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * kRotateWarps + (threadIdx.x >> 5);
-  const int64_t t = gw / p.warps_per_token;
+  const unsigned gw = blockIdx.x * kRotateWarps + (threadIdx.x >> 5), token = gw / static_cast<unsigned>(p.warps_per_token);
+  const int64_t t = token;
   if (t >= p.num_tokens) return;
-  const int part = static_cast<int>(gw - t * p.warps_per_token);
+  const int part = static_cast<int>(gw - token * p.warps_per_token);
   RowMath<T, VEC, ADJACENT, 0> math(p, lane);
-  const int rows_per_step = 32 / math.lanes();
-  const int steps_q = (p.num_q_heads + rows_per_step - 1) / rows_per_step;
-  const int steps_kv = (p.num_kv_heads + rows_per_step - 1) / rows_per_step;
+  const int rows_per_step = math.rows_per_step(), steps_q = math.steps_of(p.num_q_heads), steps_kv = math.steps_of(p.num_kv_heads);
   const int steps = steps_q + 2 * steps_kv;  // of query rows, then of key rows, then of value rows
 
   Chunk<T, VEC> x0[kDeep], x1[kDeep];
@@ -443,9 +444,7 @@ __global__ void __launch_bounds__(kRingThreads, 4) rotate_ring_kernel(const Rota
 
   const int stride = gridDim.x;
   RowMath<T, true, ADJACENT, LANES> math(p, lane);
-  const int rows_per_step = 32 / math.lanes();
-  const int steps_q = (p.num_q_heads + rows_per_step - 1) / rows_per_step;
-  const int steps_kv = (p.num_kv_heads + rows_per_step - 1) / rows_per_step;
+  const int rows_per_step = math.rows_per_step(), steps_q = math.steps_of(p.num_q_heads), steps_kv = math.steps_of(p.num_kv_heads);
 
   // slot and (lane a: axis a) position of a token
   struct Meta {
