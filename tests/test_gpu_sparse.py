@@ -1,6 +1,7 @@
 """Key bounds, block selection and block-sparse decode on the GPU against their binary64 definitions, alone and as the
-steps of a decode over a growing cache, captured and on two streams."""
+steps of a decode over a growing cache, captured, on two streams and in threads."""
 import math
+import threading
 
 import pytest
 import torch
@@ -456,4 +457,45 @@ def test_captured_step_replayed_with_new_inputs():
             ref = sparse_ref(oq.cpu().contiguous(), other.kc.cpu(), other.vc.cpu(), other.bt, fresh[3].cpu(), osel.cpu(), other.scale)
             H.assert_sparse(oout.cpu(), *ref, BF, False, "other stream")
         assert torch.equal(oout, want[0]) and torch.equal(osel, want[1])  # the same inputs, the same bits
+    assert wllm.device_errors() == 0
+
+
+def test_threads_call_at_once():
+    """Steps of four layers, each in a thread and on a stream of its own, with tables of several widths (the selection's
+    shared memory grows with them), give the bits that they give one after another."""
+    def step(layer, inputs):
+        fused, slots, pos, cl = inputs
+        q = layer.append(fused.clone(), slots, pos)
+        sel, out = layer.new()
+        layer.attend(q, cl, sel, out)
+        return q.clone(), sel, out
+
+    layers = [Layer(40 + i, lens, extra) for i, (lens, extra) in enumerate(
+        [([150, 333], 40), ([900], 3000), ([64, 1200, 31], 9000), ([2000], 20000)])]
+    work = []
+    for layer in layers:
+        n = len(layer.lens)
+        fused, slots, pos, cl, qsl = layer.tokens([40] * n)
+        layer.append(fused, slots, pos)
+        wllm.update_key_bounds(layer.kb, layer.kc, layer.btd, cl, layer.bs,
+                               query_start_loc=cl.new_tensor([0] + layer.lens).cumsum(0).to(torch.int32))
+        inputs = layer.tokens([1] * n)[:4]
+        work.append((layer, inputs, step(layer, inputs)))
+    torch.cuda.synchronize()
+    got = [None] * len(work)
+
+    def run(i):
+        layer, inputs, _ = work[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got[i] = step(layer, inputs)
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for (layer, inputs, want), have in zip(work, got):
+        assert all(torch.equal(x, y) for x, y in zip(want, have)), "a thread's step"
     assert wllm.device_errors() == 0
