@@ -28,7 +28,7 @@
 // Bound: memory, each selected K and V byte is read once per head tile.  256
 // sequences with 96 listed blocks, 28/4 heads of 128, E4M3 (401 MB): 73.6 us,
 // 0.80 of the measured copy rate; 8 sequences with 128 blocks, 32/8 heads, bf16
-// (67 MB): 17.0 us, 0.58, the rest lookups, the rings' filling and the merge.
+// (67 MB): 15.6 us, 0.64, the rest lookups, the rings' filling and the merge.
 //
 // F32 caches keep the same split and rings with binary32 FMA (no tensor cores).
 #include <cooperative_groups.h>
@@ -50,12 +50,14 @@ constexpr int kMaxSparseCluster = 8;
 // Warps of a CTA and stages of a warp's ring.  Eight warps instead of four: 256
 // sequences over an fp8 cache 76.4 instead of 73.7 us, one sequence 4.8 instead of 5.1.
 // f32 units are bound by their FMA and take more warps with a stage each.
-template <typename B, int D>
+// DEEP: a stage more, for launches that leave the shared memory to it (launch_tile).
+template <typename B, int D, bool DEEP>
 struct SparseTuning {
   static constexpr int kStage = Geom<B, D>::kStageBytes;  // 16 tokens' K and V rows
   static constexpr bool kF32 = sizeof(B) == 4;
   static constexpr int kWarps = kStage >= 32768 || (kStage >= 16384 && !kF32) ? 2 : 4;
-  static constexpr int kStages = kF32 && kStage >= 16384 ? 1 : kStage >= 8192 ? 2 : kStage >= 4096 ? 3 : 6;
+  static constexpr int kStages = (kF32 && kStage >= 16384 ? 1 : kStage >= 8192 ? 2 : kStage >= 4096 ? 3 : 6) + (DEEP ? 1 : 0);
+  static constexpr bool kDeeper = sizeof(B) == 2 && kStage >= 8192;  // whether there is a deep form
   static constexpr int kRing = kStages * kStage;          // a warp's
 };
 
@@ -509,12 +511,12 @@ struct SparseMath<float, false, D, HT> {
 
 // --- the kernel -------------------------------------------------------------------
 // T: query and output type; F8: the caches hold E4M3 codes.
-template <typename T, bool F8, int D, int HT>
-__global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, uint8_t, T>::type, D>::kWarps * 32))
+template <typename T, bool F8, int D, int HT, bool DEEP>
+__global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, uint8_t, T>::type, D, DEEP>::kWarps * 32))
     sparse_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const SparseParams p) {
   using B = typename std::conditional<F8, uint8_t, T>::type;
   using G = Geom<B, D>;
-  using Tune = SparseTuning<B, D>;
+  using Tune = SparseTuning<B, D, DEEP>;
   using Math = typename SparseMath<T, F8, D, HT>::type;
   constexpr int kWarps = Tune::kWarps, kStages = Tune::kStages;
   static_assert(sizeof(Partial<D, HT>) <= Tune::kRing, "a warp's partial takes its ring's place");
@@ -621,7 +623,7 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
 
 // CTAs of a list: as many as run at once (`resident` an SM), but no warp under
 // one unit.  Measured, us for 1, 2, 4 and 8 CTAs a list: 64 lists of 128 blocks
-// (bf16) 23.3, 17.7, 16.5, 22.0; 1024 of 96 (fp8) 73.7, 84.5, 107, 161; 4 of 64
+// (bf16, two stages) 23.3, 17.7, 16.5, 22.0; 1024 of 96 (fp8) 73.7, 84.5, 107, 161; 4 of 64
 // (f16, head_dim 64) 10.2, 7.7, 5.9, 5.1.
 int cluster_size(const SparseParams& p, int warps, int resident, int num_sms) {
   const int64_t rows = int64_t(p.num_seqs) * p.num_kv_heads * p.num_head_tiles;
@@ -635,26 +637,50 @@ dim3 grid_of(const SparseParams& p, int ctas) {
   return dim3(static_cast<unsigned>(int64_t(p.num_seqs) * p.num_kv_heads * p.num_head_tiles * ctas));
 }
 
+// One form of the kernel: its shared memory, and how many CTAs of it an SM holds.
+template <typename T, bool F8, int D, int HT, bool DEEP>
+struct SparseForm {
+  using Tune = SparseTuning<typename std::conditional<F8, uint8_t, T>::type, D, DEEP>;
+  static constexpr size_t kSmem = 1024 + Tune::kWarps * (Tune::kRing + Tune::kStages * sizeof(uint64_t)) +
+                                  HT * 8 * sizeof(float) + SparseMath<T, F8, D, HT>::type::kQueryBytes;
+
+  static int resident(int* blocks) {
+    static std::atomic<int> configured[64], found{0};
+    const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_kernel<T, F8, D, HT, DEEP>),
+                                   static_cast<int>(kSmem));
+    if (e != cudaSuccess) return e;
+    *blocks = found.load(std::memory_order_relaxed);
+    if (*blocks == 0) {
+      const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, &sparse_kernel<T, F8, D, HT, DEEP>,
+                                                                            Tune::kWarps * 32, kSmem);
+      if (err != cudaSuccess) return err;
+      found.store(*blocks, std::memory_order_relaxed);
+    }
+    return cudaSuccess;
+  }
+
+  static int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparseParams& p, int ctas, cudaStream_t stream) {
+    return launch_dependent(&sparse_kernel<T, F8, D, HT, DEEP>, grid_of(p, ctas), dim3(Tune::kWarps * 32), kSmem, ctas,
+                            stream, kmap, vmap, p);
+  }
+};
+
 template <typename T, bool F8, int D, int HT>
 int launch_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparseParams& p, int num_sms, cudaStream_t stream) {
-  using Tune = SparseTuning<typename std::conditional<F8, uint8_t, T>::type, D>;
-  static std::atomic<int> configured[64];
-  constexpr size_t smem = 1024 + Tune::kWarps * (Tune::kRing + Tune::kStages * sizeof(uint64_t)) + HT * 8 * sizeof(float) +
-                          SparseMath<T, F8, D, HT>::type::kQueryBytes;
-  const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_kernel<T, F8, D, HT>),
-                                 static_cast<int>(smem));
+  using Form = SparseForm<T, F8, D, HT, false>;
+  int blocks = 0;
+  int e = Form::resident(&blocks);
   if (e != cudaSuccess) return e;
-  static std::atomic<int> resident{0};  // CTAs an SM, by registers and shared memory
-  int blocks = resident.load(std::memory_order_relaxed);
-  if (blocks == 0) {
-    const cudaError_t err =
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, &sparse_kernel<T, F8, D, HT>, Tune::kWarps * 32, smem);
-    if (err != cudaSuccess) return err;
-    resident.store(blocks, std::memory_order_relaxed);
+  const int ctas = cluster_size(p, Form::Tune::kWarps, blocks, num_sms);
+  if constexpr (Form::Tune::kDeeper) {
+    // The deep form where all its CTAs run at once too.  Measured, us with 2 and 3 stages: 64 lists of 128 blocks (bf16)
+    // 17.0 and 15.6, 256 of 64 27.3 and 24.6, 32 of 64 with head_dim 256 12.0 and 10.8; behind a fill 19.6 and 19.5, 27.3
+    // and 24.6, 15.1 and 14.8.  Not so for E4M3 codes: 1024 lists 73.7 and 85.3 (3 and 4), 256 18.3 and 18.3.
+    using Deep = SparseForm<T, F8, D, HT, true>;
+    if ((e = Deep::resident(&blocks)) != cudaSuccess) return e;
+    if (int64_t(grid_of(p, ctas).x) <= int64_t(num_sms) * blocks) return Deep::launch(kmap, vmap, p, ctas, stream);
   }
-  const int ctas = cluster_size(p, Tune::kWarps, blocks, num_sms);
-  return launch_dependent(&sparse_kernel<T, F8, D, HT>, grid_of(p, ctas), dim3(Tune::kWarps * 32), smem, ctas, stream,
-                          kmap, vmap, p);
+  return Form::launch(kmap, vmap, p, ctas, stream);
 }
 
 template <int HT>
