@@ -60,21 +60,26 @@ __global__ void check_append_kernel(const void* slots, int slots_are_i64, int nu
     }
 }
 
-// Self-test of the bounded waits: one thread waits on an mbarrier that never
-// receives its arrival (no copy is in flight on it) and then polls a counter
-// that nothing increments, each with the library's bounded waits.  Both give
-// up after limit_ns; each timeout sets kErrWaitTimeout, as in the decode
+// Self-test of the bounded waits by one warp: half of its lanes wait on an
+// mbarrier whose phase is complete, the others on one that never receives its
+// arrival (no copy is in flight on either), and every lane has to learn that the
+// wait gave up; then one lane polls a counter that nothing increments.  Both
+// give up after limit_ns; each timeout sets kErrWaitTimeout, as in the decode
 // kernels.  The scheduler counter is then left non-zero, as a launch that
 // gave up half-way would leave it, so that the caller can check that reading
 // the error word also restores the counters.
 __global__ void wait_selftest_kernel(int* err, const int* never, int* sched_next, unsigned long long limit_ns,
                                      int* result) {
-  __shared__ uint64_t bar;
-  if (threadIdx.x != 0) return;
-  mbar_init(smem_u32(&bar), 1);
+  __shared__ uint64_t bars[2];
+  const int lane = threadIdx.x;
+  if (lane < 2) mbar_init(smem_u32(&bars[lane]), 1);
   fence_mbar_init();
-  int r = 0;
-  if (!mbar_wait_bounded(smem_u32(&bar), 0, limit_ns)) r |= 1;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&bars[0]));
+  __syncwarp();
+  const bool gave_up = !mbar_wait_warp(smem_u32(&bars[lane & 1]), 0, limit_ns);
+  int r = __all_sync(kFullMask, gave_up) ? 1 : 0;
+  if (lane != 0) return;
   if (!counter_wait_bounded(never, 1, limit_ns)) r |= 2;
   if (r != 0) {
     atomicOr(err, kErrWaitTimeout);

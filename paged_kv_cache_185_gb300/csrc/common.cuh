@@ -122,6 +122,15 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same by a whole warp, decided together: true if every lane saw the phase
+// complete.  A copy that lands right at the limit is seen by some lanes and not
+// by others; lanes that gave up alone would leave the rest in their next
+// shuffle or ldmatrix for ever.  All 32 lanes call it.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  const bool got = mbar_wait_bounded(bar, parity, limit_ns);
+  return __all_sync(kFullMask, got);
+}
+
 // Poll a counter in global memory (acquire loads) until it reaches `target`,
 // giving up after `limit_ns`.  Returns false on timeout.
 __device__ __forceinline__ bool counter_wait_bounded(const int* ctr, int target, uint64_t limit_ns) {

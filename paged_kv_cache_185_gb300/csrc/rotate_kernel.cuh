@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kRingThreads, 4) rotate_ring_kernel(const Rota
     const Meta after = fetch(t + 2 * stride);
     if (live) {
       const uint32_t bar = smem_u32(&bars[k]);
-      if (!mbar_wait_bounded(bar, (phase >> k) & 1u, p.wait_limit_ns)) {
+      if (!mbar_wait_warp(bar, (phase >> k) & 1u, p.wait_limit_ns)) {
         // give up: record it, and leave no copy in flight
         if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
         mbar_wait_bounded(bar, (phase >> k) & 1u, p.wait_limit_ns);

@@ -592,7 +592,7 @@ __global__ void __launch_bounds__((SparseTuning<typename std::conditional<F8, ui
       const int from = __ffs(to_use) - 1;
       to_use &= to_use - 1;
       const int live = __shfl_sync(kFullMask, mine.live, from);
-      if (!mbar_wait_bounded(smem_u32(&bars[stage]), phase, p.wait_limit_ns)) {
+      if (!mbar_wait_warp(smem_u32(&bars[stage]), phase, p.wait_limit_ns)) {
         // give up: record it, let what is in flight land (again with a limit), and take no more units
         if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
         for (int s = 0; s < kStages; ++s) mbar_wait_bounded(smem_u32(&bars[s]), s >= stage ? phase : phase ^ 1u, p.wait_limit_ns);
