@@ -240,9 +240,9 @@ __device__ __forceinline__ void load_q_smem(MmaState<T, D, NT>& st, const uint8_
 __device__ __forceinline__ bool consumer_sync(uint32_t bar, int& phase, uint64_t limit_ns, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
-  const bool ok = mbar_wait_bounded(bar, phase & 1, limit_ns);
+  const bool ok = mbar_wait_warp(bar, phase & 1, limit_ns);
   ++phase;
-  return __all_sync(kFullMask, ok);
+  return ok;
 }
 
 // Merge the partitions of R query rows at once (one warp): for each row
@@ -1278,7 +1278,7 @@ __global__ void __launch_bounds__(PShape<T, D, NT, F8>::kThreads) __maxnreg__((P
   T* out = reinterpret_cast<T*>(p.out);
   for (int k = 0; !failed; ++k) {
     const int s = k % S;
-    if (!mbar_wait_bounded(smem_u32(full + s), (k / S) & 1, p.wait_limit_ns)) {
+    if (!mbar_wait_warp(smem_u32(full + s), (k / S) & 1, p.wait_limit_ns)) {
       if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
       failed = true;
       break;
@@ -1321,7 +1321,7 @@ __global__ void __launch_bounds__(PShape<T, D, NT, F8>::kThreads) __maxnreg__((P
           if (lane == 0) mbar_arrive(smem_u32(empty + k % S));
           if (gflags & kLast) break;
           ++k;
-          if (!mbar_wait_bounded(smem_u32(full + k % S), (k / S) & 1, p.wait_limit_ns)) {
+          if (!mbar_wait_warp(smem_u32(full + k % S), (k / S) & 1, p.wait_limit_ns)) {
             if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
             failed = true;
             break;

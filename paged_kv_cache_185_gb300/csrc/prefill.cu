@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kPfThreads, 2)
 
   for (int k = 0; k < n_tiles; ++k) {
     const int s = k % S;
-    if (!mbar_wait_bounded(smem_u32(full + s), (k / S) & 1, p.wait_limit_ns)) {
+    if (!mbar_wait_warp(smem_u32(full + s), (k / S) & 1, p.wait_limit_ns)) {
       if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
       break;
     }

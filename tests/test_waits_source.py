@@ -32,3 +32,15 @@ def test_the_warps_wait_votes():
     assert "__all_sync(kFullMask, got)" in body[:body.index("\n}")]
     users = [f for f in glob.glob(os.path.join(build.CSRC, "*.cu*")) if "mbar_wait_warp(smem" in open(f).read()]
     assert users
+
+
+@pytest.mark.parametrize("name", ["decode_persistent.cuh", "decode_kernel.cuh", "prefill.cu", "prefill_tc.cu"])
+def test_no_branch_on_a_lanes_own_wait(name):
+    """In the decode and prefill kernels one lane waits for the warp (and tells it), the warp votes, or only copies in
+    flight are let land."""
+    text = open(os.path.join(build.CSRC, name)).read()
+    for number, code in waits(os.path.join(build.CSRC, name)):
+        assert not re.match(r"if \(!", code), f"{name}:{number}: {code}"
+        if re.match(r"const bool (ok|got) = mbar_wait_bounded", code):
+            after = "\n".join(text.split("\n")[number:number + 3])
+            assert "__all_sync(kFullMask, got)" in after, f"{name}:{number}: {code}"
