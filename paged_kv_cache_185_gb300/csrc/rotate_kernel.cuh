@@ -155,6 +155,9 @@ __device__ __forceinline__ void load_weight(const RotateParams& p, const void* w
   }
 }
 
+// c + a b where `on`, else c.
+__device__ __forceinline__ float add_product(bool on, float a, float b, float c) { return on ? fmaf(a, b, c) : c; }
+
 // What one lane does with its 16 elements of a row: its chunks, the (cos, sin)
 // of its pairs and the factors of the rows of one kind.
 // LANES: lanes of a row where head_dim is 16 * LANES, 0 where they are p.row_lanes
@@ -255,21 +258,23 @@ struct RowMath {
       for (int m = lanes() >> 1; m > 0; m >>= 1) ss += __shfl_xor_sync(kFullMask, ss, m);
       f = rsqrtf(ss * p.inv_dim + p.eps);
     }
+    // Behind the rotated part every element stands alone: a product of 0 with its neighbour would bring that one's infinity
+    // or NaN along, so the second product of a turn is left out (a branch around the turn instead: 3001 tokens half turned 14.1 us, not 13.4).
     if constexpr (ADJACENT) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float x = a[2 * i], y = a[2 * i + 1], z = b[2 * i], w = b[2 * i + 1];
-        a[2 * i] = f * (fx[i] * x - gy[i] * y);
-        a[2 * i + 1] = f * (fy[i] * y + gx[i] * x);
-        b[2 * i] = f * (fx[4 + i] * z - gy[4 + i] * w);
-        b[2 * i + 1] = f * (fy[4 + i] * w + gx[4 + i] * z);
+        a[2 * i] = f * add_product(turns, -gy[i], y, fx[i] * x);
+        a[2 * i + 1] = f * add_product(turns, gx[i], x, fy[i] * y);
+        b[2 * i] = f * add_product(turns, -gy[4 + i], w, fx[4 + i] * z);
+        b[2 * i + 1] = f * add_product(turns, gx[4 + i], z, fy[4 + i] * w);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float x = a[i], y = b[i];
-        a[i] = f * (fx[i] * x - gy[i] * y);
-        b[i] = f * (fy[i] * y + gx[i] * x);
+        a[i] = f * add_product(turns, -gy[i], y, fx[i] * x);
+        b[i] = f * add_product(turns, gx[i], x, fy[i] * y);
       }
     }
   }

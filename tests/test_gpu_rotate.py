@@ -213,3 +213,46 @@ def test_rotate_extreme_rows():
     assert (q[0] == 0).all() and (at(kc, 0) == 0).all()
     assert (at(kc, 1) == 448).all() and (at(vc, 1) == 448).all()
     assert q[2].isnan().all() and at(kc, 2).isnan().all() and at(vc, 2).isnan().all()
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (F16, F16), (F32, F32), (F16, U8)])
+@pytest.mark.parametrize("style", ["halves", "adjacent"])
+@pytest.mark.parametrize("T,Hq,D,R,shift", [(5, 4, 128, 32, 0), (5, 4, 128, 64, 1), (9, 3, 80, 16, 0), (2000, 4, 64, 32, 0), (2000, 4, 128, 32, 0)])
+def test_rotate_leaves_the_elements_behind_the_turned_ones_alone(dtype, cache, style, T, Hq, D, R, shift):
+    """Without a norm the elements from R on come out as they went in (as codes: of their own value), whatever their
+    neighbours hold: infinities and NaN do not spread, and a zero keeps its sign.  (A NaN is any NaN: rounding to the 16-bit
+    type does not keep its payload.)"""
+    a = make(T, Hq, 2, D, R, 16, dtype, cache, shift=shift, seed=9)
+    q, k, _ = parts(a["fused"], a)
+    for x in (q, k):
+        x[..., R] = float("inf")
+        x[..., R + 3] = float("nan")
+        x[..., D - 5] = -float("inf")
+        x[..., R + 1], x[..., R + 6], x[..., D - 2], x[..., D - 9] = -0.0, 0.0, -0.0, -0.0
+    same = lambda x, y: bool(((H.bits(x.contiguous()) == H.bits(y.contiguous())) | (x.isnan() & y.isnan())).all())  # noqa: E731
+    q_out, kc, _ = call(a, style=style)
+    assert same(q_out[..., R:], q[..., R:])
+    slots = a["slots"].long()
+    got = kc[slots // 16, :, slots % 16][..., R:].contiguous()
+    if cache == U8:
+        inv = torch.tensor(oracle.inv_scale(K_SCALE), dtype=F32)
+        assert torch.equal(got, oracle.e4m3_encode(k[..., R:].float() * inv))
+    else:
+        assert same(got, k[..., R:])
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (F32, F32)])
+@pytest.mark.parametrize("style", ["halves", "adjacent"])
+@pytest.mark.parametrize("T,D,R", [(6, 128, 32), (2000, 64, 32)])
+def test_rotate_norms_an_infinite_row_element_by_element(dtype, cache, style, T, D, R):
+    """x / sqrt(inf) is zero for the finite elements behind the turned ones and NaN for the infinite one alone."""
+    a = make(T, 4, 2, D, R, 16, dtype, cache, weights=dtype, seed=10)
+    q, k, _ = parts(a["fused"], a)
+    for x in (q, k):
+        x[..., R + 2] = float("inf")
+    q_out, kc, _ = call(a, style=style)
+    slots = a["slots"].long()
+    for got in (q_out, kc[slots // 16, :, slots % 16]):
+        want = torch.zeros_like(got[..., R:])
+        want[..., 2] = float("nan")
+        assert torch.equal(got[..., R:].nan_to_num(7.0), want.nan_to_num(7.0))
