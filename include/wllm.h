@@ -428,7 +428,8 @@ int wllm_rotate_and_cache_fp8(const wllm_tensor* q_out, const wllm_tensor* q, co
  *   block_tables     [B][M_b] I32; context_lens [B] I32, as in the decode.
  *   query_start_loc  [B+1] I32, contiguous: sequence b has n_b =
  *                    query_start_loc[b+1] - query_start_loc[b] new tokens, the
- *                    last n_b of its L_b = context_lens[b] cached ones.  NULL:
+ *                    last n_b of its L_b = context_lens[b] cached ones (only the
+ *                    differences count: the first entry may be any row).  NULL:
  *                    one new token for every sequence that is not empty.
  *
  * Call it after the append.  Every block that holds bs tokens of sequence b

@@ -148,9 +148,9 @@ __device__ __forceinline__ void bounds_of_block(const uint8_t* src, uint8_t* dst
 }
 
 // Units of the packed form.  Sequence b, whose new tokens are packed rows
-// qsl[b] .. qsl[b+1], owns the unit numbers from floor(qsl[b] / bs) + b on: n
-// tokens fill at most ceil(n / bs) blocks, which is no more than the distance
-// to the next sequence's first unit.
+// r = qsl[b] - qsl[0] .. qsl[b+1] - qsl[0], owns the unit numbers from
+// floor(r / bs) + b on: n tokens fill at most ceil(n / bs) blocks, which is no
+// more than the distance to the next sequence's first unit.
 template <typename Ops, int COLS>
 __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const BoundsParams p) {
   grid_wait();
@@ -159,13 +159,15 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const Bou
   const unsigned gw = blockIdx.x * kBoundsWarps + (threadIdx.x >> 5), stride = gridDim.x * kBoundsWarps;
   const int bs = 1 << p.log2_bs;
   int units = p.num_seqs;  // of every head
+  int row0 = 0;            // of the first sequence: rows of others may lie before it
   if (p.query_start_loc != nullptr) {
-    const int total = p.query_start_loc[p.num_seqs];
+    row0 = p.query_start_loc[0];
+    const int64_t total = int64_t(p.query_start_loc[p.num_seqs]) - row0;
     if (total < 0 || total > int64_t(p.num_seqs) * p.max_tokens) {  // more new tokens than the tables can name
       if (gw == 0 && lane == 0) atomicOr(p.err, kErrLen);
       return;
     }
-    units += total >> p.log2_bs;
+    units += static_cast<int>(total >> p.log2_bs);
   }
   const unsigned heads = p.num_kv_heads;
   const int hop = stride / heads, hop_h = stride % heads;
@@ -181,14 +183,14 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const Bou
       while (lo < hi) {
         const int step = (hi - lo + 31) / 32;
         const int at = lo + (lane + 1) * step;
-        const bool before = at <= hi && (p.query_start_loc[at] >> p.log2_bs) + at <= slot;
+        const bool before = at <= hi && ((p.query_start_loc[at] - row0) >> p.log2_bs) + at <= slot;
         const int k = __popc(__ballot_sync(kFullMask, before));
         hi = min(hi, lo + (k + 1) * step - 1);
         lo += k * step;
       }
       b = lo;
-      const int first = p.query_start_loc[b];
-      n = p.query_start_loc[b + 1] - first;
+      const int first = p.query_start_loc[b] - row0;
+      n = p.query_start_loc[b + 1] - row0 - first;
       j = slot - ((first >> p.log2_bs) + b);
     }
     const int len = p.context_lens[b];

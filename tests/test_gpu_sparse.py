@@ -66,6 +66,18 @@ def test_bounds_of_many_sequences_and_nan():
     assert wllm.device_errors() == 0
 
 
+@pytest.mark.parametrize("first", [1, 7, 40, 3000, 10 ** 9])
+def test_bounds_of_chunks_behind_other_rows(first):
+    """query_start_loc cut out of a batch's: its first entry is not zero (rows of other sequences come before)."""
+    g = H.gen(first)
+    lens, new = [64, 33, 0, 500], [64, 20, 0, 333]
+    bt, pool = H.block_tables(g, lens, 16)
+    kc, kb = H.cache(g, pool, 2, 16, 64, BF, bt, lens), H.cache(g, pool, 2, 2, 64, BF)
+    qsl = (i32([0] + new).cumsum(0) + first).to(torch.int32)
+    assert_bounds(run_bounds(kb, kc, bt, i32(lens), qsl), kb, kc, bt, i32(lens), new)
+    assert wllm.device_errors() == 0
+
+
 def test_bounds_record_bad_lengths_and_blocks(monkeypatch):
     g = H.gen(4)
     lens = [32, 48, 64]
