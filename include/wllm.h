@@ -426,7 +426,7 @@ int wllm_rotate_and_cache_fp8(const wllm_tensor* q_out, const wllm_tensor* q, co
  *   k_cache          [N_b][Hkv][bs][D] dense; F32, F16, BF16 or FP8_E4M3 (codes;
  *                    their bounds are codes too).
  *   block_tables     [B][M_b] I32; context_lens [B] I32, as in the decode.
- *   query_start_loc  [B+1] I32, contiguous: sequence b has n_b =
+ *   query_start_loc  [B+1] I32, contiguous, not decreasing: sequence b has n_b =
  *                    query_start_loc[b+1] - query_start_loc[b] new tokens, the
  *                    last n_b of its L_b = context_lens[b] cached ones (only the
  *                    differences count: the first entry may be any row).  NULL:
@@ -437,7 +437,9 @@ int wllm_rotate_and_cache_fp8(const wllm_tensor* q_out, const wllm_tensor* q, co
  * are touched.  Blocks filled by an earlier call (n_b = L_b: all of a
  * sequence's) can be given again.  D 64, 128 or 256, bs a power of two in
  * [8, 256].  Inconsistent lengths (bit 2) and table entries outside the pool
- * (bit 1) are recorded and skipped.  Two sequences that name one block write
+ * (bit 1) are recorded and skipped; where query_start_loc decreases (bit 2) or
+ * names more new tokens in all than the tables' B M_b bs (bit 2, nothing is
+ * written), other sequences' blocks may be left out too.  Two sequences that name one block write
  * the same bounds.
  */
 int wllm_update_key_bounds(const wllm_tensor* key_bounds, const wllm_tensor* k_cache,

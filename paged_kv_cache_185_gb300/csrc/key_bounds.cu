@@ -208,6 +208,10 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const Bou
     const int64_t run = static_cast<int64_t>(id) * p.num_kv_heads + h;
     bounds_of_block<Ops, COLS>(p.k_cache + run * bs * (COLS * 16), p.bounds + run * 2 * (COLS * 16), bs, lane);
   }
+  // starts that decrease are recorded whether or not a unit met them: behind the loop, where other warps' copies hide the loads
+  if (p.query_start_loc != nullptr)
+    for (int64_t i = int64_t(gw) * 32 + lane; i < p.num_seqs; i += int64_t(stride) * 32)
+      if (p.query_start_loc[i + 1] < p.query_start_loc[i]) atomicOr(p.err, kErrLen);
 }
 
 template <typename Ops, int COLS>

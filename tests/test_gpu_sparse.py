@@ -78,6 +78,16 @@ def test_bounds_of_chunks_behind_other_rows(first):
     assert wllm.device_errors() == 0
 
 
+@pytest.mark.parametrize("starts", [[0, 32, 31, 90], [0, 40, 30, 31], [0, 100, 50, 200], [5, 4, 4, 4], [0, 64, 64, 63]])
+def test_bounds_record_starts_that_decrease(starts):
+    g = H.gen(14)
+    lens = [320, 480, 640]
+    bt, pool = H.block_tables(g, lens, 16)
+    kc, kb = H.cache(g, pool, 1, 16, 64, BF), H.cache(g, pool, 1, 2, 64, BF)
+    run_bounds(kb, kc, bt, i32(lens), i32(starts))
+    assert wllm.device_errors() == 4
+
+
 def test_bounds_record_bad_lengths_and_blocks(monkeypatch):
     g = H.gen(4)
     lens = [32, 48, 64]
