@@ -76,7 +76,9 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 
 // Programmatic dependent launch: wait until the kernels before this one in the
 // stream are complete and their writes visible; allow the next kernel's CTAs to
-// be launched (they wait in turn).
+// be launched (they wait in turn).  Such a kernel is alive while the one before it
+// writes, so what it reads is not read-only for its lifetime: plain loads, never
+// the non-coherent path (__ldg), which may be moved above the wait.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 

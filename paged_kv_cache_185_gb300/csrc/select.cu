@@ -136,7 +136,7 @@ __device__ __forceinline__ double fine_score(const uint8_t* src, const float2* w
   constexpr int kE = 16 / static_cast<int>(sizeof(B)), kLoads = 2 * D / (8 * kE);
   uint4 x[kLoads];
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(src) + 8 * i + (lane & 7));
+  for (int i = 0; i < kLoads; ++i) x[i] = reinterpret_cast<const uint4*>(src)[8 * i + (lane & 7)];
   double s = 0.0;
   float hi = 0.f, lo = 0.f;
 #pragma unroll
@@ -216,7 +216,7 @@ struct ScoreStats {
 // Physical block of candidate j; one outside the pool is recorded and read as block 0.
 __device__ __forceinline__ int physical(const SelectParams& p, const int32_t* table, int j, int cands, bool record) {
   if (j >= cands) return 0;
-  const int id = __ldg(table + j);
+  const int id = table[j];
   if (id >= 0 && id < p.num_blocks) return id;
   if (record) atomicOr(p.err, kErrBlock);
   return 0;
@@ -502,8 +502,7 @@ struct Scorer<float, float, D> {  // binary32 FMA: D/16 lanes a block, 32 elemen
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
           x[t][i] = (turn * kDeep + t) * kPer + gi < cands
-                        ? __ldg(reinterpret_cast<const float4*>(p.bounds) +
-                                (int64_t(ids[t]) * p.num_kv_heads + h) * (D / 2) + gl + kLanes * i)
+                        ? reinterpret_cast<const float4*>(p.bounds)[(int64_t(ids[t]) * p.num_kv_heads + h) * (D / 2) + gl + kLanes * i]
                         : make_float4(0.f, 0.f, 0.f, 0.f);
       lookup(p, table, cands, turn + turns);
 #pragma unroll

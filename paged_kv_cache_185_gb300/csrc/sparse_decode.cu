@@ -76,9 +76,9 @@ __device__ __forceinline__ Unit find_unit(const SparseParams& p, const int32_t* 
   const int64_t e = unit >> log2_units;
   if (e >= p.top) return u;
   // the length and the entry together, then the table: two round trips, not three
-  const int stored = __ldg(len_at), id = __ldg(list + e);
+  const int stored = *len_at, id = list[e];
   const int max_blocks = p.max_tokens >> p.log2_bs;
-  const int phys = id >= 0 && id < max_blocks ? __ldg(table + id) : -1;
+  const int phys = id >= 0 && id < max_blocks ? table[id] : -1;
   const int len = min(max(stored, 0), p.max_tokens);
   if (id < 0 || len == 0) return u;
   if (id > (len - 1) >> p.log2_bs || phys < 0 || phys >= p.num_blocks) {
