@@ -491,8 +491,8 @@ int wllm_select_blocks(const wllm_tensor* selected, const wllm_tensor* q,
  * it is the decode.  Entries past the sequence's last block and table entries
  * outside the pool are recorded (bit 1) and skipped; an empty sequence's list
  * is not looked at.  D 64, 128 or 256.  F16/BF16 run on tensor cores with fp32
- * accumulation, weights rounded to the type of q; F32 on fp32 FMA.  q rows may
- * have any alignment of their elements.
+ * accumulation, softmax weights in two words of the 16-bit type (16 or 22 bits);
+ * F32 on fp32 FMA.  q rows may have any alignment of their elements.
  */
 int wllm_paged_attention_decode_sparse(const wllm_tensor* out, const wllm_tensor* q,
                                        const wllm_tensor* k_cache, const wllm_tensor* v_cache,

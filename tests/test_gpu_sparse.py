@@ -291,6 +291,37 @@ def test_sparse_decode_matches_binary64(dtype, kind, D, Hq, Hkv, bs, lens, top):
     assert wllm.device_errors() == 0
 
 
+@pytest.mark.parametrize("dtype,kind", [(F16, F16), (BF, BF), (F16, U8), (BF, U8)])
+@pytest.mark.parametrize("Hq,Hkv,bs", [(8, 1, 16), (32, 2, 16), (5, 5, 32)])
+def test_sparse_decode_keeps_its_weights(dtype, kind, Hq, Hkv, bs):
+    """The softmax weights are not rounded to 16 bits on their way to the output.
+
+    Scores are small and lists hold 64 tokens at most, so everything but the output's own rounding is small.  A score is off
+    by at most size * (4 products of 16 terms, each instruction within 17 * 2^-22 of the magnitudes in it, = 272 * 2^-24,
+    and 8 roundings of scaling and difference), where size = max scale sum |q k|; its exponential by 2^-21 more; both
+    count twice (numerator and sum).  Two words of bf16 leave off 2^-8 * 2^-8 of a weight, two of f16 2^-11 * 2^-11 or, at
+    the subnormal end, 2^-25 of the largest, 1: with weights above 1/16 (scores within 4 log2 units) n of those over their
+    sum are at most 2^-21.  The products with v are up to 8 instructions, 17 * 2^-22 each, and merging and
+    scaling 16 roundings.  One word would leave off 2^-9 or 2^-12 of a weight: several times this bound."""
+    g = H.gen(Hq + bs)
+    D, B, scale = 64, 48, 0.0125
+    lens = [64] * B
+    bt, pool = H.block_tables(g, lens, bs)
+    kc, vc = (H.cache(g, pool, Hkv, bs, D, kind, bt, lens) for _ in range(2))
+    q = H.randn(g, B, Hq, D, dtype=dtype)
+    q = torch.where(q.abs() < 2.0 ** -13, torch.ones_like(q), q)  # exact as f16 also from bf16
+    sel = torch.arange(64 // bs, dtype=torch.int32).expand(B, Hkv, -1).contiguous()
+    got = run_sparse(q, kc, vc, bt, i32(lens), sel, scale)
+    ref, mag, size = sparse_ref(q, kc, vc, bt, i32(lens), sel, scale)
+    assert 2 * size.max() * math.log2(math.e) < 4
+    word = 2.0 ** -16 if dtype == BF and kind != U8 else 2.0 ** -22
+    d = 2 * (torch.expm1(size * 280 * H.U32)[..., None] + 2.0 ** -21) + word + 8 * 17 * 2.0 ** -22 + 16 * H.U32
+    vmax = S.values(vc).nan_to_num(0.0).abs().max() * (VS if kind == U8 else 1.0)
+    tol = d * mag + 2.0 ** -21 * vmax + H.HALF[dtype] * ref.abs() + H.TINY[dtype]
+    off = (got.double() - ref).abs()
+    assert (off <= tol).all(), f"{int((off > tol).sum())} off, worst {(off / tol).max().item():.2f} of its bound"
+
+
 @pytest.mark.parametrize("kind", [F32, BF, U8])
 def test_sparse_decode_of_every_block_is_the_decode(kind):
     g = H.gen(20)
