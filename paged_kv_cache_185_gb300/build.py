@@ -75,42 +75,47 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
+    # both outputs are made in _build/ and moved into place once everything is there
+    lib_tmp, describe_tmp = (os.path.join(BUILD, f"{os.path.basename(f)}.{os.getpid()}.tmp") for f in (LIB, DESCRIBE))
+
     def describe_module():
         """The binding's CPython module: one translation unit against torch's headers."""
         import torch
         home = os.path.dirname(os.path.abspath(torch.__file__))
         libs = os.path.join(home, "lib")
-        tmp = DESCRIBE + f".{os.getpid()}.tmp"
         cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
                "-I", sysconfig.get_paths()["include"], "-I", os.path.join(home, "include"),
                "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
                "-I", os.path.join(os.path.dirname(_cuda_lib_dir(nvcc)), "include"),
-               os.path.join(CSRC, "describe.cpp"), "-o", tmp, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+               os.path.join(CSRC, "describe.cpp"), "-o", describe_tmp, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
                "-Wl,-rpath," + libs]
-        return tmp, subprocess.run(cmd, capture_output=True, text=True)
+        return subprocess.run(cmd, capture_output=True, text=True)
 
-    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        described = ex.submit(describe_module)
-        results = list(ex.map(compile_one, SOURCES))
-        describe_tmp, r = described.result()
-    results.append(("describe.cpp", None, r))
-    failed = False
-    for src, _, r in results:
-        if verbose or ptxas_verbose or r.returncode != 0:
-            sys.stderr.write(f"--- {src}\n{r.stdout}{r.stderr}")
-        failed |= r.returncode != 0
-    if failed:
-        raise RuntimeError("nvcc failed")
-    tmp = LIB + f".{os.getpid()}.tmp"
-    link = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *[o for _, o, _ in results if o is not None],
-            "-Xlinker", "-rpath," + _cuda_lib_dir(nvcc), "-Xlinker", "-z,defs"]
-    r = subprocess.run(link, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("link failed")
-    os.replace(tmp, LIB)
-    os.replace(describe_tmp, DESCRIBE)
+    try:
+        with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+            described = ex.submit(describe_module)
+            results = list(ex.map(compile_one, SOURCES))
+            results.append(("describe.cpp", None, described.result()))
+        failed = False
+        for src, _, r in results:
+            if verbose or ptxas_verbose or r.returncode != 0:
+                sys.stderr.write(f"--- {src}\n{r.stdout}{r.stderr}")
+            failed |= r.returncode != 0
+        if failed:
+            raise RuntimeError("nvcc failed")
+        link = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", lib_tmp, *[o for _, o, _ in results if o is not None],
+                "-Xlinker", "-rpath," + _cuda_lib_dir(nvcc), "-Xlinker", "-z,defs"]
+        r = subprocess.run(link, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("link failed")
+        os.replace(lib_tmp, LIB)
+        os.replace(describe_tmp, DESCRIBE)
+    finally:
+        for tmp in (lib_tmp, describe_tmp):
+            if os.path.exists(tmp):
+                os.remove(tmp)
     return LIB
 
 
