@@ -60,7 +60,7 @@ _ROTARY_STYLE = {"halves": 0, "adjacent": 1}
 
 _lib = None
 _entries = {}   # entry points that take tensors first: name -> what _invoke takes
-_invoke = None  # _describe.call
+_invoke = None  # _describe.call, from the first call with tensors on
 _lock = threading.Lock()
 
 
@@ -70,7 +70,7 @@ def library_path() -> str:
 
 def load_library():
     """Load libwllm.so (raises if it is missing: build it with ``build()`` first)."""
-    global _lib, _invoke
+    global _lib
     if _lib is not None:
         return _lib
     with _lock:
@@ -158,14 +158,24 @@ def load_library():
         lib.wllm_bm_num_cached_blocks.restype = i64
         lib.wllm_bm_block_ref.argtypes = [vp, i32]
         lib.wllm_bm_block_ref.restype = ctypes.c_int
+        _lib = lib
+    return _lib
+
+
+def _load_calls():
+    """Bind the entry points that take tensors through the compiled module, which needs torch's libraries; the library
+    itself and its host-only calls do not."""
+    global _invoke
+    lib = load_library()
+    with _lock:
+        if _invoke is not None:
+            return
         from . import _describe as module
         for name in EXPORTED:
             f = getattr(lib, name)
-            if f.argtypes and f.argtypes[0] is P:
+            if f.argtypes and f.argtypes[0] is ctypes.POINTER(WllmTensor):
                 _entries[name] = module.bind(name, ctypes.cast(f, ctypes.c_void_p).value)
         _invoke = module.call
-        _lib = lib
-    return _lib
 
 
 def _stream_handle(device) -> int:
@@ -180,8 +190,8 @@ def _check(rc: int) -> None:
 def _call(name: str, tensors, *scalars) -> None:
     """Entry point ``name`` on ``tensors`` (None: not given) and ``scalars``, on the current stream of the tensors'
     device.  Host tensors, or tensors of several devices, raise ValueError."""
-    if _lib is None:
-        load_library()
+    if _invoke is None:
+        _load_calls()
     rc = _invoke(_entries[name], tensors, *scalars)
     if rc != WLLM_OK:
         _check(rc)

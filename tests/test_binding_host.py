@@ -1,0 +1,53 @@
+"""What the binding offers without a GPU and without its compiled module: the library itself, the host-only calls and
+descriptors for callers of the C ABI."""
+import ctypes
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+from paged_kv_cache_185_gb300 import binding, build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+def without_module(code):
+    """Run code in a process whose import of the compiled module fails."""
+    block = "import sys\nsys.modules['paged_kv_cache_185_gb300._describe'] = None\n"
+    return subprocess.run([sys.executable, "-c", block + code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+
+
+def test_library_and_block_manager_need_no_compiled_module():
+    r = without_module("""
+import paged_kv_cache_185_gb300 as w
+assert "sm_103a" in w.version() and w.launch_count() == 0
+m = w.BlockManager(8, 4)
+slots, cached = m.add_sequence(1, [1, 2, 3, 4, 5])
+assert slots.numel() == 5 and cached == 0 and m.num_free_blocks() == 6
+m.close()
+lib = w.load_library()
+assert lib.wllm_reshape_and_cache(None, None, None, None, None, None) == 1 and b"null" in lib.wllm_last_error()
+""")
+    assert r.returncode == 0, r.stderr[-1500:]
+
+
+def test_calls_with_tensors_say_that_the_module_is_missing():
+    r = without_module("""
+import torch, paged_kv_cache_185_gb300 as w
+x, i = torch.zeros(2, 2, 64), torch.zeros(2, dtype=torch.int64)
+for _ in range(2):
+    try:
+        w.reshape_and_cache(x, x, torch.zeros(3, 2, 16, 64), torch.zeros(3, 2, 16, 64), i)
+    except ImportError as e:
+        assert "_describe" in str(e)
+    else:
+        raise AssertionError("no error")
+""")
+    assert r.returncode == 0, r.stderr[-1500:]
