@@ -178,6 +178,16 @@ def _load_calls():
         _invoke = module.call
 
 
+def describe(t: torch.Tensor) -> WllmTensor:
+    """The descriptor of a tensor, for callers of the C ABI through ctypes (the tensor has to outlive its use)."""
+    if t.dim() > 4:
+        raise ValueError("at most 4 dims")
+    d = WllmTensor(t.data_ptr() if t.numel() > 0 else None, _DTYPE[t.dtype], t.dim())
+    d.shape[:t.dim()] = t.shape
+    d.stride[:t.dim()] = t.stride()
+    return d
+
+
 def _stream_handle(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 

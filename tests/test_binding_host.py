@@ -51,3 +51,24 @@ for _ in range(2):
         raise AssertionError("no error")
 """)
     assert r.returncode == 0, r.stderr[-1500:]
+
+
+def test_describe_fills_a_descriptor():
+    x = torch.zeros(3, 8, 5, dtype=torch.bfloat16)[:, 2:6, ::2]
+    d = binding.describe(x)
+    assert isinstance(d, binding.WllmTensor) and d.data == x.data_ptr() and (d.dtype, d.ndim) == (2, 3)
+    assert list(d.shape) == [3, 4, 3, 0] and list(d.stride) == [40, 5, 2, 0]
+    codes = {torch.float32: 0, torch.float16: 1, torch.int32: 3, torch.int64: 4, torch.float8_e4m3fn: 5, torch.uint8: 5}
+    for dtype, code in codes.items():
+        d = binding.describe(torch.empty(0, 7, dtype=dtype))
+        assert d.data is None and d.dtype == code and list(d.shape)[:2] == [0, 7]
+    with pytest.raises(ValueError, match="4 dims"):
+        binding.describe(torch.zeros(1, 1, 1, 1, 1))
+    with pytest.raises(KeyError):
+        binding.describe(torch.zeros(1, dtype=torch.float64))
+    # as an argument of the C ABI: the call gets as far as the first check that these host tensors fail
+    lib = binding.load_library()
+    x, c, s = torch.zeros(2, 2, 64), torch.zeros(3, 2, 16, 64), torch.zeros(3, dtype=torch.int64)
+    args = [binding.describe(t) for t in (x, x, c, c, s)]
+    assert lib.wllm_reshape_and_cache(*map(ctypes.byref, args), None) == binding.WLLM_ERR_INVALID_ARG
+    assert b"slot_mapping" in lib.wllm_last_error()
