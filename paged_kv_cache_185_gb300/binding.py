@@ -170,6 +170,10 @@ def _load_calls():
     with _lock:
         if _invoke is not None:
             return
+        from . import build
+        if build.described_for() not in ("", build.describe_key()):
+            raise ImportError(f"_describe.so was built for {build.described_for()!r}, this process has "
+                              f"{build.describe_key()!r}: run `python -m paged_kv_cache_185_gb300.build`")
         from . import _describe as module
         for name in EXPORTED:
             f = getattr(lib, name)

@@ -6,7 +6,8 @@ binding's _describe.so (calls with torch tensors) in-tree.
 Each translation unit is compiled by nvcc in parallel into ``_build/`` and
 linked into ``paged_kv_cache_185_gb300/libwllm.so`` against the shared CUDA
 runtime.  Only ``sm_103a`` code is generated.  A rebuild happens when any source
-or header is newer than the library.
+or header is newer than the library, or when _describe.so was made for another
+interpreter or another torch than this process has.
 """
 from __future__ import annotations
 
@@ -26,6 +27,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libwllm.so")
 DESCRIBE = os.path.join(PKG, "_describe.so")
+STAMP = os.path.join(BUILD, "describe.stamp")  # what _describe.so was made for
 
 SOURCES = ["api.cu", "append.cu", "decode_bf16.cu", "decode_f16.cu", "decode_f32.cu", "decode_f8_f16.cu",
            "decode_f8_bf16.cu", "prefill.cu", "prefill_tc.cu", "block_manager.cpp", "api_sparse.cu", "rotate.cu",
@@ -52,8 +54,23 @@ def _inputs():
     return files
 
 
+def describe_key() -> str:
+    """What _describe.so is bound to besides its source: the interpreter's ABI and the torch whose structures it reads."""
+    import torch
+    return f"{sysconfig.get_config_var('SOABI')} torch {torch.__version__}"
+
+
+def described_for() -> str:
+    """describe_key() of the build that made _describe.so ('' where nothing says)."""
+    try:
+        with open(STAMP) as f:
+            return f.read().strip()
+    except OSError:
+        return ""
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(DESCRIBE)):
+    if not (os.path.exists(LIB) and os.path.exists(DESCRIBE)) or described_for() != describe_key():
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(DESCRIBE))
     return all(os.path.getmtime(f) <= t for f in _inputs())
@@ -110,8 +127,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
+        if os.path.exists(STAMP):
+            os.remove(STAMP)
         os.replace(lib_tmp, LIB)
         os.replace(describe_tmp, DESCRIBE)
+        with open(STAMP, "w") as f:
+            f.write(describe_key())
     finally:
         for tmp in (lib_tmp, describe_tmp):
             if os.path.exists(tmp):

@@ -5,6 +5,7 @@ import shutil
 import subprocess
 
 import pytest
+import torch
 
 from paged_kv_cache_185_gb300 import build
 
@@ -34,7 +35,8 @@ def tree(tmp_path, monkeypatch):
     monkeypatch.setenv("PATH", f"{tools}{os.pathsep}{os.environ['PATH']}")
     monkeypatch.setenv("NVCC", str(tools / "nvcc"))
     monkeypatch.setenv("FAIL_ON", "nothing")
-    for name, file in (("BUILD", "_build"), ("LIB", "libwllm.so"), ("DESCRIBE", "_describe.so")):
+    for name, file in (("BUILD", "_build"), ("LIB", "libwllm.so"), ("DESCRIBE", "_describe.so"),
+                       ("STAMP", "_build/describe.stamp")):
         monkeypatch.setattr(build, name, str(pkg / file))
     return pkg
 
@@ -44,6 +46,28 @@ def test_a_build_leaves_its_outputs_alone_in_the_package(tree):
     assert sorted(os.listdir(tree)) == ["_build", "_describe.so", "libwllm.so"]
     assert not [f for f in os.listdir(tree / "_build") if f.endswith(".tmp")]
     assert build.up_to_date()
+
+
+def test_another_torch_or_python_means_a_rebuild(tree, monkeypatch):
+    build.build()
+    assert build.described_for() == build.describe_key() and build.up_to_date()
+    monkeypatch.setattr(torch, "__version__", "9.9")
+    assert not build.up_to_date()
+    build.build()
+    assert build.up_to_date() and "9.9" in build.described_for()
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-399")
+    assert not build.up_to_date()
+    os.remove(build.STAMP)
+    assert not build.up_to_date()  # a module of which nothing says what it was made for
+
+
+def test_calls_refuse_a_module_made_for_another_torch(monkeypatch):
+    from paged_kv_cache_185_gb300 import binding
+    build.build()
+    monkeypatch.setattr(binding, "_invoke", None)
+    monkeypatch.setattr(build, "described_for", lambda: "cpython-399 torch 9.9")
+    with pytest.raises(ImportError, match="built for 'cpython-399 torch 9.9'"):
+        binding._load_calls()
 
 
 @pytest.mark.parametrize("fail", ["select.cu", "describe.cpp", "-shared"])
