@@ -365,7 +365,7 @@ int wllm_update_key_bounds(const wllm_tensor* key_bounds, const wllm_tensor* k_c
   }
   if (d != 64 && d != 128 && d != 256)
     return fail(WLLM_ERR_UNSUPPORTED, "head_dim %lld not supported (64, 128, 256)", (long long)d);
-  if (hkv > 65535 || B > INT32_MAX / 65536) return fail(WLLM_ERR_UNSUPPORTED, "sizes too large");
+  if (hkv > 65535 || B > INT32_MAX / 8) return fail(WLLM_ERR_UNSUPPORTED, "sizes too large");
   if (B == 0 || hkv == 0) return WLLM_OK;
   if (nb < 1) return fail(WLLM_ERR_INVALID_ARG, "the pool has no blocks");
   if (!aligned(k_cache->data, 16) || !aligned(key_bounds->data, 16))

@@ -78,6 +78,19 @@ def test_bounds_of_chunks_behind_other_rows(first):
     assert wllm.device_errors() == 0
 
 
+def test_bounds_of_forty_thousand_sequences():
+    """More sequences than 16 bits count, as a decode may have; several name one block."""
+    g = H.gen(15)
+    B, pool = 40000, 700
+    lens = torch.randint(0, 33, (B,), generator=g, dtype=torch.int32)
+    bt = torch.randint(0, pool, (B, 4), generator=g, dtype=torch.int32)
+    kc, kb = H.cache(g, pool, 2, 8, 64, BF), H.cache(g, pool, 2, 2, 64, BF)
+    assert_bounds(run_bounds(kb, kc, bt, lens), kb, kc, bt, lens, (lens > 0).int())
+    qsl = torch.cat([i32([0]), lens.cumsum(0).to(torch.int32)])
+    assert_bounds(run_bounds(kb, kc, bt, lens, qsl), kb, kc, bt, lens, lens)
+    assert wllm.device_errors() == 0
+
+
 @pytest.mark.parametrize("starts", [[0, 32, 31, 90], [0, 40, 30, 31], [0, 100, 50, 200], [5, 4, 4, 4], [0, 64, 64, 63]])
 def test_bounds_record_starts_that_decrease(starts):
     g = H.gen(14)
