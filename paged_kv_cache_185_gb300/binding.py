@@ -287,6 +287,8 @@ def _rotary(style, sections, eps):
         raise ValueError(f"style must be one of {sorted(_ROTARY_STYLE)}, got {style!r}")
     if len(sections) > 4:
         raise ValueError("at most 4 sections")
+    if any(abs(n) > 0x7fffffff for n in sections):
+        raise ValueError(f"sections out of range: {sections}")
     how = WllmRotary(_ROTARY_STYLE[style], max(1, len(sections)))
     how.sections[:len(sections)] = sections
     how.eps = eps

@@ -53,6 +53,16 @@ for _ in range(2):
     assert r.returncode == 0, r.stderr[-1500:]
 
 
+def test_sections_that_do_not_fit_the_struct_are_refused():
+    """2^32 + 16 pairs are not 16."""
+    x, c = torch.zeros(2, 2, 64), torch.zeros(3, 2, 16, 64)
+    i = torch.zeros(2, dtype=torch.int64)
+    for n in (2 ** 32 + 16, -2 ** 32 + 16):
+        with pytest.raises(ValueError, match="out of range"):
+            binding.rotate_and_cache(x, x, x, x, c, c, i, torch.zeros(2, 2, dtype=torch.int64), torch.zeros(4, 64),
+                                     sections=[n, 16])
+
+
 def test_describe_fills_a_descriptor():
     x = torch.zeros(3, 8, 5, dtype=torch.bfloat16)[:, 2:6, ::2]
     d = binding.describe(x)
