@@ -14,17 +14,20 @@
 // so blocks whose scores differ by more than 2 E are in their true order.  The
 // choice between the few blocks that lie within 2 E of the border is made from
 // their scores in binary64, where the products of 16-bit elements and their
-// sums are exact for all but extreme exponents: the selection is the
-// definition's, whatever the order of the sums.
+// sums are exact for all but extreme exponents: as far as E holds, the selection
+// is the definition's, whatever the order of the sums.
 //
 // 16-bit and E4M3 bounds are scored on tensor cores (mma.sync m16n8k16): 16
 // blocks' bounds are the A operand and B's first three columns are the weights split into three 16-bit words whose sum has
 // their 24 bits, so every product is exact.  An instruction adds 16 products to
-// the running sum; with at least 22 bits kept of each term that is an error of
-// at most 17 * 2^-22 of the magnitudes in it.  Two instructions at a time start
+// the running sum, and no document bounds the error of that sum: what is assumed
+// is that at least 22 bits of each of its 17 terms are kept, an error of at most
+// 17 * 2^-22 of the magnitudes in it.  Two instructions at a time start
 // from zero and their sums are added in binary32, so those magnitudes are two
-// steps' and not the whole row's: 136 2^-24 of all of them, 2D/32 additions,
-// the sum of the columns and the G additions of a weight: c = G + 136 + 2D/32 + 8
+// steps' and not the whole row's: 136 2^-24 of all of them (measured over random,
+// cancelling and uneven products: at most 8 2^-24, which a test keeps watch on),
+// 2D/32 additions, the sum of the columns and the G additions of a weight:
+// c = G + 136 + 2D/32 + 8
 // (one chain over the row would need 68 for each of its 2D/16 instructions, and
 // with it 6 times as many binary64 scores).  E4M3 codes are
 // widened to f16, exactly; three f16 words, scaled so that the largest weight is
