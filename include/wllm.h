@@ -27,6 +27,7 @@
  * Conventions shared by every call:
  *   - Every tensor is described by a wllm_tensor: a device pointer, an element
  *     type, a rank and per-dimension sizes and strides counted in ELEMENTS.
+ *     The pointer is aligned to the element's size (anything else is refused).
  *     The caller owns every buffer; the library never frees or keeps them.
  *   - Every call is asynchronous on `stream` (a cudaStream_t; NULL is the
  *     legacy default stream) and performs no host synchronisation, except in

@@ -224,6 +224,8 @@ int check_desc(const wllm_tensor* t, const char* name, int ndim) {
   for (int i = 0; i < ndim; ++i)
     if (t->shape[i] < 0) return fail(WLLM_ERR_INVALID_ARG, "%s: negative size in dim %d", name, i);
   if (t->data == nullptr && numel(t) > 0) return fail(WLLM_ERR_INVALID_ARG, "%s: null data pointer", name);
+  if (numel(t) > 0 && !aligned(t->data, static_cast<uintptr_t>(elt_size(t->dtype))))  // the kernels' loads would fault
+    return fail(WLLM_ERR_INVALID_ARG, "%s: data must be aligned to its element size", name);
   return WLLM_OK;
 }
 

@@ -200,6 +200,32 @@ def test_sparse_refuses(lib):
     assert sparse(lib, scales=(1.0, 1.0), cache=U8, B=0) == 0
 
 
+@pytest.mark.parametrize("call,name,good", [
+    (rotate, "slots", ((6,), I64)), (rotate, "positions", ((6,), I32)), (rotate, "cos_sin", ((100, 64), F32)),
+    (rotate, "key", ((6, 2, 64), BF)), (rotate, "q_weight", ((64,), BF)),
+    (bounds, "bt", ((3, 4), I32)), (bounds, "cl", ((3,), I32)), (bounds, "qsl", ((4,), I32)),
+    (select, "sel", ((3, 2, 8), I32)), (select, "bt", ((3, 40), I32)), (select, "cl", ((3,), I32)), (select, "q", ((3, 4, 128), BF)),
+    (sparse, "sel", ((3, 2, 8), I32)), (sparse, "bt", ((3, 40), I32)), (sparse, "cl", ((3,), I32)), (sparse, "out", ((3, 4, 128), BF))])
+def test_data_off_its_elements_alignment_is_refused(lib, call, name, good):
+    """Half an element off: the kernel's load would be misaligned.  (Nothing is launched: the check comes first.)"""
+    n = lib.wllm_launch_count()
+    size = torch.empty(0, dtype=good[1]).element_size()
+    assert call(lib, {name: desc(*good, data=0x10000 + size // 2)}) == INVALID
+    assert b"align" in lib.wllm_last_error() and lib.wllm_launch_count() == n
+
+
+def test_indices_off_their_alignment_are_refused_by_the_dense_calls(lib):
+    x, c = desc((3, 2, 64), BF), desc((8, 2, 16, 64), BF)
+    odd = {d: 0x10000 + d // 2 for d in (4, 8)}
+    assert lib.wllm_reshape_and_cache(*map(ctypes.byref, (x, x, c, c, desc((3,), I64, data=odd[8]))), None) == INVALID
+    assert b"slot_mapping" in lib.wllm_last_error()
+    good = dict(bt=desc((3, 4), I32), cl=desc((3,), I32))
+    for name, bad in (("bt", desc((3, 4), I32, data=odd[4])), ("cl", desc((3,), I32, data=odd[4]))):
+        t = dict(good, **{name: bad})
+        assert lib.wllm_paged_attention_decode(*map(ctypes.byref, (x, x, c, c, t["bt"], t["cl"])), 2, 0.1, 16, None) == INVALID
+        assert b"align" in lib.wllm_last_error()
+
+
 def test_binding_refuses():
     x = torch.zeros(2, 2, 64, dtype=BF)
     c = torch.zeros(3, 2, 16, 64, dtype=BF)
