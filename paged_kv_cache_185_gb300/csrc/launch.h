@@ -222,9 +222,10 @@ struct BoundsParams {
   const int32_t* query_start_loc;
   int num_seqs, num_kv_heads, num_blocks, log2_bs;
   int max_tokens;                 // the most a block table row can name
+  unsigned check_ctas;            // set by launch_key_bounds: leading CTAs that check query_start_loc
   int* err;
 };
-int launch_key_bounds(int dtype, int head_dim, const BoundsParams& p, int num_sms, cudaStream_t stream);
+int launch_key_bounds(int dtype, int head_dim, BoundsParams p, int num_sms, cudaStream_t stream);
 
 // The blocks that a decode has to read (select.cu), by their key bounds.
 struct SelectParams {
