@@ -21,7 +21,7 @@
 //     the output, which is as much as the output's own rounding.  The second
 //     product costs nothing where memory sets the pace (256 sequences over E4M3
 //     72.0 us without and 73.6 with it, 8 long ones 15.8 and 15.7) and 7 % where
-//     two head tiles share a fragment of E4M3 codes (30.7 and 33.0).
+//     two head tiles share a fragment of E4M3 codes (30.7 and 33.3).
 // E4M3 codes are widened to f16 in registers, which is exact, with the head_dim
 // order of the fp8 decode; bf16 queries are rounded to f16 for that product.
 //
@@ -32,7 +32,7 @@
 // Bound: memory, each selected K and V byte is read once per head tile.  256
 // sequences with 96 listed blocks, 28/4 heads of 128, E4M3 (401 MB): 73.6 us,
 // 0.80 of the measured copy rate; 8 sequences with 128 blocks, 32/8 heads, bf16
-// (67 MB): 15.6 us, 0.64, the rest lookups, the rings' filling and the merge.
+// (67 MB): 15.8 us, 0.63, the rest lookups, the rings' filling and the merge.
 //
 // F32 caches keep the same split and rings with binary32 FMA (no tensor cores).
 #include <cooperative_groups.h>
@@ -194,6 +194,21 @@ __device__ __forceinline__ void merge_and_store(const SparseParams& p, cg::clust
   cluster.sync();  // a CTA's shared memory outlives its peers' reads
 }
 
+// First words of two weights: below them, so that what is left for the second
+// word is positive and an infinite value comes out infinite (a second word of 0
+// would make it NaN, a negative one too).  Cut off to the 16-bit type: the second
+// word holds the rest within 2^-15 (bf16) or 2^-21 (f16) of the weight.
+__device__ __forceinline__ uint32_t first_words(float w0, float w1, __nv_bfloat16) {
+  uint32_t r;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(w1 * 0.99999237f), "f"(w0 * 0.99999237f));  // 1 - 2^-17
+  return r;
+}
+__device__ __forceinline__ uint32_t first_words(float w0, float w1, __half) {
+  uint32_t r;
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(w1 * 0.99975586f), "f"(w0 * 0.99975586f));  // 1 - 2^-12
+  return r;
+}
+
 // The products of one warp on tensor cores.
 template <typename T, bool F8, int D, int HT>
 struct MmaMath {
@@ -201,6 +216,8 @@ struct MmaMath {
   static constexpr int kNT = HT / 8;  // tiles of 8 heads
   static constexpr int kKS = D / 16;  // k16 steps over head_dim
   static constexpr int kQueryBytes = 0;
+  // weights and their sum are taken times 2^14 in f16: second words are normal numbers then down to weights of 2^-16
+  static constexpr float kWeightShift = std::is_same<M, __half>::value ? 14.f : 0.f;
   uint32_t qf[kNT][kKS][2];
   float m[kNT], l[kNT], o[kKS][kNT][4];
 
@@ -301,11 +318,11 @@ struct MmaMath {
           o[t][a][0] *= f0, o[t][a][1] *= f1, o[t][a][2] *= f0, o[t][a][3] *= f1;
         }
       }
-      const float base = m[a] == -INFINITY ? 0.f : m[a];
+      const float base = (m[a] == -INFINITY ? 0.f : m[a]) - kWeightShift;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const float w0 = ex2_approx(x[2 * half] - base), w1 = ex2_approx(x[2 * half + 1] - base);
-        pf[a][half] = Mma<M>::pack(w0, w1);
+        pf[a][half] = first_words(w0, w1, M());
         const M* w = reinterpret_cast<const M*>(&pf[a][half]);
         pr[a][half] = Mma<M>::pack(w0 - to_f32(w[0]), w1 - to_f32(w[1]));
         l[a] += w0 + w1;

@@ -312,9 +312,9 @@ def test_sparse_decode_keeps_its_weights(dtype, kind, Hq, Hkv, bs):
     Scores are small and lists hold 64 tokens at most, so everything but the output's own rounding is small.  A score is off
     by at most size * (4 products of 16 terms, each instruction within 17 * 2^-22 of the magnitudes in it, = 272 * 2^-24,
     and 8 roundings of scaling and difference), where size = max scale sum |q k|; its exponential by 2^-21 more; both
-    count twice (numerator and sum).  Two words of bf16 leave off 2^-8 * 2^-8 of a weight, two of f16 2^-11 * 2^-11 or, at
-    the subnormal end, 2^-25 of the largest, 1: with weights above 1/16 (scores within 4 log2 units) n of those over their
-    sum are at most 2^-21.  The products with v are up to 8 instructions, 17 * 2^-22 each, and merging and
+    count twice (numerator and sum).  Two words of bf16, the first one cut off, leave off 2^-7 * 2^-8 of a weight, two of f16
+    2^-10 * 2^-11 or, at the subnormal end, 2^-25 of the largest, 1: with weights above 1/16 (scores within 4 log2 units) n
+    of those over their sum are at most 2^-21.  The products with v are up to 8 instructions, 17 * 2^-22 each, and merging and
     scaling 16 roundings.  One word would leave off 2^-9 or 2^-12 of a weight: several times this bound."""
     g = H.gen(Hq + bs)
     D, B, scale = 64, 48, 0.0125
@@ -327,12 +327,45 @@ def test_sparse_decode_keeps_its_weights(dtype, kind, Hq, Hkv, bs):
     got = run_sparse(q, kc, vc, bt, i32(lens), sel, scale)
     ref, mag, size = sparse_ref(q, kc, vc, bt, i32(lens), sel, scale)
     assert 2 * size.max() * math.log2(math.e) < 4
-    word = 2.0 ** -16 if dtype == BF and kind != U8 else 2.0 ** -22
+    word = 2.0 ** -15 if dtype == BF and kind != U8 else 2.0 ** -21
     d = 2 * (torch.expm1(size * 280 * H.U32)[..., None] + 2.0 ** -21) + word + 8 * 17 * 2.0 ** -22 + 16 * H.U32
     vmax = S.values(vc).nan_to_num(0.0).abs().max() * (VS if kind == U8 else 1.0)
     tol = d * mag + 2.0 ** -21 * vmax + H.HALF[dtype] * ref.abs() + H.TINY[dtype]
     off = (got.double() - ref).abs()
     assert (off <= tol).all(), f"{int((off > tol).sum())} off, worst {(off / tol).max().item():.2f} of its bound"
+
+
+@pytest.mark.parametrize("kind", [F32, BF, F16])
+@pytest.mark.parametrize("D,Hq,top", [(64, 4, 3), (128, 9, 40), (256, 2, 40)])
+def test_sparse_decode_of_infinite_values(kind, D, Hq, top):
+    """A value of +-inf with a positive weight comes out infinite, both signs or NaN as NaN, and other elements are as ever;
+    on a row's last token and behind it, where the value is NaN and not looked at."""
+    g = H.gen(D)
+    lens = [700, 33, 17]
+    bt, pool = H.block_tables(g, lens, 16)
+    kc, vc = (H.cache(g, pool, 1, 16, D, kind, bt, lens) for _ in range(2))
+    inf = float("inf")
+    for b, n in enumerate(lens):
+        at = lambda t: (int(bt[b, t // 16]), 0, t % 16)  # noqa: E731
+        vc[at(n - 1)][1], vc[at(0)][2], vc[at(1)][2] = inf, -inf, -inf
+        vc[at(0)][3], vc[at(n - 1)][3], vc[at(2)][5] = inf, -inf, float("nan")
+        for t in range(16):
+            vc[at(t)][D - 1] = inf
+    q = H.randn(g, 3, Hq, D, dtype=kind)
+    sel = torch.full((3, 1, top), -1, dtype=torch.int32)
+    for b, n in enumerate(lens):
+        last = (n - 1) // 16
+        sel[b, 0, :2] = i32([0, last])
+        sel[b, 0, 2:2 + min(top - 2, max(0, last - 1))] = torch.arange(1, last, dtype=torch.int32)[:top - 2]
+    got = run_sparse(q, kc, vc, bt, i32(lens), sel, 0.02)
+    ref, mag, size = sparse_ref(q, kc, vc, bt, i32(lens), sel, 0.02)
+    want = {1: inf, 2: -inf, D - 1: inf}
+    for i, x in want.items():
+        assert (ref[..., i] == x).all() and (got[..., i] == x).all(), i
+    for i in (3, 5):
+        assert ref[..., i].isnan().all() and got[..., i].isnan().all(), i
+    rest = [i for i in range(D) if i not in (1, 2, 3, 5, D - 1)]
+    H.assert_sparse(got[..., rest], ref[..., rest], mag[..., rest], size, kind, False, "beside infinities")
 
 
 @pytest.mark.parametrize("kind", [F32, BF, U8])
