@@ -391,7 +391,7 @@ typedef struct {
  * for the R/2 pairs of `style`, with the table row of the token's position on
  * the pair's axis; elements from R on are not turned.  Everything is computed
  * in binary32 and rounded once, when stored.  Values are copied bit for bit.
- * A token with a negative slot is padding: its position is not read and
+ * A token with a negative slot is padding: its position may be anything and
  * neither its caches' rows nor its row of q_out is written.  A slot or position
  * out of range sets bit 0 or 5 of the error word and leaves the token out (in
  * check mode the call then returns WLLM_ERR_OUT_OF_RANGE; it also rejects
@@ -471,7 +471,9 @@ int wllm_update_key_bounds(const wllm_tensor* key_bounds, const wllm_tensor* k_c
  * their error of the border).  Blocks come in ascending order, then -1.
  * Several query tokens of a sequence are several rows of q, block_tables and
  * context_lens.  D 64, 128 or 256, bs a power of two in [8, 256]; tables of
- * 30,720 blocks at most.  Table entries outside the pool are recorded
+ * 30,720 blocks at most (shared memory is taken by the table's width, not by the
+ * lengths: on tables of more than some 8,000 blocks a call that fills the GPU
+ * takes about a quarter longer).  Table entries outside the pool are recorded
  * (bit 1) and scored as block 0, lengths outside [0, M_b bs] (bit 2) clamped.
  */
 int wllm_select_blocks(const wllm_tensor* selected, const wllm_tensor* q,

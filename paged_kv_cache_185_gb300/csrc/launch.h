@@ -28,8 +28,9 @@ constexpr int kGridCountOffset = 48;  // 8-byte aligned: two ints
 void note_launch();
 
 // Raise a kernel's dynamic shared-memory limit to `bytes` on the current
-// device, once per device: `configured` is the kernel's own per-device record
-// (64 entries).  Thread-safe; two threads racing only repeat the attribute call.
+// device: `configured` is the kernel's own per-device record of the limit (64
+// entries).  Thread-safe: the limit is raised under a lock and never lowered, so a
+// thread that needs less cannot take away what another has just asked for.
 inline int raise_smem_limit(std::atomic<int>* configured, const void* func, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

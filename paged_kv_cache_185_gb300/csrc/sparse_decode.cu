@@ -20,7 +20,7 @@
 //     word alone, as the dense decode takes it, put 2^-9 (bf16) of a weight into
 //     the output, which is as much as the output's own rounding.  The second
 //     product costs nothing where memory sets the pace (256 sequences over E4M3
-//     72.0 us without and 73.6 with it, 8 long ones 15.8 and 15.7) and 7 % where
+//     72.0 us without and 73.7 with it, 8 long ones 15.8 and 15.7) and 8 % where
 //     two head tiles share a fragment of E4M3 codes (30.7 and 33.3).
 // E4M3 codes are widened to f16 in registers, which is exact, with the head_dim
 // order of the fp8 decode; bf16 queries are rounded to f16 for that product.

@@ -133,3 +133,73 @@ for k, c in enumerate(calls):
 assert wllm.device_errors() == 0
 """], cwd=ROOT, capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def last_blocks(g, pool, lens, bs, high):
+    """Tables over the last blocks of a pool: (tables, the same tables into a small pool of those blocks, their ids)."""
+    bt, n = H.block_tables(g, lens, bs, spare=0)
+    ids = torch.arange(pool - n, pool, dtype=torch.int32) if high else torch.arange(n, dtype=torch.int32)
+    return torch.where(bt < 0, bt, ids[bt.clamp(min=0).long()]), bt, ids.long()
+
+
+def test_a_step_at_offsets_beyond_32_bits():
+    """Caches of 2.3e9 elements each: the rotary append, the bounds, the choice and the attention on their last blocks."""
+    g = H.gen(77)
+    Hq, Hkv, D, bs, top = 16, 8, 128, 16, 6
+    pool = 140_000
+    assert pool * Hkv * bs * D > 2 ** 31
+    lens = [200, 31, 333]
+    bt, small, ids = last_blocks(g, pool, lens, bs, True)
+    kc, vc = (torch.empty(pool, Hkv, bs, D, dtype=BF, device="cuda") for _ in range(2))
+    kb = torch.zeros(pool, Hkv, 2, D, dtype=BF, device="cuda")
+    T = sum(lens)
+    pos = torch.cat([torch.arange(n) for n in lens])
+    seq = torch.arange(3).repeat_interleave(torch.tensor(lens))
+    slots = bt[seq, pos // bs].long() * bs + pos % bs
+    assert slots.min() > (pool - len(ids) - 1) * bs
+    q, k, v = (H.randn(g, T, n, D, dtype=BF) for n in (Hq, Hkv, Hkv))
+    table = H.rotary_table(400, D)
+    out_q = torch.empty(T, Hq, D, dtype=BF, device="cuda")
+    wllm.rotate_and_cache(out_q, q.cuda(), k.cuda(), v.cuda(), kc, vc, slots.cuda(), pos.cuda(), table.cuda())
+    btd, cl = bt.cuda(), i32(lens).cuda()
+    qsl = i32([0] + lens).cumsum(0).to(torch.int32)
+    wllm.update_key_bounds(kb, kc, btd, cl, bs, query_start_loc=qsl.cuda())
+    last = out_q[(qsl[1:] - 1).long().cuda()].contiguous()
+    sel = torch.empty(3, Hkv, top, dtype=torch.int32, device="cuda")
+    wllm.select_blocks(sel, last, kb, btd, cl, Hkv, bs, 1, 2)
+    out = wllm.paged_attention_decode_sparse(torch.empty_like(last), last, kc, vc, btd, cl, sel, Hkv, 0.1, bs)
+    torch.cuda.synchronize()
+    assert wllm.device_errors() == 0
+    skc, svc, skb = (x[ids.cuda()].cpu() for x in (kc, vc, kb))
+    rows = skc[(slots // bs - ids[0]), :, slots % bs]
+    H.assert_turned(rows, *S.rotate_rows(k, pos, table), BF, "keys")
+    assert torch.equal(H.bits(svc[(slots // bs - ids[0]), :, slots % bs]), H.bits(v))
+    full = S.key_bounds(skc, small, i32(lens), lens, S.values(torch.zeros_like(skb)))
+    assert torch.equal(S.values(skb), full)
+    want = S.select_blocks(last.cpu(), skb, small, i32(lens), Hkv, bs, top, 1, 2)
+    assert torch.equal(sel.cpu(), want)
+    H.assert_sparse(out.cpu(), *S.sparse_decode(last.cpu(), skc, svc, small, i32(lens), want, float(torch.tensor(0.1))), BF, False, "end")
+
+
+def test_bounds_and_choice_at_byte_offsets_beyond_32_bits():
+    """9 million blocks of E4M3 codes: 4.6 GB of bounds, 18 GB of keys."""
+    g = H.gen(78)
+    D, bs, pool, top = 256, 8, 9_000_000, 9
+    assert pool * 2 * D > 2 ** 32
+    lens = [8 * 100, 8 * 40 + 3]
+    bt, small, ids = last_blocks(g, pool, lens, bs, True)
+    kc = torch.empty(pool, 1, bs, D, dtype=U8, device="cuda")
+    kb = torch.empty(pool, 1, 2, D, dtype=U8, device="cuda")
+    host = H.cache(g, len(ids), 1, bs, D, U8)
+    kc[ids.cuda()] = host.cuda()
+    kb[ids.cuda()] = 0
+    btd, cl = bt.cuda(), i32(lens).cuda()
+    wllm.update_key_bounds(kb, kc, btd, cl, bs, query_start_loc=i32([0, lens[0], sum(lens)]).cuda())
+    q = H.randn(g, 2, 4, D, dtype=F16)
+    sel = torch.empty(2, 1, top, dtype=torch.int32, device="cuda")
+    wllm.select_blocks(sel, q.cuda(), kb, btd, cl, 1, bs, 1, 2)
+    torch.cuda.synchronize()
+    skb = kb[ids.cuda()].cpu()
+    assert torch.equal(S.values(skb), S.key_bounds(host, small, i32(lens), lens, S.values(torch.zeros_like(skb))))
+    assert torch.equal(sel.cpu(), S.select_blocks(q, skb, small, i32(lens), 1, bs, top, 1, 2))
+    assert wllm.device_errors() == 0
