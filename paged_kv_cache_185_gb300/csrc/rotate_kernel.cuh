@@ -155,8 +155,8 @@ __device__ __forceinline__ void load_weight(const RotateParams& p, const void* w
   }
 }
 
-// c + a b where `on`, else c.
-__device__ __forceinline__ float add_product(bool on, float a, float b, float c) { return on ? fmaf(a, b, c) : c; }
+// a b + c where `on`, else a b (to which -0 adds nothing, not even a sign).
+__device__ __forceinline__ float product_and(bool on, float a, float b, float c) { return fmaf(a, b, on ? c : -0.f); }
 
 // What one lane does with its 16 elements of a row: its chunks, the (cos, sin)
 // of its pairs and the factors of the rows of one kind.
@@ -260,22 +260,22 @@ struct RowMath {
     }
     // Behind the rotated part every element stands alone: a product of 0 with its neighbour would bring that one's infinity
     // or NaN along, so the second product of a turn is left out (by a branch around the turn 3001 tokens half turned took
-    // 14.1 us instead of 13.4).
+    // 14.1 us instead of 13.6).  The products are those of a plain turn, in its order.
     if constexpr (ADJACENT) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float x = a[2 * i], y = a[2 * i + 1], z = b[2 * i], w = b[2 * i + 1];
-        a[2 * i] = f * add_product(turns, -gy[i], y, fx[i] * x);
-        a[2 * i + 1] = f * add_product(turns, gx[i], x, fy[i] * y);
-        b[2 * i] = f * add_product(turns, -gy[4 + i], w, fx[4 + i] * z);
-        b[2 * i + 1] = f * add_product(turns, gx[4 + i], z, fy[4 + i] * w);
+        a[2 * i] = f * product_and(turns, fx[i], x, -(gy[i] * y));
+        a[2 * i + 1] = f * product_and(turns, fy[i], y, gx[i] * x);
+        b[2 * i] = f * product_and(turns, fx[4 + i], z, -(gy[4 + i] * w));
+        b[2 * i + 1] = f * product_and(turns, fy[4 + i], w, gx[4 + i] * z);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float x = a[i], y = b[i];
-        a[i] = f * add_product(turns, -gy[i], y, fx[i] * x);
-        b[i] = f * add_product(turns, gx[i], x, fy[i] * y);
+        a[i] = f * product_and(turns, fx[i], x, -(gy[i] * y));
+        b[i] = f * product_and(turns, fy[i], y, gx[i] * x);
       }
     }
   }
