@@ -50,6 +50,19 @@ bool same_shape(const wllm_tensor* a, const wllm_tensor* b);
 bool aligned(const void* p, uintptr_t a);
 bool positive_finite(float x);
 
+// Whether two tensors' spans of memory meet; whether the first `dims` strides and
+// the base of a tensor are multiples of `bytes`.
+bool spans_meet(const wllm_tensor* a, const wllm_tensor* b);
+bool rows_aligned(const wllm_tensor* t, int dims, int64_t bytes);
+
+// The current device's state; takes the lock that covers its creation.
+int locked_state(DeviceState** s);
+
+// Table rows and lengths of B sequences over a pool of nb blocks of bs tokens;
+// the pool's head count and block size against the call's.
+int check_tables(const wllm_tensor* block_tables, const wllm_tensor* context_lens, int64_t B, int64_t nb, int64_t bs);
+int check_pool_args(int64_t hkv, int64_t bs, int num_kv_heads, int block_size);
+
 // TMA map of a [N_b][Hkv][bs][D] pool: 3-D view {D, Hkv*bs, N_b}; one box is
 // 128 bytes of a row by min(bs, 16) rows, 128-byte swizzled.
 int make_pool_map(CUtensorMap* map, const void* base, int dtype, int64_t num_blocks, int64_t hkv, int64_t bs, int64_t d,

@@ -9,7 +9,7 @@
 
 using namespace wllm;
 
-namespace {
+namespace wllm {
 
 // Bytes that a tensor's elements span, and whether two tensors' spans meet.
 bool spans_meet(const wllm_tensor* a, const wllm_tensor* b) {
@@ -66,6 +66,10 @@ int check_pool_args(int64_t hkv, int64_t bs, int num_kv_heads, int block_size) {
     return fail(WLLM_ERR_INVALID_ARG, "block_size %d differs from cache dim %lld", block_size, (long long)bs);
   return WLLM_OK;
 }
+
+}  // namespace wllm
+
+namespace {
 
 int rotate_call(const wllm_tensor* q_out, const wllm_tensor* q, const wllm_tensor* key, const wllm_tensor* value,
                 const wllm_tensor* k_cache, const wllm_tensor* v_cache, const wllm_tensor* slot_mapping,

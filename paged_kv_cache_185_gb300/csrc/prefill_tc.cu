@@ -52,6 +52,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "prefill_rows.cuh"
 #include "tcgen05.cuh"
 
 namespace wllm {
@@ -64,7 +65,6 @@ constexpr int kTcRows = kTcTileRows * kTcTiles;       // query rows per CTA
 constexpr int kTcKv = 128;                            // kv tokens per kv tile
 constexpr int kTcThreads = (2 + 4 * kTcTiles) * 32;   // producer, MMA, four softmax warps per Q tile
 constexpr float kTcRescale = 8.f;                     // the running maximum moves by more than 8 (log2) only
-constexpr int kTcSortSeqs = 64;                       // batches of up to this many sequences: longest first
 
 template <int D>
 struct TcShape {
@@ -122,13 +122,6 @@ __device__ __forceinline__ float add_pair<__half>(float acc, uint32_t w) {
   return acc;
 }
 
-// max(a, b, c) in one three-input max.
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -158,76 +151,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int kvh = static_cast<int>(blockIdx.x % p.num_kv_heads);
   const int tgt_block = static_cast<int>(blockIdx.x / p.num_kv_heads);
 
-  // ---- which (sequence, row block) this CTA owns: sequence b owns
-  // ceil(n_b * G / 256) consecutive row blocks.  With up to kTcSortSeqs
-  // sequences they are taken longest context first (the block scheduler
-  // starts CTAs in launch order, so the longest CTAs start first and the
-  // short ones fill the end); within a sequence its last rows (the longest
-  // context) come first.
+  // ---- which (sequence, row block) this CTA owns
   if (warp == 0) {
-    int seq = -1, tile = 0, base = 0;
-    if (p.num_seqs <= kTcSortSeqs) {
-      // lane l holds sequences l and l + 32: length (the sort key) and row blocks
-      int key[2], nb[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int b = lane + 32 * h;
-        key[h] = -1;
-        nb[h] = 0;
-        if (b < p.num_seqs) {
-          int n = p.query_start_loc[b + 1] - p.query_start_loc[b];
-          n = n < 0 ? 0 : n;
-          nb[h] = static_cast<int>((static_cast<int64_t>(n) * G + kTcRows - 1) / kTcRows);
-          key[h] = p.context_lens[b];
-        }
-      }
-      // start of each of this lane's sequences in the sorted order (ties in sequence order)
-      int start[2] = {0, 0};
-      for (int bb = 0; bb < p.num_seqs; ++bb) {
-        const int kb = __shfl_sync(kFullMask, bb < 32 ? key[0] : key[1], bb & 31);
-        const int nbb = __shfl_sync(kFullMask, bb < 32 ? nb[0] : nb[1], bb & 31);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int b = lane + 32 * h;
-          if (kb > key[h] || (kb == key[h] && bb < b)) start[h] += nbb;
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int b = lane + 32 * h;
-        const bool hit = b < p.num_seqs && tgt_block >= start[h] && tgt_block < start[h] + nb[h];
-        const unsigned m = __ballot_sync(kFullMask, hit);
-        if (m != 0u) {
-          const int src = __ffs(m) - 1;
-          seq = src + 32 * h;
-          tile = __shfl_sync(kFullMask, nb[h] - 1 - (tgt_block - start[h]), src);
-        }
-      }
-    }
-    for (int b0 = 0; b0 < p.num_seqs && seq < 0 && p.num_seqs > kTcSortSeqs; b0 += 32) {
-      const int b = b0 + lane;
-      int n = 0;
-      if (b < p.num_seqs) n = p.query_start_loc[b + 1] - p.query_start_loc[b];
-      n = n < 0 ? 0 : n;
-      const int tiles = static_cast<int>((static_cast<int64_t>(n) * G + kTcRows - 1) / kTcRows);
-      int incl = tiles;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(kFullMask, incl, off);
-        if (lane >= off) incl += v;
-      }
-      const int excl = incl - tiles;
-      const int tgt = tgt_block - base;
-      const unsigned hit = __ballot_sync(kFullMask, b < p.num_seqs && tgt >= excl && tgt < incl);
-      if (hit != 0u) {
-        const int src = __ffs(hit) - 1;
-        seq = b0 + src;
-        const int t_in = tgt - __shfl_sync(kFullMask, excl, src);
-        const int t_all = __shfl_sync(kFullMask, tiles, src);
-        tile = t_all - 1 - t_in;  // the sequence's last rows (longest context) first
-      }
-      base += __shfl_sync(kFullMask, incl, 31);
-    }
+    int seq, tile;
+    row_block_of(p, kTcRows, tgt_block, lane, &seq, &tile);
     if (lane == 0) {
       info[0] = seq;
       info[1] = tile;
