@@ -517,6 +517,165 @@ int wllm_paged_attention_decode_sparse_fp8(const wllm_tensor* out, const wllm_te
                                            float scale, float k_scale, float v_scale,
                                            int block_size, wllm_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * A cache of 8-bit codes with a scale for each block and head, and its tables
+ * kept on the device.
+ *
+ * There is no counterpart to these calls in the pages.  The E4M3 caches above
+ * need scales that fit every key and value that will ever come; here each
+ * (block, kv head) of K and of V has its own, found from what is stored in it:
+ *
+ *   wllm_assign_slots                           blocks, slots, positions of a step
+ *   wllm_reshape_and_cache_block_scaled         the append, which keeps the scales
+ *   wllm_paged_attention_decode_block_scaled    one query token per sequence
+ *   wllm_paged_attention_prefill_block_scaled   chunks of query tokens
+ *
+ * k_scales and v_scales are [N_b][Hkv] F32, dense: K = code * k_scales[block]
+ * [head], V alike.  The append writes powers of two; the attention calls take
+ * any scale from 2^-40 to 2^40 (others, NaN among them, count as the nearer
+ * end; NaN as 2^-40).  Copying a block (e.g. after wllm_bm_append_token) means
+ * copying its scales too.  All can be captured in a CUDA graph (after the
+ * library's first call on the device, which allocates its error word); none
+ * allocates or waits on the host.  Calls on one stream that follow one another
+ * see each other's results.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Blocks, slots and positions for the tokens that each sequence is to get next,
+ * from its length and a list of free blocks, all on the device.
+ *
+ *   slot_mapping      [T] I64, contiguous, written: the slots of the new tokens,
+ *                     packed by sequence, then -1.
+ *   positions         [T] I64, contiguous, written: their places in their
+ *                     sequences, then 0; or NULL.
+ *   query_start_loc   [B+1] I32, contiguous, written: sequence b's rows begin
+ *                     at query_start_loc[b].
+ *   context_lens_out  [B] I32, contiguous, written: the lengths with the new
+ *                     tokens.  May be context_lens itself.
+ *   num_free_out      [1] I32, written.  May be num_free itself.
+ *   block_tables      [B][M_b] I32, rows contiguous: entries of new blocks are
+ *                     written, those before them read where they are needed.
+ *   context_lens      [B] I32, contiguous: L_b tokens held, in the first
+ *                     ceil(L_b / bs) blocks of the table's row.
+ *   new_tokens        [B] I32, contiguous: n_b >= 0 tokens to add; negative: the
+ *                     sequence has ended and gives its blocks back.
+ *   free_blocks       [F] I32, contiguous: a stack, the first num_free entries
+ *                     of which are free blocks.
+ *   num_free          [1] I32.
+ *   block_size        a power of two.
+ *
+ * First the blocks of ended sequences are put on the stack, sequence by
+ * sequence and in the order of their tables (the sequence's length becomes 0).
+ * Then, in the order of the sequences, need_b = ceil((L_b + n_b) / bs) -
+ * ceil(L_b / bs) blocks are taken from its top.  A sequence is served if
+ * L_b + n_b <= M_b bs, the n of it and of the sequences before it sum to at
+ * most T, and need_b = 0 or the need of it and of those before it is at most
+ * the number of free blocks (those that L + n <= M_b bs leaves out count for
+ * neither sum).  One that is not served gets nothing and stays as it was:
+ * query_start_loc and context_lens_out say so.
+ * A block belongs to one sequence here (shared ones are the block manager's).
+ * Lengths outside [0, M_b bs], a sum L + n above it, a num_free outside [0, F]
+ * and blocks given back beyond F set bit 2 of the error word (the sequence is
+ * not served, num_free is clamped, the blocks are lost); negative entries in a
+ * row of the table set bit 1 (no slot for their tokens).  B up to 16384.  No
+ * tensor that is written may overlap another but for the two pairs named.
+ */
+int wllm_assign_slots(const wllm_tensor* slot_mapping, const wllm_tensor* positions,
+                      const wllm_tensor* query_start_loc, const wllm_tensor* context_lens_out,
+                      const wllm_tensor* num_free_out, const wllm_tensor* block_tables,
+                      const wllm_tensor* context_lens, const wllm_tensor* new_tokens,
+                      const wllm_tensor* free_blocks, const wllm_tensor* num_free, int block_size,
+                      wllm_stream stream);
+
+/*
+ * KV append under scales of the blocks' own.
+ *
+ *   key, value       [T][Hkv][D]  F32/F16/BF16 (one type), last dimension
+ *                    contiguous, other strides free.
+ *   k_cache, v_cache [N_b][Hkv][bs][D] WLLM_FP8_E4M3, dense, 16-byte aligned.
+ *   k_scales,
+ *   v_scales         [N_b][Hkv] F32, dense.
+ *   block_tables     [B][M_b] I32; context_lens [B] I32, as in the decode: L_b
+ *                    tokens with the new ones.
+ *   query_start_loc  [B+1] I32, contiguous, not decreasing: sequence b's last
+ *                    n_b = query_start_loc[b+1] - query_start_loc[b] tokens are
+ *                    the rows from query_start_loc[b] on.  NULL: T is B, and row
+ *                    b is the last token of sequence b (no token where L_b = 0).
+ *
+ * For each block that gets new tokens, each kv head, and K and V by themselves:
+ * with m the largest finite magnitude of the new elements,
+ *   need  = 2^e for the least e in [-40, 40] with m <= 448 2^e,
+ *   scale = need if the block's first token is among the new ones, otherwise
+ *           the larger of need and the block's scale so far;
+ * the new elements are stored as E4M3(fp32(x) * fp32(1 / scale)), saturating to
+ * +-448 (NaN stays NaN); where the scale has risen the block's earlier tokens are
+ * stored again as E4M3(value(code) * fp32(old * fp32(1 / scale))), which for
+ * powers of two only rounds what falls below the normal codes.  Tokens behind
+ * the sequence's last and blocks without new tokens are left as they are.
+ * Writing a block's first token again starts its scale anew: write its others
+ * again too.  A block that two sequences append to in one call gets a mixture.
+ * Inconsistent lengths or rows outside [0, T) (bit 2) and table entries outside
+ * the pool (bit 1) are recorded and skipped; where query_start_loc decreases or
+ * its span is more than T or B M_b bs (bit 2), nothing is written.  D 64, 128 or 256, bs a
+ * power of two in [8, 256].
+ */
+int wllm_reshape_and_cache_block_scaled(const wllm_tensor* key, const wllm_tensor* value,
+                                        const wllm_tensor* k_cache, const wllm_tensor* v_cache,
+                                        const wllm_tensor* k_scales, const wllm_tensor* v_scales,
+                                        const wllm_tensor* block_tables,
+                                        const wllm_tensor* context_lens,
+                                        const wllm_tensor* query_start_loc, int block_size,
+                                        wllm_stream stream);
+
+/*
+ * Paged decode attention over such a cache:
+ *   out[b][h] = sum_j softmax_j(scale * q.K_j) * V_j
+ * out, q, block_tables, context_lens, num_kv_heads, scale and block_size as in
+ * wllm_paged_attention_decode_fp8; q and out F16 or BF16 with rows of any
+ * alignment, out apart from q; D 64 (block_size >= 16), 128 or 256.  Codes are widened to f16
+ * exactly; query rows are taken to f16 after a power of two has been divided
+ * out of each, so their size does not matter; the weights, the value's scale in
+ * them, are rounded to f16 for their product; statistics and sums are fp32.
+ *
+ *   workspace        [n] WLLM_FP8_E4M3 (bytes), contiguous, 256-byte aligned, n
+ *                    at least wllm_block_scaled_workspace_bytes(); its first
+ *                    WLLM_BLOCK_SCALED_COUNTER_BYTES must be zero before the
+ *                    first call (every call leaves them so).  Calls that share a workspace
+ *                    must be ordered on the GPU.
+ */
+#define WLLM_BLOCK_SCALED_COUNTER_BYTES 8192
+int wllm_paged_attention_decode_block_scaled(const wllm_tensor* out, const wllm_tensor* q,
+                                             const wllm_tensor* k_cache,
+                                             const wllm_tensor* v_cache,
+                                             const wllm_tensor* k_scales,
+                                             const wllm_tensor* v_scales,
+                                             const wllm_tensor* block_tables,
+                                             const wllm_tensor* context_lens,
+                                             const wllm_tensor* workspace, int num_kv_heads,
+                                             float scale, int block_size, wllm_stream stream);
+
+/* Bytes of workspace that any such call on the current device needs; 0 if the
+ * device could not be asked. */
+size_t wllm_block_scaled_workspace_bytes(void);
+
+/*
+ * Chunked-prefill attention over such a cache: out, q and query_start_loc as in
+ * wllm_paged_attention_prefill, the cache and its scales as above; q and out
+ * rows of any alignment.  D 64 (block_size >= 16) or 128; tensor-core products
+ * (f16, rounded as in the decode above) with fp32 accumulation, one launch, no
+ * workspace.
+ */
+int wllm_paged_attention_prefill_block_scaled(const wllm_tensor* out, const wllm_tensor* q,
+                                              const wllm_tensor* k_cache,
+                                              const wllm_tensor* v_cache,
+                                              const wllm_tensor* k_scales,
+                                              const wllm_tensor* v_scales,
+                                              const wllm_tensor* block_tables,
+                                              const wllm_tensor* context_lens,
+                                              const wllm_tensor* query_start_loc,
+                                              int num_kv_heads, float scale, int block_size,
+                                              wllm_stream stream);
+
 /*
  * Bytes of device workspace that wllm_paged_attention_decode needs for these
  * sizes (0 when no sequence is split).  num_kv_heads is an argument because

@@ -19,7 +19,9 @@ __all__ = ["reshape_and_cache", "paged_attention_decode", "paged_attention_decod
            "reshape_and_cache_fp8", "paged_attention_decode_fp8", "decode_step_fp8",
            "paged_attention_prefill", "paged_attention_prefill_fp8",
            "rotate_and_cache", "rotate_and_cache_fp8", "update_key_bounds", "select_blocks",
-           "paged_attention_decode_sparse", "paged_attention_decode_sparse_fp8"]
+           "paged_attention_decode_sparse", "paged_attention_decode_sparse_fp8",
+           "assign_slots", "reshape_and_cache_block_scaled", "paged_attention_decode_block_scaled",
+           "paged_attention_prefill_block_scaled", "block_scaled_workspace"]
 
 
 def __getattr__(name):

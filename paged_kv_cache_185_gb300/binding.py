@@ -31,6 +31,8 @@ EXPORTED = ("wllm_reshape_and_cache", "wllm_paged_attention_decode", "wllm_decod
             "wllm_paged_attention_decode_noalloc",
             "wllm_rotate_and_cache", "wllm_rotate_and_cache_fp8", "wllm_update_key_bounds", "wllm_select_blocks",
             "wllm_paged_attention_decode_sparse", "wllm_paged_attention_decode_sparse_fp8",
+            "wllm_assign_slots", "wllm_reshape_and_cache_block_scaled", "wllm_paged_attention_decode_block_scaled",
+            "wllm_paged_attention_prefill_block_scaled", "wllm_block_scaled_workspace_bytes",
             "wllm_paged_attention_workspace_bytes", "wllm_set_workspace",
             "wllm_partition_tokens", "wllm_device_errors", "wllm_selftest_wait_timeout", "wllm_launch_count",
             "wllm_last_error", "wllm_version",
@@ -120,6 +122,15 @@ def load_library():
         lib.wllm_paged_attention_decode_sparse_fp8.argtypes = [P] * 7 + [ctypes.c_int, f32, f32, f32, ctypes.c_int,
                                                                        ctypes.c_void_p]
         lib.wllm_paged_attention_decode_sparse_fp8.restype = ctypes.c_int
+        lib.wllm_assign_slots.argtypes = [P] * 10 + [ctypes.c_int, ctypes.c_void_p]
+        lib.wllm_assign_slots.restype = ctypes.c_int
+        lib.wllm_reshape_and_cache_block_scaled.argtypes = [P] * 9 + [ctypes.c_int, ctypes.c_void_p]
+        lib.wllm_reshape_and_cache_block_scaled.restype = ctypes.c_int
+        for attention in (lib.wllm_paged_attention_decode_block_scaled, lib.wllm_paged_attention_prefill_block_scaled):
+            attention.argtypes = [P] * 9 + [ctypes.c_int, f32, ctypes.c_int, ctypes.c_void_p]
+            attention.restype = ctypes.c_int
+        lib.wllm_block_scaled_workspace_bytes.argtypes = []
+        lib.wllm_block_scaled_workspace_bytes.restype = ctypes.c_size_t
         lib.wllm_paged_attention_workspace_bytes.argtypes = [ctypes.c_int] * 6
         lib.wllm_paged_attention_workspace_bytes.restype = ctypes.c_size_t
         lib.wllm_set_workspace.argtypes = [ctypes.c_void_p, ctypes.c_size_t]
@@ -361,6 +372,87 @@ def paged_attention_decode_sparse_fp8(out, q, k_cache, v_cache, block_tables, co
     """paged_attention_decode_sparse over E4M3 caches (K = code * k_scale, V = code * v_scale); returns ``out``."""
     _call("wllm_paged_attention_decode_sparse_fp8", (out, q, k_cache, v_cache, block_tables, context_lens, selected),
           int(num_kv_heads), float(scale), float(k_scale), float(v_scale), int(block_size))
+    return out
+
+
+def assign_slots(slot_mapping, query_start_loc, block_tables, context_lens, new_tokens, free_blocks, num_free,
+                 block_size: int, *, positions=None, context_lens_out=None, num_free_out=None) -> torch.Tensor:
+    """Blocks, slots and positions of the ``new_tokens`` [B] that each sequence is to get next (negative: it has ended
+    and gives its blocks back), from ``context_lens`` [B] and the stack ``free_blocks`` [F] of ``num_free`` [1] blocks.
+
+    Writes ``slot_mapping`` [T] and ``positions`` [T] (packed, then -1 and 0), ``query_start_loc`` [B+1], the tables'
+    new entries, and the lengths and count afterwards (in place unless ``..._out`` are given).  Returns
+    ``slot_mapping``."""
+    _call("wllm_assign_slots", (slot_mapping, positions, query_start_loc,
+                                context_lens if context_lens_out is None else context_lens_out,
+                                num_free if num_free_out is None else num_free_out, block_tables, context_lens, new_tokens,
+                                free_blocks, num_free), int(block_size))
+    return slot_mapping
+
+
+def reshape_and_cache_block_scaled(key, value, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                   block_size: int, query_start_loc=None) -> None:
+    """KV append into E4M3 caches with a scale for each block and head, ``k_scales`` and ``v_scales`` [N_b,Hkv] F32: the
+    last ``query_start_loc[b+1] - query_start_loc[b]`` tokens of each sequence, or one each.  Scales are powers of two;
+    they rise where the new tokens need it (earlier tokens of the block are stored again)."""
+    _call("wllm_reshape_and_cache_block_scaled", (key, value, k_cache, v_cache, k_scales, v_scales, block_tables,
+                                                  context_lens, query_start_loc), int(block_size))
+
+
+_COUNTER_BYTES = 8192  # WLLM_BLOCK_SCALED_COUNTER_BYTES
+_workspaces = {}       # (device, stream) -> what the calls on it share
+
+
+def block_scaled_workspace(device=None) -> torch.Tensor:
+    """A workspace of its own for paged_attention_decode_block_scaled, ready for use (see wllm.h)."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(dev):
+        n = int(load_library().wllm_block_scaled_workspace_bytes())
+        if n == 0:
+            raise WllmError(WLLM_ERR_CUDA, load_library().wllm_last_error().decode())
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        ws[:_COUNTER_BYTES].zero_()
+    return ws
+
+
+def _workspace_of(t):
+    """The workspace of the calls on the current stream of t's device, which follow one another; one of its own for a
+    call that is being captured, whose graph may be replayed on any stream."""
+    if not t.is_cuda:
+        return None  # refused by the call
+    index = t.get_device()
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    ws = _workspaces.get((index, stream))
+    if index == torch._C._cuda_getDevice():
+        capturing = torch._C._cuda_isCurrentStreamCapturing()
+    else:
+        with torch.cuda.device(index):
+            capturing = torch._C._cuda_isCurrentStreamCapturing()
+    if capturing:
+        return block_scaled_workspace(t.device)
+    if ws is None:
+        ws = _workspaces[(index, stream)] = block_scaled_workspace(t.device)
+    return ws
+
+
+def paged_attention_decode_block_scaled(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                        num_kv_heads: int, scale: float, block_size: int, workspace=None) -> torch.Tensor:
+    """Paged decode attention over E4M3 caches with a scale for each block and head; returns ``out``.
+
+    ``workspace``: from block_scaled_workspace(); by default the calls on a stream share one, and a call that is
+    captured in a graph has its own."""
+    _call("wllm_paged_attention_decode_block_scaled", (out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                                       _workspace_of(q) if workspace is None else workspace),
+          int(num_kv_heads), float(scale), int(block_size))
+    return out
+
+
+def paged_attention_prefill_block_scaled(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                         query_start_loc, num_kv_heads: int, scale: float, block_size: int) -> torch.Tensor:
+    """Chunked-prefill paged attention (packed chunks, causal) over E4M3 caches with a scale for each block and head;
+    returns ``out``."""
+    _call("wllm_paged_attention_prefill_block_scaled", (out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                                        query_start_loc), int(num_kv_heads), float(scale), int(block_size))
     return out
 
 

@@ -31,7 +31,9 @@ STAMP = os.path.join(BUILD, "describe.stamp")  # what _describe.so was made for
 
 SOURCES = ["api.cu", "append.cu", "decode_bf16.cu", "decode_f16.cu", "decode_f32.cu", "decode_f8_f16.cu",
            "decode_f8_bf16.cu", "prefill.cu", "prefill_tc.cu", "block_manager.cpp", "api_sparse.cu", "rotate.cu",
-           "rotate_f32.cu", "rotate_f16.cu", "rotate_bf16.cu", "key_bounds.cu", "select.cu", "sparse_decode.cu"]
+           "rotate_f32.cu", "rotate_f16.cu", "rotate_bf16.cu", "key_bounds.cu", "select.cu", "sparse_decode.cu",
+           "api_block_scaled.cu", "assign_slots.cu", "append_block_scaled.cu", "decode_block_scaled.cu",
+           "prefill_block_scaled.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

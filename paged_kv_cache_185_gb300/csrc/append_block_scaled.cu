@@ -1,0 +1,320 @@
+// append_block_scaled.cu -- the KV append into E4M3 caches that have a scale for
+// each block and kv head, found from what is stored.
+//
+// Mathematics: for a block that gets new tokens, a head, and K or V, with m the
+// largest finite magnitude of the new elements,
+//   need = 2^e, the least e in [-40, 40] with m <= 448 2^e,
+//   scale = need where the block's first token is new, else max(need, old scale),
+//   code = E4M3(x * (1 / scale)),
+// and where the scale has risen, the block's earlier codes are stored again times
+// old / scale.  A power of two keeps codes exact through a rise, but for those that
+// fall below 2^-6; a floating-point code gains nothing from a closer scale.
+//
+// Work split: a warp (block_size * head_dim up to 2048 elements, and always for
+// one token a sequence) or a CTA of 2 to 8 warps per (sequence's block, head, K or
+// V).  A warp holds 2048 elements in registers, 16 bytes a lane and load, all in
+// flight together; the maximum is taken in the elements' own type, met by shuffles
+// (and in shared memory), and the same registers are then stored as codes.  Larger
+// blocks are read twice.  Which blocks there are is found on the device from the
+// packed starts.  Bound: memory, each element is read once and its code written.
+#include "common.cuh"
+#include "launch.h"
+
+namespace wllm {
+namespace {
+
+constexpr int kAppendWarps = 4;        // of a CTA whose warps work by themselves
+constexpr int kWarpElements = 2048;    // that a warp holds
+constexpr int kStartsPerThread = 4;    // compared by the CTAs that check them
+
+// 16 bytes of elements: their largest magnitude so far (bits of f32 or packed
+// pairs; NaN never wins), and their values.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ uint32_t most(uint32_t m, uint32_t w) {
+    return __float_as_uint(fmaxf(__uint_as_float(m), fabsf(__uint_as_float(w))));
+  }
+  static __device__ __forceinline__ float widest(uint32_t m) { return __uint_as_float(m); }
+  static __device__ __forceinline__ uint32_t finite(uint32_t w) { return (w & 0x7fffffffu) < 0x7f800000u ? w : 0u; }
+};
+template <>
+struct Vec<__half> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ uint32_t most(uint32_t m, uint32_t w) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w & 0x7fff7fffu));
+    return r;
+  }
+  static __device__ __forceinline__ float widest(uint32_t m) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&m);
+    return fmaxf(__low2float(h), __high2float(h));
+  }
+  static __device__ __forceinline__ uint32_t finite(uint32_t w) {
+    return ((w & 0x7fffu) < 0x7c00u ? w & 0xffffu : 0u) | ((w & 0x7fff0000u) < 0x7c000000u ? w & 0xffff0000u : 0u);
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ uint32_t most(uint32_t m, uint32_t w) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w & 0x7fff7fffu));
+    return r;
+  }
+  static __device__ __forceinline__ float widest(uint32_t m) {
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t finite(uint32_t w) {
+    return ((w & 0x7fffu) < 0x7f80u ? w & 0xffffu : 0u) | ((w & 0x7fff0000u) < 0x7f800000u ? w & 0xffff0000u : 0u);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ uint4 load16(const T* src, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(src);
+  uint4 r;
+  T* e = reinterpret_cast<T*>(&r);
+#pragma unroll
+  for (int i = 0; i < Vec<T>::kN; ++i) e[i] = src[i];
+  return r;
+}
+
+// Codes of 16 bytes of elements times `inv`.
+__device__ __forceinline__ void store_codes(uint8_t* dst, const uint4& x, float inv, float) {
+  const uint32_t c = f32x2_to_e4m3x2(__uint_as_float(x.y) * inv, __uint_as_float(x.x) * inv) |
+                     f32x2_to_e4m3x2(__uint_as_float(x.w) * inv, __uint_as_float(x.z) * inv) << 16;
+  *reinterpret_cast<uint32_t*>(dst) = c;
+}
+__device__ __forceinline__ float2 pair(uint32_t w, __half) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ float2 pair(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ void store_codes(uint8_t* dst, const uint4& x, float inv, T) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = pair(w[i], T());
+    c[i] = f32x2_to_e4m3x2(f.y * inv, f.x * inv);
+  }
+  *reinterpret_cast<uint2*>(dst) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+// 2^e for the least e in the scales' range with m <= 448 2^e; 448 = 1.75 2^8.
+__device__ __forceinline__ float scale_for(float m) {
+  const int e = static_cast<int>((__float_as_uint(m) + 0x1fffffu) >> 23) - 127 - 8;
+  return __uint_as_float(static_cast<uint32_t>(127 + min(max(e, kLeastScaleExp), kMostScaleExp)) << 23);
+}
+__device__ __forceinline__ float scale_in_range(float s) {
+  constexpr float kLeast = 1.f / (1ull << -kLeastScaleExp), kMost = static_cast<float>(1ull << kMostScaleExp);
+  return fminf(fmaxf(s, kLeast), kMost);  // a NaN counts as the least
+}
+
+// Four codes times f, rounded again.
+__device__ __forceinline__ uint32_t rescaled(uint32_t codes, float f) {
+  uint32_t lo, hi;
+  e4m3x4_to_f16x2x2(codes, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return f32x2_to_e4m3x2(a.y * f, a.x * f) | f32x2_to_e4m3x2(b.y * f, b.x * f) << 16;
+}
+
+// Sequence b, whose new tokens are packed rows r = qsl[b] - qsl[0] .. qsl[b+1] -
+// qsl[0], owns the unit numbers from floor(r / bs) + 2 b on: n tokens touch at most
+// floor(n / bs) + 2 blocks, which is no more than the distance to the next
+// sequence's first unit.
+// WPU: warps of a unit (1: a CTA's warps have units of their own).
+template <typename T, int D, int WPU>
+__global__ void __launch_bounds__(WPU == 1 ? kAppendWarps * 32 : WPU * 32) append_block_scaled_kernel(const ScaledAppendParams p) {
+  constexpr int kVecs = D / Vec<T>::kN;                          // 16-byte vectors of a row
+  constexpr int kLoads = kWarpElements / Vec<T>::kN / 32;        // a lane's
+  constexpr int kRows = kWarpElements / D;                       // rows that a warp holds
+  constexpr int kUnitsPerCta = WPU == 1 ? kAppendWarps : 1;
+  __shared__ float met[2][8];
+  grid_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x < p.check_ctas) {  // starts that decrease are recorded whether or not a unit meets them
+#pragma unroll
+    for (int k = 0; k < kStartsPerThread; ++k) {
+      const int64_t i = (int64_t(blockIdx.x) * kStartsPerThread + k) * blockDim.x + threadIdx.x;
+      if (i < p.num_seqs && p.query_start_loc[i + 1] < p.query_start_loc[i]) atomicOr(p.err, kErrLen);
+    }
+    return;
+  }
+  const int part = WPU == 1 ? 0 : warp;  // of the unit
+  const bool speaker = lane == 0 && part == 0;
+  const int bs = 1 << p.log2_bs;
+  int64_t slots = p.num_seqs;  // of every head, K and V
+  int row_first = 0;
+  if (p.query_start_loc != nullptr) {
+    row_first = p.query_start_loc[0];
+    const int64_t total = int64_t(p.query_start_loc[p.num_seqs]) - row_first;
+    if (total < 0 || total > p.num_tokens || total > int64_t(p.num_seqs) * p.max_tokens) {
+      if (blockIdx.x == p.check_ctas && threadIdx.x == 0) atomicOr(p.err, kErrLen);
+      return;
+    }
+    slots = (total >> p.log2_bs) + 2 * int64_t(p.num_seqs);
+  }
+  const int sides = 2 * p.num_kv_heads;
+  const int64_t units = slots * sides;
+  const int64_t first = int64_t(blockIdx.x - p.check_ctas) * kUnitsPerCta + (WPU == 1 ? warp : 0);
+  const int64_t stride = int64_t(gridDim.x - p.check_ctas) * kUnitsPerCta;
+  int turn = 0;
+  for (int64_t unit = first; unit < units; unit += stride) {
+    const int slot = static_cast<int>(unit / sides), side = static_cast<int>(unit - int64_t(slot) * sides);
+    const int h = side >> 1, kv = side & 1;
+    int b = slot, n = 1, j = 0, row = slot;
+    if (p.query_start_loc != nullptr) {
+      // largest b whose first unit is not behind this one: 32 probes at a time
+      int lo = 0, hi = p.num_seqs - 1;
+      while (lo < hi) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = lo + (lane + 1) * step;
+        const bool before = at <= hi && ((p.query_start_loc[at] - row_first) >> p.log2_bs) + 2 * at <= slot;
+        const int k = __popc(__ballot_sync(kFullMask, before));
+        hi = min(hi, lo + (k + 1) * step - 1);
+        lo += k * step;
+      }
+      b = lo;
+      row = p.query_start_loc[b];
+      n = p.query_start_loc[b + 1] - row;
+      j = slot - (((row - row_first) >> p.log2_bs) + 2 * b);
+    }
+    const int len = p.context_lens[b];
+    if (p.query_start_loc == nullptr && len == 0) continue;  // an empty sequence of the one-token form has no new token
+    if (n < 0 || n > len || len > p.max_tokens || j < 0 || row < 0 || n > p.num_tokens - row) {
+      if (speaker) atomicOr(p.err, kErrLen);
+      continue;
+    }
+    if (n == 0) continue;
+    const int begin = len - n;                        // position of the first new token
+    const int at = (begin >> p.log2_bs) + j;          // this unit's block of the sequence
+    if (at > (len - 1) >> p.log2_bs) continue;
+    const int id = p.block_tables[b * p.bt_stride + at];
+    if (id < 0 || id >= p.num_blocks) {
+      if (speaker) atomicOr(p.err, kErrBlock);
+      continue;
+    }
+    const int off = max(0, begin - (at << p.log2_bs));           // first new token in the block
+    const int count = min(bs, len - (at << p.log2_bs)) - off;    // new tokens in it
+    const T* src = static_cast<const T*>(p.src[kv]) + (row + ((at << p.log2_bs) + off - begin)) * p.src_st[kv] + h * p.src_sh[kv];
+    const int64_t run = int64_t(id) * p.num_kv_heads + h;
+    uint8_t* codes = p.cache[kv] + run * bs * D;
+    float* scale_at = p.scales[kv] + run;
+    const float held = off > 0 ? *scale_at : 0.f;
+
+    // the new elements: into registers, or through them where there are more
+    const int64_t st = p.src_st[kv];
+    uint4 x[kLoads];
+    uint32_t most = 0u;
+    auto load = [&](int r0) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int v = i * 32 + lane, r = r0 + v / kVecs;
+        x[i] = r < count ? load16(src + r * st + (v % kVecs) * Vec<T>::kN, p.vec) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    auto measure = [&](bool finite_only) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = Vec<T>::most(most, finite_only ? Vec<T>::finite(w[e]) : w[e]);
+      }
+    };
+    const bool once = count <= kRows * WPU;
+    auto largest = [&](bool finite_only) {
+      most = 0u;
+      for (int r0 = part * kRows; r0 < count; r0 += kRows * WPU) {
+        if (!once || !finite_only) load(r0);
+        measure(finite_only);
+      }
+      float m = Vec<T>::widest(most);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, d));
+      if constexpr (WPU > 1) {
+        if (lane == 0) met[turn & 1][warp] = m;
+        __syncthreads();  // the room of the turn before last is free: every warp has passed the last turn's
+#pragma unroll
+        for (int w = 0; w < WPU; ++w) m = fmaxf(m, met[turn & 1][w]);
+        ++turn;
+      }
+      return m;
+    };
+    float m = largest(false);
+    if (m == INFINITY) m = largest(true);  // infinities do not count (the same for all the unit's warps)
+    const float need = scale_for(m), old = scale_in_range(held);
+    const float scale = off > 0 ? fmaxf(need, old) : need;
+    const float inv = 1.f / scale;
+    for (int r0 = part * kRows; r0 < count; r0 += kRows * WPU) {
+      if (!once) load(r0);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int v = i * 32 + lane, r = r0 + v / kVecs;
+        if (r < count) store_codes(codes + (off + r) * D + (v % kVecs) * Vec<T>::kN, x[i], inv, T());
+      }
+    }
+    if (off > 0 && scale > old) {
+      const float f = old * inv;
+      uint4* again = reinterpret_cast<uint4*>(codes);
+      for (int v = part * 32 + lane; v < off * (D / 16); v += 32 * WPU) {
+        const uint4 c = again[v];
+        again[v] = make_uint4(rescaled(c.x, f), rescaled(c.y, f), rescaled(c.z, f), rescaled(c.w, f));
+      }
+    }
+    if (speaker) *scale_at = scale;
+  }
+}
+
+template <typename T, int D, int WPU>
+int launch_one(ScaledAppendParams p, int num_sms, cudaStream_t stream) {
+  constexpr int kThreads = WPU == 1 ? kAppendWarps * 32 : WPU * 32, kUnits = WPU == 1 ? kAppendWarps : 1;
+  constexpr int kStarts = kStartsPerThread * kThreads;
+  // packed: how many blocks the chunks touch is on the device; as many CTAs as that can be, or as run at once
+  const int64_t slots = p.query_start_loc == nullptr ? p.num_seqs : (int64_t(p.num_tokens) >> p.log2_bs) + 2 * int64_t(p.num_seqs);
+  const int64_t units = slots * 2 * p.num_kv_heads, resident = int64_t(num_sms) * (2048 / kThreads);
+  p.check_ctas = p.query_start_loc != nullptr ? static_cast<unsigned>((int64_t(p.num_seqs) + kStarts - 1) / kStarts) : 0u;
+  int64_t ctas = (units + kUnits - 1) / kUnits;
+  if (ctas > resident) ctas = resident;
+  return launch_dependent(&append_block_scaled_kernel<T, D, WPU>, dim3(static_cast<unsigned>(ctas) + p.check_ctas), dim3(kThreads),
+                          0, 0, stream, p);
+}
+
+template <typename T, int D>
+int launch_dim(const ScaledAppendParams& p, int num_sms, cudaStream_t stream) {
+  const int warps = p.query_start_loc == nullptr ? 1 : (D << p.log2_bs) / kWarpElements;  // that hold a block
+  if (warps <= 1) return launch_one<T, D, 1>(p, num_sms, stream);
+  if (warps == 2) return launch_one<T, D, 2>(p, num_sms, stream);
+  if (warps == 4) return launch_one<T, D, 4>(p, num_sms, stream);
+  return launch_one<T, D, 8>(p, num_sms, stream);
+}
+
+template <typename T>
+int launch_type(const ScaledAppendParams& p, int head_dim, int num_sms, cudaStream_t stream) {
+  switch (head_dim) {
+    case 64: return launch_dim<T, 64>(p, num_sms, stream);
+    case 128: return launch_dim<T, 128>(p, num_sms, stream);
+    case 256: return launch_dim<T, 256>(p, num_sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+int launch_append_block_scaled(int dtype, int head_dim, ScaledAppendParams p, int num_sms, cudaStream_t stream) {
+  int e;
+  switch (dtype) {
+    case 0: e = launch_type<float>(p, head_dim, num_sms, stream); break;
+    case 1: e = launch_type<__half>(p, head_dim, num_sms, stream); break;
+    case 2: e = launch_type<__nv_bfloat16>(p, head_dim, num_sms, stream); break;
+    default: return cudaErrorInvalidValue;
+  }
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+}  // namespace wllm

@@ -1,0 +1,225 @@
+// assign_slots.cu -- block tables, slots, positions and packed starts of the
+// tokens that each sequence is to get next, from lengths and a stack of free
+// blocks on the device.
+//
+// Mathematics: with held_b = ceil(L_b / bs) and need_b = ceil((L_b + n_b) / bs)
+// - held_b, everything follows from prefix sums over the sequences: of the blocks
+// that ended sequences give back (their places on the stack), of the tokens
+// wanted and of the blocks needed (who is served, and which places of the stack
+// are whose), and of the tokens granted (the packed starts).  A row finds its
+// sequence by a binary search in the starts.
+//
+// Work split: one cluster of 1 or 8 CTAs.  Every CTA makes all the sums for
+// itself (a thousand sequences are one load a thread and two scans), keeps starts,
+// lengths and places of the stack in shared memory, and then takes its share of
+// the rows and table entries; so nothing is exchanged but one cluster barrier,
+// which parts what is read from what is written in place (lengths, the count, the
+// stack).  Bound: latency, a chain of dependent reads (length, stack entry, table).
+#include <cooperative_groups.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace cg = cooperative_groups;
+
+namespace wllm {
+namespace {
+
+constexpr int kSlotThreads = 1024;
+constexpr int kSlotWarps = kSlotThreads / 32;
+
+__device__ __forceinline__ long long up(long long x, int d) { return __shfl_up_sync(kFullMask, x, d); }
+
+// Exclusive sums over the block's threads; *total: of all of them.  `room` is
+// shared memory for one element a warp and one more.
+template <int N>
+__device__ __forceinline__ void block_scan(long long (&x)[N], long long (&total)[N], long long* room) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long in[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) in[i] = x[i];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const long long y = up(x[i], d);
+      if (lane >= d) x[i] += y;
+    }
+  __syncthreads();  // the room's last use
+  if (lane == 31)
+#pragma unroll
+    for (int i = 0; i < N; ++i) room[i * (kSlotWarps + 1) + warp] = x[i];
+  __syncthreads();
+  if (warp < N) {
+    const long long mine = room[warp * (kSlotWarps + 1) + lane];
+    long long y = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long z = up(y, d);
+      if (lane >= d) y += z;
+    }
+    __syncwarp();
+    room[warp * (kSlotWarps + 1) + lane] = y - mine;
+    if (lane == 31) room[warp * (kSlotWarps + 1) + 32] = y;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    total[i] = room[i * (kSlotWarps + 1) + 32];
+    x[i] += room[i * (kSlotWarps + 1) + warp] - in[i];
+  }
+}
+
+// What sequence b asks for; `valid`: L + n tokens fit its row of the table.
+struct Ask {
+  int len, held, need, want;
+  bool ended, valid, bad;
+};
+
+__device__ __forceinline__ Ask ask_of(const SlotsParams& p, int b) {
+  const int len = p.context_lens[b], n = p.new_tokens[b];
+  Ask a{len, 0, 0, 0, n < 0, false, false};
+  const bool known = len >= 0 && len <= p.max_tokens;
+  const int round = (1 << p.log2_bs) - 1;
+  if (known) a.held = static_cast<int>((static_cast<long long>(len) + round) >> p.log2_bs);
+  a.valid = known && !a.ended && static_cast<long long>(len) + n <= p.max_tokens;
+  a.bad = !known || (!a.ended && !a.valid);
+  if (a.valid) {
+    a.want = n;
+    a.need = static_cast<int>((static_cast<long long>(len) + n + round) >> p.log2_bs) - a.held;
+  }
+  return a;
+}
+
+__global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotsParams p) {
+  extern __shared__ __align__(16) int32_t table_of_seqs[];  // [B+1] starts, [B] lengths, [B] places of the stack
+  __shared__ long long room[3 * (kSlotWarps + 1)];
+  int32_t* starts = table_of_seqs;
+  int32_t* lens = starts + p.num_seqs + 1;
+  int32_t* tops = lens + p.num_seqs;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int tid = threadIdx.x, lane = tid & 31;
+  grid_wait();
+  grid_launch_dependents();
+
+  // this thread's sequences, one after another
+  const int per = (p.num_seqs + kSlotThreads - 1) / kSlotThreads;
+  const int b0 = min(tid * per, p.num_seqs), b1 = min(b0 + per, p.num_seqs);
+  const int stored = *p.num_free;
+  long long sum[3] = {0, 0, 0}, total[3];  // blocks given back, tokens wanted, blocks needed
+  bool bad = false;
+  Ask first{};  // of b0, which is all of them up to 1024 sequences
+  for (int b = b0; b < b1; ++b) {
+    const Ask a = ask_of(p, b);
+    if (b == b0) first = a;
+    bad |= a.bad;
+    sum[0] += a.ended ? a.held : 0;
+    sum[1] += a.want;
+    sum[2] += a.need;
+  }
+  block_scan<3>(sum, total, room);
+  const int had = min(max(stored, 0), p.free_room);
+  const int count = static_cast<int>(min(static_cast<long long>(had) + total[0], static_cast<long long>(p.free_room)));
+  if (rank == 0 && (bad || (tid == 0 && (stored != had || had + total[0] > p.free_room)))) atomicOr(p.err, kErrLen);
+
+  // who is served
+  long long got[2] = {0, 0}, all[2], want = sum[1], need = sum[2];
+  for (int b = b0; b < b1; ++b) {
+    const Ask a = b == b0 ? first : ask_of(p, b);
+    want += a.want, need += a.need;
+    const bool served = a.valid && want <= p.num_rows && (a.need == 0 || need <= count);
+    lens[b] = a.len;
+    // the place of its first block; of an ended sequence: where its blocks go, as -1 - place
+    tops[b] = a.ended ? -1 - static_cast<int>(min(had + sum[0], static_cast<long long>(p.free_room))) : static_cast<int>(count - 1 - (need - a.need));
+    if (a.ended) sum[0] += a.held;
+    got[0] += served ? a.want : 0;
+    got[1] += served ? a.need : 0;
+  }
+  block_scan<2>(got, all, room);
+  {
+    long long w = sum[1], r = sum[2];
+    int at = static_cast<int>(got[0]);
+    for (int b = b0; b < b1; ++b) {
+      const Ask a = b == b0 ? first : ask_of(p, b);
+      w += a.want, r += a.need;
+      const bool served = a.valid && w <= p.num_rows && (a.need == 0 || r <= count);
+      starts[b] = at;
+      at += served ? a.want : 0;
+    }
+    if (b1 == p.num_seqs && (b1 > b0 || tid == 0)) starts[p.num_seqs] = at;
+  }
+  __syncthreads();
+
+  // blocks of ended sequences go on the stack; a warp a sequence
+  const int warps = ctas * kSlotWarps, warp = rank * kSlotWarps + (tid >> 5);
+  const int round = (1 << p.log2_bs) - 1;
+  if (total[0] > 0) {
+    for (int b = warp; b < p.num_seqs; b += warps) {
+      const int len = lens[b];
+      if (tops[b] >= 0 || len < 0 || len > p.max_tokens || p.new_tokens[b] >= 0) continue;
+      const int32_t* row = p.block_tables + b * p.bt_stride;
+      const int held = static_cast<int>((static_cast<long long>(len) + round) >> p.log2_bs), to = -1 - tops[b];
+      for (int k = lane; k < held && to + k < p.free_room; k += 32) p.free_blocks[to + k] = row[k];
+    }
+  }
+  // everything that is written in place below has been read by every CTA, and the stack is written
+  cluster.sync();
+
+  const int rows = starts[p.num_seqs];
+  for (int b = rank * kSlotThreads + tid; b < p.num_seqs; b += ctas * kSlotThreads) {
+    const int n = starts[b + 1] - starts[b], len = lens[b];
+    p.starts[b] = starts[b];
+    p.lens_out[b] = p.new_tokens[b] < 0 ? 0 : len + n;
+  }
+  if (rank == 0 && tid == 0) {
+    p.starts[p.num_seqs] = rows;
+    *p.free_out = count - static_cast<int>(all[1]);
+  }
+  // table entries of new blocks; a warp a sequence
+  for (int b = warp; b < p.num_seqs; b += warps) {
+    const int n = starts[b + 1] - starts[b], len = lens[b];
+    if (n == 0) continue;
+    const int held = static_cast<int>((static_cast<long long>(len) + round) >> p.log2_bs);
+    const int end = static_cast<int>((static_cast<long long>(len) + n + round) >> p.log2_bs), top = tops[b];
+    int32_t* row = p.block_tables + b * p.bt_stride;
+    for (int j = held + lane; j < end; j += 32) row[j] = p.free_blocks[top - (j - held)];
+  }
+  // rows
+  for (int t = rank * kSlotThreads + tid; t < p.num_rows; t += ctas * kSlotThreads) {
+    long long slot = -1, pos = 0;
+    if (t < rows) {
+      int lo = 0, hi = p.num_seqs - 1;  // the last sequence that begins at or before t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (starts[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      const int len = lens[lo];
+      const int at = len + (t - starts[lo]);
+      const int held = static_cast<int>((static_cast<long long>(len) + round) >> p.log2_bs), j = at >> p.log2_bs;
+      const int block = j < held ? p.block_tables[lo * p.bt_stride + j] : p.free_blocks[tops[lo] - (j - held)];
+      pos = at;
+      if (block >= 0) slot = (static_cast<long long>(block) << p.log2_bs) + (at & round);
+      else atomicOr(p.err, kErrBlock);
+    }
+    p.slots[t] = slot;
+    if (p.positions != nullptr) p.positions[t] = pos;
+  }
+}
+
+}  // namespace
+
+int launch_assign_slots(const SlotsParams& p, cudaStream_t stream) {
+  static std::atomic<int> configured[64];
+  const int smem = (3 * p.num_seqs + 1) * static_cast<int>(sizeof(int32_t));
+  const int e0 = raise_smem_limit(configured, reinterpret_cast<const void*>(&assign_slots_kernel), smem);
+  if (e0 != cudaSuccess) return e0;
+  const int ctas = p.num_rows > 2 * kSlotThreads || p.num_seqs > kSlotThreads ? 8 : 1;
+  const int e = launch_dependent(&assign_slots_kernel, dim3(ctas), dim3(kSlotThreads), smem, ctas, stream, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+}  // namespace wllm

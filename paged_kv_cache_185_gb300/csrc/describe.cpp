@@ -152,6 +152,10 @@ const Kind kinds[] = {
     WLLM_ENTRY(wllm_select_blocks),
     WLLM_ENTRY(wllm_paged_attention_decode_sparse),
     WLLM_ENTRY(wllm_paged_attention_decode_sparse_fp8),
+    WLLM_ENTRY(wllm_assign_slots),
+    WLLM_ENTRY(wllm_reshape_and_cache_block_scaled),
+    WLLM_ENTRY(wllm_paged_attention_decode_block_scaled),
+    WLLM_ENTRY(wllm_paged_attention_prefill_block_scaled),
 };
 #undef WLLM_ENTRY
 

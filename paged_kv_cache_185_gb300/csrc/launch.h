@@ -268,6 +268,84 @@ struct SparseParams {
 int launch_sparse_decode(int dtype, bool kv_fp8, int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap,
                          SparseParams p, int num_sms, cudaStream_t stream);
 
+// Blocks, slots and positions of a step's new tokens (assign_slots.cu).
+struct SlotsParams {
+  int64_t* slots;                 // [T]
+  int64_t* positions;             // [T] or null
+  int32_t* starts;                // [B+1]
+  int32_t* lens_out;              // [B], may be context_lens
+  int32_t* free_out;              // [1], may be num_free
+  int32_t* block_tables;
+  int64_t bt_stride;
+  const int32_t* context_lens;
+  const int32_t* new_tokens;
+  int32_t* free_blocks;
+  const int32_t* num_free;
+  int num_seqs, num_rows, free_room, log2_bs;
+  int max_tokens;                 // the most a block table row can name
+  int* err;
+};
+constexpr int kMaxSlotSeqs = 16384;  // their starts, lengths and places sit in a CTA's shared memory
+int launch_assign_slots(const SlotsParams& p, cudaStream_t stream);
+
+// Exponents of the scales that the block-scaled append writes, and the range
+// that the attention takes.
+constexpr int kLeastScaleExp = -40, kMostScaleExp = 40;
+
+// The append into E4M3 caches with a scale a block and head
+// (append_block_scaled.cu).  A null query_start_loc means one new token a
+// sequence.  Strides in elements.
+struct ScaledAppendParams {
+  const void* src[2];             // key, value
+  int64_t src_st[2], src_sh[2];
+  uint8_t* cache[2];
+  float* scales[2];
+  const int32_t* block_tables;
+  int64_t bt_stride;
+  const int32_t* context_lens;
+  const int32_t* query_start_loc;
+  int num_seqs, num_tokens, num_kv_heads, num_blocks, log2_bs;
+  int max_tokens;                 // the most a block table row can name
+  int vec;                        // rows at 16-byte boundaries
+  unsigned check_ctas;            // set by the launch: leading CTAs that check query_start_loc
+  int* err;
+};
+int launch_append_block_scaled(int dtype, int head_dim, ScaledAppendParams p, int num_sms, cudaStream_t stream);
+
+// Decode attention over such a cache (decode_block_scaled.cu).
+struct ScaledDecodeParams {
+  void* out;                      // [B][Hq][D]
+  const void* q;
+  int64_t q_sb, q_sh, o_sb, o_sh; // strides (elements)
+  const float* k_scales;
+  const float* v_scales;
+  const int32_t* block_tables;
+  int64_t bt_stride;
+  const int32_t* context_lens;
+  int num_seqs, num_q_heads, num_kv_heads, group, head_tiles, num_blocks, log2_bs, max_tokens;
+  int bf16;                       // type of q and out: bf16, else f16
+  int q_pairs, o_pairs;           // rows allow 4-byte accesses
+  float scale_log2;               // scale * log2(e)
+  int* counters;                  // workspace: one a CTA, zero between calls
+  float* parts;                   // workspace: two partial results a CTA
+  unsigned long long wait_limit_ns;
+  int* err;
+};
+int launch_decode_block_scaled(int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap, ScaledDecodeParams p,
+                               int num_sms, cudaStream_t stream);
+size_t decode_block_scaled_workspace(int num_sms);
+
+// Chunked prefill over such a cache (prefill_block_scaled.cu): PrefillParams
+// with scale_log2 of any sign, and what else it needs.
+struct ScaledPrefillParams {
+  PrefillParams base;
+  const float* k_scales;
+  const float* v_scales;
+  int q_vec, o_vec;               // rows at 16-byte boundaries
+};
+int launch_prefill_block_scaled(int dtype, int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                const ScaledPrefillParams& p, int64_t num_tokens, int64_t num_seqs, cudaStream_t stream);
+
 // Check-mode kernels: record index errors in the device error word.
 int launch_check_decode(const int32_t* block_tables, int64_t bt_stride,
                         const int32_t* context_lens, int num_seqs, int max_blocks,
