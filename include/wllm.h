@@ -638,12 +638,10 @@ int wllm_reshape_and_cache_block_scaled(const wllm_tensor* key, const wllm_tenso
  * them, are rounded to f16 for their product; statistics and sums are fp32.
  *
  *   workspace        [n] WLLM_FP8_E4M3 (bytes), contiguous, 256-byte aligned, n
- *                    at least wllm_block_scaled_workspace_bytes(); its first
- *                    WLLM_BLOCK_SCALED_COUNTER_BYTES must be zero before the
- *                    first call (every call leaves them so).  Calls that share a workspace
- *                    must be ordered on the GPU.
+ *                    at least wllm_block_scaled_workspace_bytes(); what is in it
+ *                    does not matter, before or after.  Calls that share a
+ *                    workspace must be ordered on the GPU.
  */
-#define WLLM_BLOCK_SCALED_COUNTER_BYTES 8192
 int wllm_paged_attention_decode_block_scaled(const wllm_tensor* out, const wllm_tensor* q,
                                              const wllm_tensor* k_cache,
                                              const wllm_tensor* v_cache,

@@ -399,50 +399,32 @@ def reshape_and_cache_block_scaled(key, value, k_cache, v_cache, k_scales, v_sca
                                                   context_lens, query_start_loc), int(block_size))
 
 
-_COUNTER_BYTES = 8192  # WLLM_BLOCK_SCALED_COUNTER_BYTES
-_workspaces = {}       # (device, stream) -> what the calls on it share
+@functools.lru_cache(maxsize=None)
+def _block_scaled_workspace_bytes(index: int) -> int:
+    with torch.cuda.device(index):
+        n = int(load_library().wllm_block_scaled_workspace_bytes())
+    if n == 0:
+        raise WllmError(WLLM_ERR_CUDA, load_library().wllm_last_error().decode())
+    return n
 
 
 def block_scaled_workspace(device=None) -> torch.Tensor:
-    """A workspace of its own for paged_attention_decode_block_scaled, ready for use (see wllm.h)."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with torch.cuda.device(dev):
-        n = int(load_library().wllm_block_scaled_workspace_bytes())
-        if n == 0:
-            raise WllmError(WLLM_ERR_CUDA, load_library().wllm_last_error().decode())
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        ws[:_COUNTER_BYTES].zero_()
-    return ws
-
-
-def _workspace_of(t):
-    """The workspace of the calls on the current stream of t's device, which follow one another; one of its own for a
-    call that is being captured, whose graph may be replayed on any stream."""
-    if not t.is_cuda:
-        return None  # refused by the call
-    index = t.get_device()
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    ws = _workspaces.get((index, stream))
-    if index == torch._C._cuda_getDevice():
-        capturing = torch._C._cuda_isCurrentStreamCapturing()
-    else:
-        with torch.cuda.device(index):
-            capturing = torch._C._cuda_isCurrentStreamCapturing()
-    if capturing:
-        return block_scaled_workspace(t.device)
-    if ws is None:
-        ws = _workspaces[(index, stream)] = block_scaled_workspace(t.device)
-    return ws
+    """A workspace for paged_attention_decode_block_scaled (see wllm.h)."""
+    dev = torch.device("cuda" if device is None else device)
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    return torch.empty(_block_scaled_workspace_bytes(index), dtype=torch.uint8, device=torch.device("cuda", index))
 
 
 def paged_attention_decode_block_scaled(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                                         num_kv_heads: int, scale: float, block_size: int, workspace=None) -> torch.Tensor:
     """Paged decode attention over E4M3 caches with a scale for each block and head; returns ``out``.
 
-    ``workspace``: from block_scaled_workspace(); by default the calls on a stream share one, and a call that is
-    captured in a graph has its own."""
+    ``workspace``: from block_scaled_workspace(); by default a call takes one from torch's allocator, which orders it by
+    the stream (and keeps it with the graph that the call is captured in)."""
+    if workspace is None and q.is_cuda:
+        workspace = block_scaled_workspace(q.device)
     _call("wllm_paged_attention_decode_block_scaled", (out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-                                                       _workspace_of(q) if workspace is None else workspace),
+                                                       workspace),
           int(num_kv_heads), float(scale), int(block_size))
     return out
 

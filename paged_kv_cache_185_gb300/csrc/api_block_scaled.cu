@@ -267,8 +267,7 @@ int wllm_paged_attention_decode_block_scaled(const wllm_tensor* out, const wllm_
   p.q_pairs = rows_aligned(q, 2, 4);
   p.o_pairs = rows_aligned(out, 2, 4);
   p.scale_log2 = scale * kLog2e;
-  p.counters = static_cast<int*>(workspace->data);
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace->data) + WLLM_BLOCK_SCALED_COUNTER_BYTES);
+  p.parts = static_cast<float*>(workspace->data);
   p.wait_limit_ns = wait_limit();
   p.err = s->err;
   CUtensorMap kmap, vmap;

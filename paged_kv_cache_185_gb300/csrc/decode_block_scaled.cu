@@ -21,18 +21,28 @@
 //
 // Work split: all units, ordered by sequence, kv head and head tile, are cut into
 // as many equal runs as CTAs fit the GPU, so that rows of any length fill it
-// evenly; a CTA's warps take its units in turn.  At the end of a row the warps'
-// results meet in the stages they have just left, while the next row's copies go
-// on.  A row that several CTAs share is written as partial results (two at most a
-// CTA: the row it begins in and the row it ends in), and the CTA that counts in
-// last merges them in their order: nobody waits, and the result does not depend
-// on who was last.
+// evenly; a CTA's warps take its units in turn.  At the end of a row each warp
+// leaves its results in shared memory and goes on; behind its next unit it merges a
+// quarter of what all left, so hardly a warp waits for another.  A row that several
+// runs share is left as partial results (two at most a run: the row it begins in and
+// the row it ends in), which a second kernel, a programmatic dependent, merges in
+// their order: the result does not depend on timing, and nothing in the workspace
+// outlives the call.
+//
+// Bound: memory, each code is read once.  8 sequences of 32K to 131K tokens, 32/8
+// heads of 128 (1407 MB): 224 us, 0.94 of the measured copy rate; 256 of 300 to 6000,
+// 28/4 heads (829 MB): 144 us, 0.86, the rest the setup and the ends of 4 rows a CTA;
+// one of 16000, 32/4 heads of 64 (8 MB): 12.3 us, all latency.  What it took: warps
+// that wait for nothing at a row's end 171 us instead of 235 (256 sequences), the
+// quarters merged behind the next unit 153, partial results merged by the second
+// kernel instead of the CTA that counts in last, and entries looked up 8 units at a
+// time, 144 (16000 tokens: 17.0 and 12.3).
 #include <atomic>
+#include <climits>
 
 #include "decode_kernel.cuh"
 #include "launch.h"
 #include "mma_e4m3.cuh"
-#include "wllm.h"
 
 namespace wllm {
 namespace {
@@ -41,7 +51,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kWeightShift = 14.f;
 constexpr int kMostCtas = 4;      // of an SM
-constexpr int kLeastUnits = 2;    // of a warp, before another CTA takes part
+constexpr int kLeastUnits = 4;    // of a warp, before another CTA takes part
 
 template <int D, int NT>
 struct Shape {
@@ -52,12 +62,11 @@ struct Shape {
   static constexpr int kOctets = 2 * kSub;               // runs of 8 tokens, each of one block
   static constexpr int kSide = kSub * G::kTileBytes;     // a unit's K (or V)
   static constexpr int kStage = 2 * kSide;
-  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kStages = D == 64 ? 4 : D * NT == 128 ? 3 : 2;
   static constexpr int kRing = kStages * kStage;         // a warp's
   static constexpr int kScales = 8;                      // of a stage: K's octets at 0, V's at 4
-  static constexpr int kSmem = 1024 + kWarps * kRing;
-  static constexpr int kPart = kHeads * D + 2 * kHeads;  // floats of a partial result: outputs, maxima, sums
-  static_assert(kHeads * D * 4 <= kStage, "a warp's outputs take a stage's place");
+  static constexpr int kOut = kHeads * D;                // a warp's outputs
+  static constexpr int kPart = kOut + 2 * kHeads;        // floats of a partial result: outputs, maxima, sums
 };
 
 __device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
@@ -67,7 +76,6 @@ __device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
 __device__ __forceinline__ void arrive_behind_copies(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ float scale_in_range(float s) {
   constexpr float kLeast = 1.f / (1ull << -kLeastScaleExp), kMost = static_cast<float>(1ull << kMostScaleExp);
@@ -75,12 +83,24 @@ __device__ __forceinline__ float scale_in_range(float s) {
 }
 __device__ __forceinline__ float lg2(float x) {
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kNone = -3.402823466e38f;  // the maximum of nothing: 2^(kNone - m) is 0
 
 __device__ __forceinline__ int length_of(const ScaledDecodeParams& p, int b) {
   return min(max(p.context_lens[b], 0), p.max_tokens);
+}
+
+// x / y of numbers that are not negative; 32-bit division where they allow it.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
 }
 
 // A CTA's run of units as segments: the units of one row (sequence, kv head, head
@@ -88,26 +108,29 @@ __device__ __forceinline__ int length_of(const ScaledDecodeParams& p, int b) {
 template <int UNIT>
 struct Segments {
   long long remaining;  // units of the run from this segment on
-  int b, row, rows;     // sequence; row of it, of how many
+  int b, h, tile;       // the row
   int len, units;       // the sequence's
   int at, count;        // the segment: units at .. at + count - 1 of the row
   int turn;             // the run's units before it, modulo the warps
   int window, lens;     // lengths of sequences window .. window + 31, a lane each
 
+  __device__ __forceinline__ void look_at(const ScaledDecodeParams& p, int i) {
+    window = i & ~31;
+    const int mine = window + (threadIdx.x & 31);
+    lens = mine < p.num_seqs ? length_of(p, mine) : 0;
+  }
   __device__ __forceinline__ int length(const ScaledDecodeParams& p, int i) {
-    if ((i & ~31) != window) {
-      window = i & ~31;
-      const int mine = window + (threadIdx.x & 31);
-      lens = mine < p.num_seqs ? length_of(p, mine) : 0;
-    }
+    if ((i & ~31) != window) look_at(p, i);
     return __shfl_sync(kFullMask, lens, i & 31);
   }
-  __device__ __forceinline__ void start(const ScaledDecodeParams& p, int first, long long offset, long long run, int rows_) {
-    window = -1, rows = rows_, b = first, turn = 0, remaining = run;
-    len = length(p, b);
+  // A run that begins with unit `offset` of sequence `first`, which has `length` tokens.
+  __device__ __forceinline__ void start(const ScaledDecodeParams& p, int first, int length, long long offset, long long run) {
+    b = first, len = length, turn = 0, remaining = run;
+    look_at(p, first);
     units = (len + UNIT - 1) / UNIT;
-    row = static_cast<int>(offset / units);
+    const int row = static_cast<int>(quotient(offset, units));
     at = static_cast<int>(offset - static_cast<long long>(row) * units);
+    h = row / p.head_tiles, tile = row - h * p.head_tiles;
     count = static_cast<int>(min(static_cast<long long>(units - at), remaining));
   }
   __device__ __forceinline__ bool next(const ScaledDecodeParams& p) {
@@ -115,8 +138,9 @@ struct Segments {
     turn = (turn + count) & (kWarps - 1);
     if (remaining <= 0) return false;
     at = 0;
-    if (++row == rows) {
-      row = 0;
+    if (++tile == p.head_tiles) tile = 0, ++h;
+    if (h == p.num_kv_heads) {
+      h = 0;
       do {
         if (++b >= p.num_seqs) return false;
         len = length(p, b);
@@ -138,29 +162,38 @@ struct Math {
   uint32_t q[NT][kKS][2];
   float o[kKS][NT][4], m[NT][2], l[NT][2], factor[NT][2];  // factor: of a raw score, without the block's scale
 
-  // Heads 0 .. heads-1 from `src` on, rows `sh` elements apart.
-  template <typename T>
-  __device__ __forceinline__ void load_q(const T* src, int64_t sh, int heads, bool pairs, float scale_log2) {
+  // Elements of heads 0 .. heads-1 from `src` on, rows `sh` elements apart, as they are: asked for here, ...
+  __device__ __forceinline__ void ask_q(const uint16_t* src, int64_t sh, int heads, bool pairs) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool valid = 8 * nt + g < heads;
-      const T* at = src + (valid ? 8 * nt + g : 0) * sh;
-      uint32_t raw[kKS][2], most = 0u;
+      const uint16_t* at = src + (valid ? 8 * nt + g : 0) * sh + 4 * c;
 #pragma unroll
       for (int s = 0; s < kKS; ++s)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const T* d = at + 16 * s + 4 * c + 2 * e;
-          uint32_t x;
-          if (pairs) {
-            x = *reinterpret_cast<const uint32_t*>(d);
-          } else {
-            x = *reinterpret_cast<const uint16_t*>(d) | static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(d + 1)) << 16;
-          }
-          raw[s][e] = valid ? x : 0u;
-          most = max(most, max(raw[s][e] & 0x7fffu, (raw[s][e] >> 16) & 0x7fffu));  // magnitudes' order is their bits'
+          const uint16_t* d = at + 16 * s + 2 * e;
+          const uint32_t x = pairs ? *reinterpret_cast<const uint32_t*>(d) : d[0] | static_cast<uint32_t>(d[1]) << 16;
+          q[nt][s][e] = x;
         }
+    }
+  }
+  // ... and taken to f16 here (columns without a head become zero); the state begins anew.
+  template <typename T>
+  __device__ __forceinline__ void take_q(int heads, float scale_log2) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (8 * nt + g >= heads) {
+#pragma unroll
+        for (int s = 0; s < kKS; ++s) q[nt][s][0] = q[nt][s][1] = 0u;
+      }
+      uint32_t most = 0u;  // magnitudes' order is their bits'
+#pragma unroll
+      for (int s = 0; s < kKS; ++s)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) most = max(most, max(q[nt][s][e] & 0x7fffu, (q[nt][s][e] >> 16) & 0x7fffu));
       most = max(most, __shfl_xor_sync(kFullMask, most, 1));
       most = max(most, __shfl_xor_sync(kFullMask, most, 2));
       // largest magnitude to 2^14 .. 2^15; exponent fields of binary32
@@ -173,13 +206,13 @@ struct Math {
       for (int s = 0; s < kKS; ++s)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const T* x = reinterpret_cast<const T*>(&raw[s][e]);
+          const T* x = reinterpret_cast<const T*>(&q[nt][s][e]);
           q[nt][s][e] = Mma<__half>::pack(to_f32(x[0]) * up, to_f32(x[1]) * up);
         }
       factor[nt][0] = __shfl_sync(kFullMask, down, 8 * c);
       factor[nt][1] = __shfl_sync(kFullMask, down, 8 * c + 4);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) m[nt][i] = -INFINITY, l[nt][i] = 0.f;
+      for (int i = 0; i < 2; ++i) m[nt][i] = kNone, l[nt][i] = 0.f;
 #pragma unroll
       for (int t = 0; t < kKS; ++t)
 #pragma unroll
@@ -224,24 +257,32 @@ struct Math {
       ks[i] = scale_in_range(scales[i]);
       const float vs = scale_in_range(scales[4 + i]);
       add[i] = lg2(vs);
-      inv[i] = __frcp_rn(vs);
+      inv[i] = rcp(vs);
     }
     uint32_t w[S::kSub][NT][2];
     float alpha[NT][2];
     bool moved = false;
-    const bool full = live >= S::kUnit;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float top[2] = {-INFINITY, -INFINITY};
+      float top[2] = {m[nt][0], m[nt][1]};
 #pragma unroll
       for (int j = 0; j < S::kSub; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = 2 * j + (e >> 1);
-          const float x = fmaf(s[j][nt][e], factor[nt][e & 1] * ks[i], add[i]);
-          s[j][nt][e] = full || 8 * i + g < live ? x : -INFINITY;
-          top[e & 1] = fmaxf(top[e & 1], s[j][nt][e]);
+          s[j][nt][e] = fmaf(s[j][nt][e], factor[nt][e & 1] * ks[i], add[i]);
         }
+      if (live < S::kUnit) {
+#pragma unroll
+        for (int j = 0; j < S::kSub; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (16 * j + 8 * (e >> 1) + g >= live) s[j][nt][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j < S::kSub; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top[e & 1] = fmaxf(top[e & 1], s[j][nt][e]);
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
@@ -249,11 +290,10 @@ struct Math {
       float base[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float mn = fmaxf(m[nt][i], top[i]);
-        alpha[nt][i] = m[nt][i] == -INFINITY ? 0.f : exp2f(m[nt][i] - mn);
-        moved |= mn > m[nt][i];
-        m[nt][i] = mn;
-        base[i] = (mn == -INFINITY ? 0.f : mn) - kWeightShift;
+        alpha[nt][i] = ex2_approx(m[nt][i] - top[i]);
+        moved |= top[i] > m[nt][i];
+        m[nt][i] = top[i];
+        base[i] = top[i] - kWeightShift;
         l[nt][i] *= alpha[nt][i];
       }
 #pragma unroll
@@ -301,70 +341,85 @@ struct Math {
     }
   }
 
-  // Outputs [heads][D] to `at`, maxima and sums to `ms` and `ls`.
-  __device__ __forceinline__ void store(float* at, float* ms, float* ls) {
+  // The sums over all lanes' tokens, in every lane of a column.
+  __device__ __forceinline__ void sum_up() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[nt][i] += __shfl_xor_sync(kFullMask, l[nt][i], off);
+  }
+  // Outputs in the fragments' order (16 bytes a lane and store), maxima and sums by head.
+  __device__ __forceinline__ void store(float4* at, float* ms, float* ls) const {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = l[nt][i];
+      for (int i = 0; i < 2; ++i)
+        if (g == 0) ms[8 * nt + 2 * c + i] = m[nt][i], ls[8 * nt + 2 * c + i] = l[nt][i];
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) x += __shfl_xor_sync(kFullMask, x, off);
-        if (g == 0) ms[8 * nt + 2 * c + i] = m[nt][i], ls[8 * nt + 2 * c + i] = x;
-      }
-#pragma unroll
-      for (int t = 0; t < kKS; ++t) {  // rows g and g + 8 are elements 16t + 2g and 16t + 2g + 1
-        const int d = 16 * t + 2 * g;
-        *reinterpret_cast<float2*>(at + (8 * nt + 2 * c) * D + d) = make_float2(o[t][nt][0], o[t][nt][2]);
-        *reinterpret_cast<float2*>(at + (8 * nt + 2 * c + 1) * D + d) = make_float2(o[t][nt][1], o[t][nt][3]);
-      }
+      for (int t = 0; t < kKS; ++t) at[(nt * kKS + t) * 32 + lane] = make_float4(o[t][nt][0], o[t][nt][1], o[t][nt][2], o[t][nt][3]);
     }
   }
 };
 
-// Four outputs of a row.
-__device__ __forceinline__ void store_out(const ScaledDecodeParams& p, int64_t at, float4 v) {
-  uint32_t lo, hi;
-  if (p.bf16) {
-    lo = Mma<__nv_bfloat16>::pack(v.x, v.y), hi = Mma<__nv_bfloat16>::pack(v.z, v.w);
-  } else {
-    lo = Mma<__half>::pack(v.x, v.y), hi = Mma<__half>::pack(v.z, v.w);
-  }
+// Two neighbouring outputs.
+__device__ __forceinline__ void store_out(const ScaledDecodeParams& p, int64_t at, float x, float y) {
+  const uint32_t w = p.bf16 ? Mma<__nv_bfloat16>::pack(x, y) : Mma<__half>::pack(x, y);
   uint16_t* out = static_cast<uint16_t*>(p.out) + at;
   if (p.o_pairs) {
-    reinterpret_cast<uint32_t*>(out)[0] = lo, reinterpret_cast<uint32_t*>(out)[1] = hi;
+    *reinterpret_cast<uint32_t*>(out) = w;
   } else {
-    out[0] = static_cast<uint16_t>(lo), out[1] = static_cast<uint16_t>(lo >> 16);
-    out[2] = static_cast<uint16_t>(hi), out[3] = static_cast<uint16_t>(hi >> 16);
+    out[0] = static_cast<uint16_t>(w), out[1] = static_cast<uint16_t>(w >> 16);
   }
 }
 
+// A row that runs share, left to the merge by the run that has its first unit
+// (0 sharers: the run leaves none).
+struct SharedRow {
+  int b, h, tile, sharers;
+};
+
+// What a CTA has in shared memory.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads)
+struct Shared {
+  using S = Shape<D, NT>;
+  uint8_t ring[kWarps][S::kRing];
+  float4 out[kWarps][S::kOut / 4];  // the warps' outputs of the segment that has ended, in the fragments' order, ...
+  float m[kWarps][S::kHeads], l[kWarps][S::kHeads];  // ... maxima and sums, ...
+  int has[kWarps];                  // ... and whether there are any
+  float scales[kWarps][S::kStages][S::kScales];
+  uint64_t bars[kWarps][S::kStages], stored, free;
+  long long sums[kWarps], first_offset;
+  int first_seq, first_len;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 2)
     decode_block_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                                const ScaledDecodeParams p) {
   using S = Shape<D, NT>;
   using G = typename S::G;
-  extern __shared__ __align__(16) uint8_t unaligned[];
-  __shared__ uint64_t bars[kWarps][S::kStages];
-  __shared__ float scales[kWarps][S::kStages][S::kScales];
-  __shared__ float part_m[kWarps][S::kHeads], part_l[kWarps][S::kHeads];
-  __shared__ int part_stage[kWarps];
-  __shared__ long long sums[kWarps], first_offset;
-  __shared__ int first_seq, last_in;
-  uint8_t* raw = unaligned + ((1024 - (smem_u32(unaligned) & 1023)) & 1023);  // swizzled boxes start at 1024 bytes
+  constexpr int kKS = D / 16;
+  extern __shared__ __align__(1024) uint8_t raw[];  // swizzled boxes start at 1024 bytes
+  Shared<D, NT>& sh = *reinterpret_cast<Shared<D, NT>*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint8_t* ring = raw + warp * S::kRing;
+  uint8_t* ring = sh.ring[warp];
   // a stage: the expected bytes of its copies, and eight lanes' copies of scales
-  if (lane < S::kStages) mbar_init(smem_u32(&bars[warp][lane]), 1 + S::kScales);
+  if (lane < S::kStages) mbar_init(smem_u32(&sh.bars[warp][lane]), 1 + S::kScales);
+  if (tid == 0) {
+    mbar_init(smem_u32(&sh.stored), kWarps);
+    mbar_init(smem_u32(&sh.free), kWarps);
+  }
   fence_mbar_init();
   if (lane == 0) tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
   __syncwarp();
   grid_wait();
   grid_launch_dependents();
 
-  // --- this CTA's run of units
+  // --- this CTA's run of units (it leaves no shared row until it finds one)
+  if (tid == 0) static_cast<SharedRow*>(p.rows)[blockIdx.x] = SharedRow{0, 0, 0, 0};
   const int rows = p.num_kv_heads * p.head_tiles;
   const int per = (p.num_seqs + kThreads - 1) / kThreads;
   const int s0 = min(tid * per, p.num_seqs), s1 = min(s0 + per, p.num_seqs);
@@ -377,24 +432,24 @@ __global__ void __launch_bounds__(kThreads)
     const long long y = __shfl_up_sync(kFullMask, upto, d);
     if (lane >= d) upto += y;
   }
-  if (lane == 31) sums[warp] = upto;
+  if (lane == 31) sh.sums[warp] = upto;
   __syncthreads();
   long long total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) upto += sums[w];
-    total += sums[w];
+    if (w < warp) upto += sh.sums[w];
+    total += sh.sums[w];
   }
   total *= rows;
   const long long ctas = max(1ll, min(static_cast<long long>(gridDim.x), total / (kWarps * kLeastUnits)));
-  const long long c = blockIdx.x;
-  const long long u0 = c < ctas ? total * c / ctas : total, u1 = c < ctas ? total * (c + 1) / ctas : total;
+  const long long c_id = blockIdx.x;
+  const long long u0 = c_id < ctas ? quotient(total * c_id, ctas) : total, u1 = c_id < ctas ? quotient(total * (c_id + 1), ctas) : total;
   if (u0 < u1 && (upto - mine) * rows <= u0 && u0 < upto * rows) {
     long long before = upto - mine;
     for (int b = s0; b < s1; ++b) {
-      const int units = (length_of(p, b) + S::kUnit - 1) / S::kUnit;
+      const int len = length_of(p, b), units = (len + S::kUnit - 1) / S::kUnit;
       if (u0 < (before + units) * rows) {
-        first_seq = b, first_offset = u0 - before * rows;
+        sh.first_seq = b, sh.first_len = len, sh.first_offset = u0 - before * rows;
         break;
       }
       before += units;
@@ -410,8 +465,8 @@ __global__ void __launch_bounds__(kThreads)
     while (empty != 0u) {
       const int seq = __shfl_sync(kFullMask, b, __ffs(empty) - 1);
       empty &= empty - 1;
-      for (int x = lane; x < p.num_q_heads * (D / 4); x += 32)
-        store_out(p, seq * p.o_sb + (x / (D / 4)) * p.o_sh + (x % (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+      for (int x = lane; x < p.num_q_heads * (D / 2); x += 32)
+        store_out(p, seq * p.o_sb + (x / (D / 2)) * p.o_sh + (x % (D / 2)) * 2, 0.f, 0.f);
     }
   }
   __syncthreads();
@@ -419,212 +474,323 @@ __global__ void __launch_bounds__(kThreads)
 
   // --- copies: a cursor of its own runs ahead; the next unit's table entries are asked for one unit early
   Segments<S::kUnit> ahead, seg;
-  seg.start(p, first_seq, first_offset, u1 - u0, rows);
+  seg.start(p, sh.first_seq, sh.first_len, sh.first_offset, u1 - u0);
   ahead = seg;
-  int ahead_at = ahead.first_of(warp), entry = 0, next_t = 0, next_len = 0, next_h = 0;
-  bool more = true;
+  int ahead_at = ahead.first_of(warp);
   const bool two = p.log2_bs < 4;  // 8-token blocks: two 8-row boxes for 16 tokens
   const int bs_mask = (1 << p.log2_bs) - 1;
-  auto look_up = [&] {  // the cursor's unit, which becomes the next to be copied
-    while (more && ahead_at >= ahead.count) {
-      more = ahead.next(p);
+  // Table entries of up to 32 / kOctets units of one segment, a lane an octet; the
+  // batch behind the current one is asked for when that begins.
+  struct Batch {
+    int entry;
+    int t, len, h;    // first token of the first unit; of how many of the sequence; kv head
+    int units;        // 0: none is left
+  };
+  constexpr int kBatchUnits = 32 / S::kOctets;
+  auto look_up = [&](Batch& u) {  // by reference: nothing here waits for the entries
+    u.units = 0;
+    while (ahead_at >= ahead.count) {
+      if (!ahead.next(p)) return;
       ahead_at = ahead.first_of(warp);
     }
-    if (!more) return;
-    next_t = (ahead.at + ahead_at) * S::kUnit, next_len = ahead.len, next_h = ahead.row / p.head_tiles;
-    const int t = next_t + 8 * lane;
-    if (lane < S::kOctets && t < next_len) entry = p.block_tables[ahead.b * p.bt_stride + (t >> p.log2_bs)];
-    ahead_at += kWarps;
+    u.units = min(kBatchUnits, (ahead.count - ahead_at + kWarps - 1) / kWarps);
+    u.t = (ahead.at + ahead_at) * S::kUnit, u.len = ahead.len, u.h = ahead.h;
+    const int t = u.t + (lane / S::kOctets) * (kWarps * S::kUnit) + 8 * (lane % S::kOctets);
+    u.entry = 0;
+    if (lane < u.units * S::kOctets && t < u.len) u.entry = p.block_tables[ahead.b * p.bt_stride + (t >> p.log2_bs)];
+    ahead_at += u.units * kWarps;
   };
-  auto refill = [&](int stage) {
-    if (!more) return;
-    if (lane < S::kOctets && next_t + 8 * lane < next_len && (entry < 0 || entry >= p.num_blocks)) {
-      atomicOr(p.err, kErrBlock);
-      entry = 0;
+  Batch batch{}, later{};
+  int in_batch = 0;
+  auto copy = [&](int stage) {  // the next unit's
+    if (in_batch == batch.units) {
+      if (later.units == 0) return;
+      batch = later, in_batch = 0;
+      if (batch.entry < 0 || batch.entry >= p.num_blocks) {
+        atomicOr(p.err, kErrBlock);
+        batch.entry = 0;
+      }
+      look_up(later);
     }
-    const uint32_t bar = smem_u32(&bars[warp][stage]), dst = smem_u32(ring + stage * S::kStage);
+    const int from = in_batch * S::kOctets, unit_t = batch.t + in_batch * (kWarps * S::kUnit);
+    ++in_batch;
+    const uint32_t bar = smem_u32(&sh.bars[warp][stage]), dst = smem_u32(ring + stage * S::kStage);
     // one box a lane: K or V, column box, 16 tokens (or 8)
     const int x = two ? lane >> 1 : lane, octet_in = two ? lane & 1 : 0;
     const int kv = x & 1, col = (x >> 1) % G::kColBoxes, tile = (x >> 1) / G::kColBoxes;
-    const int octet = 2 * tile + octet_in, t = next_t + 8 * octet;
-    const int phys = __shfl_sync(kFullMask, entry, octet & (S::kOctets - 1));
-    const bool box = tile < S::kSub && t < next_len;
+    const int octet = 2 * tile + octet_in, t = unit_t + 8 * octet;
+    const int phys = __shfl_sync(kFullMask, batch.entry, from + (octet & (S::kOctets - 1)));
+    const bool box = tile < S::kSub && t < batch.len;
     const uint32_t box_bytes = 128u * (G::kPairRows || two ? 8u : 16u);
-    const uint32_t bytes = box_bytes * __popc(__ballot_sync(kFullMask, box));
+    const uint32_t bytes = unit_t + S::kUnit <= batch.len ? static_cast<uint32_t>(S::kStage) : box_bytes * __popc(__ballot_sync(kFullMask, box));
     if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
     __syncwarp();
     if (box) {
-      const int at = (next_h << p.log2_bs) + (t & bs_mask);
+      const int at = (batch.h << p.log2_bs) + (t & bs_mask);
       tma_load_3d(dst + kv * S::kSide + tile * G::kTileBytes + col * 2048 + octet_in * 1024, kv ? &vmap : &kmap, bar, col * 128,
                   G::kPairRows ? at >> 1 : at, phys);
     }
-    const int of = __shfl_sync(kFullMask, entry, lane & 3 & (S::kOctets - 1));
+    const int of = __shfl_sync(kFullMask, batch.entry, from + (lane & (S::kOctets - 1)));
     if (lane < S::kScales) {
       const int i = lane & 3;
-      if (i < S::kOctets && next_t + 8 * i < next_len)
-        copy4_async(smem_u32(&scales[warp][stage][lane]), (lane < 4 ? p.k_scales : p.v_scales) + int64_t(of) * p.num_kv_heads + next_h);
+      if (i < S::kOctets && unit_t + 8 * i < batch.len)
+        copy4_async(smem_u32(&sh.scales[warp][stage][lane]),
+                    (lane < 4 ? p.k_scales : p.v_scales) + int64_t(of) * p.num_kv_heads + batch.h);
       arrive_behind_copies(bar);
     }
-    look_up();
   };
-  look_up();
-#pragma unroll
-  for (int s = 0; s < S::kStages; ++s) refill(s);
+  look_up(later);
 
   int stage = 0;
-  uint32_t phase = 0u;  // of every stage, turned when the ring comes round
+  uint32_t phase = 0u, turn = 0u;  // of every stage, turned when the ring comes round; of the places, with every segment
   bool lost = false;
+  // a wait that runs out: record it, let the copies in flight land (again with a limit), and leave
+  auto give_up = [&] {
+    if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
+    for (int s = 0; s < S::kStages; ++s) mbar_wait_bounded(smem_u32(&sh.bars[warp][s]), s >= stage ? phase : phase ^ 1u, p.wait_limit_ns);
+    lost = true;
+  };
   Math<D, NT> math;
-  while (true) {
-    const int h = seg.row / p.head_tiles, tile = seg.row - h * p.head_tiles;
-    const int heads = min(S::kHeads, p.group - tile * S::kHeads);
-    const int head0 = h * p.group + tile * S::kHeads;
-    const int64_t q_at = seg.b * p.q_sb + head0 * p.q_sh;
-    if (p.bf16) math.load_q(static_cast<const __nv_bfloat16*>(p.q) + q_at, p.q_sh, heads, p.q_pairs, p.scale_log2);
-    else math.load_q(static_cast<const __half*>(p.q) + q_at, p.q_sh, heads, p.q_pairs, p.scale_log2);
+  auto ask_q = [&] {
+    math.ask_q(static_cast<const uint16_t*>(p.q) + seg.b * p.q_sb + (seg.h * p.group + seg.tile * S::kHeads) * p.q_sh, p.q_sh,
+               min(S::kHeads, p.group - seg.tile * S::kHeads), p.q_pairs);
+  };
 
-    int left = -1;  // the stage that this warp's last unit of the segment leaves
-    for (int i = seg.first_of(warp); i < seg.count && !lost; i += kWarps) {
-      if (!mbar_wait_warp(smem_u32(&bars[warp][stage]), phase, p.wait_limit_ns)) {
-        // give up: record it, let what is in flight land (again with a limit), and take no more units
-        if (lane == 0) atomicOr(p.err, kErrWaitTimeout);
-        for (int s = 0; s < S::kStages; ++s) mbar_wait_bounded(smem_u32(&bars[warp][s]), s >= stage ? phase : phase ^ 1u, p.wait_limit_ns);
-        lost = true;
-        break;
-      }
-      math.step(smem_u32(ring + stage * S::kStage), scales[warp][stage], seg.len - (seg.at + i) * S::kUnit);
-      __syncwarp();  // every lane has read the stage
-      if (i + kWarps < seg.count) refill(stage); else left = stage;
-      if (++stage == S::kStages) stage = 0, phase ^= 1u;
+  // The segment that ended last: once every warp has stored its results, each
+  // merges a quarter of the outputs.  It does so behind its first unit of the next
+  // segment, when the others have stored theirs too, so that hardly a warp waits.
+  Segments<S::kUnit> ended = seg;
+  bool owed = false;
+  auto settle = [&] {
+    owed = false;
+    if (!mbar_wait_warp(smem_u32(&sh.stored), (turn - 1u) & 1u, p.wait_limit_ns)) {
+      give_up();
+      return;
     }
-
-    // --- the segment's end: the warps' results meet
-    if (left >= 0) math.store(reinterpret_cast<float*>(ring + left * S::kStage), part_m[warp], part_l[warp]);
-    if (lane == 0) part_stage[warp] = lost ? -1 : left;
-    fence_async_smem();  // the stage is written by copies again
-    __syncthreads();
-    const bool whole = seg.count == seg.units;
-    long long row_first = 0, cta_first = 0;  // of a shared row: its first unit, the first CTA that has one
+    const int g = lane >> 2, c = lane & 3;
+    const bool whole = ended.count == ended.units;
+    const int heads = min(S::kHeads, p.group - ended.tile * S::kHeads);
+    const int64_t out_at = ended.b * p.o_sb + (ended.h * p.group + ended.tile * S::kHeads) * p.o_sh;
+    long long run_first = 0;  // of a shared row: the first run that has a unit of it
     int sharers = 1;
     float* to = nullptr;
     if (!whole) {
-      row_first = u1 - seg.remaining - seg.at;
-      cta_first = ((row_first + 1) * ctas - 1) / total;
-      sharers = static_cast<int>(((row_first + seg.units) * ctas - 1) / total - cta_first) + 1;
-      to = p.parts + (2 * c + (c == cta_first ? 1 : 0)) * S::kPart;
+      const long long row_first = u1 - ended.remaining - ended.at;
+      run_first = quotient((row_first + 1) * ctas - 1, total);
+      sharers = static_cast<int>(quotient((row_first + ended.units) * ctas - 1, total) - run_first) + 1;
+      to = p.parts + (2 * c_id + (c_id == run_first ? 1 : 0)) * S::kPart;
     }
-    for (int i = tid; i < S::kHeads * (D / 4); i += kThreads) {
-      const int a = i / (D / 4), d = (i - a * (D / 4)) * 4;
-      float top = -INFINITY, f[kWarps], sum = 0.f;
-      int at[kWarps];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        at[w] = part_stage[w];
-        if (at[w] >= 0) top = fmaxf(top, part_m[w][a]);
-      }
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int nt = 0; nt < NT; ++nt) {
+      // this lane's two heads: their factors for each warp's outputs
+      float f[kWarps][2];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (at[w] < 0) continue;
-        f[w] = part_m[w][a] == -INFINITY ? 0.f : exp2f(part_m[w][a] - top);
-        sum = fmaf(f[w], part_l[w][a], sum);
-        const float4 x = *reinterpret_cast<const float4*>(raw + w * S::kRing + at[w] * S::kStage + (a * D + d) * 4);
-        v.x = fmaf(f[w], x.x, v.x), v.y = fmaf(f[w], x.y, v.y), v.z = fmaf(f[w], x.z, v.z), v.w = fmaf(f[w], x.w, v.w);
-      }
-      if (whole) {
-        if (a < heads) {
-          const float by = 1.f / sum;
-          store_out(p, seg.b * p.o_sb + (head0 + a) * p.o_sh + d, make_float4(v.x * by, v.y * by, v.z * by, v.w * by));
+      for (int e = 0; e < 2; ++e) {
+        const int a = 8 * nt + 2 * c + e;
+        float top = kNone, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          if (sh.has[w]) top = fmaxf(top, sh.m[w][a]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          f[w][e] = sh.has[w] ? exp2f(sh.m[w][a] - top) : 0.f;
+          if (sh.has[w]) sum = fmaf(f[w][e], sh.l[w][a], sum);
         }
-      } else {
-        *reinterpret_cast<float4*>(to + a * D + d) = v;
-        if (d == 0) to[S::kHeads * D + a] = top, to[S::kHeads * D + S::kHeads + a] = sum;
+        if (!whole && warp == 0 && g == 0) to[S::kOut + a] = top, to[S::kOut + S::kHeads + a] = sum;
+        const float by = whole ? 1.f / sum : 1.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) f[w][e] *= by;
       }
-    }
-    fence_async_smem();
-    __syncthreads();
-    if (!whole) {
-      if (tid == 0) {
-        __threadfence();
-        const int before = atomicAdd(p.counters + cta_first, 1);
-        last_in = before == sharers - 1;
-        if (last_in) p.counters[cta_first] = 0;
-        __threadfence();
-      }
-      __syncthreads();
-      if (last_in) {
-        // the row's partial results in their order, eight at a time
-        for (int i = tid; i < heads * (D / 4); i += kThreads) {
-          const int a = i / (D / 4), d = (i - a * (D / 4)) * 4;
-          float top = -INFINITY, sum = 0.f;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int s0 = 0; s0 < sharers; s0 += 8) {
-            float ms[8], ls[8];
-            float4 x[8];
 #pragma unroll
-            for (int s = 0; s < 8; ++s) {
-              if (s0 + s >= sharers) continue;
-              const float* from = p.parts + (2 * (cta_first + s0 + s) + (s0 + s == 0 ? 1 : 0)) * S::kPart;
-              ms[s] = __ldcg(from + S::kHeads * D + a);
-              ls[s] = __ldcg(from + S::kHeads * D + S::kHeads + a);
-              x[s] = __ldcg(reinterpret_cast<const float4*>(from + a * D + d));
-            }
-            float higher = top;
+      for (int i = 0; i < kKS / kWarps; ++i) {
+        const int t = warp * (kKS / kWarps) + i;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-              if (s0 + s < sharers) higher = fmaxf(higher, ms[s]);
-            const float f0 = top == -INFINITY ? 0.f : exp2f(top - higher);
-            top = higher;
-            sum *= f0, v.x *= f0, v.y *= f0, v.z *= f0, v.w *= f0;
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-              if (s0 + s >= sharers) continue;
-              const float f = ms[s] == -INFINITY ? 0.f : exp2f(ms[s] - top);
-              sum = fmaf(f, ls[s], sum);
-              v.x = fmaf(f, x[s].x, v.x), v.y = fmaf(f, x[s].y, v.y), v.z = fmaf(f, x[s].z, v.z), v.w = fmaf(f, x[s].w, v.w);
-            }
-          }
-          const float by = 1.f / sum;
-          store_out(p, seg.b * p.o_sb + (head0 + a) * p.o_sh + d, make_float4(v.x * by, v.y * by, v.z * by, v.w * by));
+        for (int w = 0; w < kWarps; ++w) {
+          if (!sh.has[w]) continue;
+          const float4 x = sh.out[w][(nt * kKS + t) * 32 + lane];
+          v[0] = fmaf(f[w][0], x.x, v[0]), v[1] = fmaf(f[w][1], x.y, v[1]);
+          v[2] = fmaf(f[w][0], x.z, v[2]), v[3] = fmaf(f[w][1], x.w, v[3]);
+        }
+        if (whole) {  // entries 0, 2 and 1, 3 are neighbours of heads 2c and 2c + 1
+          const int64_t at = out_at + (8 * nt + 2 * c) * p.o_sh + 16 * t + 2 * g;
+          if (8 * nt + 2 * c < heads) store_out(p, at, v[0], v[2]);
+          if (8 * nt + 2 * c + 1 < heads) store_out(p, at + p.o_sh, v[1], v[3]);
+        } else {
+          reinterpret_cast<float4*>(to)[(nt * kKS + t) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
         }
       }
     }
-    if (left >= 0 && !lost) refill(left);
-    if (!seg.next(p)) break;
+    if (!whole && c_id == run_first && warp == 0 && lane == 0)
+      static_cast<SharedRow*>(p.rows)[c_id] = SharedRow{ended.b, ended.h, ended.tile, sharers};
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.free));
+  };
+
+  ask_q();
+#pragma unroll 1
+  for (int s = 0; s < S::kStages; ++s) copy(s);
+  while (true) {
+    const int columns = min(S::kHeads, p.group - seg.tile * S::kHeads);
+    if (p.bf16) math.template take_q<__nv_bfloat16>(columns, p.scale_log2);
+    else math.template take_q<__half>(columns, p.scale_log2);
+    int i = seg.first_of(warp);
+    const bool any = i < seg.count;
+    for (; i < seg.count; i += kWarps) {
+      if (!mbar_wait_warp(smem_u32(&sh.bars[warp][stage]), phase, p.wait_limit_ns)) {
+        give_up();
+        break;
+      }
+      math.step(smem_u32(ring + stage * S::kStage), sh.scales[warp][stage], seg.len - (seg.at + i) * S::kUnit);
+      __syncwarp();  // every lane has read the stage
+      copy(stage);
+      if (++stage == S::kStages) stage = 0, phase ^= 1u;
+      if (owed) {
+        settle();
+        if (lost) break;
+      }
+    }
+    if (lost) break;
+    if (owed) settle();  // no unit of this segment was this warp's
+    if (lost) break;
+    math.sum_up();
+    ended = seg;
+    const bool more_segments = seg.next(p);
+    if (more_segments) ask_q();  // on its way meanwhile
+    // the segment before this one has been merged by every warp
+    if (turn > 0u && !mbar_wait_warp(smem_u32(&sh.free), (turn - 1u) & 1u, p.wait_limit_ns)) {
+      give_up();
+      break;
+    }
+    if (any) math.store(sh.out[warp], sh.m[warp], sh.l[warp]);
+    if (lane == 0) sh.has[warp] = any;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.stored));
+    owed = true;
+    ++turn;
+    if (!more_segments) break;
+  }
+  if (owed && !lost) settle();
+}
+
+// Rows that runs share: CTA i merges the row that run i has the first unit of, the
+// partial results in their order.  A lane has outputs of two heads, in the
+// fragments' order; each warp takes every fourth partial result.
+constexpr int kMergeSplit = 4;
+template <int D, int NT>
+__global__ void __launch_bounds__(kMergeSplit * 32) merge_block_scaled_kernel(const ScaledDecodeParams p) {
+  using S = Shape<D, NT>;
+  constexpr int kKS = D / 16, kTiles = NT * kKS, kBatch = D == 64 ? 8 : D == 128 ? 4 : 2;
+  __shared__ float4 outs[kMergeSplit][kTiles][32];
+  __shared__ float2 ms[kMergeSplit][NT][4], ls[kMergeSplit][NT][4];
+  grid_wait();
+  grid_launch_dependents();
+  const SharedRow row = static_cast<const SharedRow*>(p.rows)[blockIdx.x];
+  if (row.sharers == 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const int64_t first = blockIdx.x;
+#pragma unroll 1
+  for (int nt = 0; nt < NT; ++nt) {
+    const int a = 8 * nt + 2 * c;  // heads a and a + 1
+    float top[2] = {kNone, kNone}, sum[2] = {0.f, 0.f}, v[kKS][4];
+#pragma unroll
+    for (int t = 0; t < kKS; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[t][e] = 0.f;
+    for (int s0 = warp; s0 < row.sharers; s0 += kMergeSplit * kBatch) {
+      float2 m[kBatch], l[kBatch];
+      float4 x[kBatch][kKS];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int s = s0 + k * kMergeSplit;
+        m[k] = make_float2(kNone, kNone);
+        if (s >= row.sharers) continue;
+        const float* from = p.parts + (2 * (first + s) + (s == 0 ? 1 : 0)) * S::kPart;
+        m[k] = *reinterpret_cast<const float2*>(from + S::kOut + a);
+        l[k] = *reinterpret_cast<const float2*>(from + S::kOut + S::kHeads + a);
+#pragma unroll
+        for (int t = 0; t < kKS; ++t) x[k][t] = reinterpret_cast<const float4*>(from)[(nt * kKS + t) * 32 + lane];
+      }
+      float higher[2] = {top[0], top[1]};
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) higher[0] = fmaxf(higher[0], m[k].x), higher[1] = fmaxf(higher[1], m[k].y);
+      const float f0 = exp2f(top[0] - higher[0]), f1 = exp2f(top[1] - higher[1]);
+      top[0] = higher[0], top[1] = higher[1];
+      sum[0] *= f0, sum[1] *= f1;
+#pragma unroll
+      for (int t = 0; t < kKS; ++t) v[t][0] *= f0, v[t][2] *= f0, v[t][1] *= f1, v[t][3] *= f1;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (s0 + k * kMergeSplit >= row.sharers) continue;
+        const float fx = exp2f(m[k].x - top[0]), fy = exp2f(m[k].y - top[1]);
+        sum[0] = fmaf(fx, l[k].x, sum[0]), sum[1] = fmaf(fy, l[k].y, sum[1]);
+#pragma unroll
+        for (int t = 0; t < kKS; ++t) {
+          v[t][0] = fmaf(fx, x[k][t].x, v[t][0]), v[t][2] = fmaf(fx, x[k][t].z, v[t][2]);
+          v[t][1] = fmaf(fy, x[k][t].y, v[t][1]), v[t][3] = fmaf(fy, x[k][t].w, v[t][3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kKS; ++t) outs[warp][nt * kKS + t][lane] = make_float4(v[t][0], v[t][1], v[t][2], v[t][3]);
+    if (g == 0) ms[warp][nt][c] = make_float2(top[0], top[1]), ls[warp][nt][c] = make_float2(sum[0], sum[1]);
+  }
+  __syncthreads();
+  const int heads = min(S::kHeads, p.group - row.tile * S::kHeads);
+  const int64_t out_at = row.b * p.o_sb + (row.h * p.group + row.tile * S::kHeads) * p.o_sh;
+  for (int i = warp; i < kTiles; i += kMergeSplit) {
+    const int nt = i / kKS, t = i - nt * kKS, a = 8 * nt + 2 * c;
+    float top[2] = {kNone, kNone}, sum[2] = {0.f, 0.f}, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kMergeSplit; ++w) top[0] = fmaxf(top[0], ms[w][nt][c].x), top[1] = fmaxf(top[1], ms[w][nt][c].y);
+#pragma unroll
+    for (int w = 0; w < kMergeSplit; ++w) {
+      const float fx = exp2f(ms[w][nt][c].x - top[0]), fy = exp2f(ms[w][nt][c].y - top[1]);
+      const float4 x = outs[w][i][lane];
+      sum[0] = fmaf(fx, ls[w][nt][c].x, sum[0]), v[0] = fmaf(fx, x.x, v[0]), v[2] = fmaf(fx, x.z, v[2]);
+      sum[1] = fmaf(fy, ls[w][nt][c].y, sum[1]), v[1] = fmaf(fy, x.y, v[1]), v[3] = fmaf(fy, x.w, v[3]);
+    }
+    const int64_t at = out_at + a * p.o_sh + 16 * t + 2 * g;
+    const float by0 = 1.f / sum[0], by1 = 1.f / sum[1];
+    if (a < heads) store_out(p, at, v[0] * by0, v[2] * by0);
+    if (a + 1 < heads) store_out(p, at + p.o_sh, v[1] * by1, v[3] * by1);
   }
 }
 
 constexpr int kMostPart = 2080;  // floats of a partial result of any form
 
-// CTAs of a launch: as many as run at once, and have a counter.
-int ctas_of(int num_sms, int resident) {
-  const int most = WLLM_BLOCK_SCALED_COUNTER_BYTES / static_cast<int>(sizeof(int));
-  const int ctas = num_sms * (resident < kMostCtas ? resident : kMostCtas);
-  return ctas < most ? ctas : most;
-}
+// CTAs of a launch: as many as run at once.
+int ctas_of(int num_sms, int resident) { return num_sms * (resident < kMostCtas ? resident : kMostCtas); }
 
 template <int D, int NT>
-int launch_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, const ScaledDecodeParams& p, int num_sms, cudaStream_t stream) {
+int launch_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, ScaledDecodeParams p, int num_sms, cudaStream_t stream) {
   using S = Shape<D, NT>;
+  constexpr int kSmem = static_cast<int>(sizeof(Shared<D, NT>));
+  static_assert(S::kPart <= kMostPart, "the workspace has room for every form's partial results");
   const void* kernel = reinterpret_cast<const void*>(&decode_block_scaled_kernel<D, NT>);
   static std::atomic<int> configured[64], found{0};
-  const int e = raise_smem_limit(configured, kernel, S::kSmem);
+  int e = raise_smem_limit(configured, kernel, kSmem);
   if (e != cudaSuccess) return e;
   int blocks = found.load(std::memory_order_relaxed);
   if (blocks == 0) {
-    const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, &decode_block_scaled_kernel<D, NT>, kThreads, S::kSmem);
+    const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, &decode_block_scaled_kernel<D, NT>, kThreads, kSmem);
     if (err != cudaSuccess) return err;
     found.store(blocks, std::memory_order_relaxed);
   }
-  static_assert(S::kPart <= kMostPart, "the workspace has room for every form's partial results");
-  return launch_dependent(&decode_block_scaled_kernel<D, NT>, dim3(static_cast<unsigned>(ctas_of(num_sms, blocks))), dim3(kThreads),
-                          S::kSmem, 0, stream, kmap, vmap, p);
+  const unsigned ctas = static_cast<unsigned>(ctas_of(num_sms, blocks));
+  p.rows = reinterpret_cast<uint8_t*>(p.parts) + size_t(ctas) * 2 * S::kPart * sizeof(float);
+  e = launch_dependent(&decode_block_scaled_kernel<D, NT>, dim3(ctas), dim3(kThreads), kSmem, 0, stream, kmap, vmap, p);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  e = launch_dependent(&merge_block_scaled_kernel<D, NT>, dim3(ctas), dim3(kMergeSplit * 32), 0, 0, stream, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
 }
 
 }  // namespace
 
 size_t decode_block_scaled_workspace(int num_sms) {
-  return WLLM_BLOCK_SCALED_COUNTER_BYTES + size_t(ctas_of(num_sms, kMostCtas)) * 2 * kMostPart * sizeof(float);
+  return size_t(ctas_of(num_sms, kMostCtas)) * (2 * kMostPart * sizeof(float) + sizeof(SharedRow));
 }
 
 int launch_decode_block_scaled(int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap, ScaledDecodeParams p, int num_sms,
@@ -638,7 +804,7 @@ int launch_decode_block_scaled(int head_dim, const CUtensorMap& kmap, const CUte
     case 128: e = wide ? launch_tile<128, 2>(kmap, vmap, p, num_sms, stream) : launch_tile<128, 1>(kmap, vmap, p, num_sms, stream); break;
     case 256: e = launch_tile<256, 1>(kmap, vmap, p, num_sms, stream); break;
   }
-  if (e == cudaSuccess) note_launch();
   return e;
 }
+
 }  // namespace wllm

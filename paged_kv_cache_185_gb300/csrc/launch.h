@@ -326,8 +326,8 @@ struct ScaledDecodeParams {
   int bf16;                       // type of q and out: bf16, else f16
   int q_pairs, o_pairs;           // rows allow 4-byte accesses
   float scale_log2;               // scale * log2(e)
-  int* counters;                  // workspace: one a CTA, zero between calls
-  float* parts;                   // workspace: two partial results a CTA
+  float* parts;                   // workspace: two partial results a CTA, ...
+  void* rows;                     // ... and the row that it leaves to the merge; set by the launch
   unsigned long long wait_limit_ns;
   int* err;
 };

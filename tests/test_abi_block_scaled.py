@@ -171,11 +171,6 @@ def test_binding_refuses():
         wllm.paged_attention_prefill_block_scaled(x, x, c, c, s, s, i[:, None], i, i, 2, 0.1, 16)
 
 
-def test_header_and_binding_agree_on_the_counters():
-    text = open(os.path.join(build.INCLUDE, "wllm.h")).read()
-    assert int(re.search(r"#define WLLM_BLOCK_SCALED_COUNTER_BYTES (\d+)", text).group(1)) == binding._COUNTER_BYTES
-
-
 FILES = ["assign_slots.cu", "append_block_scaled.cu", "decode_block_scaled.cu", "prefill_block_scaled.cu"]
 
 

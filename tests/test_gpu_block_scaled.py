@@ -713,9 +713,8 @@ def test_streams_and_threads_at_once():
 def test_a_workspace_of_the_callers():
     ws = wllm.block_scaled_workspace()
     case = attention_case(40, BF, [3000, 40], 8, 2, 128, 16)
-    check_decode(*case, 0.08, workspace=ws)
-    assert not ws[:8192].any()
-    check_decode(*case, 0.08, workspace=ws)
+    for fill in (0, 255, 1):  # what is in it does not matter
+        check_decode(*case, 0.08, workspace=ws.fill_(fill))
     for bad in (ws[:-1], ws[1:], ws[::2]):
         with pytest.raises(wllm.WllmError):
             check_decode(*case, 0.08, workspace=bad)
