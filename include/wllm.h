@@ -658,10 +658,10 @@ size_t wllm_block_scaled_workspace_bytes(void);
 
 /*
  * Chunked-prefill attention over such a cache: out, q and query_start_loc as in
- * wllm_paged_attention_prefill, the cache and its scales as above; q and out
- * rows of any alignment.  D 64 (block_size >= 16) or 128; tensor-core products
- * (f16, rounded as in the decode above) with fp32 accumulation, one launch, no
- * workspace.
+ * wllm_paged_attention_prefill, the cache, its scales and the workspace as
+ * above; q and out rows of any alignment.  D 64 (block_size >= 16) or 128;
+ * tensor-core products (f16, rounded as in the decode above) with fp32
+ * accumulation.
  */
 int wllm_paged_attention_prefill_block_scaled(const wllm_tensor* out, const wllm_tensor* q,
                                               const wllm_tensor* k_cache,
@@ -671,8 +671,8 @@ int wllm_paged_attention_prefill_block_scaled(const wllm_tensor* out, const wllm
                                               const wllm_tensor* block_tables,
                                               const wllm_tensor* context_lens,
                                               const wllm_tensor* query_start_loc,
-                                              int num_kv_heads, float scale, int block_size,
-                                              wllm_stream stream);
+                                              const wllm_tensor* workspace, int num_kv_heads,
+                                              float scale, int block_size, wllm_stream stream);
 
 /*
  * Bytes of device workspace that wllm_paged_attention_decode needs for these

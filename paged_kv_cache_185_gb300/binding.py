@@ -126,8 +126,9 @@ def load_library():
         lib.wllm_assign_slots.restype = ctypes.c_int
         lib.wllm_reshape_and_cache_block_scaled.argtypes = [P] * 9 + [ctypes.c_int, ctypes.c_void_p]
         lib.wllm_reshape_and_cache_block_scaled.restype = ctypes.c_int
-        for attention in (lib.wllm_paged_attention_decode_block_scaled, lib.wllm_paged_attention_prefill_block_scaled):
-            attention.argtypes = [P] * 9 + [ctypes.c_int, f32, ctypes.c_int, ctypes.c_void_p]
+        for tensors, attention in ((9, lib.wllm_paged_attention_decode_block_scaled),
+                                   (10, lib.wllm_paged_attention_prefill_block_scaled)):
+            attention.argtypes = [P] * tensors + [ctypes.c_int, f32, ctypes.c_int, ctypes.c_void_p]
             attention.restype = ctypes.c_int
         lib.wllm_block_scaled_workspace_bytes.argtypes = []
         lib.wllm_block_scaled_workspace_bytes.restype = ctypes.c_size_t
@@ -409,7 +410,7 @@ def _block_scaled_workspace_bytes(index: int) -> int:
 
 
 def block_scaled_workspace(device=None) -> torch.Tensor:
-    """A workspace for paged_attention_decode_block_scaled (see wllm.h)."""
+    """A workspace for the paged_attention_*_block_scaled calls (see wllm.h)."""
     dev = torch.device("cuda" if device is None else device)
     index = torch.cuda.current_device() if dev.index is None else dev.index
     return torch.empty(_block_scaled_workspace_bytes(index), dtype=torch.uint8, device=torch.device("cuda", index))
@@ -430,11 +431,15 @@ def paged_attention_decode_block_scaled(out, q, k_cache, v_cache, k_scales, v_sc
 
 
 def paged_attention_prefill_block_scaled(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-                                         query_start_loc, num_kv_heads: int, scale: float, block_size: int) -> torch.Tensor:
+                                         query_start_loc, num_kv_heads: int, scale: float, block_size: int,
+                                         workspace=None) -> torch.Tensor:
     """Chunked-prefill paged attention (packed chunks, causal) over E4M3 caches with a scale for each block and head;
-    returns ``out``."""
+    returns ``out``.  ``workspace`` as in paged_attention_decode_block_scaled."""
+    if workspace is None and q.is_cuda:
+        workspace = block_scaled_workspace(q.device)
     _call("wllm_paged_attention_prefill_block_scaled", (out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-                                                        query_start_loc), int(num_kv_heads), float(scale), int(block_size))
+                                                        query_start_loc, workspace),
+          int(num_kv_heads), float(scale), int(block_size))
     return out
 
 

@@ -2,6 +2,7 @@
 // (wllm_assign_slots, wllm_reshape_and_cache_block_scaled,
 // wllm_paged_attention_decode_block_scaled, wllm_paged_attention_prefill_block_scaled):
 // argument checks and launches.
+#include <algorithm>
 #include <initializer_list>
 
 #include "api_internal.h"
@@ -69,7 +70,7 @@ int check_attention(const wllm_tensor* out, const wllm_tensor* q, const wllm_ten
   if (!(scale == scale) || scale == INFINITY || scale == -INFINITY)
     return fail(WLLM_ERR_INVALID_ARG, "scale must be finite");
   if (d == 64 && bs < 16) return fail(WLLM_ERR_UNSUPPORTED, "head_dim 64 needs block_size >= 16");
-  if (hq > 65535 || block_tables->shape[1] * bs > INT32_MAX - 256 || q->shape[0] * hq > INT32_MAX / 8)
+  if (hq > 65535 || block_tables->shape[1] * bs > INT32_MAX / 32 || q->shape[0] * hq > INT32_MAX / 8)
     return fail(WLLM_ERR_UNSUPPORTED, "sizes too large");
   return WLLM_OK;
 }
@@ -83,6 +84,20 @@ int check_attention_data(const wllm_tensor* k_cache, const wllm_tensor* v_cache)
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+
+size_t workspace_bytes(int num_sms) {
+  return std::max(decode_block_scaled_workspace(num_sms), prefill_block_scaled_workspace(num_sms));
+}
+
+int check_workspace(const wllm_tensor* workspace, int num_sms) {
+  if (workspace->dtype != WLLM_FP8_E4M3) return fail(WLLM_ERR_INVALID_ARG, "workspace must be bytes");
+  if (workspace->shape[0] > 1 && workspace->stride[0] != 1) return fail(WLLM_ERR_INVALID_ARG, "workspace must be contiguous");
+  const size_t need = workspace_bytes(num_sms);
+  if (static_cast<size_t>(workspace->shape[0]) < need)
+    return fail(WLLM_ERR_INVALID_ARG, "workspace has %lld bytes, %zu are needed", (long long)workspace->shape[0], need);
+  if (!aligned(workspace->data, 256)) return fail(WLLM_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return WLLM_OK;
+}
 
 unsigned long long wait_limit() { return static_cast<unsigned long long>(env_int("WLLM_WAIT_LIMIT_NS", 200000000LL)); }
 
@@ -218,7 +233,7 @@ int wllm_reshape_and_cache_block_scaled(const wllm_tensor* key, const wllm_tenso
 
 size_t wllm_block_scaled_workspace_bytes(void) {
   DeviceState* s = nullptr;
-  return locked_state(&s) == WLLM_OK ? decode_block_scaled_workspace(s->num_sms) : 0;
+  return locked_state(&s) == WLLM_OK ? workspace_bytes(s->num_sms) : 0;
 }
 
 int wllm_paged_attention_decode_block_scaled(const wllm_tensor* out, const wllm_tensor* q, const wllm_tensor* k_cache,
@@ -235,16 +250,11 @@ int wllm_paged_attention_decode_block_scaled(const wllm_tensor* out, const wllm_
     return rc;
   if (d != 64 && d != 128 && d != 256)
     return fail(WLLM_ERR_UNSUPPORTED, "head_dim %lld not supported (64, 128, 256)", (long long)d);
-  if (workspace->dtype != WLLM_FP8_E4M3) return fail(WLLM_ERR_INVALID_ARG, "workspace must be bytes");
-  if (workspace->shape[0] > 1 && workspace->stride[0] != 1) return fail(WLLM_ERR_INVALID_ARG, "workspace must be contiguous");
   if (B == 0 || hq == 0) return WLLM_OK;
   if ((rc = check_attention_data(k_cache, v_cache))) return rc;
   DeviceState* s = nullptr;
   if ((rc = locked_state(&s))) return rc;
-  const size_t need = decode_block_scaled_workspace(s->num_sms);
-  if (static_cast<size_t>(workspace->shape[0]) < need)
-    return fail(WLLM_ERR_INVALID_ARG, "workspace has %lld bytes, %zu are needed", (long long)workspace->shape[0], need);
-  if (!aligned(workspace->data, 256)) return fail(WLLM_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if ((rc = check_workspace(workspace, s->num_sms))) return rc;
   ScaledDecodeParams p{};
   p.out = out->data;
   p.q = q->data;
@@ -283,10 +293,11 @@ int wllm_paged_attention_prefill_block_scaled(const wllm_tensor* out, const wllm
                                               const wllm_tensor* v_cache, const wllm_tensor* k_scales,
                                               const wllm_tensor* v_scales, const wllm_tensor* block_tables,
                                               const wllm_tensor* context_lens, const wllm_tensor* query_start_loc,
-                                              int num_kv_heads, float scale, int block_size, wllm_stream stream) {
+                                              const wllm_tensor* workspace, int num_kv_heads, float scale, int block_size,
+                                              wllm_stream stream) {
   int rc;
   if ((rc = check_desc(out, "out", 3)) || (rc = check_desc(q, "q", 3)) || (rc = check_desc(block_tables, "block_tables", 2)) ||
-      (rc = check_desc(context_lens, "context_lens", 1)))
+      (rc = check_desc(context_lens, "context_lens", 1)) || (rc = check_desc(workspace, "workspace", 1)))
     return rc;
   const int64_t T = q->shape[0], hq = q->shape[1], d = q->shape[2], B = context_lens->shape[0];
   if ((rc = check_attention(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, B, num_kv_heads, scale, block_size)) ||
@@ -321,17 +332,19 @@ int wllm_paged_attention_prefill_block_scaled(const wllm_tensor* out, const wllm
   p.wait_limit_ns = wait_limit();
   sp.k_scales = static_cast<const float*>(k_scales->data);
   sp.v_scales = static_cast<const float*>(v_scales->data);
+  sp.parts = static_cast<float*>(workspace->data);
   sp.q_vec = rows_aligned(q, 2, 16);
   sp.o_vec = rows_aligned(out, 2, 16);
   DeviceState* s = nullptr;
   if ((rc = locked_state(&s))) return rc;
+  if ((rc = check_workspace(workspace, s->num_sms))) return rc;
   p.err = s->err;
   CUtensorMap kmap, vmap;
   if ((rc = make_pool_map(&kmap, k_cache->data, WLLM_FP8_E4M3, nb, hkv, bs, d, "k_cache"))) return rc;
   if ((rc = make_pool_map(&vmap, v_cache->data, WLLM_FP8_E4M3, nb, hkv, bs, d, "v_cache"))) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = static_cast<cudaError_t>(
-      launch_prefill_block_scaled(q->dtype, static_cast<int>(d), kmap, vmap, sp, T, B, st));
+      launch_prefill_block_scaled(q->dtype, static_cast<int>(d), kmap, vmap, sp, T, B, s->num_sms, st));
   if (e != cudaSuccess) return cuda_fail(e, "block-scaled prefill launch");
   return env_flag("WLLM_CHECK") ? collect_device_errors(s, st, "paged_attention_prefill_block_scaled") : WLLM_OK;
 }

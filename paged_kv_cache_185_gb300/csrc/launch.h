@@ -341,10 +341,13 @@ struct ScaledPrefillParams {
   PrefillParams base;
   const float* k_scales;
   const float* v_scales;
+  float* parts;                   // workspace: partial results of rows whose context several CTAs share
   int q_vec, o_vec;               // rows at 16-byte boundaries
+  int splits;                     // CTAs of a row block's context; set by the launch
 };
-int launch_prefill_block_scaled(int dtype, int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                                const ScaledPrefillParams& p, int64_t num_tokens, int64_t num_seqs, cudaStream_t stream);
+int launch_prefill_block_scaled(int dtype, int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap, ScaledPrefillParams p,
+                                int64_t num_tokens, int64_t num_seqs, int num_sms, cudaStream_t stream);
+size_t prefill_block_scaled_workspace(int num_sms);
 
 // Check-mode kernels: record index errors in the device error word.
 int launch_check_decode(const int32_t* block_tables, int64_t bt_stride,

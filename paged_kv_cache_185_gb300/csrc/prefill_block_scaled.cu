@@ -13,28 +13,37 @@
 // numbers of f16 down to 2^-21.  l sums the weights before they are rounded: behind
 // a small vs a weight may round to nothing and still count in l.
 //
-// One CTA (one per SM) owns 256 query rows of one sequence and one kv head, as two
-// 128-row tiles, row r being (token r / G, query head r % G of the group), and
-// walks the rows' context in tiles of 128 tokens.  Tensor memory holds, per Q tile,
-// the scores S (128 columns), over which the softmax writes the weights P (f16, two
-// a column), and the output O.  Fourteen warps:
+// One CTA (one per SM) works on up to 256 query rows of one sequence and one kv
+// head, row r being (token r / G, query head r % G of the group), over a range of
+// the context in steps of 64 tokens, as two streams: with more than 128 rows stream
+// x has Q tile x and every step, otherwise both have the same rows and every other
+// step, and their results meet at the end.  Tensor memory holds for each stream two
+// score tiles S (64 columns; the softmax writes the weights P, f16, two a column,
+// over them) and the output O: the scores of the step after next are computed while
+// a step's weights are.  Fifteen warps:
 //
-//   warp 0 (producer): the block table, the codes of each tile's K and then V by
-//     TMA (16-row boxes, 128-byte swizzle) into a ring of raw slots, and their
-//     scales by 4-byte asynchronous copies on the same mbarrier;
-//   warps 10-13 (widening): thread r takes row r of a raw slot to f16, which is
-//     exact, in a slot laid out for the products ([head_dim / 64][128 tokens][128
-//     bytes], swizzled); V rows past the context become zeros, and so do NaN codes
-//     (their first tokens are kept, and rows that see them get NaN at the end); and
-//     once a tile the factors that each run of 8 tokens gives the softmax;
-//   warp 1 (MMA): one thread issues S_x = Q_x K^T and O_x += P_x V (M = 128, f16)
-//     for Q tile x as soon as either is ready;
-//   warps 2-5 and 6-9 (softmax of Q tile 0 and 1): thread r owns row r.  Its scores
-//     are read twice, once for the maximum and once for the weights, 32 at a time.
+//   warp 14 (producer): the block table, each step's K and V codes by TMA (16-row
+//     boxes, 128-byte swizzle) into a ring of eight raw slots, in the order in which
+//     the products need them, and their scales by 4-byte asynchronous copies on the
+//     same mbarrier;
+//   warps 0-3 (widening), a pair of warps a raw slot: thread r takes row r to f16,
+//     which is exact, in a slot laid out for the products ([head_dim / 64][64
+//     tokens][128 bytes], swizzled).  V rows past the context become zeros, and so do
+//     NaN codes (their first tokens are kept, and rows that see them get NaN at the
+//     end).  With K: the factors that each run of 8 tokens gives the softmax.
+//     (Codes through registers instead of raw slots: what an SM has in flight is then
+//     bound by the little L1 that is left, 490 us instead of FIXME for 8 chunks of 1024);
+//   warps 4-7 and 8-11 (softmax of stream 0 and 1): thread r owns row r;
+//   warps 12 and 13 (MMA of stream 0 and 1): for each step O += P V and, once that
+//     is done, the S of the step after next, which takes P's place.
 // The query rows go to f16 after a power of two was divided out of each.
 //
+// Where the row blocks do not fill the SMs, several CTAs share a block's context
+// (launch_prefill_block_scaled); their results go to the workspace, and a second
+// kernel, a programmatic dependent, merges them in their order.
+//
 // Every wait is bounded; on a timeout the CTA records the error, waits (bounded)
-// for its copies and MMAs in flight, frees its tensor memory and returns.
+// for its MMAs in flight, frees its tensor memory and returns.
 #include <atomic>
 #include <climits>
 
@@ -49,42 +58,88 @@ namespace wllm {
 namespace {
 
 constexpr int kTileRows = 128;               // rows of a Q tile (M = 128)
-constexpr int kTiles = 2;                    // Q tiles of a CTA
-constexpr int kRows = kTileRows * kTiles;
-constexpr int kKv = 128;                     // tokens of a kv tile
-constexpr int kOctets = kKv / 8;
-constexpr int kThreads = (2 + 4 * kTiles + 4) * 32;
+constexpr int kStreams = 2;
+constexpr int kRows = kTileRows * kStreams;  // of a CTA
+constexpr int kStep = 64;                    // tokens of a step
+constexpr int kOctets = kStep / 8;
+constexpr int kWideners = 4;                 // warps, in pairs
+constexpr int kSoftmax = kWideners;          // first warp of the softmax
+constexpr int kMma = kSoftmax + 4 * kStreams;  // first of the MMA warps, one a stream
+constexpr int kProducer = kMma + kStreams;
+constexpr int kThreads = (kProducer + 1) * 32;
 constexpr float kRescale = 8.f;              // the running maximum moves by more than this (log2) only
 constexpr float kWeightShift = 7.f;
-constexpr int kFactorTiles = 4;              // kv tiles whose factors are kept
-constexpr int kScaleTiles = 2;               // and whose scales are, until the factors are made
+constexpr float kNone = -3.402823466e38f;    // the maximum of nothing
+constexpr int kFactorSteps = 8;              // steps whose factors are kept
 
 template <int D>
 struct Shape {
   using G = Geom<uint8_t, D>;
   static constexpr int kQBytes = kTileRows * D * 2;        // [chunk][128 rows][128 B]
-  static constexpr int kSlotBytes = kKv * D * 2;           // [chunk][128 tokens][128 B]
-  static constexpr int kChunkStride = kKv * 128;
-  static constexpr int kRawBytes = kKv * D;
-  static constexpr int kSlots = D == 64 ? 6 : 4;           // widened K or V tiles
-  static constexpr int kRaws = D == 64 ? 4 : 2;            // tiles of codes
-  static constexpr int kFactorBytes = kFactorTiles * kOctets * 16;
-  static constexpr int kScaleBytes = kScaleTiles * 2 * kOctets * 4;
-  static constexpr int kNanBytes = D * 4;
-  static constexpr int kBarBytes = D == 64 ? 384 : 256;
-  static constexpr int kSmem = 1024 + kTiles * kQBytes + kSlots * kSlotBytes + kRaws * kRawBytes + kFactorBytes + kScaleBytes +
-                               kNanBytes + kBarBytes;
+  static constexpr int kSlotBytes = kStep * D * 2;         // [chunk][64 tokens][128 B]
+  static constexpr int kChunkStride = kStep * 128;
+  static constexpr int kRawBytes = kStep * D;
+  // widened K or V steps; two more, in place of the second Q tile, where there is only one
+  static constexpr int kSlots = 6, kMoreSlots = 8;
+  static constexpr int kRaws = 8;                          // K or V steps as codes
   static constexpr uint32_t kTmemCols = 512;
-  // tensor-memory columns of Q tile x start at x * kTileCols: S (P over its first 64), O
-  static constexpr int kTileCols = 256;
-  static constexpr int kS = 0, kO = 128;
-  static_assert(kSmem <= 232448, "227 KB");
-  // a tile's factors are written once K's slot is free, that is once the scores of tile j - kSlots / 2 are computed, and with them the weights of the tile before
-  static_assert(kFactorTiles >= kSlots / 2 + 1, "factors are not overwritten while they are needed");
-  // a tile's scales are asked for once K's raw slot is free, that is once those of tile j - kRaws / 2 are used
-  static_assert(kScaleTiles >= kRaws / 2, "nor scales");
+  // tensor-memory columns of stream x start at x * 256: two score tiles, O
+  static constexpr int kStreamCols = 256, kO = 128;
+  static_assert(kQBytes == (kMoreSlots - kSlots) * kSlotBytes, "slots in a Q tile's place");
+  // K of step s + 8 is widened into the slot that K of step s + 5 (both streams have it) or s + 4 (the stream of step s has
+  // it) gives back, whose product comes behind the weights of the stream's step two before: behind those of step s
+  static_assert(kFactorSteps == 8 && kSlots == 6 && kMoreSlots == 8, "factors are not overwritten while they are needed");
 };
-static_assert(2 * (Shape<64>::kSmem + 1024) > 233472, "a second resident CTA would contend for tensor memory");
+
+template <int D>
+struct Shared {
+  using S = Shape<D>;
+  uint8_t q[kStreams][S::kQBytes];
+  uint8_t ring[S::kSlots][S::kSlotBytes];  // items; at the end stream 1's maxima, sums and output, [D][128 rows] of f32
+  uint8_t raw[S::kRaws][S::kRawBytes];     // items as codes
+  float4 factors[kFactorSteps][kOctets];   // ks, log2 vs, 1 / vs of each run of 8 tokens
+  float scales[S::kRaws][2 * kOctets];     // K's and V's of a K item's step
+  int nan_from[D];                         // first token whose value is NaN
+  uint64_t full[S::kMoreSlots];            // widened (widening -> MMA)
+  uint64_t empty[S::kMoreSlots];           // given up by both streams (MMA -> widening)
+  uint64_t raw_full[S::kRaws];             // codes and scales landed (producer -> widening)
+  uint64_t raw_empty[S::kRaws];            // read (widening -> producer)
+  uint64_t factors_full[kFactorSteps];     // (widening -> softmax)
+  uint64_t scored[kStreams][2];            // S written (MMA -> softmax)
+  uint64_t weighed[kStreams][2];           // P written, O rescaled (softmax -> MMA)
+  uint64_t added[kStreams];                // a step's PV product done (MMA -> softmax, MMA); never more than one step ahead
+  uint64_t finished[kStreams];             // the last one done (MMA -> softmax)
+  uint64_t q_full;                         // Q written (softmax -> MMA)
+  uint64_t fin;                            // every MMA of the CTA done
+  uint32_t tmem;
+  int seq, block, any_nan;
+};
+static_assert(sizeof(Shared<128>) <= 232448, "227 KB");
+// one CTA an SM: a second one would contend for tensor memory
+constexpr int shared_bytes(int d) { return d == 64 ? 118784 : static_cast<int>(sizeof(Shared<128>)); }
+static_assert(sizeof(Shared<64>) <= 118784 && 2 * (118784 + 1024) > 233472, "");
+
+// The items of a CTA's n steps, in the order of their use: K of the first `lead`
+// steps, then V of a step and K of the step `lead` behind it in turn.
+struct Items {
+  int n, lead;
+  __device__ __forceinline__ int k(int s) const { return s < lead ? s : 2 * s - lead + 1; }
+  __device__ __forceinline__ int v(int s) const { return s <= n - lead ? lead + 2 * s : n + s; }
+  // whether item i is V, and its step
+  __device__ __forceinline__ bool is_v(int i, int* s) const {
+    if (i < min(lead, n)) {
+      *s = i;
+      return false;
+    }
+    if (i < 2 * n - lead) {
+      const int m = i - lead;
+      *s = (m >> 1) + (m & 1 ? lead : 0);
+      return !(m & 1);
+    }
+    *s = i - n;
+    return true;
+  }
+};
 
 __device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
@@ -98,10 +153,23 @@ __device__ __forceinline__ float scale_in_range(float s) {
 }
 __device__ __forceinline__ float lg2(float x) {
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t h2(float lo, float hi) { return Mma<__half>::pack(lo, hi); }
+// Two elements at once.
+__device__ __forceinline__ void fma2(float& x, float& y, float by, float add) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(by), "f"(add));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 s, t;\n\tmov.b64 s, {%0, %1};\n\tmov.b64 t, {%2, %3};\n\t"
+      "add.rn.f32x2 s, s, t;\n\tmov.b64 {%0, %1}, s;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
 
 // Eight elements of a row, 16-bit.
 template <typename T>
@@ -114,10 +182,10 @@ __device__ __forceinline__ uint4 load8(const T* src, bool vec) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float* v, float by, bool vec) {
+__device__ __forceinline__ void store8(T* dst, const float* v, bool vec) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = Mma<T>::pack(v[2 * i] * by, v[2 * i + 1] * by);
+  for (int i = 0; i < 4; ++i) w[i] = Mma<T>::pack(v[2 * i], v[2 * i + 1]);
   if (vec) {
     *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
@@ -127,6 +195,38 @@ __device__ __forceinline__ void store8(T* dst, const float* v, float by, bool ve
   }
 }
 
+// The rows of one block and the context that they see.
+struct Rows {
+  int b, n_rows, row0, pos0, s0;
+  int end[kStreams];  // tokens that a row of Q tile x sees at most (0: the tile has no row)
+};
+__device__ __forceinline__ Rows rows_of(const PrefillParams& p, int b, int block, bool tell) {
+  Rows r{b, 0, 0, 0, 0, {0, 0}};
+  if (b < 0) return r;
+  const int l_max = p.max_blocks * p.block_size;
+  r.s0 = p.query_start_loc[b];
+  int n = p.query_start_loc[b + 1] - r.s0;
+  if (r.s0 < 0 || n < 0 || static_cast<int64_t>(r.s0) + n > p.num_tokens) {  // inconsistent query starts
+    if (tell) atomicOr(p.err, kErrLen);
+    return r;
+  }
+  int L = p.context_lens[b];
+  if (L < 0 || L > l_max || n > L) {
+    if (tell) atomicOr(p.err, kErrLen);
+    L = L < 0 ? 0 : (L > l_max ? l_max : L);
+    n = n > L ? L : n;
+  }
+  r.n_rows = n * p.group;
+  r.row0 = block * kRows;
+  r.pos0 = L - n;
+#pragma unroll
+  for (int x = 0; x < kStreams; ++x) {  // (no rows only when n was clamped, error already flagged)
+    const int rx = r.row0 + x * kTileRows;
+    if (rx < r.n_rows) r.end[x] = r.pos0 + (min(r.n_rows, rx + kTileRows) - 1) / p.group + 1;
+  }
+  return r;
+}
+
 // RUN: tokens of a run with one scale that the softmax tells apart, 8 for blocks
 // of 8 tokens, else 16.
 template <typename T, int D, int RUN>
@@ -134,71 +234,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_block_scaled_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                                 const ScaledPrefillParams sp) {
   using S = Shape<D>;
-  using G8 = typename S::G;
   const PrefillParams& p = sp.base;
-  constexpr int R = S::kSlots, RR = S::kRaws;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* q_s = smem;                                  // [2][Q tile]
-  uint8_t* ring = q_s + kTiles * S::kQBytes;            // widened tiles: K, V, K, V, ...
-  uint8_t* raw = ring + R * S::kSlotBytes;              // tiles of codes, in the same order
-  float4* factors = reinterpret_cast<float4*>(raw + RR * S::kRawBytes);              // [tile][octet] ks, log2 vs, 1 / vs
-  float* scales = reinterpret_cast<float*>(factors + kFactorTiles * kOctets);        // [tile][K, V][octet]
-  int* nan_from = reinterpret_cast<int*>(scales + kScaleTiles * 2 * kOctets);        // [D] first token whose value is NaN
-  uint64_t* full = reinterpret_cast<uint64_t*>(nan_from + D);  // [R] widened (widening -> MMA)
-  uint64_t* empty = full + R;      // [R] read by every product (MMA -> widening)
-  uint64_t* rfull = empty + R;     // [RR] codes and scales landed (producer -> widening)
-  uint64_t* rempty = rfull + RR;   // [RR] codes read (widening -> producer)
-  uint64_t* ffull = rempty + RR;   // [kFactorTiles] a tile's factors written (widening -> softmax)
-  uint64_t* sfull = ffull + kFactorTiles;  // [tile] S written (MMA -> softmax)
-  uint64_t* pfull = sfull + 2;     // [tile] P written, O rescaled (softmax -> MMA)
-  uint64_t* pvdone = pfull + 2;    // [tile] the PV product done (MMA -> MMA, softmax)
-  uint64_t* qfull = pvdone + 2;    // Q written (softmax -> MMA)
-  uint64_t* fin = qfull + 1;       // every MMA of the CTA done
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(fin + 1);
-  int* info = reinterpret_cast<int*>(tslot + 1);  // [0] sequence (-1: none), [1] its row block, [2] whether a value is NaN
-  static_assert((2 * R + 2 * RR + kFactorTiles + 8) * 8 + 16 <= S::kBarBytes, "room for the barriers");
+  extern __shared__ __align__(1024) uint8_t raw[];
+  Shared<D>& sh = *reinterpret_cast<Shared<D>*>(raw);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group;
-  const int kvh = static_cast<int>(blockIdx.x % p.num_kv_heads);
-  const int tgt_block = static_cast<int>(blockIdx.x / p.num_kv_heads);
+  // CTA i: part i % splits of kv head (i / splits) % Hkv of a row block, so that what shares a block is launched together
+  const int part = static_cast<int>(blockIdx.x % sp.splits);
+  const int kvh = static_cast<int>(blockIdx.x / sp.splits % p.num_kv_heads);
+  const int tgt_block = static_cast<int>(blockIdx.x / sp.splits / p.num_kv_heads);
   if (warp == 0) {
-    if (lane == 0) tma_prefetch_desc(&kmap), tma_prefetch_desc(&vmap);
     if (lane == 0) {
-      for (int s = 0; s < R; ++s) {
-        mbar_init(smem_u32(full + s), 4);
-        mbar_init(smem_u32(empty + s), 1);
+      for (int s = 0; s < S::kMoreSlots; ++s) {
+        mbar_init(smem_u32(sh.full + s), kWideners / 2);
+        mbar_init(smem_u32(sh.empty + s), kStreams);
       }
-      for (int s = 0; s < RR; ++s) {
-        mbar_init(smem_u32(rfull + s), 1 + 32);
-        mbar_init(smem_u32(rempty + s), 4);
+      for (int s = 0; s < S::kRaws; ++s) {
+        mbar_init(smem_u32(sh.raw_full + s), 1 + 32);
+        mbar_init(smem_u32(sh.raw_empty + s), kWideners / 2);
       }
-      for (int s = 0; s < kFactorTiles; ++s) mbar_init(smem_u32(ffull + s), 1);
-      for (int x = 0; x < kTiles; ++x) {
-        mbar_init(smem_u32(sfull + x), 1);
-        mbar_init(smem_u32(pfull + x), 4);
-        mbar_init(smem_u32(pvdone + x), 1);
+      for (int s = 0; s < kFactorSteps; ++s) mbar_init(smem_u32(sh.factors_full + s), 1);
+      for (int x = 0; x < kStreams; ++x) {
+        for (int h = 0; h < 2; ++h) {
+          mbar_init(smem_u32(&sh.scored[x][h]), 1);
+          mbar_init(smem_u32(&sh.weighed[x][h]), 4);
+        }
+        mbar_init(smem_u32(sh.added + x), 1);
+        mbar_init(smem_u32(sh.finished + x), 1);
       }
-      mbar_init(smem_u32(qfull), 4 * kTiles);
-      mbar_init(smem_u32(fin), 1);
+      mbar_init(smem_u32(&sh.q_full), 4 * kStreams);
+      mbar_init(smem_u32(&sh.fin), kStreams);
       fence_mbar_init();
     }
+    for (int d = lane; d < D; d += 32) sh.nan_from[d] = INT_MAX;
     __syncwarp();
     grid_wait();
-    int seq, tile;
-    row_block_of(p, kRows, tgt_block, lane, &seq, &tile);
-    if (lane == 0) info[0] = seq, info[1] = tile, info[2] = 0;
-    for (int d = lane; d < D; d += 32) nan_from[d] = INT_MAX;
+    int seq, block;
+    row_block_of(p, kRows, tgt_block, lane, &seq, &block);
+    if (lane == 0) sh.seq = seq, sh.block = block, sh.any_nan = 0;
   } else {
     grid_wait();
   }
   grid_launch_dependents();
-  if (warp == 1) tc::alloc(smem_u32(tslot), S::kTmemCols);
+  if (warp == kMma) tc::alloc(smem_u32(&sh.tmem), S::kTmemCols);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tslot;
+  const uint32_t tmem = sh.tmem;
 
   // starts that decrease are recorded whether or not a row block meets them, by the CTA that is launched last
   if (blockIdx.x == gridDim.x - 1) {
@@ -206,39 +289,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.query_start_loc[i + 1] < p.query_start_loc[i]) atomicOr(p.err, kErrLen);
   }
 
-  // ---- the block's rows and the context they see (uniform over the CTA)
-  const int b = info[0];
-  int n_rows = 0, row0 = 0, pos0 = 0, s0 = 0;
-  int nt[kTiles] = {0, 0};  // kv tiles each Q tile needs
-  int kv_end = 0;           // tokens any row of the block sees
-  if (b >= 0) {
-    const int l_max = p.max_blocks * p.block_size;
-    s0 = p.query_start_loc[b];
-    int n = p.query_start_loc[b + 1] - s0;
-    if (s0 < 0 || n < 0 || static_cast<int64_t>(s0) + n > p.num_tokens) {  // inconsistent query starts
-      if (threadIdx.x == 0) atomicOr(p.err, kErrLen);
-    } else {
-      int L = p.context_lens[b];
-      if (L < 0 || L > l_max || n > L) {
-        if (threadIdx.x == 0) atomicOr(p.err, kErrLen);
-        L = L < 0 ? 0 : (L > l_max ? l_max : L);
-        n = n > L ? L : n;
-      }
-      n_rows = n * G;
-      row0 = info[1] * kRows;
-      pos0 = L - n;
+  const Rows rows = rows_of(p, sh.seq, sh.block, threadIdx.x == 0);
+  const int b = rows.b, kv_end = max(rows.end[0], rows.end[1]);
+  // this CTA's steps, step0 on, and each stream's (of all of them, or every other one)
+  const int all_steps = (kv_end + kStep - 1) / kStep;
+  const int step0 = all_steps * part / sp.splits, n_steps = all_steps * (part + 1) / sp.splits - step0;
+  const bool same_rows = rows.end[1] == 0;
+  int steps[kStreams];
 #pragma unroll
-      for (int x = 0; x < kTiles; ++x) {  // (no rows only when n was clamped, error already flagged)
-        const int rx = row0 + x * kTileRows;
-        if (rx < n_rows) {
-          const int end_x = pos0 + (min(n_rows, rx + kTileRows) - 1) / G + 1;
-          nt[x] = (end_x + kKv - 1) / kKv;
-          kv_end = max(kv_end, end_x);
-        }
-      }
-    }
-  }
-  const int n_tiles = max(nt[0], nt[1]);
+  for (int x = 0; x < kStreams; ++x)
+    steps[x] = same_rows ? (n_steps + 1 - x) / 2 : max(0, min(n_steps, (rows.end[x] + kStep - 1) / kStep - step0));
+  const bool work = n_steps > 0;
+  const Items items{n_steps, same_rows ? 4 : 2};
+  uint8_t* const ring = same_rows ? sh.q[1] : sh.ring[0];
+  const int slots = same_rows ? S::kMoreSlots : S::kSlots;
 
   // one lane waits, the warp learns the outcome
   auto wait_warp = [&](uint64_t* bar, int parity) -> bool {
@@ -248,168 +312,81 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   bool ok = true;
 
-  if (warp == 0 && n_tiles > 0) {
+  if (warp == kProducer && work) {
     // ------------------------------- producer -------------------------------
-    constexpr int kBoxes = kKv / 16;  // 16-token boxes of a kv tile (times the row's column boxes, one for D <= 128)
     const int32_t* bt_row = p.block_tables + static_cast<int64_t>(b) * p.bt_stride;
-    int issued = 0;                   // raw slots whose copies were issued
-    for (int j = 0; ok && j < n_tiles; ++j) {
-      // lanes 0..15: the table entry of each run of 8 tokens
-      int entry = 0;
-      const int t8 = j * kKv + 8 * (lane & 15);
-      if (t8 < kv_end) {
-        entry = bt_row[t8 >> p.log2_bs];
-        if (entry < 0 || entry >= p.num_blocks) {
-          atomicOr(p.err, kErrBlock);
-          entry = 0;
-        }
+    // Table entries of four steps, a lane a run of 8 tokens: V's group, the next one (K is up to four steps ahead) and the
+    // one behind it.  The loads are unconditional (behind the end: of the last token), so nothing waits for them here.
+    auto entries = [&](int group) { return bt_row[min((step0 + 4 * group) * kStep + 8 * lane, kv_end - 1) >> p.log2_bs]; };
+    auto checked = [&](int entry) {
+      if (entry >= 0 && entry < p.num_blocks) return entry;
+      atomicOr(p.err, kErrBlock);
+      return 0;
+    };
+    int here = entries(0), there = entries(1), behind = entries(2), group = 0;
+    here = checked(here), there = checked(there);
+    int issued = 0;
+    for (int i = 0; i < 2 * n_steps; ++i) {
+      const int rs = i % S::kRaws;
+      if (!wait_warp(sh.raw_empty + rs, ((i / S::kRaws) & 1) ^ 1)) {
+        ok = false;
+        break;
       }
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {  // K, then V
-        const int c = 2 * j + half, s = c % RR;
-        if (!wait_warp(rempty + s, ((c / RR) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        const uint32_t slot = smem_u32(raw + s * S::kRawBytes), bar = smem_u32(rfull + s);
-        // a box a lane: 16 tokens, or 8 where blocks have no more
-        const int octet = RUN == 8 ? lane & 15 : (2 * lane) & 15;
-        const int phys = __shfl_sync(kFullMask, entry, octet);
-        const int t = j * kKv + 8 * octet;
-        const bool live = lane < (RUN == 8 ? kOctets : kBoxes) && t < kv_end;
-        constexpr uint32_t kBoxBytes = RUN == 8 ? 1024u : static_cast<uint32_t>(G8::kTileBytes);
-        const uint32_t bytes = kBoxBytes * __popc(__ballot_sync(kFullMask, live));
-        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-        __syncwarp();
-        if (live) {
-          const int at = kvh * p.block_size + (t & (p.block_size - 1));
-          tma_load_3d(slot + lane * kBoxBytes, half ? &vmap : &kmap, bar, 0, G8::kPairRows ? at >> 1 : at, phys);
-        }
-        if (half == 0 && t8 < kv_end)  // both scales of a run come with its K: lanes 0-15 K's, 16-31 V's
-          copy4_async(smem_u32(scales + (j % kScaleTiles) * 2 * kOctets + lane),
-                      (lane < 16 ? sp.k_scales : sp.v_scales) + static_cast<int64_t>(entry) * p.num_kv_heads + kvh);
-        arrive_behind_copies(bar);
-        ++issued;
+      int s;
+      const bool is_v = items.is_v(i, &s);
+      if (is_v && s >> 2 != group) {
+        here = there, there = checked(behind), ++group;
+        behind = entries(group + 2);
       }
+      const int entry = s >> 2 == group ? here : there;
+      // a box a lane: 16 tokens, or 8 where blocks have no more
+      constexpr int kBoxes = RUN == 8 ? kOctets : kOctets / 2;
+      constexpr uint32_t kBoxBytes = RUN == 8 ? 1024u : static_cast<uint32_t>(S::G::kTileBytes);
+      const int octet = RUN == 8 ? lane & 7 : (2 * lane) & 7, t = (step0 + s) * kStep + 8 * octet;
+      const int phys = __shfl_sync(kFullMask, entry, (s & 3) * kOctets + octet);
+      const bool live = lane < kBoxes && t < kv_end;
+      const uint32_t bar = smem_u32(sh.raw_full + rs);
+      const uint32_t bytes = kBoxBytes * __popc(__ballot_sync(kFullMask, live));
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+      __syncwarp();
+      if (live) {
+        const int at = kvh * p.block_size + (t & (p.block_size - 1));
+        tma_load_3d(smem_u32(sh.raw[rs]) + lane * kBoxBytes, is_v ? &vmap : &kmap, bar, 0, S::G::kPairRows ? at >> 1 : at, phys);
+      }
+      const int of = __shfl_sync(kFullMask, entry, (s & 3) * kOctets + (lane & 7));
+      if (!is_v && lane < 2 * kOctets)  // both scales of a run come with its K: lanes 0-7 K's, 8-15 V's
+        copy4_async(smem_u32(&sh.scales[rs][lane]),
+                    (lane < kOctets ? sp.k_scales : sp.v_scales) + static_cast<int64_t>(of) * p.num_kv_heads + kvh);
+      arrive_behind_copies(bar);
+      ++issued;
     }
     // every copy still in flight lands before the CTA may leave
-    for (int c = issued - RR > 0 ? issued - RR : 0; c < issued; ++c)
-      if (!wait_warp(rfull + c % RR, (c / RR) & 1)) ok = false;
-  } else if (warp == 1 && n_tiles > 0) {
-    // --------------------------------- MMA ----------------------------------
-    if (lane == 0) {
-      constexpr uint32_t kIdS = tc::f16_idesc(false, false, false, kTileRows, kKv);
-      constexpr uint32_t kIdO = tc::f16_idesc(false, false, true, kTileRows, D);
-      const uint32_t q_a = smem_u32(q_s), ring_a = smem_u32(ring);
-      // the operations of one kind in order: kv tile by kv tile, Q tile 0 then
-      // 1, skipping Q tiles that need fewer kv tiles
-      const int m2 = min(nt[0], nt[1]);
-      const int total = nt[0] + nt[1];
-      auto op_at = [&](int k, int& j, int& x) {
-        if (k < 2 * m2) {
-          j = k >> 1;
-          x = k & 1;
-        } else {
-          j = m2 + (k - 2 * m2);
-          x = nt[0] > nt[1] ? 0 : 1;
-        }
-      };
-      // the last operation of its kind on kv tile j (then the slot can go back)
-      auto last_on_tile = [&](int j, int x) { return x == 1 || j >= nt[1]; };
-      ok = mbar_wait_bounded(smem_u32(qfull), 0, p.wait_limit_ns);
-      int ks = 0, kp = 0;  // next S product, next PV product
-      uint64_t t_idle = 0;
-      int idle = 0;        // polls since the last issue (the timer is read every 64)
-      while (ok && kp < total) {
-        bool did = false;
-        if (ks < total) {
-          int j, x;
-          op_at(ks, j, x);
-          const int c = 2 * j, s = c % R;
-          // S_x(j) overwrites P_x(j-1): O_x += P_x(j-1) V must be done
-          if (mbar_test_wait(smem_u32(full + s), (c / R) & 1) &&
-              (j == 0 || mbar_test_wait(smem_u32(pvdone + x), (j - 1) & 1))) {
-            tc::fence_after_sync();
-            const uint64_t qd = tc::sw128_desc(q_a + x * S::kQBytes, 16, 1024);
-            const uint64_t kd = tc::sw128_desc(ring_a + s * S::kSlotBytes, 16, 1024);
-            const uint32_t d = tmem + x * S::kTileCols + S::kS;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              // descriptor start addresses advance in 16-byte units
-              const uint32_t qo = ((kk >> 2) * kTileRows * 128 + (kk & 3) * 32) >> 4;
-              const uint32_t ko = ((kk >> 2) * S::kChunkStride + (kk & 3) * 32) >> 4;
-              tc::mma_f16(d, qd + qo, kd + ko, kIdS, kk > 0 ? 1u : 0u);
-            }
-            tc::commit(smem_u32(sfull + x));
-            if (last_on_tile(j, x)) tc::commit(smem_u32(empty + s));
-            ++ks;
-            did = true;
-          }
-        }
-        if (kp < ks) {
-          int j, x;
-          op_at(kp, j, x);
-          const int c = 2 * j + 1, s = c % R;
-          if (mbar_test_wait(smem_u32(pfull + x), j & 1) && mbar_test_wait(smem_u32(full + s), (c / R) & 1)) {
-            tc::fence_after_sync();
-            const uint64_t vd = tc::sw128_desc(ring_a + s * S::kSlotBytes, S::kChunkStride, 1024);
-            const uint32_t d = tmem + x * S::kTileCols + S::kO;
-            const uint32_t pa = tmem + x * S::kTileCols + S::kS;  // P: 8 columns per 16 tokens
-#pragma unroll
-            for (int kk = 0; kk < kKv / 16; ++kk)
-              tc::mma_f16_ts(d, pa + kk * 8, vd + ((kk * 2048) >> 4), kIdO, (j > 0 || kk > 0) ? 1u : 0u);
-            tc::commit(smem_u32(pvdone + x));
-            if (last_on_tile(j, x)) tc::commit(smem_u32(empty + s));
-            ++kp;
-            did = true;
-          }
-        }
-        if (did) {
-          idle = 0;
-        } else if ((++idle & 63) == 0) {  // a bounded wait: no issue for wait_limit_ns gives up
-          const uint64_t now = global_timer_ns();
-          if (idle == 64) t_idle = now;
-          else if (now - t_idle > p.wait_limit_ns) ok = false;
-        }
-      }
-      tc::commit(smem_u32(fin));  // every MMA issued above, on every path
-    }
-    __syncwarp();
-    ok = __shfl_sync(kFullMask, ok ? 1 : 0, 0) != 0;
-  } else if (warp >= 2 + 4 * kTiles && n_tiles > 0) {
+    for (int i = max(0, issued - S::kRaws); i < issued; ++i)
+      if (!wait_warp(sh.raw_full + i % S::kRaws, (i / S::kRaws) & 1)) ok = false;
+  } else if (warp < kWideners && work) {
     // ------------------------------- widening -------------------------------
-    const int r = threadIdx.x - (2 + 4 * kTiles) * 32;  // row of the kv tile
-    constexpr int kRawChunks = D / 16;                  // 16-byte chunks of a row of codes
-    for (int c = 0; c < 2 * n_tiles; ++c) {
-      const int j = c >> 1, rs = c % RR, s = c % R;
-      if (!wait_warp(rfull + rs, (c / RR) & 1)) {
+    const int r = threadIdx.x & 63;     // row of the step
+    constexpr int kRawChunks = D / 16;  // 16-byte chunks of a row of codes
+    int at = warp >> 1, turn = 1;       // slot; parity of its being free
+    for (int i = warp >> 1; i < 2 * n_steps; i += kWideners / 2) {
+      const int rs = i % S::kRaws;
+      int s;
+      const bool is_v = items.is_v(i, &s);
+      if (!wait_warp(sh.raw_full + rs, (i / S::kRaws) & 1) || !wait_warp(sh.empty + at, turn)) {
         ok = false;
         break;
       }
-      if (!wait_warp(empty + s, ((c / R) & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
-      if (!(c & 1) && warp == 2 + 4 * kTiles) {
-        if (lane < kOctets) {
-          const float* of = scales + (j % kScaleTiles) * 2 * kOctets + lane;
-          const float ks = scale_in_range(of[0]), vs = scale_in_range(of[kOctets]);
-          factors[(j % kFactorTiles) * kOctets + lane] = make_float4(ks, lg2(vs) + kWeightShift, __frcp_rn(vs), 0.f);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(ffull + j % kFactorTiles));
-      }
-      const uint8_t* src = raw + rs * S::kRawBytes + (r >> 4) * G8::kTileBytes;
-      uint8_t* dst = ring + s * S::kSlotBytes + r * 128;
-      const bool zero = (c & 1) && j * kKv + r >= kv_end;  // V rows past the context may hold anything
-      uint32_t full_code = 0u;  // 0x80 in a byte: a NaN code, 0x7f or 0xff, was there
+      const uint8_t* src = sh.raw[rs] + (r >> 4) * S::G::kTileBytes;
+      uint8_t* dst = ring + at * S::kSlotBytes + r * 128;
+      const int token = (step0 + s) * kStep + r;
+      const bool zero = is_v && token >= kv_end;  // V rows past the context may hold anything
+      uint32_t nan_bits = 0u;                     // 0x80 in a byte: a NaN code, 0x7f or 0xff, was there
 #pragma unroll
       for (int ch = 0; ch < kRawChunks; ++ch) {
-        const uint4 x = zero ? make_uint4(0u, 0u, 0u, 0u) : *reinterpret_cast<const uint4*>(src + code_offset<D>(r & 15, ch));
-        if (c & 1) {
-          full_code |= ((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u) |
-                       ((x.z & 0x7f7f7f7fu) + 0x01010101u) | ((x.w & 0x7f7f7f7fu) + 0x01010101u);
-        }
+        uint4 x = *reinterpret_cast<const uint4*>(src + code_offset<D>(r & 15, ch));
+        if (zero) x = make_uint4(0u, 0u, 0u, 0u);
+        nan_bits |= ((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u) |
+                    ((x.z & 0x7f7f7f7fu) + 0x01010101u) | ((x.w & 0x7f7f7f7fu) + 0x01010101u);
         uint4 lo, hi;
         e4m3x4_to_f16x2x2(x.x, lo.x, lo.y);
         e4m3x4_to_f16x2x2(x.y, lo.z, lo.w);
@@ -420,43 +397,136 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4*>(to + ((c16 ^ (r & 7)) << 4)) = lo;
         *reinterpret_cast<uint4*>(to + (((c16 + 1) ^ (r & 7)) << 4)) = hi;
       }
-      if (full_code & 0x80808080u) {
-        // NaN would reach rows that do not see this token (zero times NaN): it goes into the products as zero, and rows
+      if (is_v && (nan_bits & 0x80808080u)) {
+        // NaN would reach rows that do not see its token (zero times NaN): it goes into the products as zero, and rows
         // from this token on get it at their end
         for (int d = 0; d < D; ++d) {
           if ((src[code_offset<D>(r & 15, d >> 4) + (d & 15)] & 0x7f) != 0x7f) continue;
-          atomicMin(nan_from + d, j * kKv + r);
-          info[2] = 1;
+          atomicMin(sh.nan_from + d, token);
+          sh.any_nan = 1;
           *reinterpret_cast<uint16_t*>(dst + (d >> 6) * S::kChunkStride + ((((d >> 3) & 7) ^ (r & 7)) << 4) + (d & 7) * 2) = 0;
         }
       }
       tc::fence_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(full + s));
-        mbar_arrive(smem_u32(rempty + rs));
+      if (lane == 0) mbar_arrive(smem_u32(sh.full + at));
+      if (!is_v && !(warp & 1)) {
+        if (lane < kOctets) {
+          const float ks = scale_in_range(sh.scales[rs][lane]), vs = scale_in_range(sh.scales[rs][kOctets + lane]);
+          sh.factors[s % kFactorSteps][lane] = make_float4(ks, lg2(vs) + kWeightShift, __frcp_rn(vs), 0.f);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(sh.factors_full + s % kFactorSteps));
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(sh.raw_empty + rs));
+      at += kWideners / 2;
+      if (at >= slots) at -= slots, turn ^= 1;
     }
-  } else if (warp >= 2 && n_tiles > 0) {
+  } else if (warp >= kMma && warp < kProducer && work) {
+    // --------------------------------- MMA ----------------------------------
+    // The whole warp goes through the loop and one lane issues: what the products are told (descriptors, columns) is
+    // then uniform over the warp, as the instruction takes it.  (One lane by itself needed 0.3 to 0.5 us for 8 products.)
+    constexpr uint32_t kIdS = tc::f16_idesc(false, false, false, kTileRows, kStep);
+    constexpr uint32_t kIdO = tc::f16_idesc(false, false, true, kTileRows, D);
+    const int x = warp - kMma;  // this warp's stream
+    const bool same = __shfl_sync(kFullMask, same_rows ? 1 : 0, 0) != 0;
+    const int n = __shfl_sync(kFullMask, steps[x], 0), all = __shfl_sync(kFullMask, n_steps, 0);
+    const uint32_t base = __shfl_sync(kFullMask, tmem, 0) + x * S::kStreamCols;
+    const Items order{all, same ? 4 : 2};
+    const uint32_t ring_a = same ? smem_u32(sh.q[1]) : smem_u32(sh.ring);
+    const uint64_t qd = tc::sw128_desc(smem_u32(sh.q) + (same ? 0 : x) * S::kQBytes, 16, 1024);
+    auto wait = [&](uint64_t* bar, int parity) { ok = ok && mbar_wait_warp(smem_u32(bar), static_cast<uint32_t>(parity), p.wait_limit_ns); };
+    struct Slot {
+      int at, turn;
+    };
+    auto slot_of = [&](int item) {
+      return same ? Slot{item % S::kMoreSlots, item / S::kMoreSlots & 1} : Slot{item % S::kSlots, item / S::kSlots & 1};
+    };
+    auto step_of = [&](int i) { return same ? 2 * i + x : i; };
+    // a slot goes back once both streams have given it up; where only one has it, it does so twice
+    auto give_up = [&](Slot s) {
+      tc::commit(smem_u32(sh.empty + s.at));
+      if (same) tc::commit(smem_u32(sh.empty + s.at));
+    };
+    auto scores = [&](int i, int h) {
+      const Slot s = slot_of(order.k(step_of(i)));
+      wait(sh.full + s.at, s.turn);
+      if (i >= 2) wait(sh.added + x, h);  // the weights whose place it takes have been read
+      if (!ok) return;
+      tc::fence_after_sync();
+      const uint64_t kd = tc::sw128_desc(ring_a + s.at * S::kSlotBytes, 16, 1024);
+      if (tc::elect()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          // descriptor start addresses advance in 16-byte units
+          const uint32_t qo = ((kk >> 2) * kTileRows * 128 + (kk & 3) * 32) >> 4;
+          const uint32_t ko = ((kk >> 2) * S::kChunkStride + (kk & 3) * 32) >> 4;
+          tc::mma_f16(base + h * kStep, qd + qo, kd + ko, kIdS, kk > 0 ? 1u : 0u);
+        }
+        tc::commit(smem_u32(&sh.scored[x][h]));
+        give_up(s);
+      }
+      __syncwarp();
+    };
+    auto values = [&](int i, int h) {
+      const Slot s = slot_of(order.v(step_of(i)));
+      wait(sh.full + s.at, s.turn);
+      wait(&sh.weighed[x][h], (i >> 1) & 1);
+      if (!ok) return;
+      tc::fence_after_sync();
+      const uint64_t vd = tc::sw128_desc(ring_a + s.at * S::kSlotBytes, S::kChunkStride, 1024);
+      const uint32_t go_on = i > 0 ? 1u : 0u;
+      if (tc::elect()) {
+#pragma unroll
+        for (int kk = 0; kk < kStep / 16; ++kk)  // P: 8 columns per 16 tokens
+          tc::mma_f16_ts(base + S::kO, base + h * kStep + kk * 8, vd + ((kk * 2048) >> 4), kIdO, kk > 0 ? 1u : go_on);
+        tc::commit(smem_u32(sh.added + x));
+        if (i + 1 == n) tc::commit(smem_u32(sh.finished + x));
+        give_up(s);
+      }
+      __syncwarp();
+    };
+    wait(&sh.q_full, 0);
+    if (ok && n > 0) scores(0, 0);
+    if (ok && n > 1) scores(1, 1);
+    for (int i = 0; ok && i < n; i += 2) {
+      values(i, 0);
+      if (ok && i + 2 < n) scores(i + 2, 0);
+      if (ok && i + 1 < n) values(i + 1, 1);
+      if (ok && i + 3 < n) scores(i + 3, 1);
+    }
+    // steps that only the other stream has: given up once they are there
+    if (!same)
+      for (int i = n; ok && i < all; ++i)
+        for (int v = 0; v < 2; ++v) {
+          const Slot s = slot_of(v ? order.v(i) : order.k(i));
+          wait(sh.full + s.at, s.turn);
+          if (ok && lane == 0) mbar_arrive(smem_u32(sh.empty + s.at));
+        }
+    if (tc::elect()) tc::commit(smem_u32(&sh.fin));  // every MMA issued above, on every path
+    __syncwarp();
+  } else if (warp >= kSoftmax && warp < kMma && rows.end[0] > 0) {
     // ------------------------------- softmax --------------------------------
-    const int x = (warp - 2) >> 2;           // this warp's Q tile
+    const int x = (warp - kSoftmax) >> 2;    // this warp's stream
     const int quarter = warp & 3;            // the TMEM lanes this warp reaches
-    const int r = quarter * 32 + lane;       // this thread's row of the tile
-    const int rowg = row0 + x * kTileRows + r;
-    const bool valid = rowg < n_rows;
+    const int r = quarter * 32 + lane;       // this thread's row of the Q tile
+    const int rowg = rows.row0 + (same_rows ? 0 : x * kTileRows) + r;
+    const bool valid = rowg < rows.n_rows;
     const int tok = valid ? rowg / G : 0;
     const int gh = valid ? rowg - tok * G : 0;
-    const int pos = valid ? pos0 + tok : 0;  // padding rows see token 0 only (output dropped)
-    const uint32_t trow = tmem + x * S::kTileCols + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int pos = valid ? rows.pos0 + tok : 0;  // padding rows see token 0 only (output dropped)
+    const uint32_t trow = tmem + x * S::kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
     float sl2;  // of a raw score, without the block's scale; positive
     {
-      uint8_t* qx = q_s + x * S::kQBytes;
-      const T* qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(s0 + tok) * p.q_st + static_cast<int64_t>(kvh * G + gh) * p.q_sh;
+      uint8_t* qx = sh.q[x];
+      const T* qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(rows.s0 + tok) * p.q_st + static_cast<int64_t>(kvh * G + gh) * p.q_sh;
       uint4 v[D / 8];
       uint32_t most = 0u;
 #pragma unroll
+      for (int i = 0; i < D / 8; ++i) v[i] = valid ? load8(qrow + 8 * i, sp.q_vec) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        v[i] = valid ? load8(qrow + 8 * i, sp.q_vec) : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
@@ -478,113 +548,157 @@ __global__ void __launch_bounds__(kThreads, 1)
           const T* q2 = reinterpret_cast<const T*>(&w[e]);
           f[e] = h2(to_f32(q2[0]) * up, to_f32(q2[1]) * up);
         }
-        *reinterpret_cast<uint4*>(qx + (i >> 3) * (kTileRows * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
-            make_uint4(f[0], f[1], f[2], f[3]);
+        if (x == 0 || !same_rows)
+          *reinterpret_cast<uint4*>(qx + (i >> 3) * (kTileRows * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
+              make_uint4(f[0], f[1], f[2], f[3]);
       }
       tc::fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(qfull));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
     }
-    float m = -INFINITY, l = 0.f;
-    const int ntx = x ? nt[1] : nt[0];
-    constexpr int kRuns = 32 / RUN;  // of 32 columns
-    for (int j = 0; j < ntx; ++j) {
-      const float4* of = factors + (j % kFactorTiles) * kOctets;
-      if (!wait_warp(ffull + j % kFactorTiles, (j / kFactorTiles) & 1) || !wait_warp(sfull + x, j & 1)) {
+    float m = kNone, l = 0.f;
+    const int n = steps[x];
+    constexpr int kRuns = kStep / RUN;
+    for (int i = 0; i < n; ++i) {
+      const int h = i & 1, s = same_rows ? 2 * i + x : i;  // step, counted from step0
+      const float4* of = sh.factors[s % kFactorSteps];
+      if (!wait_warp(sh.factors_full + s % kFactorSteps, (s / kFactorSteps) & 1) || !wait_warp(&sh.scored[x][h], (i >> 1) & 1)) {
         ok = false;
         break;
       }
       tc::fence_after_sync();
-      const int t0 = j * kKv;
-      // tokens past pos are the causal edge, or were never staged
-      const bool edge = t0 + kKv - 1 > pos;
-      float mx = -INFINITY;
+      float v[2][32];
+      tc::ld32(trow + h * kStep, v[0]);
+      tc::ld32(trow + h * kStep + 32, v[1]);
+      tc::wait_ld();
+      const int t0 = (step0 + s) * kStep;
+      if (t0 + kStep - 1 > pos) {  // the causal edge (and tokens that were never staged)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float v[32];
-        tc::ld32(trow + S::kS + 32 * q, v);
-        tc::wait_ld();
-        if (edge) {
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = t0 + 32 * q + i <= pos ? v[i] : -INFINITY;
-        }
+          for (int e = 0; e < 32; ++e) v[q][e] = t0 + 32 * q + e <= pos ? v[q][e] : -INFINITY;
+      }
+      float by[kRuns], add[kRuns], mx = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < kRuns; ++g) {
-          float top = -INFINITY;
+      for (int g = 0; g < kRuns; ++g) {
+        const float4 f = of[g * (RUN / 8)];
+        by[g] = fmaxf(sl2 * f.x, 1e-37f);  // positive: minus infinity stays
+        add[g] = f.y;
+        float top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < RUN; i += 2) top = max3f(top, v[RUN * g + i], v[RUN * g + i + 1]);
-          const float4 f = of[(32 * q + RUN * g) / 8];
-          mx = fmaxf(mx, fmaf(top, fmaxf(sl2 * f.x, 1e-37f), f.y));  // positive: minus infinity stays
-        }
+        for (int e = 0; e < RUN; e += 2) top = max3f(top, v[(RUN * g + e) >> 5][(RUN * g + e) & 31], v[(RUN * g + e) >> 5][(RUN * g + e + 1) & 31]);
+        mx = fmaxf(mx, fmaf(top, by[g], add[g]));
       }
       float alpha = 1.f;
-      if (mx - kWeightShift > m + kRescale) {  // also the first kv tile (m = -inf): token 0 is always seen
+      if (mx - kWeightShift > m + kRescale) {  // also a row's first token
         alpha = ex2_approx(m - (mx - kWeightShift));
         m = mx - kWeightShift;
       }
       l *= alpha;
+      uint32_t w[kStep / 2];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float v[32];
-        tc::ld32(trow + S::kS + 32 * q, v);
-        tc::wait_ld();
-        if (edge) {
+      for (int g = 0; g < kRuns; ++g) {
+        const float a = add[g] - m;
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = t0 + 32 * q + i <= pos ? v[i] : -INFINITY;
+        for (int e = 0; e < RUN; e += 2) {
+          float y0 = v[(RUN * g + e) >> 5][(RUN * g + e) & 31], y1 = v[(RUN * g + e) >> 5][(RUN * g + e + 1) & 31];
+          fma2(y0, y1, by[g], a);
+          y0 = ex2_approx(y0), y1 = ex2_approx(y1);
+          add2(s0, s1, y0, y1);
+          w[(RUN * g + e) / 2] = h2(y0, y1);
         }
-        uint32_t w[16];
-#pragma unroll
-        for (int g = 0; g < kRuns; ++g) {
-          const float4 f = of[(32 * q + RUN * g) / 8];
-          const float by = fmaxf(sl2 * f.x, 1e-37f), add = f.y - m;
-          float sum[2] = {0.f, 0.f};
-#pragma unroll
-          for (int i = 0; i < RUN; i += 2) {
-            const float a = ex2_approx(fmaf(v[RUN * g + i], by, add)), c = ex2_approx(fmaf(v[RUN * g + i + 1], by, add));
-            sum[0] += a, sum[1] += c;
-            w[(RUN * g + i) / 2] = h2(a, c);
-          }
-          l = fmaf(sum[0] + sum[1], f.z, l);
-        }
-        // P takes columns 16q .. 16q + 15, whose scores have been read
-        tc::st16(trow + S::kS + 16 * q, w);
+        l = fmaf(s0 + s1, of[g * (RUN / 8)].z, l);
       }
-      if (j > 0 && __any_sync(kFullMask, alpha != 1.f)) {
-        // O is at rest: its last product completed before S_j was issued
+      tc::st32(trow + h * kStep, *reinterpret_cast<const float(*)[32]>(&w));  // over the scores
+      if (__any_sync(kFullMask, alpha != 1.f) && i > 0) {
+        // O is rescaled at rest: behind the product of the step before
+        if (!wait_warp(sh.added + x, (i - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
           tc::ld32(trow + S::kO + 32 * c, o);
           tc::wait_ld();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= alpha;
+          for (int e = 0; e < 32; ++e) o[e] *= alpha;
           tc::st32(trow + S::kO + 32 * c, o);
         }
       }
       tc::wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(pfull + x));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.weighed[x][h]));
     }
-    if (ok && ntx > 0) ok = wait_warp(pvdone + x, (ntx - 1) & 1);  // this tile's last PV product
-    if (ok && ntx > 0) {
-      tc::fence_after_sync();
-      const float inv = 1.f / l;
-      T* orow = static_cast<T*>(p.out) + static_cast<int64_t>(s0 + tok) * p.o_st + static_cast<int64_t>(kvh * G + gh) * p.o_sh;
+    if (ok && n > 0) ok = wait_warp(sh.finished + x, 0);
+    tc::fence_after_sync();
+    // rows that both streams have: stream 1 leaves its results in the ring, which nothing reads any more
+    float mine = 1.f, other = 0.f;
+    float* left = reinterpret_cast<float*>(sh.ring);  // [D][128 rows], then maxima and sums
+    static_assert((D + 2) * kTileRows * 4 <= S::kSlots * S::kSlotBytes, "the ring has room");
+    const bool both = same_rows && steps[1] > 0;
+    if (same_rows) {
+      asm volatile("bar.sync 1, %0;" ::"r"(4 * kStreams * 32) : "memory");
+      if (x == 1) {
+        left[D * kTileRows + r] = m, left[(D + 1) * kTileRows + r] = l;
+#pragma unroll 1
+        for (int c = 0; both && c < D / 32; ++c) {
+          float o[32];
+          tc::ld32(trow + S::kO + 32 * c, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) left[(32 * c + e) * kTileRows + r] = o[e];
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"r"(4 * kStreams * 32) : "memory");
+      if (x == 0 && both) {
+        const float m2 = left[D * kTileRows + r], top = fmaxf(m, m2);
+        mine = ex2_approx(m - top), other = ex2_approx(m2 - top);
+        l = fmaf(l, mine, other * left[(D + 1) * kTileRows + r]);
+        m = top;
+      }
+    }
+    if (ok && (x == 0 || !same_rows)) {
+      const int64_t row = static_cast<int64_t>(rows.s0 + tok) * p.num_q_heads + kvh * G + gh;  // of the output's
+      const float inv = sp.splits > 1 ? 1.f : 1.f / l;
+      T* orow = static_cast<T*>(p.out) + static_cast<int64_t>(rows.s0 + tok) * p.o_st + static_cast<int64_t>(kvh * G + gh) * p.o_sh;
+      float* prow = sp.parts + (row * sp.splits + part) * (D + 4);
+      const bool any_nan = sh.any_nan != 0;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
-        tc::ld32(trow + S::kO + 32 * c, o);
-        tc::wait_ld();
+        if (n > 0) {
+          tc::ld32(trow + S::kO + 32 * c, o);
+          tc::wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+        if (both) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = fmaf(o[e], mine, other * left[(32 * c + e) * kTileRows + r]);
+        }
+        if (any_nan) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = sh.nan_from[32 * c + e] <= pos ? NAN : o[e];
+        }
         if (valid) {
-          if (info[2]) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = nan_from[32 * c + i] <= pos ? NAN : o[i];
+          for (int e = 0; e < 32; ++e) o[e] *= inv;
+          if (sp.splits > 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(prow + 32 * c + 4 * e) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else {
+#pragma unroll
+            for (int q8 = 0; q8 < 4; ++q8) store8(orow + 32 * c + 8 * q8, o + 8 * q8, sp.o_vec);
           }
-#pragma unroll
-          for (int q8 = 0; q8 < 4; ++q8) store8(orow + 32 * c + 8 * q8, o + 8 * q8, inv, sp.o_vec);
         }
       }
+      if (sp.splits > 1 && valid) prow[D] = m, prow[D + 1] = l;
     }
   }
   if (!ok && lane == 0) atomicOr(p.err, kErrWaitTimeout);
@@ -592,21 +706,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- teardown: every MMA has completed before the columns are freed
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 1) {
-    if (n_tiles > 0) wait_warp(fin, 0);
+  if (warp == kMma) {
+    if (work) wait_warp(&sh.fin, 0);
     tc::fence_after_sync();
     tc::dealloc(tmem, S::kTmemCols);
   }
 }
 
+// Rows whose context several CTAs shared: a warp a row, the partial results in
+// their order.
+constexpr int kMergeWarps = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_prefill_kernel(const ScaledPrefillParams sp) {
+  const PrefillParams& p = sp.base;
+  __shared__ int found[2];
+  grid_wait();
+  grid_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // CTA i: rows i % kParts ... of kv head and row block as the kernel before numbers them
+  constexpr int kParts = 8;
+  const int part = static_cast<int>(blockIdx.x % kParts), kvh = static_cast<int>(blockIdx.x / kParts % p.num_kv_heads);
+  if (warp == 0) {
+    int seq, block;
+    row_block_of(p, kRows, static_cast<int>(blockIdx.x / kParts / p.num_kv_heads), lane, &seq, &block);
+    if (lane == 0) found[0] = seq, found[1] = block;
+  }
+  __syncthreads();
+  const Rows rows = rows_of(p, found[0], found[1], false);
+  const int end = min(rows.row0 + kRows, rows.n_rows);
+  for (int i = rows.row0 + part * (kRows / kParts) + warp; i < min(end, rows.row0 + (part + 1) * (kRows / kParts)); i += kMergeWarps) {
+    const int tok = i / p.group, head = kvh * p.group + (i - tok * p.group);
+    const float* from = sp.parts + (static_cast<int64_t>(rows.s0 + tok) * p.num_q_heads + head) * sp.splits * (D + 4);
+    // lane s has part s's maximum and sum
+    const float m = lane < sp.splits ? from[lane * (D + 4) + D] : kNone;
+    const float l = lane < sp.splits ? from[lane * (D + 4) + D + 1] : 0.f;
+    float v[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) v[e] = 0.f;
+    float top = m;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, d));
+    const float f = exp2f(m - top);
+    float sum = f * l;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
+    for (int s0 = 0; s0 < sp.splits; s0 += 8) {
+      float x[8][D / 32];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) x[s][e] = s0 + s < sp.splits ? from[(s0 + s) * (D + 4) + lane + 32 * e] : 0.f;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const float g = __shfl_sync(kFullMask, f, (s0 + s) & 31);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+          if (s0 + s < sp.splits) v[e] = fmaf(g, x[s][e], v[e]);
+      }
+    }
+    T* out = static_cast<T*>(p.out) + static_cast<int64_t>(rows.s0 + tok) * p.o_st + head * p.o_sh;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) out[lane + 32 * e] = from_f32<T>(v[e] / sum);
+  }
+}
+
 template <typename T, int D, int RUN>
 int launch_inst(const CUtensorMap& kmap, const CUtensorMap& vmap, const ScaledPrefillParams& p, int64_t blocks, cudaStream_t stream) {
-  using S = Shape<D>;
+  constexpr int kSmem = shared_bytes(D);
   static std::atomic<int> configured[64];
-  const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&prefill_block_scaled_kernel<T, D, RUN>), S::kSmem);
+  int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&prefill_block_scaled_kernel<T, D, RUN>), kSmem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(&prefill_block_scaled_kernel<T, D, RUN>, dim3(static_cast<unsigned>(blocks * p.base.num_kv_heads)),
-                          dim3(kThreads), S::kSmem, 0, stream, kmap, vmap, p);
+  e = launch_dependent(&prefill_block_scaled_kernel<T, D, RUN>, dim3(static_cast<unsigned>(blocks * p.base.num_kv_heads * p.splits)),
+                       dim3(kThreads), kSmem, 0, stream, kmap, vmap, p);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  if (p.splits == 1) return e;
+  e = launch_dependent(&merge_prefill_kernel<T, D>, dim3(static_cast<unsigned>(blocks * p.base.num_kv_heads * 8)),
+                       dim3(kMergeWarps * 32), 0, 0, stream, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
 }
 
 template <typename T>
@@ -618,17 +796,25 @@ int launch_type(int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap, 
   return cudaErrorInvalidValue;
 }
 
+constexpr int kMostSplits = 16;
+
 }  // namespace
 
-int launch_prefill_block_scaled(int dtype, int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                                const ScaledPrefillParams& p, int64_t num_tokens, int64_t num_seqs, cudaStream_t stream) {
+size_t prefill_block_scaled_workspace(int num_sms) { return size_t(num_sms) * kRows * (128 + 4) * sizeof(float); }
+
+int launch_prefill_block_scaled(int dtype, int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap, ScaledPrefillParams p,
+                                int64_t num_tokens, int64_t num_seqs, int num_sms, cudaStream_t stream) {
   // an upper bound on the row blocks: sum_b ceil(n_b G / 256) <= ceil(T G / 256) + B
   const int64_t blocks = (num_tokens * p.base.group + kRows - 1) / kRows + num_seqs;
   if (blocks <= 0) return cudaSuccess;
-  const int e = dtype == 2 ? launch_type<__nv_bfloat16>(head_dim, kmap, vmap, p, blocks, stream)
-                           : launch_type<__half>(head_dim, kmap, vmap, p, blocks, stream);
-  if (e == cudaSuccess) note_launch();
-  return e;
+  // as many CTAs for a row block's context as the SMs allow, each with a step for both streams at least
+  const int64_t tiles = (int64_t(p.base.max_blocks) * p.base.block_size + 2 * kStep - 1) / (2 * kStep);
+  int64_t splits = num_sms / (blocks * p.base.num_kv_heads);
+  if (splits > kMostSplits) splits = kMostSplits;
+  if (splits > tiles) splits = tiles;
+  p.splits = splits < 1 ? 1 : static_cast<int>(splits);
+  return dtype == 2 ? launch_type<__nv_bfloat16>(head_dim, kmap, vmap, p, blocks, stream)
+                    : launch_type<__half>(head_dim, kmap, vmap, p, blocks, stream);
 }
 
 }  // namespace wllm

@@ -77,6 +77,13 @@ __host__ __device__ constexpr uint32_t f16_idesc(bool bf16, bool a_mn, bool b_mn
 // ---------------------------------------------------------------------------
 // MMA issue and completion (one thread)
 // ---------------------------------------------------------------------------
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // D[tmem] (+)= A[smem] * B[smem]; accumulate == 0 overwrites D.
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                         uint32_t accumulate) {

@@ -108,8 +108,7 @@ def test_append_refuses_sizes(lib):
 
 def attention(lib, kind, change=(), B=3, T=None, Hq=4, Hkv=2, D=128, bs=16, dt=BF, scale=0.1, heads=None, size=None):
     T = (B if kind == "decode" else 7) if T is None else T
-    last = "ws" if kind == "decode" else "qsl"
-    names = ("out", "q", "kc", "vc", "ks", "vs", "bt", "cl", last)
+    names = ("out", "q", "kc", "vc", "ks", "vs", "bt", "cl") + (("ws",) if kind == "decode" else ("qsl", "ws"))
     a = dict(out=desc((T, Hq, D), dt), q=desc((T, Hq, D), dt), kc=desc((8, Hkv, bs, D), U8), vc=desc((8, Hkv, bs, D), U8),
              ks=desc((8, Hkv), F32), vs=desc((8, Hkv), F32), bt=desc((B, 4), I32), cl=desc((B,), I32), qsl=desc((B + 1,), I32),
              ws=desc((1 << 26,), U8, data=0x40000000))
@@ -136,7 +135,6 @@ def test_attention_refuses_sizes(lib, kind):
     assert attention(lib, kind, D=96) == UNSUPPORTED
     assert attention(lib, kind, D=512) == UNSUPPORTED
     assert attention(lib, kind, bs=4) == UNSUPPORTED
-    assert attention(lib, kind, D=64, bs=8) == UNSUPPORTED
     assert attention(lib, kind, dict(kc=desc((0, 2, 16, 128), U8, data=None), vc=desc((0, 2, 16, 128), U8, data=None),
                                      ks=desc((0, 2), F32, data=None), vs=desc((0, 2), F32, data=None))) == INVALID
     assert attention(lib, kind, B=0, T=0) == 0
@@ -151,11 +149,16 @@ def test_prefill_refuses(lib):
     assert attention(lib, "prefill", T=0) == 0
 
 
-def test_decode_refuses_workspaces(lib):
-    assert attention(lib, "decode", dict(ws=None)) == INVALID
-    assert attention(lib, "decode", dict(ws=desc((1 << 26,), I32))) == INVALID
-    assert attention(lib, "decode", dict(ws=desc((1 << 25, 2), U8))) == INVALID
-    assert attention(lib, "decode", dict(ws=desc((1 << 26,), U8, stride=(2,)))) == INVALID
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_attention_refuses_workspaces(lib, kind):
+    assert attention(lib, kind, dict(ws=None)) == INVALID
+    assert attention(lib, kind, dict(ws=desc((1 << 25, 2), U8))) == INVALID
+    assert attention(lib, kind, dict(ws=desc((1 << 25,), U8, data=None))) == INVALID
+
+
+@pytest.mark.parametrize("kind", ["decode", "prefill"])
+def test_attention_refuses_half_boxes(lib, kind):
+    assert attention(lib, kind, D=64, bs=8) == UNSUPPORTED
 
 
 def test_binding_refuses():
@@ -186,4 +189,4 @@ def test_kernels_read_what_others_write_by_plain_loads(name):
 def test_no_lane_gives_up_alone(name):
     """One lane waits for its warp and tells it, the warp votes, or only copies in flight are let land."""
     for number, code in waits(os.path.join(build.CSRC, name)):
-        assert re.match(r"(for \(.*\) mbar_wait_bounded\(|(if \(lane == 0\) )?(got|ok) = mbar_wait_bounded\()", code), f"{name}:{number}: {code}"
+        assert re.match(r"(for \(.*\) mbar_wait_bounded\(|(if \(lane == 0\) |const bool )?(got|ok) = mbar_wait_bounded\()", code), f"{name}:{number}: {code}"
