@@ -20,12 +20,12 @@
 // step, and their results meet at the end.  Tensor memory holds for each stream two
 // score tiles S (64 columns; the softmax writes the weights P, f16, two a column,
 // over them) and the output O: the scores of the step after next are computed while
-// a step's weights are.  Fifteen warps:
+// a step's weights are.  Sixteen warps:
 //
-//   warp 14 (producer): the block table, each step's K and V codes by TMA (16-row
-//     boxes, 128-byte swizzle) into a ring of eight raw slots, in the order in which
-//     the products need them, and their scales by 4-byte asynchronous copies on the
-//     same mbarrier;
+//   warps 14 and 15 (producers, of every other item): the block table, each step's K
+//     and V codes by TMA (16-row boxes, 128-byte swizzle) into a ring of eight raw
+//     slots, in the order in which the products need them; with K both scales, by
+//     4-byte asynchronous copies on the same mbarrier;
 //   warps 0-3 (widening), a pair of warps a raw slot: thread r takes row r to f16,
 //     which is exact, in a slot laid out for the products ([head_dim / 64][64
 //     tokens][128 bytes], swizzled).  V rows past the context become zeros, and so do
@@ -65,8 +65,8 @@ constexpr int kOctets = kStep / 8;
 constexpr int kWideners = 4;                 // warps, in pairs
 constexpr int kSoftmax = kWideners;          // first warp of the softmax
 constexpr int kMma = kSoftmax + 4 * kStreams;  // first of the MMA warps, one a stream
-constexpr int kProducer = kMma + kStreams;
-constexpr int kThreads = (kProducer + 1) * 32;
+constexpr int kProducer = kMma + kStreams;   // first of two producers
+constexpr int kThreads = (kProducer + 2) * 32;
 constexpr float kRescale = 8.f;              // the running maximum moves by more than this (log2) only
 constexpr float kWeightShift = 7.f;
 constexpr float kNone = -3.402823466e38f;    // the maximum of nothing
@@ -182,13 +182,11 @@ __device__ __forceinline__ uint4 load8(const T* src, bool vec) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* dst, const float* v, bool vec) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = Mma<T>::pack(v[2 * i], v[2 * i + 1]);
+__device__ __forceinline__ void store8(T* dst, const uint4& v, bool vec) {
   if (vec) {
-    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(dst) = v;
   } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint16_t* e = reinterpret_cast<uint16_t*>(dst);
 #pragma unroll
     for (int i = 0; i < 4; ++i) e[2 * i] = static_cast<uint16_t>(w[i]), e[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
@@ -244,6 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int part = static_cast<int>(blockIdx.x % sp.splits);
   const int kvh = static_cast<int>(blockIdx.x / sp.splits % p.num_kv_heads);
   const int tgt_block = static_cast<int>(blockIdx.x / sp.splits / p.num_kv_heads);
+  if (warp == kProducer && lane == 0) tma_prefetch_desc(&kmap);
+  if (warp == kProducer + 1 && lane == 0) tma_prefetch_desc(&vmap);
   if (warp == 0) {
     if (lane == 0) {
       for (int s = 0; s < S::kMoreSlots; ++s) {
@@ -312,57 +312,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   bool ok = true;
 
-  if (warp == kProducer && work) {
-    // ------------------------------- producer -------------------------------
+  if (warp >= kProducer && work) {
+    // ------------------------------- producers ------------------------------
+    // Items by turns: an item's raw slot then has had the same producer (and the same pair of widening warps) before,
+    // which is what makes a wait for the slot's phase before one for that phase and not the one before it.
     const int32_t* bt_row = p.block_tables + static_cast<int64_t>(b) * p.bt_stride;
-    // Table entries of four steps, a lane a run of 8 tokens: V's group, the next one (K is up to four steps ahead) and the
-    // one behind it.  The loads are unconditional (behind the end: of the last token), so nothing waits for them here.
+    // Table entries of four steps, a lane a run of 8 tokens: those of the furthest step so far, the four before and the four
+    // behind them.  The loads are unconditional (behind the end: of the last token), so nothing waits for them here.
     auto entries = [&](int group) { return bt_row[min((step0 + 4 * group) * kStep + 8 * lane, kv_end - 1) >> p.log2_bs]; };
     auto checked = [&](int entry) {
       if (entry >= 0 && entry < p.num_blocks) return entry;
       atomicOr(p.err, kErrBlock);
       return 0;
     };
-    int here = entries(0), there = entries(1), behind = entries(2), group = 0;
-    here = checked(here), there = checked(there);
-    int issued = 0;
-    for (int i = 0; i < 2 * n_steps; ++i) {
-      const int rs = i % S::kRaws;
+    // a box a lane: 16 tokens, or 8 where blocks have no more
+    constexpr int kBoxes = RUN == 8 ? kOctets : kOctets / 2;
+    constexpr uint32_t kBoxBytes = RUN == 8 ? 1024u : static_cast<uint32_t>(S::G::kTileBytes);
+    const int octet = RUN == 8 ? lane & 7 : (2 * lane) & 7, row_base = kvh * p.block_size;
+    const float* scales_of = (lane < kOctets ? sp.k_scales : sp.v_scales) + kvh;
+    int before = 0, here = checked(entries(0)), behind = entries(1), group = 0;
+    int i = warp - kProducer;
+    for (; i < 2 * n_steps; i += 2) {
+      int s;
+      const bool is_v = items.is_v(i, &s);
+      if (s >> 2 > group) before = here, here = checked(behind), ++group, behind = entries(group + 1);
+      const int entry = s >> 2 == group ? here : before, rs = i % S::kRaws;
+      const int phys = __shfl_sync(kFullMask, entry, (s & 3) * kOctets + octet);
+      const int of = __shfl_sync(kFullMask, entry, (s & 3) * kOctets + (lane & 7));
+      const int t = (step0 + s) * kStep + 8 * octet, at = row_base + (t & (p.block_size - 1));
+      const bool live = lane < kBoxes && t < kv_end;
+      const uint32_t bytes = kBoxBytes * __popc(__ballot_sync(kFullMask, live));
+      const uint32_t bar = smem_u32(sh.raw_full + rs);
       if (!wait_warp(sh.raw_empty + rs, ((i / S::kRaws) & 1) ^ 1)) {
         ok = false;
         break;
       }
-      int s;
-      const bool is_v = items.is_v(i, &s);
-      if (is_v && s >> 2 != group) {
-        here = there, there = checked(behind), ++group;
-        behind = entries(group + 2);
-      }
-      const int entry = s >> 2 == group ? here : there;
-      // a box a lane: 16 tokens, or 8 where blocks have no more
-      constexpr int kBoxes = RUN == 8 ? kOctets : kOctets / 2;
-      constexpr uint32_t kBoxBytes = RUN == 8 ? 1024u : static_cast<uint32_t>(S::G::kTileBytes);
-      const int octet = RUN == 8 ? lane & 7 : (2 * lane) & 7, t = (step0 + s) * kStep + 8 * octet;
-      const int phys = __shfl_sync(kFullMask, entry, (s & 3) * kOctets + octet);
-      const bool live = lane < kBoxes && t < kv_end;
-      const uint32_t bar = smem_u32(sh.raw_full + rs);
-      const uint32_t bytes = kBoxBytes * __popc(__ballot_sync(kFullMask, live));
       if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
       __syncwarp();
-      if (live) {
-        const int at = kvh * p.block_size + (t & (p.block_size - 1));
+      if (live)
         tma_load_3d(smem_u32(sh.raw[rs]) + lane * kBoxBytes, is_v ? &vmap : &kmap, bar, 0, S::G::kPairRows ? at >> 1 : at, phys);
-      }
-      const int of = __shfl_sync(kFullMask, entry, (s & 3) * kOctets + (lane & 7));
       if (!is_v && lane < 2 * kOctets)  // both scales of a run come with its K: lanes 0-7 K's, 8-15 V's
-        copy4_async(smem_u32(&sh.scales[rs][lane]),
-                    (lane < kOctets ? sp.k_scales : sp.v_scales) + static_cast<int64_t>(of) * p.num_kv_heads + kvh);
+        copy4_async(smem_u32(&sh.scales[rs][lane]), scales_of + static_cast<int64_t>(of) * p.num_kv_heads);
       arrive_behind_copies(bar);
-      ++issued;
     }
     // every copy still in flight lands before the CTA may leave
-    for (int i = max(0, issued - S::kRaws); i < issued; ++i)
-      if (!wait_warp(sh.raw_full + i % S::kRaws, (i / S::kRaws) & 1)) ok = false;
+    for (int u = max(i - S::kRaws, warp - kProducer); u < i; u += 2)
+      if (!wait_warp(sh.raw_full + u % S::kRaws, (u / S::kRaws) & 1)) ok = false;
   } else if (warp < kWideners && work) {
     // ------------------------------- widening -------------------------------
     const int r = threadIdx.x & 63;     // row of the step
@@ -517,39 +512,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int gh = valid ? rowg - tok * G : 0;
     const int pos = valid ? rows.pos0 + tok : 0;  // padding rows see token 0 only (output dropped)
     const uint32_t trow = tmem + x * S::kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
-    float sl2;  // of a raw score, without the block's scale; positive
+    // The warp's 32 rows are read and written together, kLanes lanes a row, so that a load or store touches few lines.
+    constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;
+    const int first_row = rows.row0 + (same_rows ? 0 : x * kTileRows) + quarter * 32, sub = lane / kLanes, piece = lane % kLanes;
+    float sl2 = 0.f;  // of a raw score, without the block's scale; positive
     {
       uint8_t* qx = sh.q[x];
-      const T* qrow = static_cast<const T*>(p.q) + static_cast<int64_t>(rows.s0 + tok) * p.q_st + static_cast<int64_t>(kvh * G + gh) * p.q_sh;
-      uint4 v[D / 8];
-      uint32_t most = 0u;
+      uint4 v[kLanes];
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) v[i] = valid ? load8(qrow + 8 * i, sp.q_vec) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < kLanes; ++i) {
+        // (a row behind the last: the last)
+        const int row = min(first_row + i * kRowsAtOnce + sub, rows.n_rows - 1), token = row / G;
+        v[i] = load8(static_cast<const T*>(p.q) + static_cast<int64_t>(rows.s0 + token) * p.q_st +
+                         static_cast<int64_t>(kvh * G + row - token * G) * p.q_sh + 8 * piece, sp.q_vec);
+      }
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
+      for (int i = 0; i < kLanes; ++i) {
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t most = 0u;
 #pragma unroll
         for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-      }
-      // largest magnitude to 2^14 .. 2^15 (exponent fields of binary32); a negative scale's sign goes to the query, a
-      // scale of zero makes the scores zero
-      const uint16_t top_bits = static_cast<uint16_t>(most);
-      const float top = to_f32(*reinterpret_cast<const T*>(&top_bits));
-      const int field = min(max(127 + 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
-      float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-      sl2 = p.scale_log2 == 0.f ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * fabsf(p.scale_log2);
-      up = p.scale_log2 < 0.f ? -up : p.scale_log2 == 0.f ? 0.f : up;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        for (int d = 1; d < kLanes; d <<= 1) most = max(most, __shfl_xor_sync(kFullMask, most, d));
+        // largest magnitude to 2^14 .. 2^15 (exponent fields of binary32); a negative scale's sign goes to the query, a
+        // scale of zero makes the scores zero
+        const uint16_t top_bits = static_cast<uint16_t>(most);
+        const float top = to_f32(*reinterpret_cast<const T*>(&top_bits));
+        const int field = min(max(127 + 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
+        float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+        const float down = p.scale_log2 == 0.f ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * fabsf(p.scale_log2);
+        up = p.scale_log2 < 0.f ? -up : p.scale_log2 == 0.f ? 0.f : up;
+        const float of_row = __shfl_sync(kFullMask, down, lane % kRowsAtOnce * kLanes);
+        if (lane / kRowsAtOnce == i) sl2 = of_row;  // lane's own row
         uint32_t f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const T* q2 = reinterpret_cast<const T*>(&w[e]);
           f[e] = h2(to_f32(q2[0]) * up, to_f32(q2[1]) * up);
         }
+        const int rr = quarter * 32 + i * kRowsAtOnce + sub;
         if (x == 0 || !same_rows)
-          *reinterpret_cast<uint4*>(qx + (i >> 3) * (kTileRows * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(qx + (piece >> 3) * (kTileRows * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4)) =
               make_uint4(f[0], f[1], f[2], f[3]);
       }
       tc::fence_async_smem();
@@ -662,11 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (ok && (x == 0 || !same_rows)) {
-      const int64_t row = static_cast<int64_t>(rows.s0 + tok) * p.num_q_heads + kvh * G + gh;  // of the output's
       const float inv = sp.splits > 1 ? 1.f : 1.f / l;
-      T* orow = static_cast<T*>(p.out) + static_cast<int64_t>(rows.s0 + tok) * p.o_st + static_cast<int64_t>(kvh * G + gh) * p.o_sh;
-      float* prow = sp.parts + (row * sp.splits + part) * (D + 4);
       const bool any_nan = sh.any_nan != 0;
+      // 32 columns of the warp's rows at a time, through shared memory (Q's place, which nothing reads any more)
+      uint4* turn = reinterpret_cast<uint4*>(sh.q[x] + quarter * 4096);  // [32 rows][8 pieces], piece c at c ^ (row % 8)
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         float o[32];
@@ -685,20 +687,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = sh.nan_from[32 * c + e] <= pos ? NAN : o[e];
         }
-        if (valid) {
+        __syncwarp();
+        if (sp.splits > 1) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= inv;
-          if (sp.splits > 1) {
+          for (int e = 0; e < 8; ++e)
+            turn[lane * 8 + (e ^ (lane & 7))] = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                                                           __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
+          __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<float4*>(prow + 32 * c + 4 * e) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          } else {
+          for (int i = 0; i < 8; ++i) {  // eight lanes a row
+            const int row_in = 4 * i + (lane >> 3), row = first_row + row_in, token = row / G;
+            if (row >= rows.n_rows) continue;
+            float* prow = sp.parts + ((static_cast<int64_t>(rows.s0 + token) * p.num_q_heads + kvh * G + row - token * G) * sp.splits + part) * (D + 4);
+            *reinterpret_cast<uint4*>(prow + 32 * c + 4 * (lane & 7)) = turn[row_in * 8 + ((lane & 7) ^ (row_in & 7))];
+          }
+        } else {
 #pragma unroll
-            for (int q8 = 0; q8 < 4; ++q8) store8(orow + 32 * c + 8 * q8, o + 8 * q8, sp.o_vec);
+          for (int e = 0; e < 4; ++e)
+            turn[lane * 8 + (e ^ (lane & 7))] =
+                make_uint4(Mma<T>::pack(o[8 * e] * inv, o[8 * e + 1] * inv), Mma<T>::pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                           Mma<T>::pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv), Mma<T>::pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // four lanes a row
+            const int row_in = 8 * i + (lane >> 2), row = first_row + row_in, token = row / G;
+            if (row >= rows.n_rows) continue;
+            T* orow = static_cast<T*>(p.out) + static_cast<int64_t>(rows.s0 + token) * p.o_st + static_cast<int64_t>(kvh * G + row - token * G) * p.o_sh;
+            store8(orow + 32 * c + 8 * (lane & 3), turn[row_in * 8 + ((lane & 3) ^ (row_in & 7))], sp.o_vec);
           }
         }
       }
-      if (sp.splits > 1 && valid) prow[D] = m, prow[D + 1] = l;
+      if (sp.splits > 1 && valid) {
+        float* prow = sp.parts + ((static_cast<int64_t>(rows.s0 + tok) * p.num_q_heads + kvh * G + gh) * sp.splits + part) * (D + 4);
+        prow[D] = m, prow[D + 1] = l;
+      }
     }
   }
   if (!ok && lane == 0) atomicOr(p.err, kErrWaitTimeout);
