@@ -72,6 +72,38 @@ constexpr float kWeightShift = 7.f;
 constexpr float kNone = -3.402823466e38f;    // the maximum of nothing
 constexpr int kFactorSteps = 8;              // steps whose factors are kept
 
+// The rows of one block and the context that they see.
+struct Rows {
+  int b, n_rows, row0, pos0, s0;
+  int end[kStreams];  // tokens that a row of Q tile x sees at most (0: the tile has no row)
+};
+__device__ __forceinline__ Rows rows_of(const PrefillParams& p, int b, int block, bool tell) {
+  Rows r{b, 0, 0, 0, 0, {0, 0}};
+  if (b < 0) return r;
+  const int l_max = p.max_blocks * p.block_size;
+  r.s0 = p.query_start_loc[b];
+  int n = p.query_start_loc[b + 1] - r.s0;
+  if (r.s0 < 0 || n < 0 || static_cast<int64_t>(r.s0) + n > p.num_tokens) {  // inconsistent query starts
+    if (tell) atomicOr(p.err, kErrLen);
+    return r;
+  }
+  int L = p.context_lens[b];
+  if (L < 0 || L > l_max || n > L) {
+    if (tell) atomicOr(p.err, kErrLen);
+    L = L < 0 ? 0 : (L > l_max ? l_max : L);
+    n = n > L ? L : n;
+  }
+  r.n_rows = n * p.group;
+  r.row0 = block * kRows;
+  r.pos0 = L - n;
+#pragma unroll
+  for (int x = 0; x < kStreams; ++x) {  // (no rows only when n was clamped, error already flagged)
+    const int rx = r.row0 + x * kTileRows;
+    if (rx < r.n_rows) r.end[x] = r.pos0 + (min(r.n_rows, rx + kTileRows) - 1) / p.group + 1;
+  }
+  return r;
+}
+
 template <int D>
 struct Shape {
   using G = Geom<uint8_t, D>;
@@ -99,6 +131,7 @@ struct Shared {
   uint8_t raw[S::kRaws][S::kRawBytes];     // items as codes
   float4 factors[kFactorSteps][kOctets];   // ks, log2 vs, 1 / vs of each run of 8 tokens
   float scales[S::kRaws][2 * kOctets];     // K's and V's of a K item's step
+  uint8_t row_field[kStreams][kTileRows];  // the exponent field of the power of two that a query row was scaled by
   int nan_from[D];                         // first token whose value is NaN
   uint64_t full[S::kMoreSlots];            // widened (widening -> MMA)
   uint64_t empty[S::kMoreSlots];           // given up by both streams (MMA -> widening)
@@ -112,12 +145,13 @@ struct Shared {
   uint64_t q_full;                         // Q written (softmax -> MMA)
   uint64_t fin;                            // every MMA of the CTA done
   uint32_t tmem;
-  int seq, block, any_nan;
+  int any_nan;
+  Rows rows;
 };
 static_assert(sizeof(Shared<128>) <= 232448, "227 KB");
 // one CTA an SM: a second one would contend for tensor memory
-constexpr int shared_bytes(int d) { return d == 64 ? 118784 : static_cast<int>(sizeof(Shared<128>)); }
-static_assert(sizeof(Shared<64>) <= 118784 && 2 * (118784 + 1024) > 233472, "");
+constexpr int shared_bytes(int d) { return d == 64 ? 119808 : static_cast<int>(sizeof(Shared<128>)); }
+static_assert(sizeof(Shared<64>) <= 119808 && 2 * (119808 + 1024) > 233472, "");
 
 // The items of a CTA's n steps, in the order of their use: K of the first `lead`
 // steps, then V of a step and K of the step `lead` behind it in turn.
@@ -171,6 +205,16 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
       : "f"(a), "f"(b));
 }
 
+// Token and head (of the group) of a row, and of the rows behind it: one division for all.
+struct RowAt {
+  int token, head;
+  __device__ __forceinline__ RowAt(int row, int group) : token(row / group) { head = row - token * group; }
+  __device__ __forceinline__ void advance(int rows, int group) {
+    head += rows;
+    while (head >= group) head -= group, ++token;
+  }
+};
+
 // Eight elements of a row, 16-bit.
 template <typename T>
 __device__ __forceinline__ uint4 load8(const T* src, bool vec) {
@@ -191,38 +235,6 @@ __device__ __forceinline__ void store8(T* dst, const uint4& v, bool vec) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) e[2 * i] = static_cast<uint16_t>(w[i]), e[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
   }
-}
-
-// The rows of one block and the context that they see.
-struct Rows {
-  int b, n_rows, row0, pos0, s0;
-  int end[kStreams];  // tokens that a row of Q tile x sees at most (0: the tile has no row)
-};
-__device__ __forceinline__ Rows rows_of(const PrefillParams& p, int b, int block, bool tell) {
-  Rows r{b, 0, 0, 0, 0, {0, 0}};
-  if (b < 0) return r;
-  const int l_max = p.max_blocks * p.block_size;
-  r.s0 = p.query_start_loc[b];
-  int n = p.query_start_loc[b + 1] - r.s0;
-  if (r.s0 < 0 || n < 0 || static_cast<int64_t>(r.s0) + n > p.num_tokens) {  // inconsistent query starts
-    if (tell) atomicOr(p.err, kErrLen);
-    return r;
-  }
-  int L = p.context_lens[b];
-  if (L < 0 || L > l_max || n > L) {
-    if (tell) atomicOr(p.err, kErrLen);
-    L = L < 0 ? 0 : (L > l_max ? l_max : L);
-    n = n > L ? L : n;
-  }
-  r.n_rows = n * p.group;
-  r.row0 = block * kRows;
-  r.pos0 = L - n;
-#pragma unroll
-  for (int x = 0; x < kStreams; ++x) {  // (no rows only when n was clamped, error already flagged)
-    const int rx = r.row0 + x * kTileRows;
-    if (rx < r.n_rows) r.end[x] = r.pos0 + (min(r.n_rows, rx + kTileRows) - 1) / p.group + 1;
-  }
-  return r;
 }
 
 // RUN: tokens of a run with one scale that the softmax tells apart, 8 for blocks
@@ -272,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_wait();
     int seq, block;
     row_block_of(p, kRows, tgt_block, lane, &seq, &block);
-    if (lane == 0) sh.seq = seq, sh.block = block, sh.any_nan = 0;
+    if (lane == 0) sh.rows = rows_of(p, seq, block, true), sh.any_nan = 0;
   } else {
     grid_wait();
   }
@@ -289,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.query_start_loc[i + 1] < p.query_start_loc[i]) atomicOr(p.err, kErrLen);
   }
 
-  const Rows rows = rows_of(p, sh.seq, sh.block, threadIdx.x == 0);
+  const Rows rows = sh.rows;
   const int b = rows.b, kv_end = max(rows.end[0], rows.end[1]);
   // this CTA's steps, step0 on, and each stream's (of all of them, or every other one)
   const int all_steps = (kv_end + kStep - 1) / kStep;
@@ -515,20 +527,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The warp's 32 rows are read and written together, kLanes lanes a row, so that a load or store touches few lines.
     constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;
     const int first_row = rows.row0 + (same_rows ? 0 : x * kTileRows) + quarter * 32, sub = lane / kLanes, piece = lane % kLanes;
-    float sl2 = 0.f;  // of a raw score, without the block's scale; positive
     {
-      uint8_t* qx = sh.q[x];
-      uint4 v[kLanes];
-#pragma unroll
-      for (int i = 0; i < kLanes; ++i) {
-        // (a row behind the last: the last)
-        const int row = min(first_row + i * kRowsAtOnce + sub, rows.n_rows - 1), token = row / G;
-        v[i] = load8(static_cast<const T*>(p.q) + static_cast<int64_t>(rows.s0 + token) * p.q_st +
-                         static_cast<int64_t>(kvh * G + row - token * G) * p.q_sh + 8 * piece, sp.q_vec);
+      // The rows go to shared memory as they are and every lane rewrites its own pieces: rolled loops, because
+      // straight-line code runs once and is fetched more slowly than it runs.  Rows that both streams have are halved
+      // between them.
+      uint8_t* const qx = sh.q[same_rows ? 0 : x];
+      const int rows_here = same_rows ? 16 : 32, in_tile = quarter * 32 + (same_rows ? 16 * x + sub : sub);
+      const auto place = [&](int rr) {
+        return reinterpret_cast<uint4*>(qx + (piece >> 3) * (kTileRows * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4));
+      };
+      const int first = rows.row0 + (same_rows ? 0 : x * kTileRows) + in_tile;
+      RowAt at(first, G);
+#pragma unroll 2
+      for (int j = 0; j < rows_here; j += kRowsAtOnce) {
+        const bool there = first + j < rows.n_rows;  // (a row behind the last: the first)
+        const T* from = static_cast<const T*>(p.q) + static_cast<int64_t>(rows.s0 + (there ? at.token : 0)) * p.q_st +
+                        static_cast<int64_t>(kvh * G + (there ? at.head : 0)) * p.q_sh + 8 * piece;
+        if (sp.q_vec)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(place(in_tile + j))), "l"(from) : "memory");
+        else
+          *place(in_tile + j) = load8(from, false);
+        at.advance(kRowsAtOnce, G);
       }
-#pragma unroll
-      for (int i = 0; i < kLanes; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 4
+      for (int j = 0; j < rows_here; j += kRowsAtOnce) {
+        const uint4 v = *place(in_tile + j);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t most = 0u;
 #pragma unroll
         for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
@@ -540,25 +565,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float top = to_f32(*reinterpret_cast<const T*>(&top_bits));
         const int field = min(max(127 + 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
         float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-        const float down = p.scale_log2 == 0.f ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * fabsf(p.scale_log2);
         up = p.scale_log2 < 0.f ? -up : p.scale_log2 == 0.f ? 0.f : up;
-        const float of_row = __shfl_sync(kFullMask, down, lane % kRowsAtOnce * kLanes);
-        if (lane / kRowsAtOnce == i) sl2 = of_row;  // lane's own row
+        if (piece == 0) sh.row_field[same_rows ? 0 : x][in_tile + j] = static_cast<uint8_t>(field);
         uint32_t f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const T* q2 = reinterpret_cast<const T*>(&w[e]);
           f[e] = h2(to_f32(q2[0]) * up, to_f32(q2[1]) * up);
         }
-        const int rr = quarter * 32 + i * kRowsAtOnce + sub;
-        if (x == 0 || !same_rows)
-          *reinterpret_cast<uint4*>(qx + (piece >> 3) * (kTileRows * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4)) =
-              make_uint4(f[0], f[1], f[2], f[3]);
+        *place(in_tile + j) = make_uint4(f[0], f[1], f[2], f[3]);
       }
       tc::fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.q_full));
+      if (same_rows) asm volatile("bar.sync 1, %0;" ::"r"(4 * kStreams * 32) : "memory");
     }
+    // of a raw score, without the block's scale: what undoes the row's, times the scale's magnitude; positive
+    const float sl2 =
+        p.scale_log2 == 0.f ? 1.f : __uint_as_float((254u - sh.row_field[same_rows ? 0 : x][r]) << 23) * fabsf(p.scale_log2);
     float m = kNone, l = 0.f;
     const int n = steps[x];
     constexpr int kRuns = kStep / RUN;
@@ -667,6 +691,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && (x == 0 || !same_rows)) {
       const float inv = sp.splits > 1 ? 1.f : 1.f / l;
       const bool any_nan = sh.any_nan != 0;
+      // where this lane's pieces go: of rows lane / 4 + 8 i of the output, or lane / 8 + 4 i of the partial results
+      int64_t to[8];
+      {
+        const int each = sp.splits > 1 ? 4 : 8;
+        RowAt at(first_row + (sp.splits > 1 ? lane >> 3 : lane >> 2), G);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          to[i] = sp.splits > 1 ? ((static_cast<int64_t>(rows.s0 + at.token) * p.num_q_heads + kvh * G + at.head) * sp.splits + part) * (D + 4)
+                                : static_cast<int64_t>(rows.s0 + at.token) * p.o_st + static_cast<int64_t>(kvh * G + at.head) * p.o_sh;
+          at.advance(each, G);
+        }
+      }
       // 32 columns of the warp's rows at a time, through shared memory (Q's place, which nothing reads any more)
       uint4* turn = reinterpret_cast<uint4*>(sh.q[x] + quarter * 4096);  // [32 rows][8 pieces], piece c at c ^ (row % 8)
 #pragma unroll 1
@@ -696,10 +732,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {  // eight lanes a row
-            const int row_in = 4 * i + (lane >> 3), row = first_row + row_in, token = row / G;
-            if (row >= rows.n_rows) continue;
-            float* prow = sp.parts + ((static_cast<int64_t>(rows.s0 + token) * p.num_q_heads + kvh * G + row - token * G) * sp.splits + part) * (D + 4);
-            *reinterpret_cast<uint4*>(prow + 32 * c + 4 * (lane & 7)) = turn[row_in * 8 + ((lane & 7) ^ (row_in & 7))];
+            const int row_in = 4 * i + (lane >> 3);
+            if (first_row + row_in < rows.n_rows)
+              *reinterpret_cast<uint4*>(sp.parts + to[i] + 32 * c + 4 * (lane & 7)) = turn[row_in * 8 + ((lane & 7) ^ (row_in & 7))];
           }
         } else {
 #pragma unroll
@@ -710,10 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // four lanes a row
-            const int row_in = 8 * i + (lane >> 2), row = first_row + row_in, token = row / G;
-            if (row >= rows.n_rows) continue;
-            T* orow = static_cast<T*>(p.out) + static_cast<int64_t>(rows.s0 + token) * p.o_st + static_cast<int64_t>(kvh * G + row - token * G) * p.o_sh;
-            store8(orow + 32 * c + 8 * (lane & 3), turn[row_in * 8 + ((lane & 3) ^ (row_in & 7))], sp.o_vec);
+            const int row_in = 8 * i + (lane >> 2);
+            if (first_row + row_in < rows.n_rows)
+              store8(static_cast<T*>(p.out) + to[i] + 32 * c + 8 * (lane & 3), turn[row_in * 8 + ((lane & 3) ^ (row_in & 7))], sp.o_vec);
           }
         }
       }
