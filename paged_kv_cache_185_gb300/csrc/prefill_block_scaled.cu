@@ -537,43 +537,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         return reinterpret_cast<uint4*>(qx + (piece >> 3) * (kTileRows * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4));
       };
       const int first = rows.row0 + (same_rows ? 0 : x * kTileRows) + in_tile;
-      RowAt at(first, G);
-#pragma unroll 2
-      for (int j = 0; j < rows_here; j += kRowsAtOnce) {
-        const bool there = first + j < rows.n_rows;  // (a row behind the last: the first)
-        const T* from = static_cast<const T*>(p.q) + static_cast<int64_t>(rows.s0 + (there ? at.token : 0)) * p.q_st +
-                        static_cast<int64_t>(kvh * G + (there ? at.head : 0)) * p.q_sh + 8 * piece;
-        if (sp.q_vec)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(place(in_tile + j))), "l"(from) : "memory");
-        else
-          *place(in_tile + j) = load8(from, false);
-        at.advance(kRowsAtOnce, G);
+      {
+        const int token = first / G;
+        int head = first - token * G;
+        const T* from = static_cast<const T*>(p.q) + static_cast<int64_t>(rows.s0 + token) * p.q_st +
+                        static_cast<int64_t>(kvh * G + head) * p.q_sh + 8 * piece;
+        // kRowsAtOnce rows on: so many heads, or a token more and as many less than the group
+        const int heads_on = kRowsAtOnce % G;
+        const int64_t on = kRowsAtOnce / G * p.q_st + heads_on * p.q_sh, over = p.q_st - G * p.q_sh;
+        if (sp.q_vec) {
+#pragma unroll 4
+          for (int j = 0; j < rows_here; j += kRowsAtOnce) {  // (zeros behind the last row)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(in_tile + j))), "l"(from),
+                         "r"(first + j < rows.n_rows ? 16 : 0) : "memory");
+            head += heads_on, from += on;
+            if (head >= G) head -= G, from += over;
+          }
+        } else {
+          for (int j = 0; j < rows_here; j += kRowsAtOnce) {
+            *place(in_tile + j) = first + j < rows.n_rows ? load8(from, false) : make_uint4(0u, 0u, 0u, 0u);
+            head += heads_on, from += on;
+            if (head >= G) head -= G, from += over;
+          }
+        }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 4
-      for (int j = 0; j < rows_here; j += kRowsAtOnce) {
-        const uint4 v = *place(in_tile + j);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t most = 0u;
+      constexpr int kTogether = 4;  // pieces whose steps overlap
+#pragma unroll 1
+      for (int j = 0; j < rows_here; j += kTogether * kRowsAtOnce) {
+        uint4 v[kTogether];
+        uint32_t most[kTogether];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) most = max(most, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-#pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) most = max(most, __shfl_xor_sync(kFullMask, most, d));
-        // largest magnitude to 2^14 .. 2^15 (exponent fields of binary32); a negative scale's sign goes to the query, a
-        // scale of zero makes the scores zero
-        const uint16_t top_bits = static_cast<uint16_t>(most);
-        const float top = to_f32(*reinterpret_cast<const T*>(&top_bits));
-        const int field = min(max(127 + 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
-        float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-        up = p.scale_log2 < 0.f ? -up : p.scale_log2 == 0.f ? 0.f : up;
-        if (piece == 0) sh.row_field[same_rows ? 0 : x][in_tile + j] = static_cast<uint8_t>(field);
-        uint32_t f[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const T* q2 = reinterpret_cast<const T*>(&w[e]);
-          f[e] = h2(to_f32(q2[0]) * up, to_f32(q2[1]) * up);
+        for (int u = 0; u < kTogether; ++u) {
+          v[u] = *place(in_tile + j + u * kRowsAtOnce);
+          most[u] = __vmaxu2(__vmaxu2(v[u].x & 0x7fff7fffu, v[u].y & 0x7fff7fffu), __vmaxu2(v[u].z & 0x7fff7fffu, v[u].w & 0x7fff7fffu));
         }
-        *place(in_tile + j) = make_uint4(f[0], f[1], f[2], f[3]);
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1)
+#pragma unroll
+          for (int u = 0; u < kTogether; ++u) most[u] = __vmaxu2(most[u], __shfl_xor_sync(kFullMask, most[u], d));
+#pragma unroll
+        for (int u = 0; u < kTogether; ++u) {
+          // largest magnitude to 2^14 .. 2^15 (exponent fields of binary32); a negative scale's sign goes to the query, a
+          // scale of zero makes the scores zero
+          const uint16_t top_bits = static_cast<uint16_t>(max(most[u] & 0xffffu, most[u] >> 16));
+          const float top = to_f32(*reinterpret_cast<const T*>(&top_bits));
+          const int field = min(max(127 + 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
+          float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
+          up = p.scale_log2 < 0.f ? -up : p.scale_log2 == 0.f ? 0.f : up;
+          const int rr = in_tile + j + u * kRowsAtOnce;
+          if (piece == 0) sh.row_field[same_rows ? 0 : x][rr] = static_cast<uint8_t>(field);
+          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          uint32_t f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const T* q2 = reinterpret_cast<const T*>(&w[e]);
+            f[e] = h2(to_f32(q2[0]) * up, to_f32(q2[1]) * up);
+          }
+          *place(rr) = make_uint4(f[0], f[1], f[2], f[3]);
+        }
       }
       tc::fence_async_smem();
       __syncwarp();
@@ -691,23 +713,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && (x == 0 || !same_rows)) {
       const float inv = sp.splits > 1 ? 1.f : 1.f / l;
       const bool any_nan = sh.any_nan != 0;
-      // where this lane's pieces go: of rows lane / 4 + 8 i of the output, or lane / 8 + 4 i of the partial results
+      // where this lane's pieces go, of rows lane / 8 + 4 i
       int64_t to[8];
       {
-        const int each = sp.splits > 1 ? 4 : 8;
-        RowAt at(first_row + (sp.splits > 1 ? lane >> 3 : lane >> 2), G);
+        RowAt at(first_row + (lane >> 3), G);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           to[i] = sp.splits > 1 ? ((static_cast<int64_t>(rows.s0 + at.token) * p.num_q_heads + kvh * G + at.head) * sp.splits + part) * (D + 4)
                                 : static_cast<int64_t>(rows.s0 + at.token) * p.o_st + static_cast<int64_t>(kvh * G + at.head) * p.o_sh;
-          at.advance(each, G);
+          at.advance(4, G);
         }
       }
-      // 32 columns of the warp's rows at a time, through shared memory (Q's place, which nothing reads any more)
-      uint4* turn = reinterpret_cast<uint4*>(sh.q[x] + quarter * 4096);  // [32 rows][8 pieces], piece c at c ^ (row % 8)
-#pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
+      // 64 columns of the warp's rows at a time (of partial results 32), through shared memory (Q's place, which nothing
+      // reads any more): [32 rows][8 pieces], piece c at c ^ (row % 8)
+      uint4* turn = reinterpret_cast<uint4*>(sh.q[x] + quarter * 4096);
+      const auto columns = [&](int c, float (&o)[32]) {
         if (n > 0) {
           tc::ld32(trow + S::kO + 32 * c, o);
           tc::wait_ld();
@@ -723,32 +743,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = sh.nan_from[32 * c + e] <= pos ? NAN : o[e];
         }
-        __syncwarp();
+      };
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        columns(c, o);
+        const int half = sp.splits > 1 ? 0 : 4 * (c & 1);
+        if (half == 0) __syncwarp();
         if (sp.splits > 1) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             turn[lane * 8 + (e ^ (lane & 7))] = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
                                                            __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {  // eight lanes a row
-            const int row_in = 4 * i + (lane >> 3);
-            if (first_row + row_in < rows.n_rows)
-              *reinterpret_cast<uint4*>(sp.parts + to[i] + 32 * c + 4 * (lane & 7)) = turn[row_in * 8 + ((lane & 7) ^ (row_in & 7))];
-          }
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            turn[lane * 8 + (e ^ (lane & 7))] =
+            turn[lane * 8 + ((half + e) ^ (lane & 7))] =
                 make_uint4(Mma<T>::pack(o[8 * e] * inv, o[8 * e + 1] * inv), Mma<T>::pack(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
                            Mma<T>::pack(o[8 * e + 4] * inv, o[8 * e + 5] * inv), Mma<T>::pack(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-          __syncwarp();
+          if (half == 0) continue;
+        }
+        __syncwarp();
+        uint4 row[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // four lanes a row
-            const int row_in = 8 * i + (lane >> 2);
-            if (first_row + row_in < rows.n_rows)
-              store8(static_cast<T*>(p.out) + to[i] + 32 * c + 8 * (lane & 3), turn[row_in * 8 + ((lane & 3) ^ (row_in & 7))], sp.o_vec);
-          }
+        for (int i = 0; i < 8; ++i) row[i] = turn[(4 * i + (lane >> 3)) * 8 + ((lane & 7) ^ ((4 * i + (lane >> 3)) & 7))];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (first_row + 4 * i + (lane >> 3) >= rows.n_rows) break;
+          if (sp.splits > 1)
+            *reinterpret_cast<uint4*>(sp.parts + to[i] + 32 * c + 4 * (lane & 7)) = row[i];
+          else
+            store8(static_cast<T*>(p.out) + to[i] + 32 * (c - 1) + 8 * (lane & 7), row[i], sp.o_vec);
         }
       }
       if (sp.splits > 1 && valid) {
