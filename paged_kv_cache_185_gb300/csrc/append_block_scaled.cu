@@ -72,16 +72,6 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ uint4 load16(const T* src, bool vec) {
-  if (vec) return *reinterpret_cast<const uint4*>(src);
-  uint4 r;
-  T* e = reinterpret_cast<T*>(&r);
-#pragma unroll
-  for (int i = 0; i < Vec<T>::kN; ++i) e[i] = src[i];
-  return r;
-}
-
 // Codes of 16 bytes of elements times `inv`.
 __device__ __forceinline__ void store_codes(uint8_t* dst, const uint4& x, float inv, float) {
   const uint32_t c = f32x2_to_e4m3x2(__uint_as_float(x.y) * inv, __uint_as_float(x.x) * inv) |
@@ -122,13 +112,18 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t codes, float f) {
   return f32x2_to_e4m3x2(a.y * f, a.x * f) | f32x2_to_e4m3x2(b.y * f, b.x * f) << 16;
 }
 
+constexpr int append_threads(int wpu) { return 32 * (wpu == 1 ? kAppendWarps : wpu); }
+// that run at once; the registers of 20 warps (96 a thread) are enough for one warp a unit
+constexpr int append_warps_per_sm(int wpu) { return wpu == 1 ? 20 : 16; }
+
 // Sequence b, whose new tokens are packed rows r = qsl[b] - qsl[0] .. qsl[b+1] -
 // qsl[0], owns the unit numbers from floor(r / bs) + 2 b on: n tokens touch at most
 // floor(n / bs) + 2 blocks, which is no more than the distance to the next
 // sequence's first unit.
 // WPU: warps of a unit (1: a CTA's warps have units of their own).
 template <typename T, int D, int WPU>
-__global__ void __launch_bounds__(WPU == 1 ? kAppendWarps * 32 : WPU * 32) append_block_scaled_kernel(const ScaledAppendParams p) {
+__global__ void __launch_bounds__(append_threads(WPU), append_warps_per_sm(WPU) * 32 / append_threads(WPU))
+    append_block_scaled_kernel(const ScaledAppendParams p) {
   constexpr int kVecs = D / Vec<T>::kN;                          // 16-byte vectors of a row
   constexpr int kLoads = kWarpElements / Vec<T>::kN / 32;        // a lane's
   constexpr int kRows = kWarpElements / D;                       // rows that a warp holds
@@ -163,10 +158,19 @@ __global__ void __launch_bounds__(WPU == 1 ? kAppendWarps * 32 : WPU * 32) appen
   const int64_t units = slots * sides;
   const int64_t first = int64_t(blockIdx.x - p.check_ctas) * kUnitsPerCta + (WPU == 1 ? warp : 0);
   const int64_t stride = int64_t(gridDim.x - p.check_ctas) * kUnitsPerCta;
-  int turn = 0;
-  for (int64_t unit = first; unit < units; unit += stride) {
+  struct Unit {
+    const T* src;    // first new element
+    uint8_t* codes;  // of the block and head
+    float* scale_at;
+    float held;      // the scale so far, where the block has earlier tokens
+    int off, count;  // first new token in the block; new tokens in it (0: nothing to do)
+    int kv;
+  };
+  const auto locate = [&](int64_t unit, Unit& u) {
     const int slot = static_cast<int>(unit / sides), side = static_cast<int>(unit - int64_t(slot) * sides);
-    const int h = side >> 1, kv = side & 1;
+    const int h = side >> 1;
+    u.kv = side & 1;
+    u.count = 0;
     int b = slot, n = 1, j = 0, row = slot;
     if (p.query_start_loc != nullptr) {
       // largest b whose first unit is not behind this one: 32 probes at a time
@@ -185,39 +189,65 @@ __global__ void __launch_bounds__(WPU == 1 ? kAppendWarps * 32 : WPU * 32) appen
       j = slot - (((row - row_first) >> p.log2_bs) + 2 * b);
     }
     const int len = p.context_lens[b];
-    if (p.query_start_loc == nullptr && len == 0) continue;  // an empty sequence of the one-token form has no new token
+    if (p.query_start_loc == nullptr && len == 0) return;  // an empty sequence of the one-token form has no new token
     if (n < 0 || n > len || len > p.max_tokens || j < 0 || row < 0 || n > p.num_tokens - row) {
       if (speaker) atomicOr(p.err, kErrLen);
-      continue;
+      return;
     }
-    if (n == 0) continue;
+    if (n == 0) return;
     const int begin = len - n;                        // position of the first new token
     const int at = (begin >> p.log2_bs) + j;          // this unit's block of the sequence
-    if (at > (len - 1) >> p.log2_bs) continue;
+    if (at > (len - 1) >> p.log2_bs) return;
     const int id = p.block_tables[b * p.bt_stride + at];
     if (id < 0 || id >= p.num_blocks) {
       if (speaker) atomicOr(p.err, kErrBlock);
-      continue;
+      return;
     }
-    const int off = max(0, begin - (at << p.log2_bs));           // first new token in the block
-    const int count = min(bs, len - (at << p.log2_bs)) - off;    // new tokens in it
-    const T* src = static_cast<const T*>(p.src[kv]) + (row + ((at << p.log2_bs) + off - begin)) * p.src_st[kv] + h * p.src_sh[kv];
+    u.off = max(0, begin - (at << p.log2_bs));
+    u.count = min(bs, len - (at << p.log2_bs)) - u.off;
+    u.src = static_cast<const T*>(p.src[u.kv]) + (row + ((at << p.log2_bs) + u.off - begin)) * p.src_st[u.kv] + h * p.src_sh[u.kv];
     const int64_t run = int64_t(id) * p.num_kv_heads + h;
-    uint8_t* codes = p.cache[kv] + run * bs * D;
-    float* scale_at = p.scales[kv] + run;
-    const float held = off > 0 ? *scale_at : 0.f;
+    u.codes = p.cache[u.kv] + run * bs * D;
+    u.scale_at = p.scales[u.kv] + run;
+    u.held = 0.f;
+    if (u.off > 0) u.held = *u.scale_at;
+  };
 
+  int turn = 0;
+  Unit u, next{};
+  if (first < units) locate(first, next);
+  for (int64_t unit = first; unit < units; unit += stride) {
+    u = next;
     // the new elements: into registers, or through them where there are more
-    const int64_t st = p.src_st[kv];
+    const int64_t st = p.src_st[u.kv];
     uint4 x[kLoads];
     uint32_t most = 0u;
+    const auto row_of = [&](int i) { return (i * 32 + lane) / kVecs; };  // of load i, among the rows that a warp holds
     auto load = [&](int r0) {
+      const T* base = u.src + (r0 + lane / kVecs) * st + (lane % kVecs) * Vec<T>::kN;
+      const auto piece = [&](int i) { return base + i * 32 / kVecs * st + i * 32 % kVecs * Vec<T>::kN; };
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int v = i * 32 + lane, r = r0 + v / kVecs;
-        x[i] = r < count ? load16(src + r * st + (v % kVecs) * Vec<T>::kN, p.vec) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < kLoads; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.vec) {  // a loop for each kind of load: a choice inside it would wait for every load
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          if (r0 + row_of(i) < u.count) x[i] = *reinterpret_cast<const uint4*>(piece(i));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+          if (r0 + row_of(i) < u.count) {
+            const T* from = piece(i);
+            T* e = reinterpret_cast<T*>(&x[i]);
+#pragma unroll
+            for (int k = 0; k < Vec<T>::kN; ++k) e[k] = from[k];
+          }
       }
     };
+    load(part * kRows);
+    // the next unit is looked up while these are on their way
+    next.count = 0;
+    if (unit + stride < units) locate(unit + stride, next);
+    if (u.count == 0) continue;
     auto measure = [&](bool finite_only) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -226,11 +256,11 @@ __global__ void __launch_bounds__(WPU == 1 ? kAppendWarps * 32 : WPU * 32) appen
         for (int e = 0; e < 4; ++e) most = Vec<T>::most(most, finite_only ? Vec<T>::finite(w[e]) : w[e]);
       }
     };
-    const bool once = count <= kRows * WPU;
+    const bool once = u.count <= kRows * WPU;
     auto largest = [&](bool finite_only) {
       most = 0u;
-      for (int r0 = part * kRows; r0 < count; r0 += kRows * WPU) {
-        if (!once || !finite_only) load(r0);
+      for (int r0 = part * kRows; r0 < u.count; r0 += kRows * WPU) {
+        if (!once && (finite_only || r0 != part * kRows)) load(r0);
         measure(finite_only);
       }
       float m = Vec<T>::widest(most);
@@ -247,36 +277,36 @@ __global__ void __launch_bounds__(WPU == 1 ? kAppendWarps * 32 : WPU * 32) appen
     };
     float m = largest(false);
     if (m == INFINITY) m = largest(true);  // infinities do not count (the same for all the unit's warps)
-    const float need = scale_for(m), old = scale_in_range(held);
-    const float scale = off > 0 ? fmaxf(need, old) : need;
+    const float need = scale_for(m), old = scale_in_range(u.held);
+    const float scale = u.off > 0 ? fmaxf(need, old) : need;
     const float inv = 1.f / scale;
-    for (int r0 = part * kRows; r0 < count; r0 += kRows * WPU) {
+    for (int r0 = part * kRows; r0 < u.count; r0 += kRows * WPU) {
       if (!once) load(r0);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int v = i * 32 + lane, r = r0 + v / kVecs;
-        if (r < count) store_codes(codes + (off + r) * D + (v % kVecs) * Vec<T>::kN, x[i], inv, T());
+        const int v = i * 32 + lane, r = r0 + row_of(i);
+        if (r < u.count) store_codes(u.codes + (u.off + r) * D + (v % kVecs) * Vec<T>::kN, x[i], inv, T());
       }
     }
-    if (off > 0 && scale > old) {
+    if (u.off > 0 && scale > old) {
       const float f = old * inv;
-      uint4* again = reinterpret_cast<uint4*>(codes);
-      for (int v = part * 32 + lane; v < off * (D / 16); v += 32 * WPU) {
+      uint4* again = reinterpret_cast<uint4*>(u.codes);
+      for (int v = part * 32 + lane; v < u.off * (D / 16); v += 32 * WPU) {
         const uint4 c = again[v];
         again[v] = make_uint4(rescaled(c.x, f), rescaled(c.y, f), rescaled(c.z, f), rescaled(c.w, f));
       }
     }
-    if (speaker) *scale_at = scale;
+    if (speaker) *u.scale_at = scale;
   }
 }
 
 template <typename T, int D, int WPU>
 int launch_one(ScaledAppendParams p, int num_sms, cudaStream_t stream) {
-  constexpr int kThreads = WPU == 1 ? kAppendWarps * 32 : WPU * 32, kUnits = WPU == 1 ? kAppendWarps : 1;
+  constexpr int kThreads = append_threads(WPU), kUnits = WPU == 1 ? kAppendWarps : 1;
   constexpr int kStarts = kStartsPerThread * kThreads;
   // packed: how many blocks the chunks touch is on the device; as many CTAs as that can be, or as run at once
   const int64_t slots = p.query_start_loc == nullptr ? p.num_seqs : (int64_t(p.num_tokens) >> p.log2_bs) + 2 * int64_t(p.num_seqs);
-  const int64_t units = slots * 2 * p.num_kv_heads, resident = int64_t(num_sms) * (2048 / kThreads);
+  const int64_t units = slots * 2 * p.num_kv_heads, resident = int64_t(num_sms) * (append_warps_per_sm(WPU) * 32 / kThreads);
   p.check_ctas = p.query_start_loc != nullptr ? static_cast<unsigned>((int64_t(p.num_seqs) + kStarts - 1) / kStarts) : 0u;
   int64_t ctas = (units + kUnits - 1) / kUnits;
   if (ctas > resident) ctas = resident;

@@ -29,19 +29,22 @@ namespace {
 
 constexpr int kSlotThreads = 1024;
 constexpr int kSlotWarps = kSlotThreads / 32;
+constexpr int kSlotCtas = 16;
+constexpr int kRowsTogether = 2;
 
 __device__ __forceinline__ long long up(long long x, int d) { return __shfl_up_sync(kFullMask, x, d); }
 
 // Exclusive sums over the block's threads; *total: of all of them.  `room` is
-// shared memory for one element a warp and one more.
+// shared memory for one element a warp and one more; a warp that is not `used`
+// has zeros only.
 template <int N>
-__device__ __forceinline__ void block_scan(long long (&x)[N], long long (&total)[N], long long* room) {
+__device__ __forceinline__ void block_scan(long long (&x)[N], long long (&total)[N], long long* room, bool used) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long in[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) in[i] = x[i];
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1)
+  for (int d = 1; d < 32 && used; d <<= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const long long y = up(x[i], d);
@@ -93,6 +96,20 @@ __device__ __forceinline__ Ask ask_of(const SlotsParams& p, int b) {
   return a;
 }
 
+// A warp copies n entries, the loads of several rounds together.
+__device__ __forceinline__ void copy_entries(int32_t* to, const int32_t* from, int from_step, int n, int lane) {
+  constexpr int kRounds = 4;
+  for (int k0 = lane; k0 < n; k0 += 32 * kRounds) {
+    int32_t v[kRounds];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+      if (k0 + 32 * i < n) v[i] = from[(k0 + 32 * i) * from_step];
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+      if (k0 + 32 * i < n) to[k0 + 32 * i] = v[i];
+  }
+}
+
 __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotsParams p) {
   extern __shared__ __align__(16) int32_t table_of_seqs[];  // [B+1] starts, [B] lengths, [B] places of the stack
   __shared__ long long room[3 * (kSlotWarps + 1)];
@@ -120,7 +137,8 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotsP
     sum[1] += a.want;
     sum[2] += a.need;
   }
-  block_scan<3>(sum, total, room);
+  const bool used = (tid & ~31) * per < p.num_seqs;
+  block_scan<3>(sum, total, room, used);
   const int had = min(max(stored, 0), p.free_room);
   const int count = static_cast<int>(min(static_cast<long long>(had) + total[0], static_cast<long long>(p.free_room)));
   if (rank == 0 && (bad || (tid == 0 && (stored != had || had + total[0] > p.free_room)))) atomicOr(p.err, kErrLen);
@@ -138,7 +156,7 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotsP
     got[0] += served ? a.want : 0;
     got[1] += served ? a.need : 0;
   }
-  block_scan<2>(got, all, room);
+  block_scan<2>(got, all, room, used);
   {
     long long w = sum[1], r = sum[2];
     int at = static_cast<int>(got[0]);
@@ -154,7 +172,7 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotsP
   __syncthreads();
 
   // blocks of ended sequences go on the stack; a warp a sequence
-  const int warps = ctas * kSlotWarps, warp = rank * kSlotWarps + (tid >> 5);
+  const int warps = ctas * kSlotWarps, warp = (tid >> 5) * ctas + rank;
   const int round = (1 << p.log2_bs) - 1;
   if (total[0] > 0) {
     for (int b = warp; b < p.num_seqs; b += warps) {
@@ -162,13 +180,14 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotsP
       if (tops[b] >= 0 || len < 0 || len > p.max_tokens || p.new_tokens[b] >= 0) continue;
       const int32_t* row = p.block_tables + b * p.bt_stride;
       const int held = static_cast<int>((static_cast<long long>(len) + round) >> p.log2_bs), to = -1 - tops[b];
-      for (int k = lane; k < held && to + k < p.free_room; k += 32) p.free_blocks[to + k] = row[k];
+      copy_entries(p.free_blocks + to, row, 1, min(held, p.free_room - to), lane);
     }
   }
   // everything that is written in place below has been read by every CTA, and the stack is written
   cluster.sync();
 
   const int rows = starts[p.num_seqs];
+  const int top_step = p.num_seqs > 1 ? 1 << (31 - __clz(p.num_seqs - 1)) : 0;
   for (int b = rank * kSlotThreads + tid; b < p.num_seqs; b += ctas * kSlotThreads) {
     const int n = starts[b + 1] - starts[b], len = lens[b];
     p.starts[b] = starts[b];
@@ -185,27 +204,39 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotsP
     const int held = static_cast<int>((static_cast<long long>(len) + round) >> p.log2_bs);
     const int end = static_cast<int>((static_cast<long long>(len) + n + round) >> p.log2_bs), top = tops[b];
     int32_t* row = p.block_tables + b * p.bt_stride;
-    for (int j = held + lane; j < end; j += 32) row[j] = p.free_blocks[top - (j - held)];
+    copy_entries(row + held, p.free_blocks + top, -1, end - held, lane);
   }
-  // rows
-  for (int t = rank * kSlotThreads + tid; t < p.num_rows; t += ctas * kSlotThreads) {
-    long long slot = -1, pos = 0;
-    if (t < rows) {
-      int lo = 0, hi = p.num_seqs - 1;  // the last sequence that begins at or before t
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (starts[mid] <= t) lo = mid; else hi = mid - 1;
+  // rows: kRowsTogether a lane, so that their searches and look-ups overlap
+  const unsigned num_rows = static_cast<unsigned>(p.num_rows);
+  for (unsigned t0 = warp * 32 * kRowsTogether + lane; t0 < num_rows; t0 += warps * 32 * kRowsTogether) {
+    int b[kRowsTogether], at[kRowsTogether], block[kRowsTogether];
+#pragma unroll
+    for (int k = 0; k < kRowsTogether; ++k) b[k] = 0;
+    for (int step = top_step; step > 0; step >>= 1)  // the last sequence that begins at or before the row
+#pragma unroll
+      for (int k = 0; k < kRowsTogether; ++k)
+        if (b[k] + step < p.num_seqs && static_cast<unsigned>(starts[b[k] + step]) <= t0 + 32 * k) b[k] += step;
+#pragma unroll
+    for (int k = 0; k < kRowsTogether; ++k) {
+      const unsigned t = t0 + 32 * k;
+      at[k] = block[k] = 0;
+      if (t < static_cast<unsigned>(rows)) {
+        const int len = lens[b[k]];
+        at[k] = len + static_cast<int>(t) - starts[b[k]];
+        const int held = static_cast<int>((static_cast<long long>(len) + round) >> p.log2_bs), j = at[k] >> p.log2_bs;
+        const int32_t* from = j < held ? p.block_tables + b[k] * p.bt_stride + j : p.free_blocks + (tops[b[k]] - (j - held));
+        block[k] = *from;
       }
-      const int len = lens[lo];
-      const int at = len + (t - starts[lo]);
-      const int held = static_cast<int>((static_cast<long long>(len) + round) >> p.log2_bs), j = at >> p.log2_bs;
-      const int block = j < held ? p.block_tables[lo * p.bt_stride + j] : p.free_blocks[tops[lo] - (j - held)];
-      pos = at;
-      if (block >= 0) slot = (static_cast<long long>(block) << p.log2_bs) + (at & round);
-      else atomicOr(p.err, kErrBlock);
     }
-    p.slots[t] = slot;
-    if (p.positions != nullptr) p.positions[t] = pos;
+#pragma unroll
+    for (int k = 0; k < kRowsTogether; ++k) {
+      const unsigned t = t0 + 32 * k;
+      if (t >= num_rows) break;
+      const bool good = t < static_cast<unsigned>(rows) && block[k] >= 0;
+      if (t < static_cast<unsigned>(rows) && !good) atomicOr(p.err, kErrBlock);
+      p.slots[t] = good ? (static_cast<long long>(block[k]) << p.log2_bs) + (at[k] & round) : -1;
+      if (p.positions != nullptr) p.positions[t] = at[k];
+    }
   }
 }
 
@@ -213,11 +244,18 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotsP
 
 int launch_assign_slots(const SlotsParams& p, cudaStream_t stream) {
   static std::atomic<int> configured[64];
+  static std::atomic<bool> wide[64];  // clusters of more than 8 CTAs are allowed, per device
+  int dev = 0;
+  cudaError_t c = cudaGetDevice(&dev);
+  if (c == cudaSuccess && !(dev < 64 && wide[dev].load(std::memory_order_acquire))) {
+    c = cudaFuncSetAttribute(reinterpret_cast<const void*>(&assign_slots_kernel), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (c == cudaSuccess && dev < 64) wide[dev].store(true, std::memory_order_release);
+  }
+  if (c != cudaSuccess) return c;
   const int smem = (3 * p.num_seqs + 1) * static_cast<int>(sizeof(int32_t));
   const int e0 = raise_smem_limit(configured, reinterpret_cast<const void*>(&assign_slots_kernel), smem);
   if (e0 != cudaSuccess) return e0;
-  const int ctas = p.num_rows > 2 * kSlotThreads || p.num_seqs > kSlotThreads ? 8 : 1;
-  const int e = launch_dependent(&assign_slots_kernel, dim3(ctas), dim3(kSlotThreads), smem, ctas, stream, p);
+  const int e = launch_dependent(&assign_slots_kernel, dim3(kSlotCtas), dim3(kSlotThreads), smem, kSlotCtas, stream, p);
   if (e == cudaSuccess) note_launch();
   return e;
 }
