@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(append_threads(WPU), append_warps_per_sm(WPU) 
   constexpr int kLoads = kWarpElements / Vec<T>::kN / 32;        // a lane's
   constexpr int kRows = kWarpElements / D;                       // rows that a warp holds
   constexpr int kUnitsPerCta = WPU == 1 ? kAppendWarps : 1;
-  __shared__ float met[2][8];
+  __shared__ float met[2][4];
   grid_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -316,11 +316,10 @@ int launch_one(ScaledAppendParams p, int num_sms, cudaStream_t stream) {
 
 template <typename T, int D>
 int launch_dim(const ScaledAppendParams& p, int num_sms, cudaStream_t stream) {
-  const int warps = p.query_start_loc == nullptr ? 1 : (D << p.log2_bs) / kWarpElements;  // that hold a block
+  const int warps = p.query_start_loc == nullptr ? 1 : (D << p.log2_bs) / (2 * kWarpElements);
   if (warps <= 1) return launch_one<T, D, 1>(p, num_sms, stream);
   if (warps == 2) return launch_one<T, D, 2>(p, num_sms, stream);
-  if (warps == 4) return launch_one<T, D, 4>(p, num_sms, stream);
-  return launch_one<T, D, 8>(p, num_sms, stream);
+  return launch_one<T, D, 4>(p, num_sms, stream);
 }
 
 template <typename T>
