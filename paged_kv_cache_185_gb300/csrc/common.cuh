@@ -74,6 +74,22 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Whether two phases are both complete, asked one behind the other without waiting
+// for the first answer.
+__device__ __forceinline__ bool mbar_try_both(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar_a), "r"(parity_a), "r"(bar_b), "r"(parity_b)
+      : "memory");
+  return ok != 0;
+}
+
 // Programmatic dependent launch: wait until the kernels before this one in the
 // stream are complete and their writes visible; allow the next kernel's CTAs to
 // be launched (they wait in turn).  Such a kernel is alive while the one before it

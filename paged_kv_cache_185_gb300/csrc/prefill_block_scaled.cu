@@ -322,6 +322,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) got = mbar_wait_bounded(smem_u32(bar), static_cast<uint32_t>(parity), p.wait_limit_ns);
     return __shfl_sync(kFullMask, got ? 1 : 0, 0) != 0;
   };
+  // two waits, asked together by every lane: mostly both are over already, and asking takes longer than waiting
+  auto wait_both = [&](uint64_t* a, int parity_a, uint64_t* b, int parity_b) -> bool {
+    if (__all_sync(kFullMask, mbar_try_both(smem_u32(a), static_cast<uint32_t>(parity_a), smem_u32(b), static_cast<uint32_t>(parity_b))))
+      return true;
+    const bool got_a = wait_warp(a, parity_a), got_b = wait_warp(b, parity_b);
+    return got_a && got_b;
+  };
   bool ok = true;
 
   if (warp >= kProducer && work) {
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rs = i % S::kRaws;
       int s;
       const bool is_v = items.is_v(i, &s);
-      if (!wait_warp(sh.raw_full + rs, (i / S::kRaws) & 1) || !wait_warp(sh.empty + at, turn)) {
+      if (!wait_both(sh.raw_full + rs, (i / S::kRaws) & 1, sh.empty + at, turn)) {
         ok = false;
         break;
       }
@@ -458,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto scores = [&](int i, int h) {
       const Slot s = slot_of(order.k(step_of(i)));
-      wait(sh.full + s.at, s.turn);
-      if (i >= 2) wait(sh.added + x, h);  // the weights whose place it takes have been read
+      // (behind step 1: the weights whose place it takes have been read)
+      ok = i < 2 ? wait_warp(sh.full + s.at, s.turn) : wait_both(sh.full + s.at, s.turn, sh.added + x, h);
       if (!ok) return;
       tc::fence_after_sync();
       const uint64_t kd = tc::sw128_desc(ring_a + s.at * S::kSlotBytes, 16, 1024);
@@ -478,8 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto values = [&](int i, int h) {
       const Slot s = slot_of(order.v(step_of(i)));
-      wait(sh.full + s.at, s.turn);
-      wait(&sh.weighed[x][h], (i >> 1) & 1);
+      ok = wait_both(sh.full + s.at, s.turn, &sh.weighed[x][h], (i >> 1) & 1);
       if (!ok) return;
       tc::fence_after_sync();
       const uint64_t vd = tc::sw128_desc(ring_a + s.at * S::kSlotBytes, S::kChunkStride, 1024);
@@ -611,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < n; ++i) {
       const int h = i & 1, s = same_rows ? 2 * i + x : i;  // step, counted from step0
       const float4* of = sh.factors[s % kFactorSteps];
-      if (!wait_warp(sh.factors_full + s % kFactorSteps, (s / kFactorSteps) & 1) || !wait_warp(&sh.scored[x][h], (i >> 1) & 1)) {
+      if (!wait_both(sh.factors_full + s % kFactorSteps, (s / kFactorSteps) & 1, &sh.scored[x][h], (i >> 1) & 1)) {
         ok = false;
         break;
       }
