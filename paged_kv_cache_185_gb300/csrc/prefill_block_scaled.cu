@@ -395,9 +395,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int token = (step0 + s) * kStep + r;
       const bool zero = is_v && token >= kv_end;  // V rows past the context may hold anything
       uint32_t nan_bits = 0u;                     // 0x80 in a byte: a NaN code, 0x7f or 0xff, was there
+      uint4 codes[kRawChunks];  // read before anything is stored, which would have to be waited for one by one
+#pragma unroll
+      for (int ch = 0; ch < kRawChunks; ++ch) codes[ch] = *reinterpret_cast<const uint4*>(src + code_offset<D>(r & 15, ch));
 #pragma unroll
       for (int ch = 0; ch < kRawChunks; ++ch) {
-        uint4 x = *reinterpret_cast<const uint4*>(src + code_offset<D>(r & 15, ch));
+        uint4 x = codes[ch];
         if (zero) x = make_uint4(0u, 0u, 0u, 0u);
         nan_bits |= ((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u) |
                     ((x.z & 0x7f7f7f7fu) + 0x01010101u) | ((x.w & 0x7f7f7f7fu) + 0x01010101u);
