@@ -398,6 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint4 codes[kRawChunks];  // read before anything is stored, which would have to be waited for one by one
 #pragma unroll
       for (int ch = 0; ch < kRawChunks; ++ch) codes[ch] = *reinterpret_cast<const uint4*>(src + code_offset<D>(r & 15, ch));
+      const bool factors = !is_v && !(warp & 1);
+      if (factors && lane < kOctets) {
+        const float ks = scale_in_range(sh.scales[rs][lane]), vs = scale_in_range(sh.scales[rs][kOctets + lane]);
+        sh.factors[s % kFactorSteps][lane] = make_float4(ks, lg2(vs) + kWeightShift, __frcp_rn(vs), 0.f);
+      }
 #pragma unroll
       for (int ch = 0; ch < kRawChunks; ++ch) {
         uint4 x = codes[ch];
@@ -426,17 +431,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(sh.full + at));
-      if (!is_v && !(warp & 1)) {
-        if (lane < kOctets) {
-          const float ks = scale_in_range(sh.scales[rs][lane]), vs = scale_in_range(sh.scales[rs][kOctets + lane]);
-          sh.factors[s % kFactorSteps][lane] = make_float4(ks, lg2(vs) + kWeightShift, __frcp_rn(vs), 0.f);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(sh.factors_full + s % kFactorSteps));
+      if (lane == 0) {
+        mbar_arrive(smem_u32(sh.full + at));
+        if (factors) mbar_arrive(smem_u32(sh.factors_full + s % kFactorSteps));
+        mbar_arrive(smem_u32(sh.raw_empty + rs));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(sh.raw_empty + rs));
       at += kWideners / 2;
       if (at >= slots) at -= slots, turn ^= 1;
     }
