@@ -393,11 +393,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint8_t* src = sh.raw[rs] + (r >> 4) * S::G::kTileBytes;
       uint8_t* dst = ring + at * S::kSlotBytes + r * 128;
       const int token = (step0 + s) * kStep + r;
-      const bool zero = is_v && token >= kv_end;  // V rows past the context may hold anything
       uint32_t nan_bits = 0u;                     // 0x80 in a byte: a NaN code, 0x7f or 0xff, was there
       uint4 codes[kRawChunks];  // read before anything is stored, which would have to be waited for one by one
 #pragma unroll
       for (int ch = 0; ch < kRawChunks; ++ch) codes[ch] = *reinterpret_cast<const uint4*>(src + code_offset<D>(r & 15, ch));
+      if (is_v && token >= kv_end) {  // V rows past the context may hold anything
+#pragma unroll
+        for (int ch = 0; ch < kRawChunks; ++ch) codes[ch] = make_uint4(0u, 0u, 0u, 0u);
+      }
       const bool factors = !is_v && !(warp & 1);
       if (factors && lane < kOctets) {
         const float ks = scale_in_range(sh.scales[rs][lane]), vs = scale_in_range(sh.scales[rs][kOctets + lane]);
@@ -406,7 +409,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int ch = 0; ch < kRawChunks; ++ch) {
         uint4 x = codes[ch];
-        if (zero) x = make_uint4(0u, 0u, 0u, 0u);
         nan_bits |= ((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u) |
                     ((x.z & 0x7f7f7f7fu) + 0x01010101u) | ((x.w & 0x7f7f7f7fu) + 0x01010101u);
         uint4 lo, hi;
@@ -528,9 +530,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = quarter * 32 + lane;       // this thread's row of the Q tile
     const int rowg = rows.row0 + (same_rows ? 0 : x * kTileRows) + r;
     const bool valid = rowg < rows.n_rows;
-    const int tok = valid ? rowg / G : 0;
-    const int gh = valid ? rowg - tok * G : 0;
-    const int pos = valid ? rows.pos0 + tok : 0;  // padding rows see token 0 only (output dropped)
+    const int tok = min(rowg, rows.n_rows - 1) / G;  // (a row behind the last sees what the last does; its output is dropped)
+    const int gh = rowg - tok * G;
+    const int pos = rows.pos0 + tok;
     const uint32_t trow = tmem + x * S::kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
     // The warp's 32 rows are read and written together, kLanes lanes a row, so that a load or store touches few lines.
     constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;
@@ -615,6 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.scale_log2 == 0.f ? 1.f : __uint_as_float((254u - sh.row_field[same_rows ? 0 : x][r]) << 23) * fabsf(p.scale_log2);
     float m = kNone, l = 0.f;
     const int n = steps[x];
+    // rows behind the last get no weights: what the products make of the places they leave stays in such rows
+    const bool idle = first_row >= rows.n_rows;
     constexpr int kRuns = kStep / RUN;
     for (int i = 0; i < n; ++i) {
       const int h = i & 1, s = same_rows ? 2 * i + x : i;  // step, counted from step0
@@ -622,6 +626,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_both(sh.factors_full + s % kFactorSteps, (s / kFactorSteps) & 1, &sh.scored[x][h], (i >> 1) & 1)) {
         ok = false;
         break;
+      }
+      if (idle) {
+        if (lane == 0) mbar_arrive(smem_u32(&sh.weighed[x][h]));
+        continue;
       }
       tc::fence_after_sync();
       float v[2][32];
@@ -718,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = top;
       }
     }
-    if (ok && (x == 0 || !same_rows)) {
+    if (ok && !idle && (x == 0 || !same_rows)) {
       const float inv = sp.splits > 1 ? 1.f : 1.f / l;
       const bool any_nan = sh.any_nan != 0;
       // where this lane's pieces go, of rows lane / 8 + 4 i
