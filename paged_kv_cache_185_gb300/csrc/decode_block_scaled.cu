@@ -51,7 +51,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kWeightShift = 14.f;
 constexpr int kMostCtas = 4;      // of an SM
-constexpr int kLeastUnits = 4;    // of a warp, before another CTA takes part
+constexpr int kLeastUnits = 4;    // of a warp, before another CTA takes part (where rows have as many)
 
 template <int D, int NT>
 struct Shape {
@@ -440,8 +440,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (w < warp) upto += sh.sums[w];
     total += sh.sums[w];
   }
+  // a run has the units of a mean row at least, up to kLeastUnits a warp: a long row in fewer pieces has fewer results to
+  // merge, but a CTA with many short rows has an end for each
+  const long long least = max(1ll, min(static_cast<long long>(kWarps * kLeastUnits), quotient(total, p.num_seqs)));
   total *= rows;
-  const long long ctas = max(1ll, min(static_cast<long long>(gridDim.x), total / (kWarps * kLeastUnits)));
+  const long long ctas = max(1ll, min(static_cast<long long>(gridDim.x), quotient(total, least)));
   const long long c_id = blockIdx.x;
   const long long u0 = c_id < ctas ? quotient(total * c_id, ctas) : total, u1 = c_id < ctas ? quotient(total * (c_id + 1), ctas) : total;
   if (u0 < u1 && (upto - mine) * rows <= u0 && u0 < upto * rows) {
