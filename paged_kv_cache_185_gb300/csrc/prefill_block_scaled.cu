@@ -45,14 +45,14 @@
 // kernel, a programmatic dependent, merges them in their order.
 //
 // Bound: 8 chunks of 1024 tokens behind up to 5000 earlier ones, 28/4 heads of 128,
-// block_size 16 (337 GFLOP): 328 us, 1029 TFLOP/s, 0.53 of the measured cuBLAS rate.
+// block_size 16 (337 GFLOP): 327 us, 1032 TFLOP/s, 0.54 of the measured cuBLAS rate.
 // A step of 64 tokens takes 0.95 us and moves 192 KB through shared memory (the Q tile
 // for the scores, codes in and out, both products' operands), which alone takes 0.8;
 // the tensor pipe is busy 42 % of the time and 61 % of the issue slots are used.
-// Chunks of 5 tokens of 64 sequences (300 to 6000 tokens, same heads; 211 MB): 83 us,
-// 0.38 of the copy rate: 35 of 128 rows are used, and each step waits for its codes
-// to be widened.  One chunk of 100 tokens, 32/8 heads, 2100 tokens: 28 us, latency
-// (look-ups, 4 us of query rows, 6 or 7 steps, 3 us of outputs, the second kernel).
+// Chunks of 5 tokens of 64 sequences (300 to 6000 tokens, same heads; 211 MB): 77 us,
+// 0.41 of the copy rate: 35 of 128 rows are used, and each step waits for its codes
+// to be widened.  One chunk of 100 tokens, 32/8 heads, 2100 tokens: 27 us, latency
+// (look-ups, 3 us of query rows, 6 or 7 steps, 3 us of outputs, the second kernel).
 //
 // Every wait is bounded; on a timeout the CTA records the error, waits (bounded)
 // for its MMAs in flight, frees its tensor memory and returns.
@@ -546,8 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int gh = rowg - tok * G;
     const int pos = rows.pos0 + tok;
     const uint32_t trow = tmem + x * S::kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
-    // The warp's 32 rows are read and written together, kLanes lanes a row, so that a load or store touches few lines.
-    constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;
+    // The warp's 32 rows are read together, kLanes lanes a row (each two pieces of 16 bytes), so that a load touches few lines.
+    constexpr int kLanes = D / 16, kRowsAtOnce = 32 / kLanes;
     const int first_row = rows.row0 + (same_rows ? 0 : x * kTileRows) + quarter * 32, sub = lane / kLanes, piece = lane % kLanes;
     {
       // The rows go to shared memory as they are and every lane rewrites its own pieces: rolled loops, because
@@ -555,10 +555,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // between them.
       uint8_t* const qx = sh.q[same_rows ? 0 : x];
       const int rows_here = same_rows ? 16 : 32, in_tile = quarter * 32 + (same_rows ? 16 * x + sub : sub);
-      const auto place = [&](int rr) {
-        return reinterpret_cast<uint4*>(qx + (piece >> 3) * (kTileRows * 128) + rr * 128 + (((piece & 7) ^ (rr & 7)) << 4));
+      const auto place = [&](int rr, int k) {
+        const int c = piece + k * kLanes;
+        return reinterpret_cast<uint4*>(qx + (c >> 3) * (kTileRows * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
       };
       const int first = rows.row0 + (same_rows ? 0 : x * kTileRows) + in_tile;
+      const float sign = p.scale_log2 < 0.f ? -1.f : p.scale_log2 == 0.f ? 0.f : 1.f;
       {
         const int token = first / G;
         int head = first - token * G;
@@ -568,31 +570,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int heads_on = kRowsAtOnce % G;
         const int64_t on = kRowsAtOnce / G * p.q_st + heads_on * p.q_sh, over = p.q_st - G * p.q_sh;
         if (sp.q_vec) {
-#pragma unroll 4
+#pragma unroll 2
           for (int j = 0; j < rows_here; j += kRowsAtOnce) {  // (zeros behind the last row)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(in_tile + j))), "l"(from),
-                         "r"(first + j < rows.n_rows ? 16 : 0) : "memory");
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(in_tile + j, k))),
+                           "l"(from + k * 8 * kLanes), "r"(first + j < rows.n_rows ? 16 : 0) : "memory");
             head += heads_on, from += on;
             if (head >= G) head -= G, from += over;
           }
         } else {
           for (int j = 0; j < rows_here; j += kRowsAtOnce) {
-            *place(in_tile + j) = first + j < rows.n_rows ? load8(from, false) : make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < 2; ++k)
+              *place(in_tile + j, k) = first + j < rows.n_rows ? load8(from + k * 8 * kLanes, false) : make_uint4(0u, 0u, 0u, 0u);
             head += heads_on, from += on;
             if (head >= G) head -= G, from += over;
           }
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-      constexpr int kTogether = 4;  // pieces whose steps overlap
+      constexpr int kTogether = 2;  // rows of a lane whose steps overlap
 #pragma unroll 1
       for (int j = 0; j < rows_here; j += kTogether * kRowsAtOnce) {
-        uint4 v[kTogether];
+        uint4 v[kTogether][2];
         uint32_t most[kTogether];
 #pragma unroll
         for (int u = 0; u < kTogether; ++u) {
-          v[u] = *place(in_tile + j + u * kRowsAtOnce);
-          most[u] = __vmaxu2(__vmaxu2(v[u].x & 0x7fff7fffu, v[u].y & 0x7fff7fffu), __vmaxu2(v[u].z & 0x7fff7fffu, v[u].w & 0x7fff7fffu));
+          most[u] = 0u;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint4 c = v[u][k] = *place(in_tile + j + u * kRowsAtOnce, k);
+            most[u] = __vmaxu2(most[u], __vmaxu2(__vmaxu2(c.x & 0x7fff7fffu, c.y & 0x7fff7fffu), __vmaxu2(c.z & 0x7fff7fffu, c.w & 0x7fff7fffu)));
+          }
         }
 #pragma unroll
         for (int d = 1; d < kLanes; d <<= 1)
@@ -605,18 +614,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint16_t top_bits = static_cast<uint16_t>(max(most[u] & 0xffffu, most[u] >> 16));
           const float top = to_f32(*reinterpret_cast<const T*>(&top_bits));
           const int field = min(max(127 + 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
-          float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-          up = p.scale_log2 < 0.f ? -up : p.scale_log2 == 0.f ? 0.f : up;
+          const float up = __uint_as_float(static_cast<uint32_t>(field) << 23) * sign;
           const int rr = in_tile + j + u * kRowsAtOnce;
           if (piece == 0) sh.row_field[same_rows ? 0 : x][rr] = static_cast<uint8_t>(field);
-          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-          uint32_t f[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const T* q2 = reinterpret_cast<const T*>(&w[e]);
-            f[e] = h2(to_f32(q2[0]) * up, to_f32(q2[1]) * up);
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w[4] = {v[u][k].x, v[u][k].y, v[u][k].z, v[u][k].w};
+            uint32_t f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const T* q2 = reinterpret_cast<const T*>(&w[e]);
+              f[e] = h2(to_f32(q2[0]) * up, to_f32(q2[1]) * up);
+            }
+            *place(rr, k) = make_uint4(f[0], f[1], f[2], f[3]);
           }
-          *place(rr) = make_uint4(f[0], f[1], f[2], f[3]);
         }
       }
       tc::fence_async_smem();
@@ -917,7 +928,7 @@ int launch_prefill_block_scaled(int dtype, int head_dim, const CUtensorMap& kmap
   const int64_t blocks = (num_tokens * p.base.group + kRows - 1) / kRows + num_seqs;
   if (blocks <= 0) return cudaSuccess;
   // as many CTAs for a row block's context as the SMs allow, each with a step for both streams at least (one chunk of 100
-  // tokens, 32/8 heads, 2100 tokens: 6 CTAs a block 27.7 us with the merge, one 44.0)
+  // tokens, 32/8 heads, 2100 tokens: 6 CTAs a block 27.2 us with the merge, one 44.0)
   const int64_t tiles = (int64_t(p.base.max_blocks) * p.base.block_size + 2 * kStep - 1) / (2 * kStep);
   int64_t splits = num_sms / (blocks * p.base.num_kv_heads);
   if (splits > kMostSplits) splits = kMostSplits;
