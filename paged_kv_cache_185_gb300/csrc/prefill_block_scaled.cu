@@ -45,13 +45,13 @@
 // kernel, a programmatic dependent, merges them in their order.
 //
 // Bound: 8 chunks of 1024 tokens behind up to 5000 earlier ones, 28/4 heads of 128,
-// block_size 16 (337 GFLOP): 327 us, 1032 TFLOP/s, 0.54 of the measured cuBLAS rate.
+// block_size 16 (337 GFLOP): 328 us, 1029 TFLOP/s, 0.53 of the measured cuBLAS rate.
 // A step of 64 tokens takes 0.95 us and moves 192 KB through shared memory (the Q tile
 // for the scores, codes in and out, both products' operands), which alone takes 0.8;
 // the tensor pipe is busy 42 % of the time and 61 % of the issue slots are used.
 // Chunks of 5 tokens of 64 sequences (300 to 6000 tokens, same heads; 211 MB): 77 us,
 // 0.41 of the copy rate: 35 of 128 rows are used, and each step waits for its codes
-// to be widened.  One chunk of 100 tokens, 32/8 heads, 2100 tokens: 27 us, latency
+// to be widened.  One chunk of 100 tokens, 32/8 heads, 2100 tokens: 26 us, latency
 // (look-ups, 3 us of query rows, 6 or 7 steps, 3 us of outputs, the second kernel).
 //
 // Every wait is bounded; on a timeout the CTA records the error, waits (bounded)
@@ -159,6 +159,7 @@ struct Shared {
   uint32_t tmem;
   int any_nan;
   Rows rows;
+  int step0, n_steps;                      // this CTA's range of the context
 };
 static_assert(sizeof(Shared<128>) <= 232448, "227 KB");
 // one CTA an SM: a second one would contend for tensor memory
@@ -226,6 +227,9 @@ struct RowAt {
     while (head >= group) head -= group, ++token;
   }
 };
+
+// How many of the CTAs launched for a row block share its context: each has a step for both streams at least.
+__device__ __forceinline__ int parts_of(int splits, int steps) { return min(splits, max(1, (steps + 1) / 2)); }
 
 // Eight elements of a row, 16-bit.
 template <typename T>
@@ -296,7 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_wait();
     int seq, block;
     row_block_of(p, kRows, tgt_block, lane, &seq, &block);
-    if (lane == 0) sh.rows = rows_of(p, seq, block, true), sh.any_nan = 0;
+    if (lane == 0) {
+      Rows r = rows_of(p, seq, block, true);
+      const int steps = (max(r.end[0], r.end[1]) + kStep - 1) / kStep, parts = parts_of(sp.splits, steps);
+      if (part >= parts) r.end[0] = r.end[1] = 0;  // nothing for this CTA
+      sh.step0 = part < parts ? steps * part / parts : 0;
+      sh.n_steps = part < parts ? steps * (part + 1) / parts - sh.step0 : 0;
+      sh.rows = r, sh.any_nan = 0;
+    }
   } else {
     grid_wait();
   }
@@ -316,8 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Rows rows = sh.rows;
   const int b = rows.b, kv_end = max(rows.end[0], rows.end[1]);
   // this CTA's steps, step0 on, and each stream's (of all of them, or every other one)
-  const int all_steps = (kv_end + kStep - 1) / kStep;
-  const int step0 = all_steps * part / sp.splits, n_steps = all_steps * (part + 1) / sp.splits - step0;
+  const int step0 = sh.step0, n_steps = sh.n_steps;
   const bool same_rows = rows.end[1] == 0;
   int steps[kStreams];
 #pragma unroll
@@ -853,13 +863,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_prefill_kernel(const S
   }
   __syncthreads();
   const Rows rows = rows_of(p, found[0], found[1], false);
+  const int parts = parts_of(sp.splits, (max(rows.end[0], rows.end[1]) + kStep - 1) / kStep);
   const int end = min(rows.row0 + kRows, rows.n_rows);
   for (int i = rows.row0 + part * (kRows / kParts) + warp; i < min(end, rows.row0 + (part + 1) * (kRows / kParts)); i += kMergeWarps) {
     const int tok = i / p.group, head = kvh * p.group + (i - tok * p.group);
     const float* from = sp.parts + (static_cast<int64_t>(rows.s0 + tok) * p.num_q_heads + head) * sp.splits * (D + 4);
     // lane s has part s's maximum and sum
-    const float m = lane < sp.splits ? from[lane * (D + 4) + D] : kNone;
-    const float l = lane < sp.splits ? from[lane * (D + 4) + D + 1] : 0.f;
+    const float m = lane < parts ? from[lane * (D + 4) + D] : kNone;
+    const float l = lane < parts ? from[lane * (D + 4) + D + 1] : 0.f;
     float v[D / 32];
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) v[e] = 0.f;
@@ -870,18 +881,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_prefill_kernel(const S
     float sum = f * l;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kFullMask, sum, d);
-    for (int s0 = 0; s0 < sp.splits; s0 += 8) {
+    for (int s0 = 0; s0 < parts; s0 += 8) {
       float x[8][D / 32];
 #pragma unroll
       for (int s = 0; s < 8; ++s)
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) x[s][e] = s0 + s < sp.splits ? from[(s0 + s) * (D + 4) + lane + 32 * e] : 0.f;
+        for (int e = 0; e < D / 32; ++e) x[s][e] = s0 + s < parts ? from[(s0 + s) * (D + 4) + lane + 32 * e] : 0.f;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         const float g = __shfl_sync(kFullMask, f, (s0 + s) & 31);
 #pragma unroll
         for (int e = 0; e < D / 32; ++e)
-          if (s0 + s < sp.splits) v[e] = fmaf(g, x[s][e], v[e]);
+          if (s0 + s < parts) v[e] = fmaf(g, x[s][e], v[e]);
       }
     }
     T* out = static_cast<T*>(p.out) + static_cast<int64_t>(rows.s0 + tok) * p.o_st + head * p.o_sh;
@@ -916,7 +927,7 @@ int launch_type(int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap, 
   return cudaErrorInvalidValue;
 }
 
-constexpr int kMostSplits = 16;
+constexpr int kMostSplits = 32;  // a lane of the merge each
 
 }  // namespace
 
@@ -924,15 +935,23 @@ size_t prefill_block_scaled_workspace(int num_sms) { return size_t(num_sms) * kR
 
 int launch_prefill_block_scaled(int dtype, int head_dim, const CUtensorMap& kmap, const CUtensorMap& vmap, ScaledPrefillParams p,
                                 int64_t num_tokens, int64_t num_seqs, int num_sms, cudaStream_t stream) {
-  // an upper bound on the row blocks: sum_b ceil(n_b G / 256) <= ceil(T G / 256) + B
-  const int64_t blocks = (num_tokens * p.base.group + kRows - 1) / kRows + num_seqs;
+  // The most row blocks that there can be: k chunks that are not empty have sum_b ceil(n_b G / 256) <= k + sum_b floor((n_b G
+  // - 1) / 256) <= k + floor((T G - k) / 256), which grows with k.
+  const int64_t most = num_tokens < num_seqs ? num_tokens : num_seqs;
+  const int64_t blocks = most + (num_tokens * p.base.group - most) / kRows;
   if (blocks <= 0) return cudaSuccess;
-  // as many CTAs for a row block's context as the SMs allow, each with a step for both streams at least (one chunk of 100
-  // tokens, 32/8 heads, 2100 tokens: 6 CTAs a block 27.2 us with the merge, one 44.0)
+  // CTAs for a row block's context: as many as the SMs allow, or as three quarters of them do if that makes a CTA's run
+  // longer by 4 steps at most: the merge's CTAs then start beside them instead of behind them (they find no registers on an
+  // SM that has one).  One chunk of 100 tokens, 32/8 heads: 7 instead of 9 CTAs a block 26.2 us instead of 29.9 (2100 tokens),
+  // 9 instead of 6 79.9 instead of 96.8 (30000), one 44.0 (2100).  How long the contexts are only the device knows.
   const int64_t tiles = (int64_t(p.base.max_blocks) * p.base.block_size + 2 * kStep - 1) / (2 * kStep);
-  int64_t splits = num_sms / (blocks * p.base.num_kv_heads);
-  if (splits > kMostSplits) splits = kMostSplits;
-  if (splits > tiles) splits = tiles;
+  const auto splits_on = [&](int64_t sms) {
+    const int64_t most_splits = tiles < kMostSplits ? tiles : kMostSplits, s = sms / (blocks * p.base.num_kv_heads);
+    return s > most_splits ? most_splits : s;
+  };
+  int64_t splits = splits_on(num_sms);
+  const int64_t fewer = splits_on(num_sms * 3 / 4);
+  if (fewer > 0 && 2 * tiles * (splits - fewer) <= 4 * splits * fewer) splits = fewer;
   p.splits = splits < 1 ? 1 : static_cast<int>(splits);
   return dtype == 2 ? launch_type<__nv_bfloat16>(head_dim, kmap, vmap, p, blocks, stream)
                     : launch_type<__half>(head_dim, kmap, vmap, p, blocks, stream);

@@ -533,6 +533,14 @@ def test_prefill_rows_of_any_alignment(dtype, d):
     check_prefill(*attention_case(11, dtype, [50, 0, 333], 6, 2, d, 16, rows=rows), starts, 0.05, layout="odd")
 
 
+@pytest.mark.parametrize("lens,new", [([300], [60]), ([64], [64]), ([65], [1]), ([129], [100]), ([1000, 70, 0, 1], [40, 70, 0, 1])])
+@pytest.mark.parametrize("width", [None, 130, 1500])
+def test_prefill_contexts_shorter_than_the_tables(lens, new, width):
+    """Few row blocks, whose contexts are shared by as many CTAs as they are long, not as the tables are wide."""
+    starts, rows = chunks(lens, new)
+    check_prefill(*attention_case(70, F16, lens, 4, 1, 128, 16, rows=rows, width=width), starts, 0.08)
+
+
 def test_prefill_many_sequences():
     g = H.gen(5)
     lens = torch.randint(1, 60, (150,), generator=g).tolist()
