@@ -635,7 +635,8 @@ int wllm_reshape_and_cache_block_scaled(const wllm_tensor* key, const wllm_tenso
  * alignment, out apart from q; D 64 (block_size >= 16), 128 or 256.  Codes are widened to f16
  * exactly; query rows are taken to f16 after a power of two has been divided
  * out of each, so their size does not matter; the weights, the value's scale in
- * them, are rounded to f16 for their product; statistics and sums are fp32.
+ * them, go to their product in two words of f16 (22 bits); statistics and sums
+ * are fp32.
  *
  *   workspace        [n] WLLM_FP8_E4M3 (bytes), contiguous, 256-byte aligned, n
  *                    at least wllm_block_scaled_workspace_bytes(); what is in it
@@ -660,8 +661,8 @@ size_t wllm_block_scaled_workspace_bytes(void);
  * Chunked-prefill attention over such a cache: out, q and query_start_loc as in
  * wllm_paged_attention_prefill, the cache, its scales and the workspace as
  * above; q and out rows of any alignment.  D 64 (block_size >= 16) or 128;
- * tensor-core products (f16, rounded as in the decode above) with fp32
- * accumulation.
+ * tensor-core products (f16, query rows as in the decode above, weights rounded
+ * to one word) with fp32 accumulation.
  */
 int wllm_paged_attention_prefill_block_scaled(const wllm_tensor* out, const wllm_tensor* q,
                                               const wllm_tensor* k_cache,

@@ -15,9 +15,12 @@
 // those of the fp8 decode (mma_e4m3.cuh): codes widened to f16 in registers, which
 // is exact, S^T = K Q^T and O^T += V^T P^T by mma.sync m16n8k16 with 8 or 16 query
 // heads of a kv head as columns.  Query rows go to f16 after a power of two was
-// divided out, so bf16 rows of any size do.  Weights are rounded to f16 times 2^14
-// (normal numbers down to 2^-28 of the largest): 2^-11 relative each, which is
-// averaged over the tokens and stays below the output's own rounding.
+// divided out, so bf16 rows of any size do.  Weights, times 2^14, go to the products as
+// two words of f16 (what the first leaves off is the second): 22 bits, or 2^-39 of the
+// largest.  One word put up to 2^-12 of each weight into the output, as much as the
+// rounding of an f16 output.  The second product costs little where memory sets the
+// pace: 8 sequences of 32K to 131K 225 us with it and 228 without, 256 of 300 to 6000
+// 147.6 and 145.6, one of 16000 12.7 and 12.5.
 //
 // Work split: all units, ordered by sequence, kv head and head tile, are cut into
 // as many equal runs as CTAs fit the GPU, so that rows of any length fill it
@@ -30,13 +33,13 @@
 // outlives the call.
 //
 // Bound: memory, each code is read once.  8 sequences of 32K to 131K tokens, 32/8
-// heads of 128 (1407 MB): 224 us, 0.94 of the measured copy rate; 256 of 300 to 6000,
-// 28/4 heads (829 MB): 144 us, 0.86, the rest the setup and the ends of 4 rows a CTA;
-// one of 16000, 32/4 heads of 64 (8 MB): 12.3 us, all latency.  What it took: warps
-// that wait for nothing at a row's end 171 us instead of 235 (256 sequences), the
-// quarters merged behind the next unit 153, partial results merged by the second
-// kernel instead of the CTA that counts in last, and entries looked up 8 units at a
-// time, 144 (16000 tokens: 17.0 and 12.3).
+// heads of 128 (1407 MB): 225 us, 0.94 of the measured copy rate; 256 of 300 to 6000,
+// 28/4 heads (829 MB): 148 us, 0.84, the rest the setup and the ends of 4 rows a CTA;
+// one of 16000, 32/4 heads of 64 (8 MB): 12.7 us, all latency.  What it took (with
+// weights of one word): warps that wait for nothing at a row's end 171 us instead of
+// 235 (256 sequences), the quarters merged behind the next unit 153, partial results
+// merged by the second kernel instead of the CTA that counts in last, and entries
+// looked up 8 units at a time, 144 (16000 tokens: 17.0 and 12.3).
 #include <atomic>
 #include <climits>
 
@@ -259,7 +262,7 @@ struct Math {
       add[i] = lg2(vs);
       inv[i] = rcp(vs);
     }
-    uint32_t w[S::kSub][NT][2];
+    uint32_t w[S::kSub][NT][2], rest[S::kSub][NT][2];  // the weights' two words
     float alpha[NT][2];
     bool moved = false;
 #pragma unroll
@@ -304,8 +307,13 @@ struct Math {
           e[i] = ex2_approx(s[j][nt][i] - base[i & 1]);
           l[nt][i & 1] = fmaf(e[i], inv[2 * j + (i >> 1)], l[nt][i & 1]);
         }
-        w[j][nt][0] = movmatrix_trans(Mma<__half>::pack(e[0], e[1]));
-        w[j][nt][1] = movmatrix_trans(Mma<__half>::pack(e[2], e[3]));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t first = Mma<__half>::pack(e[2 * i], e[2 * i + 1]);
+          const float2 taken = __half22float2(*reinterpret_cast<const __half2*>(&first));
+          w[j][nt][i] = movmatrix_trans(first);
+          rest[j][nt][i] = movmatrix_trans(Mma<__half>::pack(e[2 * i] - taken.x, e[2 * i + 1] - taken.y));
+        }
       }
     }
     if (__any_sync(kFullMask, moved)) {
@@ -335,7 +343,10 @@ struct Math {
           e4m3x4_to_f16x2x2(__byte_perm(r[2 * half + 1], 0u, 0x3120), a[2], a[3]);
           if (tail) a[0] &= keep_lo, a[1] &= keep_lo, a[2] &= keep_hi, a[3] &= keep_hi;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) Mma<__half>::run(o[2 * mp + half][nt], a, w[j][nt]);
+          for (int nt = 0; nt < NT; ++nt) {
+            Mma<__half>::run(o[2 * mp + half][nt], a, w[j][nt]);
+            Mma<__half>::run(o[2 * mp + half][nt], a, rest[j][nt]);
+          }
         }
       }
     }
