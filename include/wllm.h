@@ -661,8 +661,8 @@ size_t wllm_block_scaled_workspace_bytes(void);
  * Chunked-prefill attention over such a cache: out, q and query_start_loc as in
  * wllm_paged_attention_prefill, the cache, its scales and the workspace as
  * above; q and out rows of any alignment.  D 64 (block_size >= 16) or 128;
- * tensor-core products (f16, query rows as in the decode above, weights rounded
- * to one word) with fp32 accumulation.
+ * tensor-core products (f16, query rows and weights as in the decode above) with
+ * fp32 accumulation.
  */
 int wllm_paged_attention_prefill_block_scaled(const wllm_tensor* out, const wllm_tensor* q,
                                               const wllm_tensor* k_cache,

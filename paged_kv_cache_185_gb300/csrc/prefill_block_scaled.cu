@@ -10,17 +10,22 @@
 // as in the decode (decode_block_scaled.cu): the value's scale is part of the
 // weight.  m moves only when a row's largest x exceeds it by more than 8, so O is
 // seldom rescaled and weights stay below 2^8; they are taken times 2^7 to be normal
-// numbers of f16 down to 2^-21.  l sums the weights before they are rounded: behind
-// a small vs a weight may round to nothing and still count in l.
+// numbers of f16 down to 2^-21.  They go to the products as two words of f16 (what the
+// first leaves off is the second): 22 bits, or 2^-32 of the largest.  One word put up to
+// 2^-12 of each weight into the output, as much as the rounding of an f16 output; the
+// second costs 24 us of the 409 of 8 chunks of 1024 (below) to make and 57 to multiply,
+// and 8 of the 84 of 64 drafts.  (Cut off by a mask instead of rounded 433, with the sums of
+// two at once 419 and 8 registers spilled.)  l sums the weights before they are rounded:
+// behind a small vs a weight may round to nothing and still count in l.
 //
 // One CTA (one per SM) works on up to 256 query rows of one sequence and one kv
 // head, row r being (token r / G, query head r % G of the group), over a range of
 // the context in steps of 64 tokens, as two streams: with more than 128 rows stream
 // x has Q tile x and every step, otherwise both have the same rows and every other
 // step, and their results meet at the end.  Tensor memory holds for each stream two
-// score tiles S (64 columns; the softmax writes the weights P, f16, two a column,
-// over them) and the output O: the scores of the step after next are computed while
-// a step's weights are.  Sixteen warps:
+// score tiles S (64 columns; the softmax writes both words of the weights P, f16, two a
+// column, over them) and the output O: the scores of the step after next are computed
+// while a step's weights are.  Sixteen warps:
 //
 //   warps 14 and 15 (producers, of every other item): the block table, each step's K
 //     and V codes by TMA (16-row boxes, 128-byte swizzle) into a ring of eight raw
@@ -45,13 +50,13 @@
 // kernel, a programmatic dependent, merges them in their order.
 //
 // Bound: 8 chunks of 1024 tokens behind up to 5000 earlier ones, 28/4 heads of 128,
-// block_size 16 (337 GFLOP): 328 us, 1029 TFLOP/s, 0.53 of the measured cuBLAS rate.
-// A step of 64 tokens takes 0.95 us and moves 192 KB through shared memory (the Q tile
-// for the scores, codes in and out, both products' operands), which alone takes 0.8;
-// the tensor pipe is busy 42 % of the time and 61 % of the issue slots are used.
-// Chunks of 5 tokens of 64 sequences (300 to 6000 tokens, same heads; 211 MB): 77 us,
-// 0.41 of the copy rate: 35 of 128 rows are used, and each step waits for its codes
-// to be widened.  One chunk of 100 tokens, 32/8 heads, 2100 tokens: 26 us, latency
+// block_size 16 (337 GFLOP): 409 us, 825 TFLOP/s, 0.43 of the measured cuBLAS rate.
+// A step of 64 tokens takes 1.19 us and moves 224 KB through shared memory (the Q tile
+// for the scores, codes in and out, the products' operands, V twice), which alone takes
+// 0.93.
+// Chunks of 5 tokens of 64 sequences (300 to 6000 tokens, same heads; 211 MB): 84 us,
+// 0.38 of the copy rate: 35 of 128 rows are used, and each step waits for its codes
+// to be widened.  One chunk of 100 tokens, 32/8 heads, 2100 tokens: 28 us, latency
 // (look-ups, 3 us of query rows, 6 or 7 steps, 3 us of outputs, the second kernel).
 //
 // Every wait is bounded; on a timeout the CTA records the error, waits (bounded)
@@ -216,6 +221,13 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
       "add.rn.f32x2 s, s, t;\n\tmov.b64 {%0, %1}, s;\n\t}"
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
+}
+
+// Two numbers as two words of f16 each: what rounding to the first leaves off is the second.
+__device__ __forceinline__ void two_words(float x, float y, uint32_t& first, uint32_t& rest) {
+  first = h2(x, y);
+  const float2 taken = __half22float2(*reinterpret_cast<const __half2*>(&first));
+  rest = h2(x - taken.x, y - taken.y);
 }
 
 // Token and head (of the group) of a row, and of the rows behind it: one division for all.
@@ -518,8 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t go_on = i > 0 ? 1u : 0u;
       if (tc::elect()) {
 #pragma unroll
-        for (int kk = 0; kk < kStep / 16; ++kk)  // P: 8 columns per 16 tokens
-          tc::mma_f16_ts(base + S::kO, base + h * kStep + kk * 8, vd + ((kk * 2048) >> 4), kIdO, kk > 0 ? 1u : go_on);
+        for (int kk = 0; kk < kStep / 16; ++kk) {  // P: 16 columns per 16 tokens, the second words behind the first
+          tc::mma_f16_ts(base + S::kO, base + h * kStep + kk * 16, vd + ((kk * 2048) >> 4), kIdO, kk > 0 ? 1u : go_on);
+          tc::mma_f16_ts(base + S::kO, base + h * kStep + kk * 16 + 8, vd + ((kk * 2048) >> 4), kIdO, 1u);
+        }
         tc::commit(smem_u32(sh.added + x));
         if (i + 1 == n) tc::commit(smem_u32(sh.finished + x));
         give_up(s);
@@ -693,22 +707,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = mx - kWeightShift;
       }
       l *= alpha;
-      uint32_t w[kStep / 2];
 #pragma unroll
-      for (int g = 0; g < kRuns; ++g) {
-        const float a = add[g] - m;
-        float s0 = 0.f, s1 = 0.f;
+      for (int q = 0; q < 2; ++q) {  // 32 tokens: for 16 of them 8 columns of first words, then 8 of second ones
+        uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < RUN; e += 2) {
-          float y0 = v[(RUN * g + e) >> 5][(RUN * g + e) & 31], y1 = v[(RUN * g + e) >> 5][(RUN * g + e + 1) & 31];
-          fma2(y0, y1, by[g], a);
-          y0 = ex2_approx(y0), y1 = ex2_approx(y1);
-          add2(s0, s1, y0, y1);
-          w[(RUN * g + e) / 2] = h2(y0, y1);
+        for (int g = q * kRuns / 2; g < (q + 1) * kRuns / 2; ++g) {
+          const float a = add[g] - m;
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int e = 0; e < RUN; e += 2) {
+            const int t = (RUN * g + e) & 31, at = t >> 4 << 4 | (t & 15) >> 1;
+            float y0 = v[q][t], y1 = v[q][t + 1];
+            fma2(y0, y1, by[g], a);
+            y0 = ex2_approx(y0), y1 = ex2_approx(y1);
+            add2(s0, s1, y0, y1);
+            two_words(y0, y1, w[at], w[at + 8]);
+          }
+          l = fmaf(s0 + s1, of[g * (RUN / 8)].z, l);
         }
-        l = fmaf(s0 + s1, of[g * (RUN / 8)].z, l);
+        tc::st32(trow + h * kStep + 32 * q, *reinterpret_cast<const float(*)[32]>(&w));  // over the scores
       }
-      tc::st32(trow + h * kStep, *reinterpret_cast<const float(*)[32]>(&w));  // over the scores
       if (__any_sync(kFullMask, alpha != 1.f) && i > 0) {
         // O is rescaled at rest: behind the product of the step before
         if (!wait_warp(sh.added + x, (i - 1) & 1)) {

@@ -58,3 +58,16 @@ def test_decode_keeps_its_weights(dtype, hq, hkv, d, bs):
     wllm.paged_attention_decode_block_scaled(out, *(t.cuda() for t in x), hkv, SCALE, bs)
     ref, mag, size, _ = S.attention(*x, SCALE)
     assert_kept(out.cpu(), ref, mag, size, d, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("hq,hkv,d,bs", [f for f in FORMS if f[2] < 256])
+def test_prefill_keeps_its_weights(dtype, hq, hkv, d, bs):
+    lens = [2 + i % 15 for i in range(30)]
+    new = [min(n, 1 + i % 7) for i, n in enumerate(lens)]
+    starts = i32([0] + torch.tensor(new).cumsum(0).tolist())
+    x = case(hq + d + 1, dtype, lens, int(starts[-1]), hq, hkv, d, bs)
+    out = torch.empty_like(x[0]).cuda()
+    wllm.paged_attention_prefill_block_scaled(out, *(t.cuda() for t in x), starts.cuda(), hkv, SCALE, bs)
+    ref, mag, size, _ = S.attention(*x, SCALE, starts)
+    assert_kept(out.cpu(), ref, mag, size, d, dtype)
