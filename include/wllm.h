@@ -577,8 +577,10 @@ int wllm_paged_attention_decode_sparse_fp8(const wllm_tensor* out, const wllm_te
  * Lengths outside [0, M_b bs], a sum L + n above it, a num_free outside [0, F]
  * and blocks given back beyond F set bit 2 of the error word (the sequence is
  * not served, num_free is clamped, the blocks are lost); negative entries in a
- * row of the table set bit 1 (no slot for their tokens).  B up to 16384.  No
- * tensor that is written may overlap another but for the two pairs named.
+ * row of the table set bit 1 (no slot for their tokens; they are left out when the
+ * row is given back, and nobody is served from what they would have been).  B up to
+ * 16384.  No tensor that is written may overlap another but for the two pairs
+ * named.
  */
 int wllm_assign_slots(const wllm_tensor* slot_mapping, const wllm_tensor* positions,
                       const wllm_tensor* query_start_loc, const wllm_tensor* context_lens_out,

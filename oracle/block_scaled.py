@@ -17,15 +17,17 @@ LEAST, MOST = 2.0 ** -40, 2.0 ** 40
 
 
 def assign_slots(block_tables, context_lens, new_tokens, free_blocks, num_free, rows, block_size):
-    """(slots, positions, starts, lengths, count, tables, stack) after the call, of valid arguments."""
+    """(slots, positions, starts, lengths, count, tables, stack) after the call, of valid arguments but for negative
+    entries in rows that are given back."""
     table, lens, stack = block_tables.clone(), context_lens.tolist(), free_blocks.tolist()
     new, count, width = new_tokens.tolist(), int(num_free), block_tables.shape[1]
     blocks = lambda n: -(-n // block_size)  # noqa: E731
     for b, n in enumerate(new):
         if n < 0:
             for k in range(blocks(lens[b])):
-                stack[count] = int(table[b, k])
-                count += 1
+                if int(table[b, k]) >= 0:
+                    stack[count] = int(table[b, k])
+                    count += 1
             lens[b] = 0
     slots, positions, starts = [], [], [0]
     asked_tokens = asked_blocks = used = 0

@@ -14,12 +14,15 @@
 // lengths and places of the stack in shared memory, and then takes its share of
 // the rows and table entries; so nothing is exchanged but one cluster barrier,
 // which parts what is read from what is written in place (lengths, the count, the
-// stack).  A lane takes two rows at once (their searches and look-ups overlap), a
+// stack).  Only where a row that is given back turns out to hold entries that name no
+// block does the stack get shorter behind the sums: it is then closed up and they are
+// made again.  A lane takes two rows at once (their searches and look-ups overlap), a
 // warp four rounds of table entries.  Bound: latency, a chain of dependent reads
 // (length, stack entry, table) between barriers, and with many rows the stores of 16
 // SMs: 32 sequences with a token each 3.9 us, 512 with 7900 new tokens and 24 that
-// end 6.0, 40 prompts in 65536 rows 5.8.  With 8 CTAs 3.8, 8.8 and 8.1; with one
-// 4.1, 18.6 and 38.
+// end 6.2, 40 prompts in 65536 rows 5.9.  With 8 CTAs 3.8, 8.8 and 8.1; with one
+// 4.1, 18.6 and 38 (before rows that are given back were looked through: 3.8, 5.9 and
+// 5.7 with 16).
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -101,9 +104,11 @@ __device__ __forceinline__ Ask ask_of(const SlotsParams& p, int b) {
   return a;
 }
 
-// A warp copies n entries, the loads of several rounds together.
-__device__ __forceinline__ void copy_entries(int32_t* to, const int32_t* from, int from_step, int n, int lane) {
+// A warp copies n entries, the loads of several rounds together; whether one of this
+// lane's is negative.
+__device__ __forceinline__ bool copy_entries(int32_t* to, const int32_t* from, int from_step, int n, int lane) {
   constexpr int kRounds = 4;
+  bool negative = false;
   for (int k0 = lane; k0 < n; k0 += 32 * kRounds) {
     int32_t v[kRounds];
 #pragma unroll
@@ -111,19 +116,23 @@ __device__ __forceinline__ void copy_entries(int32_t* to, const int32_t* from, i
       if (k0 + 32 * i < n) v[i] = from[(k0 + 32 * i) * from_step];
 #pragma unroll
     for (int i = 0; i < kRounds; ++i)
-      if (k0 + 32 * i < n) to[k0 + 32 * i] = v[i];
+      if (k0 + 32 * i < n) to[k0 + 32 * i] = v[i], negative |= v[i] < 0;
   }
+  return negative;
 }
 
 __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotsParams p) {
   extern __shared__ __align__(16) int32_t table_of_seqs[];  // [B+1] starts, [B] lengths, [B] places of the stack
   __shared__ long long room[3 * (kSlotWarps + 1)];
+  __shared__ int kept;  // entries of the stack once it has been closed up; -1: it need not be, -2: it has to be
   int32_t* starts = table_of_seqs;
   int32_t* lens = starts + p.num_seqs + 1;
   int32_t* tops = lens + p.num_seqs;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   const int tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) kept = -1;
+  cluster.barrier_arrive();  // behind it every CTA of the cluster has begun, and its `kept` is set
   grid_wait();
   grid_launch_dependents();
 
@@ -145,24 +154,27 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotsP
   const bool used = (tid & ~31) * per < p.num_seqs;
   block_scan<3>(sum, total, room, used);
   const int had = min(max(stored, 0), p.free_room);
-  const int count = static_cast<int>(min(static_cast<long long>(had) + total[0], static_cast<long long>(p.free_room)));
+  int count = static_cast<int>(min(static_cast<long long>(had) + total[0], static_cast<long long>(p.free_room)));
   if (rank == 0 && (bad || (tid == 0 && (stored != had || had + total[0] > p.free_room)))) atomicOr(p.err, kErrLen);
 
-  // who is served
-  long long got[2] = {0, 0}, all[2], want = sum[1], need = sum[2];
-  for (int b = b0; b < b1; ++b) {
-    const Ask a = b == b0 ? first : ask_of(p, b);
-    want += a.want, need += a.need;
-    const bool served = a.valid && want <= p.num_rows && (a.need == 0 || need <= count);
-    lens[b] = a.len;
-    // the place of its first block; of an ended sequence: where its blocks go, as -1 - place
-    tops[b] = a.ended ? -1 - static_cast<int>(min(had + sum[0], static_cast<long long>(p.free_room))) : static_cast<int>(count - 1 - (need - a.need));
-    if (a.ended) sum[0] += a.held;
-    got[0] += served ? a.want : 0;
-    got[1] += served ? a.need : 0;
-  }
-  block_scan<2>(got, all, room, used);
-  {
+  const int warps = ctas * kSlotWarps, warp = (tid >> 5) * ctas + rank;
+  const int round = (1 << p.log2_bs) - 1;
+  long long all[2];  // tokens and blocks granted
+  // who is served of `count` free blocks
+  const auto serve = [&](int count) {
+    long long got[2] = {0, 0}, back = sum[0], want = sum[1], need = sum[2];
+    for (int b = b0; b < b1; ++b) {
+      const Ask a = b == b0 ? first : ask_of(p, b);
+      want += a.want, need += a.need;
+      const bool served = a.valid && want <= p.num_rows && (a.need == 0 || need <= count);
+      lens[b] = a.len;
+      // the place of its first block; of an ended sequence: where its blocks go, as -1 - place
+      tops[b] = a.ended ? -1 - static_cast<int>(min(had + back, static_cast<long long>(p.free_room))) : static_cast<int>(count - 1 - (need - a.need));
+      if (a.ended) back += a.held;
+      got[0] += served ? a.want : 0;
+      got[1] += served ? a.need : 0;
+    }
+    block_scan<2>(got, all, room, used);
     long long w = sum[1], r = sum[2];
     int at = static_cast<int>(got[0]);
     for (int b = b0; b < b1; ++b) {
@@ -173,23 +185,43 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotsP
       at += served ? a.want : 0;
     }
     if (b1 == p.num_seqs && (b1 > b0 || tid == 0)) starts[p.num_seqs] = at;
-  }
-  __syncthreads();
+    __syncthreads();
+  };
+  serve(count);
 
   // blocks of ended sequences go on the stack; a warp a sequence
-  const int warps = ctas * kSlotWarps, warp = (tid >> 5) * ctas + rank;
-  const int round = (1 << p.log2_bs) - 1;
+  cluster.barrier_wait();
   if (total[0] > 0) {
+    bool negative = false;
     for (int b = warp; b < p.num_seqs; b += warps) {
       const int len = lens[b];
       if (tops[b] >= 0 || len < 0 || len > p.max_tokens || p.new_tokens[b] >= 0) continue;
       const int32_t* row = p.block_tables + b * p.bt_stride;
       const int held = static_cast<int>((static_cast<long long>(len) + round) >> p.log2_bs), to = -1 - tops[b];
-      copy_entries(p.free_blocks + to, row, 1, min(held, p.free_room - to), lane);
+      negative |= copy_entries(p.free_blocks + to, row, 1, min(held, p.free_room - to), lane);
     }
+    if (__builtin_expect(negative, 0))
+      for (int r = 0; r < ctas; ++r) *cluster.map_shared_rank(&kept, r) = -2;
   }
   // everything that is written in place below has been read by every CTA, and the stack is written
   cluster.sync();
+  if (__builtin_expect(total[0] > 0 && kept != -1, 0)) {
+    // what names no block leaves the stack, and what is there now is granted anew
+    if (rank == 0 && tid < 32) {
+      int to = had;
+      for (int k0 = had; k0 < count; k0 += 32) {
+        const int v = k0 + lane < count ? p.free_blocks[k0 + lane] : -1;
+        const unsigned good = __ballot_sync(kFullMask, v >= 0);
+        if (v >= 0) p.free_blocks[to + __popc(good & ((1u << lane) - 1u))] = v;
+        to += __popc(good);
+      }
+      if (lane < ctas) *cluster.map_shared_rank(&kept, lane) = to;
+      if (lane == 0) atomicOr(p.err, kErrBlock);
+    }
+    cluster.sync();
+    count = kept;
+    serve(count);
+  }
 
   const int rows = starts[p.num_seqs];
   const int top_step = p.num_seqs > 1 ? 1 << (31 - __clz(p.num_seqs - 1)) : 0;
