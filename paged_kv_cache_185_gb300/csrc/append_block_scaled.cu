@@ -17,10 +17,13 @@
 // (and in shared memory), and the same registers are then stored as codes.  What is
 // more is read twice, the second time from L2.  Which blocks there are is found on the
 // device from the packed starts; while a unit's elements are on their way the warp
-// looks up its next one.
+// looks up its next one.  Every CTA also looks at all the packed starts before it
+// writes, so that nothing is written where they decrease (16 chunks 17.9 us with and
+// 18.1 without; one token each of 1024 sequences, 4 heads of 128, 13.0 and 12.6, of
+// 16384, 1 head of 64, 48.2 and 45.6).
 //
 // Bound: memory, each element is read once and its code written.  16 chunks of up to
-// 1024 tokens, 8 heads of 128, bf16, block_size 16 (86 MB): 18.2 us, 0.71 of the
+// 1024 tokens, 8 heads of 128, bf16, block_size 16 (86 MB): 17.9 us, 0.72 of the
 // measured copy rate, the rest launch, first look-ups and the last round of units; 256
 // sequences with a token each 3.1 us, 8 2.4, both latency.  Warps a unit, measured with
 // 16 chunks of 1024 in blocks of 4096 elements: one 21.2 us, two 22.6; of 8192: one
@@ -33,7 +36,6 @@ namespace {
 
 constexpr int kAppendWarps = 4;        // of a CTA whose warps work by themselves
 constexpr int kWarpElements = 2048;    // that a warp holds
-constexpr int kStartsPerThread = 4;    // compared by the CTAs that check them
 
 // 16 bytes of elements: their largest magnitude so far (bits of f32 or packed
 // pairs; NaN never wins), and their values.
@@ -140,32 +142,36 @@ __global__ void __launch_bounds__(append_threads(WPU), append_warps_per_sm(WPU) 
   grid_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x < p.check_ctas) {  // starts that decrease are recorded whether or not a unit meets them
-#pragma unroll
-    for (int k = 0; k < kStartsPerThread; ++k) {
-      const int64_t i = (int64_t(blockIdx.x) * kStartsPerThread + k) * blockDim.x + threadIdx.x;
-      if (i < p.num_seqs && p.query_start_loc[i + 1] < p.query_start_loc[i]) atomicOr(p.err, kErrLen);
-    }
-    return;
-  }
   const int part = WPU == 1 ? 0 : warp;  // of the unit
   const bool speaker = lane == 0 && part == 0;
   const int bs = 1 << p.log2_bs;
   int64_t slots = p.num_seqs;  // of every head, K and V
   int row_first = 0;
+  bool falls = false;  // a start that decreases
   if (p.query_start_loc != nullptr) {
+    constexpr int kThreads = 32 * (WPU == 1 ? kAppendWarps : WPU), kStarts = 4;  // of a thread, asked for together
+    for (int i0 = threadIdx.x; i0 < p.num_seqs; i0 += kStarts * kThreads) {
+      int here[kStarts], behind[kStarts];
+#pragma unroll
+      for (int k = 0; k < kStarts; ++k) {
+        const int i = min(i0 + k * kThreads, p.num_seqs - 1);
+        here[k] = p.query_start_loc[i], behind[k] = p.query_start_loc[i + 1];
+      }
+#pragma unroll
+      for (int k = 0; k < kStarts; ++k) falls |= behind[k] < here[k];
+    }
     row_first = p.query_start_loc[0];
     const int64_t total = int64_t(p.query_start_loc[p.num_seqs]) - row_first;
     if (total < 0 || total > p.num_tokens || total > int64_t(p.num_seqs) * p.max_tokens) {
-      if (blockIdx.x == p.check_ctas && threadIdx.x == 0) atomicOr(p.err, kErrLen);
+      if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrLen);
       return;
     }
     slots = (total >> p.log2_bs) + 2 * int64_t(p.num_seqs);
   }
   const int sides = 2 * p.num_kv_heads;
   const int64_t units = slots * sides;
-  const int64_t first = int64_t(blockIdx.x - p.check_ctas) * kUnitsPerCta + (WPU == 1 ? warp : 0);
-  const int64_t stride = int64_t(gridDim.x - p.check_ctas) * kUnitsPerCta;
+  const int64_t first = int64_t(blockIdx.x) * kUnitsPerCta + (WPU == 1 ? warp : 0);
+  const int64_t stride = int64_t(gridDim.x) * kUnitsPerCta;
   struct Unit {
     const T* src;    // first new element
     uint8_t* codes;  // of the block and head
@@ -224,6 +230,11 @@ __global__ void __launch_bounds__(append_threads(WPU), append_warps_per_sm(WPU) 
   int turn = 0;
   Unit u, next{};
   if (first < units) locate(first, next);
+  // every CTA looks at all the starts, so that none writes where they are not what they have to be
+  if (p.query_start_loc != nullptr && __syncthreads_or(falls)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, kErrLen);
+    return;
+  }
   for (int64_t unit = first; unit < units; unit += stride) {
     u = next;
     // the new elements: into registers, or through them where there are more
@@ -309,17 +320,15 @@ __global__ void __launch_bounds__(append_threads(WPU), append_warps_per_sm(WPU) 
 }
 
 template <typename T, int D, int WPU>
-int launch_one(ScaledAppendParams p, int num_sms, cudaStream_t stream) {
+int launch_one(const ScaledAppendParams& p, int num_sms, cudaStream_t stream) {
   constexpr int kThreads = append_threads(WPU), kUnits = WPU == 1 ? kAppendWarps : 1;
-  constexpr int kStarts = kStartsPerThread * kThreads;
   // packed: how many blocks the chunks touch is on the device; as many CTAs as that can be, or as run at once
   const int64_t slots = p.query_start_loc == nullptr ? p.num_seqs : (int64_t(p.num_tokens) >> p.log2_bs) + 2 * int64_t(p.num_seqs);
   const int64_t units = slots * 2 * p.num_kv_heads, resident = int64_t(num_sms) * (append_warps_per_sm(WPU) * 32 / kThreads);
-  p.check_ctas = p.query_start_loc != nullptr ? static_cast<unsigned>((int64_t(p.num_seqs) + kStarts - 1) / kStarts) : 0u;
   int64_t ctas = (units + kUnits - 1) / kUnits;
   if (ctas > resident) ctas = resident;
-  return launch_dependent(&append_block_scaled_kernel<T, D, WPU>, dim3(static_cast<unsigned>(ctas) + p.check_ctas), dim3(kThreads),
-                          0, 0, stream, p);
+  return launch_dependent(&append_block_scaled_kernel<T, D, WPU>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, 0,
+                          stream, p);
 }
 
 template <typename T, int D>
@@ -342,7 +351,7 @@ int launch_type(const ScaledAppendParams& p, int head_dim, int num_sms, cudaStre
 
 }  // namespace
 
-int launch_append_block_scaled(int dtype, int head_dim, ScaledAppendParams p, int num_sms, cudaStream_t stream) {
+int launch_append_block_scaled(int dtype, int head_dim, const ScaledAppendParams& p, int num_sms, cudaStream_t stream) {
   int e;
   switch (dtype) {
     case 0: e = launch_type<float>(p, head_dim, num_sms, stream); break;

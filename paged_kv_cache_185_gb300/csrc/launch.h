@@ -307,10 +307,9 @@ struct ScaledAppendParams {
   int num_seqs, num_tokens, num_kv_heads, num_blocks, log2_bs;
   int max_tokens;                 // the most a block table row can name
   int vec;                        // rows at 16-byte boundaries
-  unsigned check_ctas;            // set by the launch: leading CTAs that check query_start_loc
   int* err;
 };
-int launch_append_block_scaled(int dtype, int head_dim, ScaledAppendParams p, int num_sms, cudaStream_t stream);
+int launch_append_block_scaled(int dtype, int head_dim, const ScaledAppendParams& p, int num_sms, cudaStream_t stream);
 
 // Decode attention over such a cache (decode_block_scaled.cu).
 struct ScaledDecodeParams {
