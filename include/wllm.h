@@ -572,7 +572,8 @@ int wllm_paged_attention_decode_sparse_fp8(const wllm_tensor* out, const wllm_te
  * most T, and need_b = 0 or the need of it and of those before it is at most
  * the number of free blocks (those that L + n <= M_b bs leaves out count for
  * neither sum).  One that is not served gets nothing and stays as it was:
- * query_start_loc and context_lens_out say so.
+ * query_start_loc and context_lens_out say so.  Calls that take a row for each
+ * sequence instead of query_start_loc fit steps that serve all with one token.
  * A block belongs to one sequence here (shared ones are the block manager's).
  * Lengths outside [0, M_b bs], a sum L + n above it, a num_free outside [0, F]
  * and blocks given back beyond F set bit 2 of the error word (the sequence is
@@ -603,6 +604,12 @@ int wllm_assign_slots(const wllm_tensor* slot_mapping, const wllm_tensor* positi
  *                    n_b = query_start_loc[b+1] - query_start_loc[b] tokens are
  *                    the rows from query_start_loc[b] on.  NULL: T is B, and row
  *                    b is the last token of sequence b (no token where L_b = 0).
+ *                    NULL is for steps in which every sequence that is not empty
+ *                    has got exactly one token: of one that has got none (not
+ *                    served, or n_b = 0 in wllm_assign_slots) it would store the
+ *                    last token again, from row b, and nothing could tell.  What
+ *                    wllm_assign_slots writes to query_start_loc is right in every
+ *                    case, with the rows packed as its slots and positions are.
  *
  * For each block that gets new tokens, each kv head, and K and V by themselves:
  * with m the largest finite magnitude of the new elements,
@@ -633,7 +640,9 @@ int wllm_reshape_and_cache_block_scaled(const wllm_tensor* key, const wllm_tenso
  * Paged decode attention over such a cache:
  *   out[b][h] = sum_j softmax_j(scale * q.K_j) * V_j
  * out, q, block_tables, context_lens, num_kv_heads, scale and block_size as in
- * wllm_paged_attention_decode_fp8; q and out F16 or BF16 with rows of any
+ * wllm_paged_attention_decode_fp8 (row b is a query of sequence b: where
+ * wllm_assign_slots has not served every sequence with one token, rows are packed
+ * and the prefill below takes them); q and out F16 or BF16 with rows of any
  * alignment, out apart from q; D 64 (block_size >= 16), 128 or 256.  Codes are widened to f16
  * exactly; query rows are taken to f16 after a power of two has been divided
  * out of each, so their size does not matter; the weights, the value's scale in

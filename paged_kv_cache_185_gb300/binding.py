@@ -382,7 +382,8 @@ def assign_slots(slot_mapping, query_start_loc, block_tables, context_lens, new_
     and gives its blocks back), from ``context_lens`` [B] and the stack ``free_blocks`` [F] of ``num_free`` [1] blocks.
 
     Writes ``slot_mapping`` [T] and ``positions`` [T] (packed, then -1 and 0), ``query_start_loc`` [B+1], the tables'
-    new entries, and the lengths and count afterwards (in place unless ``..._out`` are given).  Returns
+    new entries, and the lengths and count afterwards (in place unless ``..._out`` are given).  A sequence for which rows
+    or blocks do not suffice is not served: it gets no row, and the rows of those behind it move up.  Returns
     ``slot_mapping``."""
     _call("wllm_assign_slots", (slot_mapping, positions, query_start_loc,
                                 context_lens if context_lens_out is None else context_lens_out,
@@ -395,7 +396,11 @@ def reshape_and_cache_block_scaled(key, value, k_cache, v_cache, k_scales, v_sca
                                    block_size: int, query_start_loc=None) -> None:
     """KV append into E4M3 caches with a scale for each block and head, ``k_scales`` and ``v_scales`` [N_b,Hkv] F32: the
     last ``query_start_loc[b+1] - query_start_loc[b]`` tokens of each sequence, or one each.  Scales are powers of two;
-    they rise where the new tokens need it (earlier tokens of the block are stored again)."""
+    they rise where the new tokens need it (earlier tokens of the block are stored again).
+
+    Without ``query_start_loc`` every sequence that is not empty must have got exactly one token; where assign_slots may
+    have served a sequence with none, pass what it wrote to ``query_start_loc`` (row b would else be stored over the last
+    token of sequence b)."""
     _call("wllm_reshape_and_cache_block_scaled", (key, value, k_cache, v_cache, k_scales, v_scales, block_tables,
                                                   context_lens, query_start_loc), int(block_size))
 
@@ -418,7 +423,8 @@ def block_scaled_workspace(device=None) -> torch.Tensor:
 
 def paged_attention_decode_block_scaled(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                                         num_kv_heads: int, scale: float, block_size: int, workspace=None) -> torch.Tensor:
-    """Paged decode attention over E4M3 caches with a scale for each block and head; returns ``out``.
+    """Paged decode attention over E4M3 caches with a scale for each block and head; returns ``out``.  Row b is a query of
+    sequence b; steps of packed rows (assign_slots with a sequence that got no token) go to the prefill call.
 
     ``workspace``: from block_scaled_workspace(); by default a call takes one from torch's allocator, which orders it by
     the stream (and keeps it with the graph that the call is captured in)."""
