@@ -783,15 +783,10 @@ int launch_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, ScaledDecodePa
   constexpr int kSmem = static_cast<int>(sizeof(Shared<D, NT>));
   static_assert(S::kPart <= kMostPart, "the workspace has room for every form's partial results");
   const void* kernel = reinterpret_cast<const void*>(&decode_block_scaled_kernel<D, NT>);
-  static std::atomic<int> configured[64], found{0};
-  int e = raise_smem_limit(configured, kernel, kSmem);
+  static std::atomic<int> configured[64], found[64];
+  int blocks = 0, e = raise_smem_limit(configured, kernel, kSmem);
   if (e != cudaSuccess) return e;
-  int blocks = found.load(std::memory_order_relaxed);
-  if (blocks == 0) {
-    const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, &decode_block_scaled_kernel<D, NT>, kThreads, kSmem);
-    if (err != cudaSuccess) return err;
-    found.store(blocks, std::memory_order_relaxed);
-  }
+  if ((e = resident_ctas(found, &decode_block_scaled_kernel<D, NT>, kThreads, kSmem, &blocks)) != cudaSuccess) return e;
   const unsigned ctas = static_cast<unsigned>(ctas_of(num_sms, blocks));
   p.rows = reinterpret_cast<uint8_t*>(p.parts) + size_t(ctas) * 2 * S::kPart * sizeof(float);
   e = launch_dependent(&decode_block_scaled_kernel<D, NT>, dim3(ctas), dim3(kThreads), kSmem, 0, stream, kmap, vmap, p);

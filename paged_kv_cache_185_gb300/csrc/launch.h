@@ -46,6 +46,21 @@ inline int raise_smem_limit(std::atomic<int>* configured, const void* func, int 
   return cudaSuccess;
 }
 
+// CTAs of a kernel that run at once on an SM of the current device: `found` is the
+// kernel's own per-device record (64 entries, 0: not asked yet).
+template <typename... P>
+int resident_ctas(std::atomic<int>* found, void (*kernel)(P...), int threads, size_t smem, int* ctas) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool tracked = dev >= 0 && dev < 64;
+  *ctas = tracked ? found[dev].load(std::memory_order_relaxed) : 0;
+  if (*ctas > 0) return cudaSuccess;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kernel, threads, smem);
+  if (e == cudaSuccess && tracked) found[dev].store(*ctas, std::memory_order_relaxed);
+  return e;
+}
+
 // Launch as a programmatic dependent of the kernel before it in the stream: its
 // CTAs may start early, so the kernel calls grid_wait() before it touches global
 // memory.  `cluster` > 0: thread-block clusters of that many CTAs along x.

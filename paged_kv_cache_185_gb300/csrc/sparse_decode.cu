@@ -671,18 +671,10 @@ struct SparseForm {
                                   HT * 8 * sizeof(float) + SparseMath<T, F8, D, HT>::type::kQueryBytes;
 
   static int resident(int* blocks) {
-    static std::atomic<int> configured[64], found{0};
+    static std::atomic<int> configured[64], found[64];
     const int e = raise_smem_limit(configured, reinterpret_cast<const void*>(&sparse_kernel<T, F8, D, HT, DEEP>),
                                    static_cast<int>(kSmem));
-    if (e != cudaSuccess) return e;
-    *blocks = found.load(std::memory_order_relaxed);
-    if (*blocks == 0) {
-      const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, &sparse_kernel<T, F8, D, HT, DEEP>,
-                                                                            Tune::kWarps * 32, kSmem);
-      if (err != cudaSuccess) return err;
-      found.store(*blocks, std::memory_order_relaxed);
-    }
-    return cudaSuccess;
+    return e != cudaSuccess ? e : resident_ctas(found, &sparse_kernel<T, F8, D, HT, DEEP>, Tune::kWarps * 32, kSmem, blocks);
   }
 
   static int launch(const CUtensorMap& kmap, const CUtensorMap& vmap, const SparseParams& p, int ctas, cudaStream_t stream) {
