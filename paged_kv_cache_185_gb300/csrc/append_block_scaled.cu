@@ -109,10 +109,6 @@ __device__ __forceinline__ float scale_for(float m) {
   const int e = static_cast<int>((__float_as_uint(m) + 0x1fffffu) >> 23) - 127 - 8;
   return __uint_as_float(static_cast<uint32_t>(127 + min(max(e, kLeastScaleExp), kMostScaleExp)) << 23);
 }
-__device__ __forceinline__ float scale_in_range(float s) {
-  constexpr float kLeast = 1.f / (1ull << -kLeastScaleExp), kMost = static_cast<float>(1ull << kMostScaleExp);
-  return fminf(fmaxf(s, kLeast), kMost);  // a NaN counts as the least
-}
 
 // Four codes times f, rounded again.
 __device__ __forceinline__ uint32_t rescaled(uint32_t codes, float f) {

@@ -24,6 +24,21 @@ enum : int {
 
 constexpr unsigned kFullMask = 0xffffffffu;
 
+// Exponents of the scales that the block-scaled append writes, and the range
+// that the attention over such a cache takes.
+constexpr int kLeastScaleExp = -40, kMostScaleExp = 40;
+__device__ __forceinline__ float scale_in_range(float s) {
+  constexpr float kLeast = 1.f / (1ull << -kLeastScaleExp), kMost = static_cast<float>(1ull << kMostScaleExp);
+  return fminf(fmaxf(s, kLeast), kMost);  // a NaN counts as the least
+}
+
+// log2(x), approximate, of a normal number.
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -88,6 +103,15 @@ __device__ __forceinline__ bool mbar_try_both(uint32_t bar_a, uint32_t parity_a,
       : "r"(bar_a), "r"(parity_a), "r"(bar_b), "r"(parity_b)
       : "memory");
   return ok != 0;
+}
+
+// An asynchronous copy of 4 bytes to shared memory (cp.async, of this thread's).
+__device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+// One of the barrier's arrivals, once this thread's asynchronous copies have landed.
+__device__ __forceinline__ void arrive_behind_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Programmatic dependent launch: wait until the kernels before this one in the

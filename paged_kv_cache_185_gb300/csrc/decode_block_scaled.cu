@@ -72,23 +72,6 @@ struct Shape {
   static constexpr int kPart = kOut + 2 * kHeads;        // floats of a partial result: outputs, maxima, sums
 };
 
-__device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
-}
-// One of the barrier's arrivals, once this thread's asynchronous copies have landed.
-__device__ __forceinline__ void arrive_behind_copies(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ float scale_in_range(float s) {
-  constexpr float kLeast = 1.f / (1ull << -kLeastScaleExp), kMost = static_cast<float>(1ull << kMostScaleExp);
-  return fminf(fmaxf(s, kLeast), kMost);  // a NaN counts as the least
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

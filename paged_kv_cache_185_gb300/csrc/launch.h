@@ -303,10 +303,6 @@ struct SlotsParams {
 constexpr int kMaxSlotSeqs = 16384;  // their starts, lengths and places sit in a CTA's shared memory
 int launch_assign_slots(const SlotsParams& p, cudaStream_t stream);
 
-// Exponents of the scales that the block-scaled append writes, and the range
-// that the attention takes.
-constexpr int kLeastScaleExp = -40, kMostScaleExp = 40;
-
 // The append into E4M3 caches with a scale a block and head
 // (append_block_scaled.cu).  A null query_start_loc means one new token a
 // sequence.  Strides in elements.

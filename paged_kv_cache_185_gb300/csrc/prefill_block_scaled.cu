@@ -193,21 +193,6 @@ struct Items {
   }
 };
 
-__device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
-}
-__device__ __forceinline__ void arrive_behind_copies(uint32_t bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ float scale_in_range(float s) {
-  constexpr float kLeast = 1.f / (1ull << -kLeastScaleExp), kMost = static_cast<float>(1ull << kMostScaleExp);
-  return fminf(fmaxf(s, kLeast), kMost);  // a NaN counts as the least
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t h2(float lo, float hi) { return Mma<__half>::pack(lo, hi); }
 // Two elements at once.
 __device__ __forceinline__ void fma2(float& x, float& y, float by, float add) {
