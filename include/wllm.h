@@ -646,8 +646,8 @@ int wllm_reshape_and_cache_block_scaled(const wllm_tensor* key, const wllm_tenso
  * alignment, out apart from q; D 64 (block_size >= 16), 128 or 256.  Codes are widened to f16
  * exactly; query rows are taken to f16 after a power of two has been divided
  * out of each, so their size does not matter; the weights, the value's scale in
- * them, go to their product in two words of f16 (22 bits); statistics and sums
- * are fp32.
+ * them, go to their product in two words of f16 (22 bits); scores, statistics
+ * and sums are fp32 (a score beyond its range gives NaN).
  *
  *   workspace        [n] WLLM_FP8_E4M3 (bytes), contiguous, 256-byte aligned, n
  *                    at least wllm_block_scaled_workspace_bytes(); what is in it

@@ -31,6 +31,9 @@ __device__ __forceinline__ float scale_in_range(float s) {
   constexpr float kLeast = 1.f / (1ull << -kLeastScaleExp), kMost = static_cast<float>(1ull << kMostScaleExp);
   return fminf(fmaxf(s, kLeast), kMost);  // a NaN counts as the least
 }
+// The most that a query row's factor may be: times any scale it stays finite, so that a raw score of zero stays zero.
+// (A larger one makes scores that are not equal so unequal that one token has all the weight, with or without it.)
+constexpr float kMostRowFactor = static_cast<float>(1ull << 62) * (1ull << (127 - 62 - kMostScaleExp));
 
 // log2(x), approximate, of a normal number.
 __device__ __forceinline__ float lg2(float x) {

@@ -187,7 +187,8 @@ struct Math {
       const float top = to_f32(*reinterpret_cast<const T*>(&top_bits));
       const int field = min(max(127 + 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 1), 253);
       const float up = __uint_as_float(static_cast<uint32_t>(field) << 23);
-      const float down = __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * scale_log2;
+      const float undo = __uint_as_float(static_cast<uint32_t>(254 - field) << 23) * scale_log2;
+      const float down = fminf(fmaxf(undo, -kMostRowFactor), kMostRowFactor);
 #pragma unroll
       for (int s = 0; s < kKS; ++s)
 #pragma unroll

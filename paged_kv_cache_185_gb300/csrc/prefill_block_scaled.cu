@@ -645,8 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (same_rows) asm volatile("bar.sync 1, %0;" ::"r"(4 * kStreams * 32) : "memory");
     }
     // of a raw score, without the block's scale: what undoes the row's, times the scale's magnitude; positive
-    const float sl2 =
-        p.scale_log2 == 0.f ? 1.f : __uint_as_float((254u - sh.row_field[same_rows ? 0 : x][r]) << 23) * fabsf(p.scale_log2);
+    const float sl2 = p.scale_log2 == 0.f ? 1.f
+                                          : fminf(__uint_as_float((254u - sh.row_field[same_rows ? 0 : x][r]) << 23) * fabsf(p.scale_log2),
+                                                  kMostRowFactor);
     float m = kNone, l = 0.f;
     const int n = steps[x];
     // rows behind the last get no weights: what the products make of the places they leave stays in such rows
