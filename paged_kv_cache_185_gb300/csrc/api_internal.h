@@ -1,6 +1,7 @@
 // api_internal.h -- what the translation units behind the C ABI share: status
 // and message of a failed call, per-device state, and descriptor checks.
-// Defined in api.cu; not part of the public header.
+// Defined in api.cu, from spans_meet to check_pool_args in api_sparse.cu; not part
+// of the public header.
 #pragma once
 
 #include <cuda.h>

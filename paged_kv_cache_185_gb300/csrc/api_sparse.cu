@@ -42,8 +42,8 @@ int locked_state(DeviceState** s) {
   return device_state(s);
 }
 
-// A block pool [N_b][Hkv][bs][D], its table rows and lengths: what the three
-// block-sparse calls share.
+// A block pool [N_b][Hkv][bs][D], its table rows and lengths: what the block-sparse
+// and the block-scaled calls share.
 int check_tables(const wllm_tensor* block_tables, const wllm_tensor* context_lens, int64_t B, int64_t nb, int64_t bs) {
   if (block_tables->dtype != WLLM_I32) return fail(WLLM_ERR_INVALID_ARG, "block_tables: dtype must be I32");
   if (context_lens->dtype != WLLM_I32) return fail(WLLM_ERR_INVALID_ARG, "context_lens: dtype must be I32");

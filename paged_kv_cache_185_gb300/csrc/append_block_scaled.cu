@@ -26,8 +26,8 @@
 // 1024 tokens, 8 heads of 128, bf16, block_size 16 (86 MB): 17.9 us, 0.72 of the
 // measured copy rate, the rest launch, first look-ups and the last round of units; 256
 // sequences with a token each 3.1 us, 8 2.4, both latency.  Warps a unit, measured with
-// 16 chunks of 1024 in blocks of 4096 elements: one 21.2 us, two 22.6; of 8192: one
-// 25.5, two 23.6, four 23.7; of 16384: one 26.9, two 27.6, four 24.5, eight 25.4.
+// 16 chunks of 1024 in blocks of 4096 elements: one 19.8 us, two 19.8, four 27.6; of
+// 8192: one 23.9, two 21.9, four 21.2; of 16384: one 24.9, two 22.5, four 22.4.
 #include "common.cuh"
 #include "launch.h"
 

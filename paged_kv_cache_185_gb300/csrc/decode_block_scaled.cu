@@ -20,7 +20,7 @@
 // largest.  One word put up to 2^-12 of each weight into the output, as much as the
 // rounding of an f16 output.  The second product costs little where memory sets the
 // pace: 8 sequences of 32K to 131K 225 us with it and 228 without, 256 of 300 to 6000
-// 147.6 and 145.6, one of 16000 12.7 and 12.5.
+// 147.6 and 145.6, one of 16000 12.5 and 12.5.
 //
 // Work split: all units, ordered by sequence, kv head and head tile, are cut into
 // as many equal runs as CTAs fit the GPU, so that rows of any length fill it
@@ -35,7 +35,7 @@
 // Bound: memory, each code is read once.  8 sequences of 32K to 131K tokens, 32/8
 // heads of 128 (1407 MB): 225 us, 0.94 of the measured copy rate; 256 of 300 to 6000,
 // 28/4 heads (829 MB): 148 us, 0.84, the rest the setup and the ends of 4 rows a CTA;
-// one of 16000, 32/4 heads of 64 (8 MB): 12.7 us, all latency.  What it took (with
+// one of 16000, 32/4 heads of 64 (8 MB): 12.5 us, all latency.  What it took (with
 // weights of one word): warps that wait for nothing at a row's end 171 us instead of
 // 235 (256 sequences), the quarters merged behind the next unit 153, partial results
 // merged by the second kernel instead of the CTA that counts in last, and entries
@@ -436,8 +436,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     total += sh.sums[w];
   }
   // a run has the units of a mean row at least, up to kLeastUnits a warp: a long row in fewer pieces has fewer results to
-  // merge, but a CTA with many short rows has an end for each.  One sequence of 16000 tokens, 4 kv heads of 64: 12.1 us with
-  // 1 unit a warp at least, 12.4 with 4, 15.6 with 8; 96 of 4 tokens, 4 kv heads of 128: 9.5 us, 40 without the mean row
+  // merge, but a CTA with many short rows has an end for each.  One sequence of 16000 tokens, 4 kv heads of 64: 12.4 us with
+  // 1 unit a warp at least, 12.5 with 4, 16.1 with 8; 96 of 4 tokens, 4 kv heads of 128: 9.6 us, 41 without the mean row
   const long long least = max(1ll, min(static_cast<long long>(kWarps * kLeastUnits), quotient(total, p.num_seqs)));
   total *= rows;
   const long long ctas = max(1ll, min(static_cast<long long>(gridDim.x), quotient(total, least)));

@@ -13,8 +13,8 @@
 // numbers of f16 down to 2^-21.  They go to the products as two words of f16 (what the
 // first leaves off is the second): 22 bits, or 2^-32 of the largest.  One word put up to
 // 2^-12 of each weight into the output, as much as the rounding of an f16 output; the
-// second costs 24 us of the 409 of 8 chunks of 1024 (below) to make and 57 to multiply,
-// and 8 of the 84 of 64 drafts.  (Cut off by a mask instead of rounded 433, with the sums of
+// second costs 24 us of the 410 of 8 chunks of 1024 (below) to make and 57 to multiply,
+// and 8 of the 85 of 64 drafts.  (Cut off by a mask instead of rounded 433, with the sums of
 // two at once 419 and 8 registers spilled.)  l sums the weights before they are rounded:
 // behind a small vs a weight may round to nothing and still count in l.
 //
@@ -36,7 +36,7 @@
 //     tokens][128 bytes], swizzled).  V rows past the context become zeros, and so do
 //     NaN codes (their first tokens are kept, and rows that see them get NaN at the
 //     end).  With K: the factors that each run of 8 tokens gives the softmax.
-//     (Codes through registers instead of raw slots: what an SM has in flight is then
+//     (With weights of one word: codes through registers instead of raw slots, what an SM has in flight is then
 //     bound by the little L1 that is left, 490 us instead of 372 for 8 chunks of 1024.
 //     A warp an item instead of a pair: 369 instead of 346, more of the few slots are
 //     then being written);
@@ -50,14 +50,14 @@
 // kernel, a programmatic dependent, merges them in their order.
 //
 // Bound: 8 chunks of 1024 tokens behind up to 5000 earlier ones, 28/4 heads of 128,
-// block_size 16 (337 GFLOP): 409 us, 825 TFLOP/s, 0.43 of the measured cuBLAS rate.
+// block_size 16 (337 GFLOP): 410 us, 822 TFLOP/s, 0.43 of the measured cuBLAS rate.
 // A step of 64 tokens takes 1.19 us and moves 224 KB through shared memory (the Q tile
 // for the scores, codes in and out, the products' operands, V twice), which alone takes
 // 0.93.
-// Chunks of 5 tokens of 64 sequences (300 to 6000 tokens, same heads; 211 MB): 84 us,
-// 0.38 of the copy rate: 35 of 128 rows are used, and each step waits for its codes
+// Chunks of 5 tokens of 64 sequences (300 to 6000 tokens, same heads; 211 MB): 85 us,
+// 0.37 of the copy rate: 35 of 128 rows are used, and each step waits for its codes
 // to be widened.  One chunk of 100 tokens, 32/8 heads, 2100 tokens: 28 us, latency
-// (look-ups, 3 us of query rows, 6 or 7 steps, 3 us of outputs, the second kernel).
+// (look-ups, 3 us of query rows, 4 or 5 steps, 3 us of outputs, the second kernel).
 //
 // Every wait is bounded; on a timeout the CTA records the error, waits (bounded)
 // for its MMAs in flight, frees its tensor memory and returns.
@@ -946,8 +946,9 @@ int launch_prefill_block_scaled(int dtype, int head_dim, const CUtensorMap& kmap
   if (blocks <= 0) return cudaSuccess;
   // CTAs for a row block's context: as many as the SMs allow, or as three quarters of them do if that makes a CTA's run
   // longer by 4 steps at most: the merge's CTAs then start beside them instead of behind them (they find no registers on an
-  // SM that has one).  One chunk of 100 tokens, 32/8 heads: 7 instead of 9 CTAs a block 26.2 us instead of 29.9 (2100 tokens),
-  // 9 instead of 6 79.9 instead of 96.8 (30000), one 44.0 (2100).  How long the contexts are only the device knows.
+  // SM that has one).  One chunk of 100 tokens, 32/8 heads: 7 instead of 9 CTAs a block 27.9 us instead of 32.9 (2100 tokens),
+  // 9 instead of 7 103 instead of 111 (30000), one 50 (2100).  How long the contexts are only the device knows, and how many
+  // of the batch's places are in use: in a batch padded to 64 places one live sequence has one CTA a block.
   const int64_t tiles = (int64_t(p.base.max_blocks) * p.base.block_size + 2 * kStep - 1) / (2 * kStep);
   const auto splits_on = [&](int64_t sms) {
     const int64_t most_splits = tiles < kMostSplits ? tiles : kMostSplits, s = sms / (blocks * p.base.num_kv_heads);

@@ -5,8 +5,9 @@
 // Conventions used by the kernels of this library:
 //   - one warp allocates and frees the CTA's TMEM columns (a power of two
 //     >= 32); the allocation is freed on every exit path;
-//   - one thread issues every tcgen05.mma of a CTA (cta_group::1, kind::f16,
-//     fp32 accumulation, M = 128: accumulator row i lives in TMEM lane i);
+//   - one thread issues every tcgen05.mma of an accumulator (cta_group::1,
+//     kind::f16, fp32 accumulation, M = 128: accumulator row i lives in TMEM
+//     lane i); a CTA with two row tiles has two such threads, a warp each;
 //   - operands sit in shared memory with the 128-byte swizzle: 8-row x
 //     128-byte atoms, 1024-byte aligned, the 16-byte chunk c of row r stored
 //     at chunk position c ^ (r % 8) -- the layout a TMA copy with
